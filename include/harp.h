@@ -75,7 +75,8 @@ typedef enum {
   HARP_F32 = 0,  /* IEEE binary32                                  */
   HARP_BF16 = 1, /* bfloat16 (upper half of a binary32)            */
   HARP_I8 = 2,   /* int8 code with one fp32 scale per block        */
-  HARP_F64 = 3   /* IEEE binary64 (parameters only)                */
+  HARP_F64 = 3,  /* IEEE binary64 (parameters only)                */
+  HARP_E8M0 = 4  /* a power of two, 2^(byte - 127) (scales only)   */
 } harp_dtype;
 
 #define HARP_MAX_STAGES 16
@@ -327,6 +328,116 @@ harp_status rht_compose(const harp_schedule* s, int64_t d, const int8_t* signs,
                         int32_t k, const void* x, int64_t ldx, void* y,
                         int64_t ldy, int64_t rows, harp_dtype io_dtype,
                         int32_t inverse, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Rotated layers in 8 bits: what a rotated row or weight is turned into
+ * [TS §1-§3: the rotation's purpose is low-bit storage of what it mixes].
+ *
+ * Coded matrices.  A coded matrix of R rows and C columns is
+ *   codes:  R x C bytes, E4M3 (1 sign, 4 exponent, 3 mantissa bits, largest
+ *           value 448, no infinity, 0x7f / 0xff = NaN), row stride in bytes;
+ *   scales: one per block, [ceil(R / block_rows)][ceil(C / 128)], contiguous,
+ *           fp32 (HARP_F32, 4-byte aligned) or a power of two (HARP_E8M0, one
+ *           byte).  A block is block_rows x 128 (the last ones may be
+ *           smaller): 1 x 128 for rows (activations), 128 x 128 for weights.
+ * Element (r, c) stands for code * scale of its block.
+ *
+ * Coding rule.  scale = max(max|v| / 448, 2^-120) over the block, for
+ * HARP_E8M0 rounded up to a power of two; code = v / scale rounded to nearest,
+ * ties to even.  The quotient is taken with the scale before its rounding to
+ * fp32 and is an fp32 value.  A block that holds a NaN or an infinity (or, in
+ * the norm, whose row's 1/rms is not finite) gets a NaN scale (E8M0: 255) and
+ * NaN codes.
+ *
+ * The transpose of a 128 x 128-coded matrix is its transposed codes with its
+ * transposed scales.
+ *
+ * Sizes: rows, n, k and cols at most 2^30; row strides at least the row
+ * length.  Any length and alignment is computed; the products' fastest loads
+ * need 16-byte aligned bases and row strides and lengths of whole 16 bytes.
+ * Outputs must not overlap inputs except where said.
+ * ---------------------------------------------------------------------- */
+
+/* Codes and scales of rows x cols values (F32 or BF16), in blocks of
+ * block_rows x 128, block_rows 1 or 128.  rows == 0 returns HARP_OK without a
+ * launch; cols >= 1. */
+harp_status harp_quantize_q8(const void* x, int64_t ldx, harp_dtype x_dtype,
+                             int64_t rows, int64_t cols, int32_t block_rows,
+                             uint8_t* codes, int64_t ldc, void* scales,
+                             harp_dtype scale_dtype, hipStream_t stream);
+
+/* Residual addition, root-mean-square norm and coding of each row:
+ *   h = x + residual (residual NULL: h = x),  r = 1 / sqrt(mean(h^2) + eps),
+ *   codes, scales = 1 x 128 coding of  h * r * gamma  (gamma NULL: all ones).
+ * h and r are fp32 inside; h_out (needs a residual; NULL: not written)
+ * receives h rounded once.  rstd (NULL: not written): r, one fp32 per row.
+ * ckpt_codes, ckpt_scales (both or neither, only with gamma): the coding of
+ * h * r, what harp_rmsnorm_q8_vjp reads; without gamma `codes` is that.
+ * x, residual, gamma (d values) and h_out are io_dtype, F32 or BF16.  h_out
+ * may be x or residual (with the same leading dimension).
+ * 1 <= d <= HARP_MAX_D; eps >= 0; rows == 0 returns HARP_OK without a launch. */
+harp_status harp_rmsnorm_q8(const void* x, int64_t ldx, const void* residual,
+                            int64_t ldr, const void* gamma, float eps,
+                            void* h_out, int64_t ldh, uint8_t* codes,
+                            int64_t ldc, void* scales, float* rstd,
+                            uint8_t* ckpt_codes, int64_t ldk, void* ckpt_scales,
+                            harp_dtype scale_dtype, int64_t rows, int64_t d,
+                            harp_dtype io_dtype, hipStream_t stream);
+
+/* Reverse mode of the norm from its 8-bit checkpoint.  With n = the coded
+ * h * r (codes, scales 1 x 128) and r = rstd, for an upstream gradient dn of
+ * the norm's output and dres of h_out (NULL: zero):
+ *   u = gamma * dn,   dh = dres + r * (u - n * mean(u * n)),
+ *   dgamma = sum over rows of dn * n   (fp32, d values, overwritten).
+ * dh is the gradient of x and of residual alike.  gamma NULL: all ones;
+ * dgamma NULL: not computed.  dn, dres, dh, gamma are io_dtype; dh may be dn
+ * or dres (with the same leading dimension).  The sum over rows is taken in a
+ * fixed order.  workspace: harp_rmsnorm_q8_vjp_workspace() bytes, 4-byte
+ * aligned, needed with dgamma only.  1 <= d <= HARP_MAX_D; rows == 0 writes
+ * zeros to dgamma.  The workspace call returns -1 for sizes out of range. */
+int64_t harp_rmsnorm_q8_vjp_workspace(int64_t rows, int64_t d);
+harp_status harp_rmsnorm_q8_vjp(const uint8_t* codes, int64_t ldc,
+                                const void* scales, harp_dtype scale_dtype,
+                                const float* rstd, const void* gamma,
+                                const void* dn, int64_t lddn, const void* dres,
+                                int64_t lddres, void* dh, int64_t lddh,
+                                float* dgamma, int64_t rows, int64_t d,
+                                harp_dtype io_dtype, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+/* y = A W^T of coded matrices: A rows x k in 1 x 128 blocks, W n x k in
+ * 128 x 128 blocks, scales of both in scale_dtype,
+ *   y[i][j] = sum over blocks b of k of
+ *             a_scale[i][b] w_scale[j / 128][b] sum over b of a[i][.] w[j][.],
+ * summed in fp32; y is F32 or BF16 (rounded once), row stride ldy.
+ * workspace: harp_matmul_q8_workspace() bytes (may be 0; -1 for sizes out of
+ * range), 16-byte aligned.  n, k >= 1; rows == 0 returns HARP_OK without a
+ * launch.  With W's transpose and coded gradient rows this is also the
+ * product's gradient with respect to A. */
+int64_t harp_matmul_q8_workspace(int64_t rows, int64_t n, int64_t k);
+harp_status harp_matmul_q8(const uint8_t* a, int64_t lda, const void* a_scales,
+                           const uint8_t* w, int64_t ldw, const void* w_scales,
+                           harp_dtype scale_dtype, int64_t rows, int64_t n,
+                           int64_t k, void* y, int64_t ldy, harp_dtype y_dtype,
+                           void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
+/* Weight gradient of that product from an 8-bit checkpoint of its input:
+ *   dw[j][c] = sum over rows i of dy[i][j] x[i][c],
+ * dy rows x n (BF16, row stride lddy), x coded rows x k (1 x 128 blocks), dw
+ * n x k, F32 or BF16 (rounded once), overwritten.  Sums in fp32, in a fixed
+ * order.  With E8M0 scales every product is exact.  With fp32 scales x is
+ * multiplied as a sum of two bf16 parts (16 significant bits) for F32 dw and
+ * as one bf16 value for BF16 dw.  workspace:
+ * harp_matmul_q8_wgrad_workspace() bytes (may be 0; -1 for sizes out of
+ * range), 16-byte aligned.  n, k >= 1; rows == 0 writes zeros. */
+int64_t harp_matmul_q8_wgrad_workspace(int64_t rows, int64_t n, int64_t k);
+harp_status harp_matmul_q8_wgrad(const void* dy, int64_t lddy, const uint8_t* x,
+                                 int64_t ldx, const void* x_scales,
+                                 harp_dtype scale_dtype, int64_t rows,
+                                 int64_t n, int64_t k, void* dw, int64_t lddw,
+                                 harp_dtype dw_dtype, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Diagnostics (host).

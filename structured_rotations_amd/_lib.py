@@ -19,6 +19,7 @@ HARP_F32 = 0
 HARP_BF16 = 1
 HARP_I8 = 2
 HARP_F64 = 3
+HARP_E8M0 = 4
 
 MAX_STAGES = 16
 NOALLOC_SCRATCH_BYTES = 8 << 20      # HARP_NOALLOC_SCRATCH_BYTES
@@ -82,6 +83,18 @@ _SIG = {
     "harp_rotate_weight": (_I32, [ctypes.POINTER(Schedule), _P, _P, _P, ctypes.POINTER(Schedule), _P, _P, _P,
                                   _I32, _P, _I64, _P, _I64, _I64, _I64, _I32, _I32, _P, ctypes.c_size_t, _P]),
     "rht_compose": (_I32, [ctypes.POINTER(Schedule), _I64, _P, _I32, _P, _I64, _P, _I64, _I64, _I32, _I32, _P]),
+    "harp_quantize_q8": (_I32, [_P, _I64, _I32, _I64, _I64, _I32, _P, _I64, _P, _I32, _P]),
+    "harp_rmsnorm_q8": (_I32, [_P, _I64, _P, _I64, _P, ctypes.c_float, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I32,
+                               _I64, _I64, _I32, _P]),
+    "harp_rmsnorm_q8_vjp_workspace": (_I64, [_I64, _I64]),
+    "harp_rmsnorm_q8_vjp": (_I32, [_P, _I64, _P, _I32, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _I32, _P,
+                                   ctypes.c_size_t, _P]),
+    "harp_matmul_q8_workspace": (_I64, [_I64, _I64, _I64]),
+    "harp_matmul_q8": (_I32, [_P, _I64, _P, _P, _I64, _P, _I32, _I64, _I64, _I64, _P, _I64, _I32, _P, ctypes.c_size_t,
+                              _P]),
+    "harp_matmul_q8_wgrad_workspace": (_I64, [_I64, _I64, _I64]),
+    "harp_matmul_q8_wgrad": (_I32, [_P, _I64, _P, _I64, _P, _I32, _I64, _I64, _I64, _P, _I64, _I32, _P,
+                                    ctypes.c_size_t, _P]),
     "harp_status_str": (ctypes.c_char_p, [_I32]),
     "harp_last_error": (ctypes.c_char_p, []),
     "harp_version": (ctypes.c_char_p, []),

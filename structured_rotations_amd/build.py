@@ -25,7 +25,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libharp.so")
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
-HIP_SOURCES = ["api.hip", "apply_tile.hip", "apply_mfma.hip", "apply_valu.hip", "apply_fast.hip", "rht.hip", "rotate_cols.hip", "col_dense.hip", "materialize.hip", "decode.hip", "vjp.hip"]
+HIP_SOURCES = ["api.hip", "apply_tile.hip", "apply_mfma.hip", "apply_valu.hip", "apply_fast.hip", "rht.hip", "rotate_cols.hip", "col_dense.hip", "materialize.hip", "decode.hip", "vjp.hip",
+               "q8_api.hip", "q8_rows.hip", "q8_matmul.hip", "q8_wgrad.hip"]
 CXX_SOURCES = ["plan.cpp"]
 
 DEVICE_FLAGS = [

@@ -1,0 +1,258 @@
+// The 8-bit operators: E4M3 codes with one fp32 or E8M0 scale per block of
+// 128 columns.  Device helpers of the format, and the host launchers that the
+// C entry points call after every argument has been checked.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.h"
+#include "kernels.h"
+
+namespace harp {
+
+constexpr int kQBlk = 128;            // columns (and rows of a weight) per scale
+constexpr float kQTop = 448.0f;       // largest E4M3 value
+constexpr float kQFloor = 0x1p-120f;  // smallest scale: 1 / scale stays finite
+
+inline int64_t q_nblk(int64_t n) { return (n + kQBlk - 1) / kQBlk; }
+
+// ------------------------------------------------------------ device side
+// Eight consecutive values of a row at their own alignment: gfx950 takes
+// dword-wide global accesses at any address, so one path serves every row
+// stride and base.
+struct __attribute__((packed, aligned(2))) Raw8H { uint32_t w[4]; };
+struct __attribute__((packed, aligned(4))) Raw8F { uint32_t w[8]; };
+struct __attribute__((packed, aligned(1))) Raw8C { uint32_t w[2]; };
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
+template <>
+__device__ __forceinline__ void load8<uint16_t>(const uint16_t* p, float (&v)[8]) {
+  const Raw8H r = *reinterpret_cast<const Raw8H*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(r.w[i]);
+    v[2 * i + 1] = bf16_hi(r.w[i]);
+  }
+}
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
+  const Raw8F r = *reinterpret_cast<const Raw8F*>(p);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+}
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
+  Raw8H r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.w[i] = pack_bf16x2_hw(v[2 * i], v[2 * i + 1]);
+  *reinterpret_cast<Raw8H*>(p) = r;
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  Raw8F r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(v[i]);
+  *reinterpret_cast<Raw8F*>(p) = r;
+}
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)pack_bf16x2_hw(v, v); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+
+// The first n (< 8) values of a chunk; the rest are zero.
+template <typename T>
+__device__ __forceinline__ void load8_tail(const T* p, int n, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = i < n ? load1(p + i) : 0.0f;
+}
+template <typename T>
+__device__ __forceinline__ void store8_tail(T* p, int n, const float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) store1(p + i, v[i]);
+}
+template <typename T>
+__device__ __forceinline__ void load8_of(const T* p, int n, float (&v)[8]) {
+  if (n >= 8) load8<T>(p, v);
+  else load8_tail<T>(p, n, v);
+}
+template <typename T>
+__device__ __forceinline__ void store8_of(T* p, int n, const float (&v)[8]) {
+  if (n >= 8) store8(p, v);
+  else store8_tail<T>(p, n, v);
+}
+
+// Four E4M3 codes of four values (round to nearest, ties to even; the inputs
+// are within 448 up to an fp32 rounding, which rounds to 448).
+__device__ __forceinline__ uint32_t enc4(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+// Four values of four E4M3 codes (exact).
+__device__ __forceinline__ void dec4(uint32_t w, float* v) {
+  const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+  const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+  v[0] = lo[0];
+  v[1] = lo[1];
+  v[2] = hi[0];
+  v[3] = hi[1];
+}
+__device__ __forceinline__ void load8_codes(const uint8_t* p, int n, float (&v)[8]) {
+  if (n >= 8) {
+    const Raw8C r = *reinterpret_cast<const Raw8C*>(p);
+    dec4(r.w[0], v);
+    dec4(r.w[1], v + 4);
+  } else {
+    uint32_t w[2] = {0, 0};
+    for (int i = 0; i < n; ++i) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+    dec4(w[0], v);
+    dec4(w[1], v + 4);
+  }
+}
+__device__ __forceinline__ void store8_codes(uint8_t* p, int n, const float (&v)[8]) {
+  Raw8C r;
+  r.w[0] = enc4(v[0], v[1], v[2], v[3]);
+  r.w[1] = enc4(v[4], v[5], v[6], v[7]);
+  if (n >= 8) *reinterpret_cast<Raw8C*>(p) = r;
+  else
+    for (int i = 0; i < n; ++i) p[i] = (uint8_t)(r.w[i >> 2] >> (8 * (i & 3)));
+}
+
+// Coding of values v = w * mult (mult: the row's 1/rms, or 1) that share a
+// block whose largest |w| has the bits amax (as bits, NaN and infinity are the
+// largest): `scale` is the block's scale, code8 turns eight w into values to
+// be rounded to codes.
+//
+// fp32 scales: code = 448 w / max|w|.  mult cancels, and the quotient is
+// corrected by its remainder, so that values that lie half way between two
+// codes (common: w is a sum of bf16 values, with few bits) are exactly there
+// and go to the even code.  448 is kept as 0.4375 * 2^10, so that nothing
+// overflows for any fp32 w.
+// E8M0 scales: code = w * (mult / scale), one rounding.
+template <bool E8>
+struct Coder {
+  float scale, num, den, rcp, cor;
+
+  __device__ __forceinline__ Coder(uint32_t amax, float mult) {
+    const float top = __uint_as_float(amax);
+    float s = fmaxf(top * mult / kQTop, kQFloor);
+    if constexpr (E8) s = __uint_as_float((__float_as_uint(s) + 0x007fffffu) & 0x7f800000u);  // up to a power of two
+    const bool bad = amax >= 0x7f800000u || !(top * mult < __uint_as_float(0x7f800000u));
+    scale = bad ? __uint_as_float(0x7fc00000u) : s;
+    num = 0.4375f;
+    den = fmaxf(top, kQTop * kQFloor / mult) * 0x1p-10f;
+    rcp = cor = 1.0f / den;
+    // far from every normal row's range: one multiplication, no correction
+    if (E8 || bad || !(mult >= 0x1p-60f && mult <= 0x1p60f && den >= 0x1p-100f)) {
+      num = bad ? scale : mult / s;
+      den = cor = 0.0f;
+      rcp = 1.0f;
+    }
+  }
+  __device__ __forceinline__ void code8(const float (&w)[8], float (&c)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = w[i] * num;
+      if constexpr (E8) {
+        c[i] = t;
+      } else {
+        const float y = t * rcp;
+        c[i] = fmaf(fmaf(-y, den, t), cor, y);
+      }
+    }
+  }
+};
+template <bool E8>
+__device__ __forceinline__ void store_scale(void* scales, int64_t i, float s) {
+  if constexpr (E8) static_cast<uint8_t*>(scales)[i] = s != s ? 255 : (uint8_t)(__float_as_uint(s) >> 23);
+  else static_cast<float*>(scales)[i] = s;
+}
+__device__ __forceinline__ float e8m0_value(uint32_t b) {
+  return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
+}
+template <bool E8>
+__device__ __forceinline__ float load_scale(const void* scales, int64_t i) {
+  if constexpr (E8) return e8m0_value(static_cast<const uint8_t*>(scales)[i]);
+  else return static_cast<const float*>(scales)[i];
+}
+
+// Largest / sum over the 16 lanes that share a block (one DPP row), in every
+// lane of it.
+template <int N>
+__device__ __forceinline__ uint32_t row_ror(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xf, 0xf, true);
+}
+__device__ __forceinline__ uint32_t row16_umax(uint32_t v) {
+  v = max(v, row_ror<8>(v));
+  v = max(v, row_ror<4>(v));
+  v = max(v, row_ror<2>(v));
+  return max(v, row_ror<1>(v));
+}
+__device__ __forceinline__ float row16_sum(float v) {
+  v += __uint_as_float(row_ror<8>(__float_as_uint(v)));
+  v += __uint_as_float(row_ror<4>(__float_as_uint(v)));
+  v += __uint_as_float(row_ror<2>(__float_as_uint(v)));
+  return v + __uint_as_float(row_ror<1>(__float_as_uint(v)));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row16_sum(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+__device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  return m;
+}
+
+// -------------------------------------------------------------- host side
+struct NormArgs {
+  const void *x, *residual, *gamma;
+  void* h;
+  uint8_t *codes, *ckpt;
+  void *scales, *ckpt_scales;
+  float* rstd;
+  int64_t ldx, ldr, ldh, ldc, ldk, rows;
+  int d;
+  float eps;
+};
+struct NormVjpArgs {
+  const uint8_t* codes;
+  const void *scales, *gamma, *dn, *dres;
+  const float* rstd;
+  void* dh;
+  float *dgamma, *partial;
+  int64_t ldc, lddn, lddres, lddh, rows;
+  int d;
+};
+struct MatmulArgs {
+  const uint8_t *a, *w;
+  const void *a_scales, *w_scales;
+  void* y;
+  float* partial;
+  int64_t lda, ldw, ldy;
+  int rows, n, k, nkb;
+};
+struct WgradArgs {
+  const uint16_t* dy;
+  const uint8_t* x;
+  const void* x_scales;
+  void* dw;
+  float* partial;
+  int64_t lddy, ldx, lddw;
+  int rows, n, k, nkb;
+};
+
+hipError_t launch_quantize_q8(const void* x, int64_t ldx, DT io, int64_t rows, int cols, bool tile, uint8_t* codes,
+                              int64_t ldc, void* scales, bool e8, hipStream_t stream);
+hipError_t launch_rmsnorm_q8(const NormArgs& a, DT io, bool e8, hipStream_t stream);
+int64_t rmsnorm_q8_vjp_workspace(int64_t rows, int64_t d);
+hipError_t launch_rmsnorm_q8_vjp(const NormVjpArgs& a, DT io, bool e8, hipStream_t stream);
+int64_t matmul_q8_workspace(int64_t rows, int64_t n, int64_t k);
+hipError_t launch_matmul_q8(const MatmulArgs& a, bool e8, DT out, hipStream_t stream);
+int64_t matmul_q8_wgrad_workspace(int64_t rows, int64_t n, int64_t k);
+hipError_t launch_matmul_q8_wgrad(const WgradArgs& a, bool e8, DT out, hipStream_t stream);
+
+}  // namespace harp
