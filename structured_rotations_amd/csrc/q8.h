@@ -129,7 +129,7 @@ __device__ __forceinline__ void store8_codes(uint8_t* p, int n, const float (&v)
 // codes (common: w is a sum of bf16 values, with few bits) are exactly there
 // and go to the even code.  448 is kept as 0.4375 * 2^10, so that nothing
 // overflows for any fp32 w.
-// E8M0 scales: code = w * (mult / scale), one rounding.
+// E8M0 scales: code = (w * mult) / scale, one rounding.
 template <bool E8>
 struct Coder {
   float scale, num, den, rcp, cor;
@@ -143,23 +143,20 @@ struct Coder {
     num = 0.4375f;
     den = fmaxf(top, kQTop * kQFloor / mult) * 0x1p-10f;
     rcp = cor = 1.0f / den;
-    // far from every normal row's range: one multiplication, no correction
+    // far from every normal row's range: no correction
     if (E8 || bad || !(mult >= 0x1p-60f && mult <= 0x1p60f && den >= 0x1p-100f)) {
-      num = bad ? scale : mult / s;
+      num = bad ? scale : mult;
       den = cor = 0.0f;
-      rcp = 1.0f;
+      rcp = 1.0f / s;
     }
   }
   __device__ __forceinline__ void code8(const float (&w)[8], float (&c)[8]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float t = w[i] * num;
-      if constexpr (E8) {
-        c[i] = t;
-      } else {
-        const float y = t * rcp;
-        c[i] = fmaf(fmaf(-y, den, t), cor, y);
-      }
+      const float y = t * rcp;
+      if constexpr (E8) c[i] = y;
+      else c[i] = fmaf(fmaf(-y, den, t), cor, y);
     }
   }
 };
