@@ -174,6 +174,41 @@ __device__ __forceinline__ float load_scale(const void* scales, int64_t i) {
   else return static_cast<const float*>(scales)[i];
 }
 
+// A tile in global memory whose loads go straight into LDS: 16 bytes per
+// lane, from the lane's byte offset plus a common one to 1024 consecutive
+// bytes of LDS at a wave-uniform address.  Lanes at or beyond `bytes` give
+// zeros.  Written out, because the compiler would wait for such a load before
+// any later LDS read, of the other buffer too; the kernels wait for all of
+// them (vmcnt) before the barrier that precedes their first use.
+using TileSrc = __amdgpu_buffer_rsrc_t;
+__device__ __forceinline__ TileSrc tile_src(const void* base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00027000);
+}
+__device__ __forceinline__ void load_lds16(TileSrc src, void* lds, unsigned lane_offset, int offset) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(at), "v"(lane_offset), "s"(src), "s"(offset)
+               : "memory");
+}
+// The same for one word per lane: 4 bytes, or one byte widened.
+template <int kBytes>
+__device__ __forceinline__ void load_lds_word(TileSrc src, void* lds, unsigned lane_offset, int offset) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+  if constexpr (kBytes == 4)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :
+                 : "s"(at), "v"(lane_offset), "s"(src), "s"(offset)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
+                 :
+                 : "s"(at), "v"(lane_offset), "s"(src), "s"(offset)
+                 : "memory");
+}
+// Lane offset that is beyond any tile.
+constexpr unsigned kNoLoad = 0x7fffff00u;
+
 // Largest / sum over the 16 lanes that share a block (one DPP row), in every
 // lane of it.
 template <int N>

@@ -23,8 +23,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
-constexpr int kUnit = 0x7f7f7f7f;  // E8M0 1.0 in every byte
-
 struct __attribute__((packed, aligned(1))) Raw16 { uint32_t w[4]; };
 
 // 16 codes of a row, the ones past its end zero.
@@ -63,13 +61,21 @@ __device__ __forceinline__ void store4<uint16_t>(uint16_t* p, int n, const f32x4
       if (i < n) p[i] = (uint16_t)((i < 2 ? lo : hi) >> (16 * (i & 1)));
 }
 
-// A fragment: the two 16-byte pieces q and q + 4 of a 128-byte row in LDS,
-// whose pieces are exchanged by the row's number (piece ^ (row & 7)) so that
-// eight rows' reads of one piece cover all banks.
-__device__ __forceinline__ i32x8 frag(const uint8_t* lds, int row, int q) {
+// Tiles in LDS: 128-byte rows (one block of 128) of eight 16-byte pieces,
+// exchanged by spread(row) so that the fragment reads below cover all banks.
+// A wave reads its weight rows in the order n = 16 (r / 4) + 4 i + r % 4 for
+// instruction i of four and row r of it: a lane's results of four
+// instructions are then 16 neighbouring n.  Eight neighbouring r are rows
+// 0..3 and 16..19 (weight) or 0..7 (activations, read in order), hence the
+// two forms.
+__device__ __forceinline__ int spread_w(int row) { return (row & 3) | ((row >> 2) & 4); }
+__device__ __forceinline__ int spread_a(int row) { return row & 7; }
+
+// A fragment: the pieces q and q + 4 of a row.
+__device__ __forceinline__ i32x8 frag(const uint8_t* lds, int row, int x, int q) {
   const uint8_t* p = lds + row * kQBlk;
-  const i32x4 a = *reinterpret_cast<const i32x4*>(p + ((q ^ (row & 7)) << 4));
-  const i32x4 b = *reinterpret_cast<const i32x4*>(p + (((q + 4) ^ (row & 7)) << 4));
+  const i32x4 a = *reinterpret_cast<const i32x4*>(p + ((q ^ x) << 4));
+  const i32x4 b = *reinterpret_cast<const i32x4*>(p + (((q ^ x) ^ 4) << 4));
   return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
@@ -86,94 +92,205 @@ __device__ __forceinline__ bf16x8_t widen(const i32x8& f, int t) {
   return r;
 }
 
-// One BM x BN tile of y per workgroup of (BM / 64) (BN / 64) waves, each with
-// 64 x 64 of it; one block of 128 per step through LDS.
-template <int BM, int BN, bool E8, typename TO>
-__global__ __launch_bounds__(BM * BN / 64) void matmul_tile_kernel(MatmulArgs g, int kb_per_split) {
-  constexpr int T = BM * BN / 64, NA = BM * 8 / T, NW = BN * 8 / T;
-  __shared__ __align__(16) uint8_t la[BM * kQBlk];
-  __shared__ __align__(16) uint8_t lw[BN * kQBlk];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int m0 = (int)blockIdx.y * BM, n0 = (int)blockIdx.x * BN;
-  const int wm = (wave / (BN / 64)) * 64, wn = (wave % (BN / 64)) * 64;
+constexpr int kChunk = 8;  // steps whose row scales are brought in together
+
+// Which tile a workgroup computes: consecutive workgroups go to the 8 dies in
+// turn, so each die takes one contiguous run of the tiles, ordered in groups
+// of 8 tiles along m, and its 32 compute units share 8 + 4 panels in its L2.
+__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int* tm, int* tn) {
+  const int total = tiles_m * tiles_n, xcd = id & 7, q = total >> 3, r = total & 7;
+  const int t = xcd * q + min(xcd, r) + (id >> 3);
+  constexpr int kGroup = 8;
+  const int per = kGroup * tiles_n, g = t / per, first = g * kGroup;
+  const int gm = min(kGroup, tiles_m - first), in = t - g * per;
+  *tm = first + in % gm;
+  *tn = in / gm;
+}
+
+// One 64 MW x (64 NT NW / 4) tile of y per workgroup of MW x NW waves, each
+// with 64 rows (m) by 16 NT columns (n) of it.  LDS holds two steps of one
+// block of 128: while a step is computed the next one is on its way, straight
+// from global memory into LDS (kDirect; rows of whole 16-byte pieces) or
+// through registers (any length and alignment).
+template <int MW, int NW, int NT, bool E8, typename TO, bool kDirect>
+__global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g, int kb_per_split, int tiles_m,
+                                                                   int tiles_n) {
+  constexpr int BM = 64 * MW, BN = 16 * NT * NW, WAVES = MW * NW;
+  constexpr int PA = BM / 8 / WAVES, PW = BN / 8 / WAVES;  // 8-row pieces of each operand a wave brings in
+  static_assert(PA * 8 * WAVES == BM && PW * 8 * WAVES == BN, "");
+  __shared__ __align__(16) uint8_t la[2][BM * kQBlk];
+  __shared__ __align__(16) uint8_t lw[2][BN * kQBlk];
+  __shared__ uint32_t ls[2][BM * kChunk];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int tm, tn;
+  tile_of((int)blockIdx.x, tiles_m, tiles_n, &tm, &tn);
+  const int m0 = tm * BM, n0 = tn * BN;
+  const int wm = (wave / NW) * 64, wn = (wave % NW) * (16 * NT);
   const int q = lane >> 4, i16 = lane & 15;
-  const int kb0 = (int)blockIdx.z * kb_per_split, kb1 = min(g.nkb, kb0 + kb_per_split);
-  f32x4 acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  const int64_t sw_row = (int64_t)((n0 + wn) / kQBlk < (g.n - 1) / kQBlk ? (n0 + wn) / kQBlk : (g.n - 1) / kQBlk) * g.nkb;
+  const int kb0 = (int)blockIdx.y * kb_per_split, kb1 = min(g.nkb, kb0 + kb_per_split);
   // bf16 results with E8M0 scales: the instruction applies the scales
   constexpr bool kHwScale = E8 && sizeof(TO) == 2, kWide = sizeof(TO) == 4;
-  for (int kb = kb0; kb < kb1; ++kb) {
+
+  // what this lane brings in: piece pc of rows 8 (wave + WAVES i) + lane / 8,
+  // to be found at lane * 16 of its 1024 bytes of LDS
+  const uint8_t* abase = g.a + (int64_t)m0 * g.lda;
+  const uint8_t* wbase = g.w + (int64_t)n0 * g.ldw;
+  const int rows_a = min(BM, g.rows - m0), rows_w = min(BN, g.n - n0);
+  const int lrow = lane >> 3;
+  const int pca = ((lane & 7) ^ lrow) * 16;
+  // spread_w of row 8 (wave + WAVES i) + lrow: WAVES is even, so bit 4 of the
+  // row is bit 1 of the wave
+  static_assert(WAVES % 4 == 0 || PW == 1, "");
+  const int pcw = ((lane & 7) ^ (lrow & 3) ^ ((wave & 2) << 1)) * 16;
+  TileSrc ra, rw;
+  unsigned va[PA], vw[PW];
+  if constexpr (kDirect) {
+    ra = tile_src(abase, (rows_a - 1) * (int)g.lda + g.k);
+    rw = tile_src(wbase, (rows_w - 1) * (int)g.ldw + g.k);
+#pragma unroll
+    for (int i = 0; i < PA; ++i) {
+      const int r = (wave + WAVES * i) * 8 + lrow;
+      va[i] = r < rows_a ? (unsigned)(r * (int)g.lda + pca) : kNoLoad;
+    }
+#pragma unroll
+    for (int i = 0; i < PW; ++i) {
+      const int r = (wave + WAVES * i) * 8 + lrow;
+      vw[i] = r < rows_w ? (unsigned)(r * (int)g.ldw + pcw) : kNoLoad;
+    }
+  }
+  auto bring = [&](int kb, int buf) {
     const int kk = kb * kQBlk;
-    u32x4 va[NA], vw[NW];
+    if constexpr (kDirect) {
+      const bool ta = kk + pca < g.k, tw = kk + pcw < g.k;
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {
-      const int u = tid + i * T, r = u >> 3, c = u & 7;
-      va[i] = load16_codes(g.a + (int64_t)(m0 + r) * g.lda + kk + c * 16, m0 + r < g.rows ? g.k - kk - c * 16 : 0);
-    }
+      for (int i = 0; i < PA; ++i) load_lds16(ra, la[buf] + (wave + WAVES * i) * 1024, ta ? va[i] : kNoLoad, kk);
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      const int u = tid + i * T, r = u >> 3, c = u & 7;
-      vw[i] = load16_codes(g.w + (int64_t)(n0 + r) * g.ldw + kk + c * 16, n0 + r < g.n ? g.k - kk - c * 16 : 0);
-    }
-    __syncthreads();
+      for (int i = 0; i < PW; ++i) load_lds16(rw, lw[buf] + (wave + WAVES * i) * 1024, tw ? vw[i] : kNoLoad, kk);
+    } else {
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {
-      const int u = tid + i * T, r = u >> 3, c = u & 7;
-      *reinterpret_cast<u32x4*>(la + r * kQBlk + ((c ^ (r & 7)) << 4)) = va[i];
-    }
+      for (int i = 0; i < PA; ++i) {
+        const int r = (wave + WAVES * i) * 8 + lrow;
+        *reinterpret_cast<u32x4*>(la[buf] + (wave + WAVES * i) * 1024 + lane * 16) =
+            load16_codes(abase + (int64_t)r * g.lda + kk + pca, r < rows_a ? g.k - kk - pca : 0);
+      }
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      const int u = tid + i * T, r = u >> 3, c = u & 7;
-      *reinterpret_cast<u32x4*>(lw + r * kQBlk + ((c ^ (r & 7)) << 4)) = vw[i];
-    }
-    __syncthreads();
-    i32x8 fa[4];
-    float s[4];
-    int sb[4], swb = 0;
-    if constexpr (kHwScale) swb = static_cast<const uint8_t*>(g.w_scales)[sw_row + kb];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = min(m0 + wm + j * 16 + i16, g.rows - 1);
-      fa[j] = frag(la, wm + j * 16 + i16, q);
-      if constexpr (kHwScale) sb[j] = static_cast<const uint8_t*>(g.a_scales)[m * g.nkb + kb];
-      else s[j] = load_scale<E8>(g.a_scales, m * g.nkb + kb) * load_scale<E8>(g.w_scales, sw_row + kb);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const i32x8 fw = frag(lw, wn + i * 16 + i16, q);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (kHwScale) {
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fa[j], acc[i][j], 0, 0, 0, swb, 0, sb[j]);
-        } else {
-          f32x4 p = {0, 0, 0, 0};
-          if constexpr (kWide) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(fw, t), widen(fa[j], t), p, 0, 0, 0);
-          } else {
-            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fa[j], p, 0, 0, 0, kUnit, 0, kUnit);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], s[j], acc[i][j][e]);
-        }
+      for (int i = 0; i < PW; ++i) {
+        const int r = (wave + WAVES * i) * 8 + lrow;
+        *reinterpret_cast<u32x4*>(lw[buf] + (wave + WAVES * i) * 1024 + lane * 16) =
+            load16_codes(wbase + (int64_t)r * g.ldw + kk + pcw, r < rows_w ? g.k - kk - pcw : 0);
       }
     }
+  };
+
+  f32x4 acc[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  // Scales of the rows: a load of one step's 64 would touch 64 cache lines, so
+  // they come kChunk steps at a time, 8 rows by 8 steps per wave's load, and
+  // wait in LDS as [row][step] (E8M0: the byte, one per word).
+  constexpr int kSB = E8 ? 1 : 4;
+  const uint8_t* sbase = static_cast<const uint8_t*>(g.a_scales) + (int64_t)m0 * g.nkb * kSB;
+  TileSrc rs;
+  if constexpr (kDirect) rs = tile_src(sbase, rows_a * g.nkb * kSB);
+  auto bring_scales = [&](int kb, int buf) {
+    const int k1 = lane & (kChunk - 1);
+#pragma unroll
+    for (int i = 0; i < PA; ++i) {
+      const int r = (wave + WAVES * i) * 8 + lrow;
+      const bool in = r < rows_a && kb + k1 < kb1;
+      if constexpr (kDirect) {
+        load_lds_word<kSB>(rs, ls[buf] + (wave + WAVES * i) * 64, in ? (unsigned)((r * g.nkb + k1) * kSB) : kNoLoad,
+                           kb * kSB);
+      } else {
+        const int64_t at = (int64_t)r * g.nkb + kb + k1;
+        uint32_t v = 0;
+        if (in) v = E8 ? sbase[at] : reinterpret_cast<const uint32_t*>(sbase)[at];
+        ls[buf][(wave + WAVES * i) * 64 + lane] = v;
+      }
+    }
+  };
+  const int64_t sw_row = (int64_t)min((n0 + wn) / kQBlk, (g.n - 1) / kQBlk) * g.nkb;
+  uint32_t sw;
+  auto load_sw = [&](int kb) {
+    if constexpr (E8) sw = static_cast<const uint8_t*>(g.w_scales)[sw_row + kb];
+    else sw = static_cast<const uint32_t*>(g.w_scales)[sw_row + kb];
+  };
+
+  bring(kb0, 0);
+  bring_scales(kb0, 0);
+  load_sw(kb0);
+  // every wave's own loads have landed before the barrier lets others read
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  for (int kb = kb0; kb < kb1; ++kb) {
+    const int step = kb - kb0, buf = step & 1, in = step % kChunk;
+    float s[4];
+    int sb[4];
+    const int swb = (int)sw;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t sa = ls[step / kChunk & 1][(wm + j * 16 + i16) * kChunk + in];
+      sb[j] = (int)sa;
+      if constexpr (!kHwScale)
+        s[j] = E8 ? e8m0_value(sa) * e8m0_value(sw) : __uint_as_float(sa) * __uint_as_float(sw);
+    }
+    if (kb + 1 < kb1) {
+      bring(kb + 1, buf ^ 1);
+      load_sw(kb + 1);
+      if (in == kChunk - 1) bring_scales(kb + 1, (step / kChunk & 1) ^ 1);
+    }
+    i32x8 fa[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fa[j] = frag(la[buf], wm + j * 16 + i16, i16 & 7, q);
+    auto weight = [&](int i) {
+      const int row = (i >> 2) * 64 + (i16 >> 2) * 16 + (i & 3) * 4 + (i16 & 3);
+      return frag(lw[buf], wn + row, (i16 & 3) | (i16 & 4), q);
+    };
+    i32x8 fw = weight(0);
+    f32x4 p[2][4];
+#pragma unroll
+    for (int i = 0; i <= NT; ++i) {
+      i32x8 next;
+      if (i + 1 < NT) next = weight(i + 1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i < NT) {
+          if constexpr (kHwScale) {
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fa[j], acc[i][j], 0, 0, 0, swb, 0, sb[j]);
+          } else if constexpr (kWide) {
+            p[i & 1][j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              p[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(fw, t), widen(fa[j], t), p[i & 1][j], 0, 0, 0);
+          } else {
+            p[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fa[j], f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+          }
+        }
+        if constexpr (!kHwScale) {
+          if (i > 0)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i - 1][j][e] = fmaf(p[(i - 1) & 1][j][e], s[j], acc[i - 1][j][e]);
+          // keep the order: a matrix instruction, then the scaling of a result of the row before
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      fw = next;
+    }
+    // this step's reads are done and the next step's loads have landed
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int m = m0 + wm + j * 16 + i16;
     if (m >= g.rows) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + wn + i * 16 + q * 4;
+    for (int i = 0; i < NT; ++i) {
+      const int n = n0 + wn + (i >> 2) * 64 + q * 16 + (i & 3) * 4;
       if (n >= g.n) continue;
-      if (gridDim.z > 1)
-        store4<float>(g.partial + ((int64_t)blockIdx.z * g.rows + m) * g.n + n, g.n - n, acc[i][j]);
+      if (gridDim.y > 1)
+        store4<float>(g.partial + ((int64_t)blockIdx.y * g.rows + m) * g.n + n, g.n - n, acc[i][j]);
       else store4<TO>(static_cast<TO*>(g.y) + (int64_t)m * g.ldy + n, g.n - n, acc[i][j]);
     }
   }
@@ -200,11 +317,28 @@ int splits_of(int64_t rows, int64_t n, int64_t k) {
   return (int)((nkb + per - 1) / per);
 }
 
+// Rows of whole, aligned 16-byte pieces whose tiles stay within a descriptor's
+// 2 GiB.
+bool direct_ok(const MatmulArgs& g) {
+  return ((reinterpret_cast<uintptr_t>(g.a) | reinterpret_cast<uintptr_t>(g.w) | (uintptr_t)g.lda | (uintptr_t)g.ldw |
+           (uintptr_t)g.k) & 15) == 0 && g.lda <= (1 << 22) && g.ldw <= (1 << 22);
+}
+
+template <int MW, int NW, int NT, bool E8, typename TO, bool kDirect>
+void tile_go(const MatmulArgs& g, int splits, hipStream_t stream) {
+  constexpr int BM = 64 * MW, BN = 16 * NT * NW;
+  const int tm = (g.rows + BM - 1) / BM, tn = (g.n + BN - 1) / BN, per = (g.nkb + splits - 1) / splits;
+  hipLaunchKernelGGL((matmul_tile_kernel<MW, NW, NT, E8, TO, kDirect>), dim3(tm * tn, splits), dim3(64 * MW * NW), 0,
+                     stream, g, per, tm, tn);
+}
+
 template <bool E8, typename TO>
 hipError_t matmul_go(const MatmulArgs& g, hipStream_t stream) {
-  const int s = splits_of(g.rows, g.n, g.k), per = (g.nkb + s - 1) / s;
-  hipLaunchKernelGGL((matmul_tile_kernel<128, 128, E8, TO>), dim3((g.n + 127) / 128, (g.rows + 127) / 128, s),
-                     dim3(256), 0, stream, g, per);
+  const int s = splits_of(g.rows, g.n, g.k);
+  const int64_t big = (int64_t)((g.rows + 255) / 256) * ((g.n + 255) / 256);
+  if (!direct_ok(g)) tile_go<2, 2, 4, E8, TO, false>(g, s, stream);
+  else if (big >= 256 && s == 1) tile_go<4, 2, 8, E8, TO, true>(g, s, stream);
+  else tile_go<2, 2, 4, E8, TO, true>(g, s, stream);
   if (s > 1) {
     const int64_t wg = ((int64_t)g.rows * g.n + 255) / 256;
     hipLaunchKernelGGL((matmul_join_kernel<TO>), dim3((unsigned)(wg < 4096 ? wg : 4096)), dim3(256), 0, stream, g, s);
