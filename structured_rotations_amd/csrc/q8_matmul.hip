@@ -296,6 +296,157 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
   }
 }
 
+// The large form, bf16 results: one 256 x 256 tile per workgroup of 8 waves,
+// each 64 rows (m) by 128 columns (n).  Nothing in the loop waits for a load
+// that was issued less than a whole step before, and the loads are never
+// drained: LDS holds two steps in three parts (A, and the two halves W0, W1
+// of each wave's weight rows), and a part is filled again for two steps on as
+// soon as every wave has read it.  Per step k, in parts of 8 result rows:
+//   row 0      multiply; A of step k is in registers
+//   barrier 1  W1(k) has landed
+//   rows 1..3  multiply; fill W1(k + 1), A(k + 2)
+//   barrier 2  A(k + 1), W0(k + 1) have landed
+//   rows 4..7  multiply; fill W0(k + 2); read A(k + 1) and row 0 of W0(k + 1)
+// The scaling of a product runs under the matrix instructions after it.
+constexpr int kBigA = 4, kBigW = 4;  // loads per wave and step: A, W (half of them W0)
+
+template <bool E8>
+__global__ __launch_bounds__(512) void matmul_big_kernel(MatmulArgs g, int tiles_m, int tiles_n) {
+  constexpr int B = 256, NT = 8;
+  __shared__ __align__(16) uint8_t la[2][B * kQBlk];
+  __shared__ __align__(16) uint8_t lw[2][B * kQBlk];
+  __shared__ uint32_t ls[2][B * kChunk];
+  __shared__ uint32_t lsw[2][9][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int tm, tn;
+  tile_of((int)blockIdx.x, tiles_m, tiles_n, &tm, &tn);
+  const int m0 = tm * B, n0 = tn * B;
+  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 128;
+  const int q = lane >> 4, i16 = lane & 15, lrow = lane >> 3;
+
+  // What this lane brings in, as in matmul_tile_kernel.  Rows past the
+  // matrix's end are past the descriptor's, too.
+  const int rows_a = min(B, g.rows - m0), rows_w = min(B, g.n - n0);
+  const TileSrc ra = tile_src(g.a + (int64_t)m0 * g.lda, (rows_a - 1) * (int)g.lda + g.k);
+  const TileSrc rw = tile_src(g.w + (int64_t)n0 * g.ldw, (rows_w - 1) * (int)g.ldw + g.k);
+  const int pca = ((lane & 7) ^ lrow) * 16, pcw = ((lane & 7) ^ (lrow & 3) ^ ((wave & 2) << 1)) * 16;
+  const unsigned va = (unsigned)((wave * 8 + lrow) * (int)g.lda + pca), vw = (unsigned)((wave * 8 + lrow) * (int)g.ldw + pcw);
+  const int last = (g.nkb - 1) * kQBlk;
+  // Past the last step the loads give zeros that nobody reads: their number
+  // per step stays what the waits below count on.
+  auto fill_a = [&](int kb, int i) {
+    load_lds16(ra, la[kb & 1] + (wave + 8 * i) * 1024, kb * kQBlk + pca < g.k ? va + 64 * i * (unsigned)g.lda : kNoLoad,
+               min(kb * kQBlk, last));
+  };
+  auto fill_w = [&](int kb, int i) {  // i even: W0, odd: W1
+    load_lds16(rw, lw[kb & 1] + (wave + 8 * i) * 1024, kb * kQBlk + pcw < g.k ? vw + 64 * i * (unsigned)g.ldw : kNoLoad,
+               min(kb * kQBlk, last));
+  };
+  // Scales of kChunk steps: one load per step of the chunk before, 64 rows by
+  // kChunk steps in each of the first four, the weight's in the fifth; the
+  // rest give zeros to words that nobody reads.  (Always one, with no branch:
+  // a branch lets the compiler move the scaling of products past it.)
+  constexpr int kSB = E8 ? 1 : 4;
+  const TileSrc rs = tile_src(static_cast<const uint8_t*>(g.a_scales) + (int64_t)m0 * g.nkb * kSB, rows_a * g.nkb * kSB);
+  const int sw_row = min((n0 + wn) / kQBlk, (g.n - 1) / kQBlk);
+  const TileSrc rsw = tile_src(static_cast<const uint8_t*>(g.w_scales) + (int64_t)sw_row * g.nkb * kSB, g.nkb * kSB);
+  const unsigned vs = (unsigned)(((wave * 8 + lrow) * g.nkb + (lane & (kChunk - 1))) * kSB);
+  const unsigned vsw = lane < kChunk ? (unsigned)(lane * kSB) : kNoLoad;
+  auto fill_scales = [&](int kb, int i) {  // load i of the chunk that starts with step kb
+    const int buf = kb / kChunk & 1, at = min(kb, g.nkb - 1) * kSB;
+    load_lds_word<kSB>(i == 4 ? rsw : rs, i < 4 ? ls[buf] + (wave + 8 * i) * 64 : lsw[buf][i == 4 ? wave : 8],
+                       i < 4 ? vs + (unsigned)(64 * i * g.nkb * kSB) : i == 4 ? vsw : kNoLoad, at);
+  };
+
+  f32x4 acc[NT][4], p[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    p[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i][j] = f32x4{0, 0, 0, 0};
+  }
+  i32x8 fa[4], fw;
+  float s[4] = {0, 0, 0, 0};
+  uint32_t sa[4], sw;
+  const int arow = wm + i16, ax = i16 & 7;
+  const int wrow = wn + (i16 >> 2) * 16 + (i16 & 3), wx = (i16 & 3) | (i16 & 4);
+  auto weight = [&](int kb, int i) { return frag(lw[kb & 1], wrow + (i >> 2) * 64 + (i & 3) * 4, wx, q); };
+  auto read_scales = [&](int kb) {
+    const int buf = kb / kChunk & 1, in = kb % kChunk;
+    sw = lsw[buf][wave][in];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sa[j] = ls[buf][(arow + j * 16) * kChunk + in];
+  };
+
+  for (int i = 0; i < kBigA; ++i) fill_a(0, i);
+  for (int i = 0; i < kBigW; i += 2) fill_w(0, i);
+  for (int i = 0; i < 5; ++i) fill_scales(0, i);
+  for (int i = 1; i < kBigW; i += 2) fill_w(0, i);
+  for (int i = 0; i < kBigA; ++i) fill_a(1, i);
+  for (int i = 0; i < kBigW; i += 2) fill_w(1, i);
+  fill_scales(0, 7);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"(kBigA + kBigW + 1) : "memory");
+#pragma unroll
+  for (int j = 0; j < 4; ++j) fa[j] = frag(la[0], arow + j * 16, ax, q);
+  fw = weight(0, 0);
+  read_scales(0);
+
+  for (int kb = 0; kb < g.nkb; ++kb) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const i32x8 next = i + 1 < NT ? weight(kb, i + 1) : weight(kb + 1, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (E8) {
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fa[j], acc[i][j], 0, 0, 0, (int)sw, 0, (int)sa[j]);
+        } else {
+          p[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fa[j], f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+          // the products of two instructions ago
+          const int pj = (j + 2) & 3, pi = j >= 2 ? i : i > 0 ? i - 1 : NT - 1;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[pi][pj][e] = fmaf(p[pj][e], s[pj], acc[pi][pj][e]);
+          if (i == 0 && j == 1) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) s[t] = __uint_as_float(sa[t]) * __uint_as_float(sw);
+          }
+        }
+        if (i == NT - 1) fa[j] = frag(la[(kb + 1) & 1], arow + j * 16, ax, q);
+        // one load per two instructions at most: more at a time fill the
+        // memory pipe's queue, and the wave stands still until they fit
+        if (i == 1 && (j & 1) == 0) fill_w(kb + 1, 1 + j);
+        if ((i == 2 || i == 3) && (j & 1) == 0) fill_a(kb + 2, (i - 2) * 2 + j / 2);
+        if ((i == 4 || i == 5) && j == 1) fill_w(kb + 2, (i - 4) * 2);
+        if (i == 6 && j == 1) fill_scales((kb / kChunk + 1) * kChunk, kb % kChunk);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      fw = next;
+      // newer than W1(kb): A(kb + 1), W0(kb + 1), a load of scales
+      if (i == 0) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"(kBigA + kBigW / 2 + 1) : "memory");
+      // newer than W0(kb + 1): a load of scales, W1(kb + 1), A(kb + 2)
+      if (i == 3) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"(kBigA + kBigW / 2 + 1) : "memory");
+    }
+    read_scales(kb + 1);
+  }
+  if constexpr (!E8) {
+#pragma unroll
+    for (int j = 2; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[NT - 1][j][e] = fmaf(p[j][e], s[j], acc[NT - 1][j][e]);
+  }
+  // no load may be in flight into LDS when the workgroup ends
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int m = m0 + wm + j * 16 + i16;
+    if (m >= g.rows) continue;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int n = n0 + wn + (i >> 2) * 64 + q * 16 + (i & 3) * 4;
+      if (n < g.n) store4<uint16_t>(static_cast<uint16_t*>(g.y) + (int64_t)m * g.ldy + n, g.n - n, acc[i][j]);
+    }
+  }
+}
+
 // y = the splits' partial results added in order.
 template <typename TO>
 __global__ __launch_bounds__(256) void matmul_join_kernel(MatmulArgs g, int splits) {
@@ -335,9 +486,10 @@ void tile_go(const MatmulArgs& g, int splits, hipStream_t stream) {
 template <bool E8, typename TO>
 hipError_t matmul_go(const MatmulArgs& g, hipStream_t stream) {
   const int s = splits_of(g.rows, g.n, g.k);
-  const int64_t big = (int64_t)((g.rows + 255) / 256) * ((g.n + 255) / 256);
+  const int tm = (g.rows + 255) / 256, tn = (g.n + 255) / 256;
   if (!direct_ok(g)) tile_go<2, 2, 4, E8, TO, false>(g, s, stream);
-  else if (big >= 256 && s == 1) tile_go<4, 2, 8, E8, TO, true>(g, s, stream);
+  else if (sizeof(TO) == 2 && (int64_t)tm * tn >= 256)
+    hipLaunchKernelGGL((matmul_big_kernel<E8>), dim3(tm * tn), dim3(512), 0, stream, g, tm, tn);
   else tile_go<2, 2, 4, E8, TO, true>(g, s, stream);
   if (s > 1) {
     const int64_t wg = ((int64_t)g.rows * g.n + 255) / 256;

@@ -367,15 +367,16 @@ def test_matmul(rows, n, k, out, kind):
 
 
 @pytest.mark.parametrize("kind", ["f32", "e8m0"])
-def test_matmul_large_sampled(kind):
-    # more than one round of the largest tiles on 256 compute units, ragged on every side
-    rows, n, k = 4200, 5130, 1168
-    say("matmul", rows, n, k, kind)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,n,k", [(4200, 5130, 1168), (4353, 4100, 128), (8192, 2064, 272), (4096, 4096, 400)])
+def test_matmul_large(rows, n, k, out, kind):
+    # a round of the largest tiles on 256 compute units, ragged on every side; one, a few and many blocks of 128
+    say("matmul", rows, n, k, out, kind)
     rng = np.random.default_rng(21)
     (ac, as_), (wc, ws) = operands(rng, rows, n, k, kind)
-    y = H.harp_matmul_q8(to_codes(ac), to_scales(as_, kind), to_codes(wc), to_scales(ws, kind), "f32")
+    y = H.harp_matmul_q8(to_codes(ac), to_scales(as_, kind), to_codes(wc), to_scales(ws, kind), out)
     torch.cuda.synchronize()
-    assert rel_rows(np64(y), Q.matmul(ac, as_, wc, ws)) <= TOL["f32"]
+    assert rel_rows(np64(y), Q.matmul(ac, as_, wc, ws)) <= TOL[out]
 
 
 @pytest.mark.parametrize("rows", [1, 50, 300])
