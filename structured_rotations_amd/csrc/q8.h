@@ -83,6 +83,33 @@ __device__ __forceinline__ void store8_of(T* p, int n, const float (&v)[8]) {
   else store8_tail<T>(p, n, v);
 }
 
+// Two of four codes as bf16, times the power of two whose E8M0 byte is the
+// exponent field of `scale`.
+__device__ __forceinline__ uint32_t widen2(uint32_t codes, uint32_t scale, bool hi) {
+  const bf16x2_t v = hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, __uint_as_float(scale), true)
+                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, __uint_as_float(scale), false);
+  uint32_t w;
+  __builtin_memcpy(&w, &v, 4);
+  return w;
+}
+struct __attribute__((packed, aligned(1))) Raw16 { uint32_t w[4]; };
+
+// 16 bytes of a row, the ones past its end (n) zero.
+__device__ __forceinline__ u32x4 load16_bytes(const uint8_t* p, int n) {
+  u32x4 v = {0, 0, 0, 0};
+  if (n >= 16) {
+    const Raw16 r = *reinterpret_cast<const Raw16*>(p);
+    v = u32x4{r.w[0], r.w[1], r.w[2], r.w[3]};
+  } else {
+    for (int i = 0; i < n; ++i) {
+      const uint32_t b = (uint32_t)p[i] << (8 * (i & 3));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] |= (i >> 2) == j ? b : 0u;
+    }
+  }
+  return v;
+}
+
 // Four E4M3 codes of four values (round to nearest, ties to even; the inputs
 // are within 448 up to an fp32 rounding, which rounds to 448).
 __device__ __forceinline__ uint32_t enc4(float a, float b, float c, float d) {
@@ -182,6 +209,11 @@ __device__ __forceinline__ float load_scale(const void* scales, int64_t i) {
 // them (vmcnt) before the barrier that precedes their first use.
 using TileSrc = __amdgpu_buffer_rsrc_t;
 __device__ __forceinline__ TileSrc tile_src(const void* base, int bytes) {
+  // both are the same in every lane; said so, or the loads may loop over lanes
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  base = reinterpret_cast<const void*>((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)at) |
+                                       (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(at >> 32)) << 32);
+  bytes = __builtin_amdgcn_readfirstlane(bytes);
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00027000);
 }
 __device__ __forceinline__ void load_lds16(TileSrc src, void* lds, unsigned lane_offset, int offset) {
@@ -206,6 +238,29 @@ __device__ __forceinline__ void load_lds_word(TileSrc src, void* lds, unsigned l
                  : "s"(at), "v"(lane_offset), "s"(src), "s"(offset)
                  : "memory");
 }
+// Loads of such a tile into registers.
+__device__ __forceinline__ u32x4 load_16(TileSrc src, unsigned lane_offset) {
+  return __builtin_amdgcn_raw_buffer_load_b128(src, lane_offset, 0, 0);
+}
+template <int kBytes>
+__device__ __forceinline__ uint32_t load_word(TileSrc src, unsigned lane_offset) {
+  if constexpr (kBytes == 4) return __builtin_amdgcn_raw_buffer_load_b32(src, lane_offset, 0, 0);
+  else return __builtin_amdgcn_raw_buffer_load_b8(src, lane_offset, 0, 0);
+}
+
+// Which tile a workgroup computes: consecutive workgroups go to the 8 dies in
+// turn, so each die takes one contiguous run of the tiles, ordered in groups
+// of 8 tiles along m, and its 32 compute units share 8 + 4 panels in its L2.
+__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int* tm, int* tn) {
+  const int total = tiles_m * tiles_n, xcd = id & 7, q = total >> 3, r = total & 7;
+  const int t = xcd * q + min(xcd, r) + (id >> 3);
+  constexpr int kGroup = 8;
+  const int per = kGroup * tiles_n, g = t / per, first = g * kGroup;
+  const int gm = min(kGroup, tiles_m - first), in = t - g * per;
+  *tm = first + in % gm;
+  *tn = in / gm;
+}
+
 // Lane offset that is beyond any tile.
 constexpr unsigned kNoLoad = 0x7fffff00u;
 

@@ -23,24 +23,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
-struct __attribute__((packed, aligned(1))) Raw16 { uint32_t w[4]; };
-
-// 16 codes of a row, the ones past its end zero.
-__device__ __forceinline__ u32x4 load16_codes(const uint8_t* p, int n) {
-  u32x4 v = {0, 0, 0, 0};
-  if (n >= 16) {
-    const Raw16 r = *reinterpret_cast<const Raw16*>(p);
-    v = u32x4{r.w[0], r.w[1], r.w[2], r.w[3]};
-  } else {
-    for (int i = 0; i < n; ++i) {
-      const uint32_t b = (uint32_t)p[i] << (8 * (i & 3));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] |= (i >> 2) == j ? b : 0u;
-    }
-  }
-  return v;
-}
-
 template <typename T>
 __device__ __forceinline__ void store4(T* p, int n, const f32x4& v);
 template <>
@@ -93,19 +75,6 @@ __device__ __forceinline__ bf16x8_t widen(const i32x8& f, int t) {
 }
 
 constexpr int kChunk = 8;  // steps whose row scales are brought in together
-
-// Which tile a workgroup computes: consecutive workgroups go to the 8 dies in
-// turn, so each die takes one contiguous run of the tiles, ordered in groups
-// of 8 tiles along m, and its 32 compute units share 8 + 4 panels in its L2.
-__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int* tm, int* tn) {
-  const int total = tiles_m * tiles_n, xcd = id & 7, q = total >> 3, r = total & 7;
-  const int t = xcd * q + min(xcd, r) + (id >> 3);
-  constexpr int kGroup = 8;
-  const int per = kGroup * tiles_n, g = t / per, first = g * kGroup;
-  const int gm = min(kGroup, tiles_m - first), in = t - g * per;
-  *tm = first + in % gm;
-  *tn = in / gm;
-}
 
 // One 64 MW x (64 NT NW / 4) tile of y per workgroup of MW x NW waves, each
 // with 64 rows (m) by 16 NT columns (n) of it.  LDS holds two steps of one
@@ -171,13 +140,13 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
       for (int i = 0; i < PA; ++i) {
         const int r = (wave + WAVES * i) * 8 + lrow;
         *reinterpret_cast<u32x4*>(la[buf] + (wave + WAVES * i) * 1024 + lane * 16) =
-            load16_codes(abase + (int64_t)r * g.lda + kk + pca, r < rows_a ? g.k - kk - pca : 0);
+            load16_bytes(abase + (int64_t)r * g.lda + kk + pca, r < rows_a ? g.k - kk - pca : 0);
       }
 #pragma unroll
       for (int i = 0; i < PW; ++i) {
         const int r = (wave + WAVES * i) * 8 + lrow;
         *reinterpret_cast<u32x4*>(lw[buf] + (wave + WAVES * i) * 1024 + lane * 16) =
-            load16_codes(wbase + (int64_t)r * g.ldw + kk + pcw, r < rows_w ? g.k - kk - pcw : 0);
+            load16_bytes(wbase + (int64_t)r * g.ldw + kk + pcw, r < rows_w ? g.k - kk - pcw : 0);
       }
     }
   };

@@ -22,107 +22,318 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kStep = 32;  // rows (m) per step
+constexpr int kStep = 64;  // rows (m) per step, two instructions' worth
 
 // LDS tile of kStep rows of W bf16 values: 32-byte segments exchanged by the
-// row's number so that neighbouring rows' reads of one segment cover all banks.
+// row's number, so that the 16 rows of a fragment read cover all banks.
 template <int W>
 __device__ __forceinline__ int seg_off(int row, int seg) {
-  constexpr int kSegs = W / 16;
-  return row * W * 2 + ((seg ^ (row & (kSegs < 16 ? kSegs - 1 : 15))) << 5);
+  return row * W * 2 + ((seg ^ (((row & 3) | (row >> 1 & 12)) & (W / 16 - 1))) << 5);
 }
 
-// The 8 values m = 8q .. 8q+7 of column seg * 16 + i16 for lane (q, i16).
+// Offset of lane (q, i16)'s part of the first column segment of a wave
+// (`first`, a multiple of the segments it reads) in a fragment read; segment
+// first + f is at this ^ 32 f.
 template <int W>
-__device__ __forceinline__ bf16x8_t frag_t(const uint8_t* lds, int seg, int lane) {
-  const int q = lane >> 4, i = lane & 15;
+__device__ __forceinline__ uint32_t frag_base(int first, int lane) {
+  return (uint32_t)(seg_off<W>(8 * (lane >> 4) + ((lane & 15) >> 2), first) + (lane & 3) * 8);
+}
+// The 8 values m = 32 sub + 8q .. + 7 of column i16 of segment f.
+template <int W>
+__device__ __forceinline__ bf16x8_t frag_t(const uint8_t* lds, uint32_t base, int sub, int f) {
   s16x4 v[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int row = 8 * q + 4 * h + (i >> 2);
+  for (int h = 0; h < 2; ++h)
     v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) s16x4*)(lds + seg_off<W>(row, seg) + (i & 3) * 8));
-  }
+        (__attribute__((address_space(3))) s16x4*)(lds + (base ^ (uint32_t)(f << 5)) + (32 * sub + 4 * h) * W * 2));
   const s16x8 r = __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
   return __builtin_bit_cast(bf16x8_t, r);
 }
 
 template <typename T>
-__device__ __forceinline__ void store4(T* p, int n, const f32x4& v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < n) store1(p + i, v[i]);
+__device__ __forceinline__ void store4(T* p, int n, const f32x4& v);
+template <>
+__device__ __forceinline__ void store4<float>(float* p, int n, const f32x4& v) {
+  struct __attribute__((packed, aligned(4))) R { float f[4]; };
+  if (n >= 4) *reinterpret_cast<R*>(p) = R{{v[0], v[1], v[2], v[3]}};
+  else
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = v[i];
+}
+template <>
+__device__ __forceinline__ void store4<uint16_t>(uint16_t* p, int n, const f32x4& v) {
+  struct __attribute__((packed, aligned(2))) R { uint32_t w[2]; };
+  const uint32_t lo = pack_bf16x2_hw(v[0], v[1]), hi = pack_bf16x2_hw(v[2], v[3]);
+  if (n >= 4) *reinterpret_cast<R*>(p) = R{{lo, hi}};
+  else
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = (uint16_t)((i < 2 ? lo : hi) >> (16 * (i & 1)));
 }
 
-// One 128 x 128 tile of dw per workgroup of 4 waves, each 64 (k) x 64 (n).
-// PARTS: bf16 parts of x.
-template <bool E8, int PARTS, typename TO>
-__global__ __launch_bounds__(256) void wgrad_tile_kernel(WgradArgs g, int m_per_split) {
-  constexpr int B = 128;
-  __shared__ __align__(16) uint8_t ld[kStep * B * 2];
-  __shared__ __align__(16) uint8_t lx[PARTS][kStep * B * 2];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int k0 = (int)blockIdx.x * B, n0 = (int)blockIdx.y * B;
-  const int wk = (wave & 1) * 4, wn = (wave >> 1) * 4;  // in segments of 16
-  const int64_t mlo = (int64_t)blockIdx.z * m_per_split, mhi = min((int64_t)g.rows, mlo + m_per_split);
-  f32x4 acc[4][4];
+// v's bytes from number `by` on (0..15), zeros behind them.
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int by) {
+  if (by & 8) v = u32x4{v[2], v[3], 0, 0};
+  if (by & 4) v = u32x4{v[1], v[2], v[3], 0};
+  const int b = 8 * (by & 3);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 4; ++i) v[i] = (uint32_t)((((uint64_t)(i < 3 ? v[i + 1] : 0) << 32) | v[i]) >> b);
+  return v;
+}
+
+// acc += a b.  kAcc: the accumulators are named as accumulation registers (a
+// wave that has 256 of them leaves the compiler no other place, and left to
+// itself it moves them about in the loop).  Nothing reads or writes one again
+// before 32 more instructions or settle().
+template <bool kAcc>
+__device__ __forceinline__ void mfma(f32x4& acc, bf16x8_t a, bf16x8_t b) {
+  if constexpr (kAcc) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+  else acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
+}
+// Lets the last results arrive.
+template <bool kAcc>
+__device__ __forceinline__ void settle() {
+  if constexpr (kAcc) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+}
+
+// How rows are brought in.  kWhole: 16-byte aligned rows of whole 16-byte
+// pieces; dy straight into LDS.  kCut: any alignment and length (8 columns of
+// dy and 16 of x at least); the piece that a row's end cuts is loaded from 16
+// bytes before the end and shifted.  kNarrow: fewer columns, by elements.
+enum Rows { kWhole, kCut, kNarrow };
+
+// One tile of dw per workgroup of 4 waves, each 16 NI (k) by 16 NJ (n) of it;
+// PARTS: bf16 parts of x.  Per step of 64 rows a wave multiplies from
+// registers (the fragments of half a step), while it
+//   first half    reads the second half's fragments, then decodes the next
+//                 step's rows, which are in registers, into the other buffer
+//   second half   (after a barrier) reads the next step's first fragments and
+//                 asks for the rows of the step after that.
+// Global loads have a whole step to arrive.
+template <int NI, int NJ, bool E8, int PARTS, typename TO, Rows kRows>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) void wgrad_tile_kernel(
+    WgradArgs g, int m_per_split, int tiles_n, int tiles_k) {
+  constexpr int BK = 32 * NI, BN = 32 * NJ, R = NI * PARTS;
+  constexpr int UD = kStep * BN / 8 / 256, UX = kStep * BK / 16 / 256;  // pieces per thread: 8 of dy, 16 of x
+  __shared__ __align__(16) uint8_t ld[2][kStep * BN * 2];
+  __shared__ __align__(16) uint8_t lx[2][PARTS][kStep * BK * 2];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int tn, tk;
+  tile_of((int)blockIdx.x, tiles_n, tiles_k, &tn, &tk);
+  const int k0 = tk * BK, n0 = tn * BN;
+  const int wk = (wave & 1) * NI, wn = (wave >> 1) * NJ;  // in segments of 16
+  const int mlo = (int)blockIdx.y * m_per_split, mhi = min(g.rows, mlo + m_per_split);
+
+  // Columns past the end give results that are not stored.  Rows past the end
+  // are past the descriptors' ends, too, and give zeros.
+  // dy, kWhole: load u of wave w brings rows (w << 3) + the bits of u in bits
+  // (1,) 2 and 5 + the lane's, so that the exchange of segments depends on u
+  // in bit 1 only.
+  constexpr int kRowsD = 512 / BN;  // rows of dy per load of a wave
+  unsigned vdd[2];
+  {
+    const int lr = lane / (BN / 8), pp = lane % (BN / 8);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  for (int64_t m0 = mlo; m0 < mhi; m0 += kStep) {
-    // 16 values (one segment) of each operand per thread: 32 rows x 8 segments
-    const int r = tid >> 3, sg = tid & 7;
-    const int64_t m = m0 + r;
-    float dv[2][8], xv[2][8];
-    float s = 0.0f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int nn = m < mhi ? g.n - (n0 + sg * 16 + h * 8) : 0, nk = m < mhi ? g.k - (k0 + sg * 16 + h * 8) : 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) dv[h][j] = xv[h][j] = 0.0f;
-      if (nn > 0) load8_of<uint16_t>(g.dy + m * g.lddy + n0 + sg * 16 + h * 8, nn, dv[h]);
-      if (nk > 0) load8_codes(g.x + m * g.ldx + k0 + sg * 16 + h * 8, nk, xv[h]);
+    for (int t = 0; t < 2; ++t) {
+      const int row = wave * 8 + lr + (kRowsD == 2 ? 2 * t : 0);
+      const int x = ((row & 3) | (row >> 1 & 12)) & (BN / 16 - 1);
+      const int col = ((pp >> 1) ^ x) * 16 + (pp & 1) * 8;
+      vdd[t] = n0 + col < g.n ? (unsigned)(row * (int)g.lddy + col) * 2u : kNoLoad;
     }
-    if (m < mhi) s = load_scale<E8>(g.x_scales, m * g.nkb + k0 / kQBlk);
-    __syncthreads();
+  }
+  auto row_of_load = [](int u) { return kRowsD == 2 ? (u >> 1 & 1) * 4 + (u >> 2) * 32 : (u & 1) * 4 + (u >> 1) * 32; };
+  // the others: piece of 8 columns (dy) or 16 (x) of a thread's rows
+  const int dcol = tid % (BN / 8) * 8, xcol = tid % (BK / 16) * 16;
+  const int drow = tid / (BN / 8), xrow = tid / (BK / 16);
+  const int dn = g.n - n0 - dcol, xn = g.k - k0 - xcol;
+  const int cut_d = kRows == kCut && dn > 0 && dn < 8 ? 16 - 2 * dn : 0, cut_x = kRows == kCut && xn > 0 && xn < 16 ? 16 - xn : 0;
+  const unsigned vd = dn > 0 ? (unsigned)((drow * (int)g.lddy + dcol) * 2 - cut_d) : kNoLoad;
+  const unsigned vx = xn > 0 ? (unsigned)(xrow * (int)g.ldx + xcol - cut_x) : kNoLoad;
+  constexpr int kSB = E8 ? 1 : 4;
+  const unsigned vs = xn > 0 ? (unsigned)(xrow * g.nkb + (k0 + xcol) / kQBlk) * kSB : kNoLoad;
+
+  u32x4 rd[UD], rx[UX];  // the next step's rows, as they come
+  uint32_t rs[UX];
+  // descriptors of a step's rows; they begin with the row, not the tile, so
+  // that a shifted piece of the first columns is inside
+  auto rows_left = [&](int m0) { return max(0, min(mhi - m0, kStep)); };
+  auto src_dy = [&](int m0) {
+    const int left = rows_left(m0);
+    return tile_src(g.dy + (int64_t)(left ? m0 : mlo) * g.lddy, left ? ((left - 1) * (int)g.lddy + g.n) * 2 : 0);
+  };
+  auto bring_dy = [&](TileSrc src, int buf, int u) {
+    const unsigned v = vdd[kRowsD == 2 ? u & 1 : 0];
+    const int row = row_of_load(u) + (kRowsD == 2 ? (u & 1) * 2 : 0);
+    load_lds16(src, ld[buf] + (row + wave * 8) * BN * 2, v + (unsigned)(n0 * 2 + row_of_load(u) * (int)g.lddy * 2), 0);
+  };
+  auto load_dy = [&](int m0) {
+    if constexpr (kRows == kCut) {
+      const TileSrc src = src_dy(m0);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      store8(reinterpret_cast<uint16_t*>(ld + seg_off<B>(r, sg) + h * 16), dv[h]);
-      float hi[8];
+      for (int u = 0; u < UD; ++u) rd[u] = load_16(src, vd + (unsigned)(n0 * 2 + u * (2048 / BN) * (int)g.lddy * 2));
+    } else if constexpr (kRows == kNarrow) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) hi[j] = xv[h][j] * s;
-      store8(reinterpret_cast<uint16_t*>(lx[0] + seg_off<B>(r, sg) + h * 16), hi);
-      if constexpr (PARTS == 2) {
-        float lo[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) lo[j] = hi[j] - bf16_to_f32((uint16_t)pack_bf16x2_hw(hi[j], hi[j]));
-        store8(reinterpret_cast<uint16_t*>(lx[PARTS - 1] + seg_off<B>(r, sg) + h * 16), lo);
+      for (int u = 0; u < UD; ++u) {
+        const int64_t m = m0 + drow + u * (2048 / BN);
+        rd[u] = load16_bytes(reinterpret_cast<const uint8_t*>(g.dy + m * g.lddy + n0 + dcol), m < mhi ? dn * 2 : 0);
       }
     }
-    __syncthreads();
-    bf16x8_t fd[4];
+  };
+  auto load_x = [&](int m0) {
+    const int left = rows_left(m0);
+    const int64_t at = left ? m0 : mlo;
+    const TileSrc sx = tile_src(g.x + at * g.ldx, left ? (left - 1) * (int)g.ldx + g.k : 0);
+    const TileSrc ss = tile_src(static_cast<const uint8_t*>(g.x_scales) + at * g.nkb * kSB, left * g.nkb * kSB);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) fd[j] = frag_t<B>(ld, wn + j, lane);
+    for (int u = 0; u < UX; ++u) {
+      const int r = u * (4096 / BK);
+      if constexpr (kRows == kNarrow)
+        rx[u] = load16_bytes(g.x + (at + xrow + r) * g.ldx + k0 + xcol, xrow + r < left ? xn : 0);
+      else rx[u] = load_16(sx, vx + (unsigned)(k0 + r * (int)g.ldx));
+      rs[u] = load_word<kSB>(ss, vs + (unsigned)(r * g.nkb * kSB));
+    }
+  };
+  auto keep_dy = [&](int buf, int u) {
+    if constexpr (kRows != kWhole) {
+      if (cut_d) rd[u] = shift_down(rd[u], cut_d);
+      *reinterpret_cast<u32x4*>(ld[buf] + seg_off<BN>(drow + u * (2048 / BN), dcol >> 4) + (dcol & 8) * 2) = rd[u];
+    }
+  };
+  static_assert(4096 / BK >= 16 || UX == 1 || (4096 / BK) % 8 == 0, "");
+  uint32_t xat = (uint32_t)seg_off<BK>(xrow, xcol >> 4);
+  auto keep_x = [&](int u) {
+    // bits 3 and 4 of the row, which u changes, exchange segments 4 and 8 apart
+    constexpr int kUp = 4096 / BK;
+    const uint32_t at = (xat ^ (uint32_t)(((u * kUp >> 1 & 12) & (BK / 16 - 1)) << 5)) + u * kUp * BK * 2;
+    if (kRows == kCut && cut_x) rx[u] = shift_down(rx[u], cut_x);
+    u32x4 w[PARTS][2];
 #pragma unroll
-    for (int p = 0; p < PARTS; ++p)
+    for (int c = 0; c < 4; ++c) {
+      if constexpr (E8 && PARTS == 1) {
+        w[0][c >> 1][2 * (c & 1)] = widen2(rx[u][c], rs[u] << 23, false);
+        w[0][c >> 1][2 * (c & 1) + 1] = widen2(rx[u][c], rs[u] << 23, true);
+      } else {
+        const float s = E8 ? e8m0_value(rs[u]) : __uint_as_float(rs[u]);
+        float v[4];
+        dec4(rx[u][c], v);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bf16x8_t fx = frag_t<B>(lx[p], wk + i, lane);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx, fd[j], acc[i][j], 0, 0, 0);
+        for (int e = 0; e < 2; ++e) {
+          const float a = v[2 * e] * s, b = v[2 * e + 1] * s;
+          const uint32_t hi = pack_bf16x2_hw(a, b);
+          w[0][c >> 1][2 * (c & 1) + e] = hi;
+          if constexpr (PARTS == 2) w[PARTS - 1][c >> 1][2 * (c & 1) + e] = pack_bf16x2_hw(a - bf16_lo(hi), b - bf16_hi(hi));
+        }
       }
+    }
+    // odd pieces write their halves in the other order: eight lanes then fill
+    // 128 different bytes
+#pragma unroll
+    for (int t = 0; t < PARTS; ++t) {
+      const bool odd = tid & 1;
+      *reinterpret_cast<u32x4*>(lx[0][t] + at + (odd ? 16 : 0)) = odd ? w[t][1] : w[t][0];
+      *reinterpret_cast<u32x4*>(lx[0][t] + at + (odd ? 0 : 16)) = odd ? w[t][0] : w[t][1];
+    }
+  };
+
+  constexpr bool kAcc = NI * NJ * 4 > 128;
+  f32x4 acc[NI][NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  settle<kAcc>();
+  bf16x8_t fx[2][R], fd[2][NJ];
+  // offsets of the buffer that is read; the other one is at ^ kFlip
+  constexpr uint32_t kFlipD = kStep * BN * 2, kFlipX = PARTS * kStep * BK * 2;
+  uint32_t fbd = frag_base<BN>(wn, lane), fbx = frag_base<BK>(wk, lane);
+  auto read_frag = [&](int set, int sub, int f) {  // fragment f of a half step: dy's first
+    if (f < NJ) fd[set][f] = frag_t<BN>(ld[0], fbd, sub, f);
+    else fx[set][f - NJ] = frag_t<BK>(lx[0][(f - NJ) / NI], fbx, sub, (f - NJ) % NI);
+  };
+  constexpr int H = R / 2, kReads = (R + NJ + H - 1) / H;  // rows of instructions in half of a half step
+  auto step = [&](int m0, int buf) {
+    // keeps the compiler from holding every segment's address in a register
+    asm volatile("" : "+v"(fbd), "+v"(fbx), "+v"(xat));
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r < H) {
+#pragma unroll
+        for (int f = r * kReads; f < (r + 1) * kReads; ++f)
+          if (f < R + NJ) read_frag(1, 1, f);
+      } else {
+        constexpr int kD = (UD + H - 1) / H, kX = (UX + H - 1) / H;
+#pragma unroll
+        for (int u = (r - H) * kD; u < (r - H + 1) * kD; ++u)
+          if (u < UD) keep_dy(buf ^ 1, u);
+#pragma unroll
+        for (int u = (r - H) * kX; u < (r - H + 1) * kX; ++u)
+          if (u < UX) keep_x(u);
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        mfma<kAcc>(acc[r % NI][j], fx[0][r], fd[0][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // this buffer has been read by every wave, the other one is complete
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    fbd ^= kFlipD;
+    fbx ^= kFlipX;
+    xat ^= kFlipX;
+    const TileSrc src = src_dy(m0 + 2 * kStep);
+    load_x(m0 + 2 * kStep);
+    load_dy(m0 + 2 * kStep);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if constexpr (kRows == kWhole) {
+        constexpr int kL = (UD + R - 1) / R;
+#pragma unroll
+        for (int u = r * kL; u < (r + 1) * kL; ++u)
+          if (u < UD) bring_dy(src, buf, u);
+      }
+      if (r < H) {
+#pragma unroll
+        for (int f = r * kReads; f < (r + 1) * kReads; ++f)
+          if (f < R + NJ) read_frag(0, 0, f);
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        mfma<kAcc>(acc[r % NI][j], fx[1][r], fd[1][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  if (mlo < mhi) {
+    if constexpr (kRows == kWhole) {
+      const TileSrc s0 = src_dy(mlo), s1 = src_dy(mlo + kStep);
+#pragma unroll
+      for (int u = 0; u < UD; ++u) bring_dy(s0, 0, u);
+#pragma unroll
+      for (int u = 0; u < UD; ++u) bring_dy(s1, 1, u);
+    }
+    load_x(mlo);
+    load_dy(mlo);
+#pragma unroll
+    for (int u = 0; u < UD; ++u) keep_dy(0, u);
+#pragma unroll
+    for (int u = 0; u < UX; ++u) keep_x(u);
+    xat ^= kFlipX;
+    load_x(mlo + kStep);
+    load_dy(mlo + kStep);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+    for (int f = 0; f < R + NJ; ++f) read_frag(0, 0, f);
+    for (int m0 = mlo, buf = 0; m0 < mhi; m0 += kStep, buf ^= 1) step(m0, buf);
+    settle<kAcc>();
+    // no load may be in flight into LDS when the workgroup ends
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < NJ; ++j) {
     const int n = n0 + (wn + j) * 16 + (lane & 15);
     if (n >= g.n) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NI; ++i) {
       const int k = k0 + (wk + i) * 16 + (lane >> 4) * 4;
       if (k >= g.k) continue;
-      if (gridDim.z > 1) store4<float>(g.partial + ((int64_t)blockIdx.z * g.n + n) * g.k + k, g.k - k, acc[i][j]);
+      if (gridDim.y > 1) store4<float>(g.partial + ((int64_t)blockIdx.y * g.n + n) * g.k + k, g.k - k, acc[i][j]);
       else store4<TO>(static_cast<TO*>(g.dw) + (int64_t)n * g.lddw + k, g.k - k, acc[i][j]);
     }
   }
@@ -139,24 +350,52 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(WgradArgs g, int splits
   }
 }
 
-int wgrad_splits(int64_t rows, int64_t n, int64_t k, int64_t* per) {
-  const int64_t tiles = ((n + 127) / 128) * ((k + 127) / 128), steps = (rows + kStep - 1) / kStep;
-  int64_t s = 1;
-  while (tiles * s < 256 && s * 2 * 4 <= steps && s < 64) s *= 2;
-  const int64_t p = (steps + s - 1) / s;
-  *per = p * kStep;
-  return p > 0 ? (int)((steps + p - 1) / p) : 1;
+// The tile and the number of splits of the rows: 256 x 256 tiles when there
+// are enough of them for the compute units, else 128 x 128.  (Two parts of x:
+// half as wide in k.)  The rows are split while tiles leave compute units
+// idle and every split keeps 4 steps.
+struct WgradShape {
+  bool big;
+  int splits, m_per_split;
+};
+WgradShape wgrad_shape(int64_t rows, int64_t n, int64_t k) {
+  WgradShape s;
+  s.big = ((n + 255) / 256) * ((k + 255) / 256) >= 192;
+  const int64_t b = s.big ? 256 : 128;
+  const int64_t tiles = ((n + b - 1) / b) * ((k + b - 1) / b), steps = (rows + kStep - 1) / kStep;
+  int64_t p = 1;
+  if (!s.big)
+    while (tiles * p < 256 && p * 2 * 4 <= steps && p < 64) p *= 2;
+  const int64_t per = (steps + p - 1) / p;
+  s.m_per_split = (int)(per * kStep);
+  s.splits = per > 0 ? (int)((steps + per - 1) / per) : 1;
+  return s;
+}
+
+template <int NI, int NJ, bool E8, int PARTS, typename TO, Rows kRows>
+void wgrad_tile_go(const WgradArgs& g, const WgradShape& s, hipStream_t stream) {
+  constexpr int BK = 32 * NI, BN = 32 * NJ;
+  const int tn = (g.n + BN - 1) / BN, tk = (g.k + BK - 1) / BK;
+  hipLaunchKernelGGL((wgrad_tile_kernel<NI, NJ, E8, PARTS, TO, kRows>), dim3(tn * tk, s.splits), dim3(256), 0, stream,
+                     g, s.m_per_split, tn, tk);
 }
 
 template <bool E8, int PARTS, typename TO>
 hipError_t wgrad_go(const WgradArgs& g, hipStream_t stream) {
-  int64_t per;
-  const int s = wgrad_splits(g.rows, g.n, g.k, &per);
-  hipLaunchKernelGGL((wgrad_tile_kernel<E8, PARTS, TO>), dim3((g.k + 127) / 128, (g.n + 127) / 128, s), dim3(256), 0,
-                     stream, g, (int)per);
-  if (s > 1) {
+  const WgradShape s = wgrad_shape(g.rows, g.n, g.k);
+  const bool whole = ((reinterpret_cast<uintptr_t>(g.dy) | reinterpret_cast<uintptr_t>(g.x) | (uintptr_t)(g.lddy * 2) |
+                       (uintptr_t)g.ldx | (uintptr_t)(g.n * 2) | (uintptr_t)g.k) & 15) == 0;
+  // a descriptor holds 64 rows in 2 GiB
+  const bool narrow = g.n < 8 || g.k < 16 || g.lddy > (1 << 22) || g.ldx > (1 << 22);
+  if (narrow) wgrad_tile_go<4 / PARTS, 4, E8, PARTS, TO, kNarrow>(g, s, stream);
+  else if (s.big && whole) wgrad_tile_go<8 / PARTS, 8, E8, PARTS, TO, kWhole>(g, s, stream);
+  else if (s.big) wgrad_tile_go<8 / PARTS, 8, E8, PARTS, TO, kCut>(g, s, stream);
+  else if (whole) wgrad_tile_go<4 / PARTS, 4, E8, PARTS, TO, kWhole>(g, s, stream);
+  else wgrad_tile_go<4 / PARTS, 4, E8, PARTS, TO, kCut>(g, s, stream);
+  if (s.splits > 1) {
     const int64_t wg = ((int64_t)g.n * g.k + 255) / 256;
-    hipLaunchKernelGGL((wgrad_join_kernel<TO>), dim3((unsigned)(wg < 4096 ? wg : 4096)), dim3(256), 0, stream, g, s);
+    hipLaunchKernelGGL((wgrad_join_kernel<TO>), dim3((unsigned)(wg < 4096 ? wg : 4096)), dim3(256), 0, stream, g,
+                       s.splits);
   }
   return hipGetLastError();
 }
@@ -164,8 +403,7 @@ hipError_t wgrad_go(const WgradArgs& g, hipStream_t stream) {
 }  // namespace
 
 int64_t matmul_q8_wgrad_workspace(int64_t rows, int64_t n, int64_t k) {
-  int64_t per;
-  const int s = wgrad_splits(rows, n, k, &per);
+  const int s = wgrad_shape(rows, n, k).splits;
   return s > 1 ? (int64_t)s * n * k * 4 : 0;
 }
 
