@@ -25,26 +25,6 @@ struct __attribute__((packed, aligned(2))) Raw8H { uint32_t w[4]; };
 struct __attribute__((packed, aligned(4))) Raw8F { uint32_t w[8]; };
 struct __attribute__((packed, aligned(1))) Raw8C { uint32_t w[2]; };
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8<uint16_t>(const uint16_t* p, float (&v)[8]) {
-  const Raw8H r = *reinterpret_cast<const Raw8H*>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(r.w[i]);
-    v[2 * i + 1] = bf16_hi(r.w[i]);
-  }
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-  const Raw8F r = *reinterpret_cast<const Raw8F*>(p);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
-}
-__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
   Raw8H r;
 #pragma unroll
@@ -60,22 +40,12 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)pack_bf16x2_hw(v, v); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
-// The first n (< 8) values of a chunk; the rest are zero.
-template <typename T>
-__device__ __forceinline__ void load8_tail(const T* p, int n, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = i < n ? load1(p + i) : 0.0f;
-}
+// The first n values of a chunk.
 template <typename T>
 __device__ __forceinline__ void store8_tail(T* p, int n, const float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) store1(p + i, v[i]);
-}
-template <typename T>
-__device__ __forceinline__ void load8_of(const T* p, int n, float (&v)[8]) {
-  if (n >= 8) load8<T>(p, v);
-  else load8_tail<T>(p, n, v);
 }
 template <typename T>
 __device__ __forceinline__ void store8_of(T* p, int n, const float (&v)[8]) {
@@ -125,25 +95,78 @@ __device__ __forceinline__ void dec4(uint32_t w, float* v) {
   v[2] = hi[0];
   v[3] = hi[1];
 }
-__device__ __forceinline__ void load8_codes(const uint8_t* p, int n, float (&v)[8]) {
-  if (n >= 8) {
-    const Raw8C r = *reinterpret_cast<const Raw8C*>(p);
-    dec4(r.w[0], v);
-    dec4(r.w[1], v + 4);
-  } else {
-    uint32_t w[2] = {0, 0};
-    for (int i = 0; i < n; ++i) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+// Eight values as they are in memory, and what they are.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const uint16_t* p, int n) {
+    if (n >= 8) {
+      const Raw8H r = *reinterpret_cast<const Raw8H*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = r.w[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+    }
+  }
+  __device__ __forceinline__ void fill(uint32_t bits) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = bits >> 16 | (bits & 0xffff0000u);
+  }
+  __device__ __forceinline__ float operator[](int i) const { return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
+};
+template <>
+struct Raw8<float> {
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const float* p, int n) {
+    if (n >= 8) {
+      const Raw8F r = *reinterpret_cast<const Raw8F*>(p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = r.w[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = i < n ? __float_as_uint(p[i]) : 0u;
+    }
+  }
+  __device__ __forceinline__ void fill(uint32_t bits) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = bits;
+  }
+  __device__ __forceinline__ float operator[](int i) const { return __uint_as_float(w[i]); }
+};
+struct RawCodes {
+  uint32_t w[2];
+  __device__ __forceinline__ void load(const uint8_t* p, int n) {
+    if (n >= 8) {
+      const Raw8C r = *reinterpret_cast<const Raw8C*>(p);
+      w[0] = r.w[0];
+      w[1] = r.w[1];
+    } else {
+      w[0] = w[1] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
     dec4(w[0], v);
     dec4(w[1], v + 4);
   }
-}
+};
 __device__ __forceinline__ void store8_codes(uint8_t* p, int n, const float (&v)[8]) {
   Raw8C r;
   r.w[0] = enc4(v[0], v[1], v[2], v[3]);
   r.w[1] = enc4(v[4], v[5], v[6], v[7]);
-  if (n >= 8) *reinterpret_cast<Raw8C*>(p) = r;
-  else
-    for (int i = 0; i < n; ++i) p[i] = (uint8_t)(r.w[i >> 2] >> (8 * (i & 3)));
+  if (n >= 8) {
+    *reinterpret_cast<Raw8C*>(p) = r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (uint8_t)(r.w[i >> 2] >> (8 * (i & 3)));
+  }
 }
 
 // Coding of values v = w * mult (mult: the row's 1/rms, or 1) that share a

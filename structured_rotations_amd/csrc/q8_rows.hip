@@ -5,6 +5,8 @@
 // All of them are bound by HBM.  A thread holds chunks of 8 consecutive
 // values (16 bytes of bf16), so a block of 128 columns is one DPP row of 16
 // lanes and its maximum is four row rotations, with no LDS.
+#include <algorithm>
+
 #include "q8.h"
 
 namespace harp {
@@ -23,8 +25,12 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* __restrict_
   const int n = blk < nblk ? cols - col : 0;
   const int64_t step = (int64_t)gridDim.y * (16 >> sh);
   for (int64_t r = (int64_t)blockIdx.y * (16 >> sh) + (unit >> sh); r < rows; r += step) {
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (n > 0) load8_of<T>(x + r * ldx + col, n, v);
+    Raw8<T> w;
+    w.fill(0);
+    if (n > 0) w.load(x + r * ldx + col, n);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = w[i];
     const Coder<E8> code(row16_umax(amax8(v)), 1.0f);
     code.code8(v, v);
     if (n > 0) {
@@ -45,18 +51,18 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const T* __restrict_
   const int64_t r0 = (int64_t)blockIdx.y * kQBlk + (threadIdx.x >> 4);
   const int col = blk * kQBlk + (threadIdx.x & 15) * 8;
   const int n = cols - col;
-  float v[8][8];
+  Raw8<T> w[8];
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = r0 + 16 * i;
-    if (r < rows && n > 0) load8_of<T>(x + r * ldx + col, n, v[i]);
-    else
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    w[i].fill(0);
+    if (r < rows && n > 0) w[i].load(x + r * ldx + col, n);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, amax8(v[i]));
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(w[i][j]) & 0x7fffffffu);
   m = row16_umax(m);
   m = max(m, (uint32_t)__shfl_xor((int)m, 16));
   m = max(m, (uint32_t)__shfl_xor((int)m, 32));
@@ -66,8 +72,11 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const T* __restrict_
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = r0 + 16 * i;
-    code.code8(v[i], v[i]);
-    if (r < rows && n > 0) store8_codes(codes + r * ldc + col, n, v[i]);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = w[i][j];
+    code.code8(v, v);
+    if (r < rows && n > 0) store8_codes(codes + r * ldc + col, n, v);
   }
   if (threadIdx.x == 0) store_scale<E8>(scales, (int64_t)blockIdx.y * nblk + blk, code.scale);
 }
@@ -86,73 +95,78 @@ __device__ __forceinline__ float block_sum(float v, float (&part)[2][16], int se
   return row16_sum(l < nw ? part[set][l] : 0.0f);
 }
 
-// One row per workgroup; the row stays in registers between the sum of
-// squares and the coding (NCH chunks of 8 per thread).
+// Rows up to 8192 leave registers for the next row.
+template <int NCH>
+constexpr bool kAhead = NCH <= 2;
+
+// A workgroup walks over rows; a row stays in registers between the sum of
+// squares and the coding (NCH chunks of 8 per thread), and (kAhead) the next
+// row is on its way meanwhile.
 template <typename T, int NCH, bool E8>
-__global__ __launch_bounds__(1024) void rmsnorm_q8_kernel(NormArgs a) {
+__global__ __launch_bounds__(kAhead<NCH> ? 512 : 1024) void rmsnorm_q8_kernel(NormArgs a) {
   __shared__ float part[2][16];
   const int nblk = (a.d + kQBlk - 1) / kQBlk;
   const T* gamma = static_cast<const T*>(a.gamma);
-  int set = 0;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, set ^= 1) {
-    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
-    const T* res = static_cast<const T*>(a.residual) + (a.residual ? r * a.ldr : 0);
-    float v[NCH][8];
-    float ss = 0.0f;
+  int col[NCH], n[NCH];
+  Raw8<T> x[NCH], res[NCH];
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    col[c] = ((int)threadIdx.x + c * (int)blockDim.x) * 8;
+    n[c] = a.d - col[c];
+    x[c].fill(0);
+    res[c].fill(0);
+  }
+  auto load = [&](int64_t r) {
+    if (r >= a.rows) return;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      const int col = ((int)threadIdx.x + c * (int)blockDim.x) * 8, n = a.d - col;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[c][j] = 0.0f;
-      if (n > 0) load8_of<T>(x + col, n, v[c]);
+      if (n[c] <= 0) continue;
+      x[c].load(static_cast<const T*>(a.x) + r * a.ldx + col[c], n[c]);
+      if (a.residual) res[c].load(static_cast<const T*>(a.residual) + r * a.ldr + col[c], n[c]);
     }
-    if (a.residual) {
-      float w[NCH][8];
+  };
+  if (kAhead<NCH>) load(blockIdx.x);
+  int set = 0;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, set ^= 1) {
+    if (!kAhead<NCH>) load(r);
+    float v[NCH][8], ss = 0.0f;
 #pragma unroll
-      for (int c = 0; c < NCH; ++c) {
-        const int col = ((int)threadIdx.x + c * (int)blockDim.x) * 8, n = a.d - col;
-        if (n > 0) load8_of<T>(res + col, n, w[c]);
+    for (int c = 0; c < NCH; ++c) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[c][j] = a.residual ? x[c][j] + res[c][j] : x[c][j];
+        ss += v[c][j] * v[c][j];
       }
-#pragma unroll
-      for (int c = 0; c < NCH; ++c) {
-        const int col = ((int)threadIdx.x + c * (int)blockDim.x) * 8, n = a.d - col;
-        if (n <= 0) continue;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[c][j] += w[c][j];
-        if (a.h) store8_of<T>(static_cast<T*>(a.h) + r * a.ldh + col, n, v[c]);
-      }
+      if (a.h && n[c] > 0) store8_of<T>(static_cast<T*>(a.h) + r * a.ldh + col[c], n[c], v[c]);
     }
-#pragma unroll
-    for (int c = 0; c < NCH; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss += v[c][j] * v[c][j];
+    if (kAhead<NCH>) load(r + gridDim.x);
     ss = block_sum(ss, part, set);
     const float rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      const int chunk = (int)threadIdx.x + c * (int)blockDim.x;
-      const int col = chunk * 8, n = a.d - col;
-float o[8];
+      const int blk = col[c] / kQBlk;
+      float o[8];
       if (gamma) {
         if (a.ckpt) {
           const Coder<E8> code(row16_umax(amax8(v[c])), rstd);
           code.code8(v[c], o);
-          if (n > 0) {
-            store8_codes(a.ckpt + r * a.ldk + col, n, o);
-            if ((threadIdx.x & 15) == 0) store_scale<E8>(a.ckpt_scales, r * nblk + (chunk >> 4), code.scale);
+          if (n[c] > 0) {
+            store8_codes(a.ckpt + r * a.ldk + col[c], n[c], o);
+            if ((threadIdx.x & 15) == 0) store_scale<E8>(a.ckpt_scales, r * nblk + blk, code.scale);
           }
         }
-        float g[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (n > 0) load8_of<T>(gamma + col, n, g);
+        Raw8<T> g;
+        g.fill(0);
+        if (n[c] > 0) g.load(gamma + col[c], n[c]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[c][j] *= g[j];
       }
       const Coder<E8> code(row16_umax(amax8(v[c])), rstd);
       code.code8(v[c], o);
-      if (n > 0) {
-        store8_codes(a.codes + r * a.ldc + col, n, o);
-        if ((threadIdx.x & 15) == 0) store_scale<E8>(a.scales, r * nblk + (chunk >> 4), code.scale);
+      if (n[c] > 0) {
+        store8_codes(a.codes + r * a.ldc + col[c], n[c], o);
+        if ((threadIdx.x & 15) == 0) store_scale<E8>(a.scales, r * nblk + blk, code.scale);
       }
     }
   }
@@ -160,125 +174,157 @@ float o[8];
 
 // --------------------------------------------------------- norm, backward
 // A workgroup walks over rows, keeping gamma and its share of dgamma's sum
-// for its columns in registers; the partial sums of the workgroups are added
-// in order by the second kernel.
+// for its columns in registers, and the row as it came: the values are made
+// from it once for the sum and once for dh, which takes fewer registers than
+// keeping them.  The next row is on its way meanwhile (kAhead; longer rows
+// read gamma and dres when they are used instead).  The partial sums of the
+// workgroups are added in order by the second kernel.
 template <typename T, int NCH, bool E8>
 __global__ __launch_bounds__(1024) void rmsnorm_q8_vjp_kernel(NormVjpArgs a) {
   __shared__ float part[2][16];
   const int nblk = (a.d + kQBlk - 1) / kQBlk;
-  float g[NCH][8], dg[NCH][8];
+  int col[NCH], n[NCH];
+  Raw8<T> g[NCH];
+  float dg[NCH][8];
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int col = ((int)threadIdx.x + c * (int)blockDim.x) * 8, n = a.d - col;
+    col[c] = ((int)threadIdx.x + c * (int)blockDim.x) * 8;
+    n[c] = a.d - col[c];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      g[c][j] = 1.0f;
-      dg[c][j] = 0.0f;
-    }
-    if (a.gamma && n > 0) load8_of<T>(static_cast<const T*>(a.gamma) + col, n, g[c]);
+    for (int j = 0; j < 8; ++j) dg[c][j] = 0.0f;
   }
-  int set = 0;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, set ^= 1) {
-    float xn[NCH][8], u[NCH][8], dr[NCH][8];
-    float dot = 0.0f;
-    const float rstd = a.rstd[r];
+  auto load_g = [&](int c) {
+    g[c].fill(0x3f800000u);
+    if (a.gamma && n[c] > 0) g[c].load(static_cast<const T*>(a.gamma) + col[c], n[c]);
+  };
+  if (kAhead<NCH>)
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) load_g(c);
+  struct Row {
+    Raw8<T> dn[NCH], dr[NCH];
+    RawCodes cd[NCH];
+    float sc[NCH], rstd;
+  } now, next;
+  auto load_dr = [&](Row& w, int64_t r, int c) {
+    w.dr[c].fill(0);
+    if (a.dres && r < a.rows && n[c] > 0)
+      w.dr[c].load(static_cast<const T*>(a.dres) + r * a.lddres + col[c], n[c]);
+  };
+  auto load = [&](Row& w, int64_t r) {
+    w.rstd = r < a.rows ? a.rstd[r] : 0.0f;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      const int chunk = (int)threadIdx.x + c * (int)blockDim.x;
-      const int col = chunk * 8, n = a.d - col;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) xn[c][j] = u[c][j] = dr[c][j] = 0.0f;
-      if (n > 0) {
-        load8_codes(a.codes + r * a.ldc + col, n, xn[c]);
-        load8_of<T>(static_cast<const T*>(a.dn) + r * a.lddn + col, n, u[c]);
-        if (a.dres) load8_of<T>(static_cast<const T*>(a.dres) + r * a.lddres + col, n, dr[c]);
-        const float s = load_scale<E8>(a.scales, r * nblk + (chunk >> 4));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) xn[c][j] = j < n ? xn[c][j] * s : 0.0f;  // 0 past the end, whatever the scale
-      }
+      w.dn[c].fill(0);
+      if (kAhead<NCH>) load_dr(w, r, c);
+      w.cd[c].w[0] = w.cd[c].w[1] = 0;
+      w.sc[c] = 0.0f;
+      if (r >= a.rows || n[c] <= 0) continue;
+      w.cd[c].load(a.codes + r * a.ldc + col[c], n[c]);
+      w.dn[c].load(static_cast<const T*>(a.dn) + r * a.lddn + col[c], n[c]);
+      w.sc[c] = load_scale<E8>(a.scales, r * nblk + col[c] / kQBlk);
     }
+  };
+  if (kAhead<NCH>) load(now, blockIdx.x);
+  int set = 0;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, set ^= 1) {
+    if (kAhead<NCH>) load(next, r + gridDim.x);
+    else load(now, r);
+    float dot = 0.0f;
 #pragma unroll
-    for (int c = 0; c < NCH; ++c)
+    for (int c = 0; c < NCH; ++c) {
+      float xn[8];
+      now.cd[c].values(xn);
+      if (!kAhead<NCH>) load_g(c);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dg[c][j] += u[c][j] * xn[c][j];
-        u[c][j] *= g[c][j];
-        dot += u[c][j] * xn[c][j];
+        xn[j] = j < n[c] ? xn[j] * now.sc[c] : 0.0f;  // 0 past the row's end, whatever the scale
+        const float u = now.dn[c][j];
+        dg[c][j] += u * xn[j];
+        dot += u * g[c][j] * xn[j];
       }
+    }
     const float mean = block_sum(dot, part, set) / (float)a.d;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      const int col = ((int)threadIdx.x + c * (int)blockDim.x) * 8, n = a.d - col;
-      if (n <= 0) continue;
-      float o[8];
+      if (n[c] <= 0) continue;
+      float xn[8], o[8];
+      now.cd[c].values(xn);
+      if (!kAhead<NCH>) {
+        load_g(c);
+        load_dr(now, r, c);
+      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = dr[c][j] + rstd * (u[c][j] - xn[c][j] * mean);
-      store8_of<T>(static_cast<T*>(a.dh) + r * a.lddh + col, n, o);
+      for (int j = 0; j < 8; ++j)
+        o[j] = now.dr[c][j] + now.rstd * (now.dn[c][j] * g[c][j] - xn[j] * now.sc[c] * mean);
+      store8_of<T>(static_cast<T*>(a.dh) + r * a.lddh + col[c], n[c], o);
     }
+    if (kAhead<NCH>) now = next;
   }
   if (a.partial) {
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int col = ((int)threadIdx.x + c * (int)blockDim.x) * 8, n = a.d - col;
-      if (n > 0) store8_of<float>(a.partial + (int64_t)blockIdx.x * a.d + col, n, dg[c]);
-    }
+    for (int c = 0; c < NCH; ++c)
+      if (n[c] > 0) store8_of<float>(a.partial + (int64_t)blockIdx.x * a.d + col[c], n[c], dg[c]);
   }
 }
 
-// dgamma = the partial sums added in order: 16 columns by 16 slices of them
-// per workgroup.  parts == 0 writes zeros.
-__global__ __launch_bounds__(256) void dgamma_kernel(const float* __restrict__ partial, int parts, int d,
-                                                     float* __restrict__ dgamma) {
-  __shared__ float sum[16][17];
+// dgamma = the partial sums added in a fixed order: 16 columns by 64 slices of
+// them per workgroup, four loads in flight each.  parts == 0 writes zeros.
+__global__ __launch_bounds__(1024) void dgamma_kernel(const float* __restrict__ partial, int parts, int d,
+                                                      float* __restrict__ dgamma) {
+  __shared__ float sum[64][17];
   const int c = threadIdx.x & 15, slice = threadIdx.x >> 4;
   const int col = (int)blockIdx.x * 16 + c;
-  float s = 0.0f;
+  float s[4] = {0, 0, 0, 0};
   if (col < d)
-    for (int p = slice; p < parts; p += 16) s += partial[(int64_t)p * d + col];
-  sum[slice][c] = s;
+    for (int p = slice; p < parts; p += 256)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (p + 64 * i < parts) s[i] += partial[(int64_t)(p + 64 * i) * d + col];
+  sum[slice][c] = (s[0] + s[1]) + (s[2] + s[3]);
   __syncthreads();
   if (slice == 0 && col < d) {
     float t = 0.0f;
-    for (int i = 0; i < 16; ++i) t += sum[i][c];
+    for (int i = 0; i < 64; ++i) t += sum[i][c];
     dgamma[col] = t;
   }
 }
 
-// Threads and chunks per thread for a row of d values: the row is held by one
-// workgroup of whole waves.
-struct RowShape {
-  int threads, nch;
-};
-RowShape row_shape(int d) {
-  const int nch = d <= 2048 ? 1 : d <= 16384 ? 2 : 4;
-  const int chunks = (d + 7) / 8;
-  return {((chunks + nch - 1) / nch + 63) / 64 * 64, nch};
-}
+// Threads for a row of d values with nch chunks of 8 each: whole waves.
+int row_threads(int d, int nch) { return ((d + 7) / 8 + nch * 64 - 1) / (nch * 64) * 64; }
 
+// Chunks per thread of the norm: two from 4096 on (16384 x 5120 bf16 with a
+// checkpoint: one chunk 165 us, two 134 us; a row of 4096 is then 8 waves or
+// 4, and one row alone is faster with 8).
 template <typename T, bool E8>
 hipError_t norm_go(const NormArgs& a, hipStream_t stream) {
-  const RowShape s = row_shape(a.d);
-  const dim3 grid((unsigned)(a.rows < (1 << 20) ? a.rows : (1 << 20)));
-  if (s.nch == 1) hipLaunchKernelGGL((rmsnorm_q8_kernel<T, 1, E8>), grid, dim3(s.threads), 0, stream, a);
-  else if (s.nch == 2) hipLaunchKernelGGL((rmsnorm_q8_kernel<T, 2, E8>), grid, dim3(s.threads), 0, stream, a);
-  else hipLaunchKernelGGL((rmsnorm_q8_kernel<T, 4, E8>), grid, dim3(s.threads), 0, stream, a);
+  const int nch = a.d <= 4096 ? 1 : a.d <= 8192 ? 2 : 4, threads = row_threads(a.d, nch);
+  // about as many workgroups as fit the compute units at once
+  const int64_t fit = 256 * (int64_t)std::max(1, 1024 / threads);
+  const dim3 grid((unsigned)std::min(a.rows, fit));
+  if (nch == 1) hipLaunchKernelGGL((rmsnorm_q8_kernel<T, 1, E8>), grid, dim3(threads), 0, stream, a);
+  else if (nch == 2) hipLaunchKernelGGL((rmsnorm_q8_kernel<T, 2, E8>), grid, dim3(threads), 0, stream, a);
+  else hipLaunchKernelGGL((rmsnorm_q8_kernel<T, 4, E8>), grid, dim3(threads), 0, stream, a);
   return hipGetLastError();
 }
 
-int vjp_groups(int64_t rows) { return (int)(rows < 1024 ? rows : 1024); }
+// Workgroups of the backward pass: each writes a row of partial sums, so no
+// more than keep the compute units busy (16384 x 5120: 512 of 640 threads
+// 127 us, 1024 135 us; two chunks per thread 186 us, for want of registers).
+int vjp_threads(int64_t d) { return row_threads((int)d, d <= 8192 ? 1 : 4); }
+int vjp_groups(int64_t rows, int64_t d) {
+  return (int)std::min(rows, 256 * (int64_t)std::min(8, std::max(2, 1024 / vjp_threads(d))));
+}
 
 template <typename T, bool E8>
 hipError_t norm_vjp_go(const NormVjpArgs& a, hipStream_t stream) {
-  const RowShape s = row_shape(a.d);
-  const int groups = vjp_groups(a.rows);
+  const int groups = vjp_groups(a.rows, a.d), threads = vjp_threads(a.d);
   if (groups > 0) {
     const dim3 grid(groups);
-    if (s.nch == 1) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 1, E8>), grid, dim3(s.threads), 0, stream, a);
-    else if (s.nch == 2) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 2, E8>), grid, dim3(s.threads), 0, stream, a);
-    else hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 4, E8>), grid, dim3(s.threads), 0, stream, a);
+    if (a.d <= 8192) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 1, E8>), grid, dim3(threads), 0, stream, a);
+    else hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 4, E8>), grid, dim3(threads), 0, stream, a);
   }
   if (a.dgamma)
-    hipLaunchKernelGGL(dgamma_kernel, dim3((a.d + 15) / 16), dim3(256), 0, stream, a.partial, groups, a.d, a.dgamma);
+    hipLaunchKernelGGL(dgamma_kernel, dim3((a.d + 15) / 16), dim3(1024), 0, stream, a.partial, groups, a.d, a.dgamma);
   return hipGetLastError();
 }
 
@@ -328,7 +374,7 @@ hipError_t launch_rmsnorm_q8(const NormArgs& a, DT io, bool e8, hipStream_t stre
   return e8 ? norm_go<uint16_t, true>(a, stream) : norm_go<uint16_t, false>(a, stream);
 }
 
-int64_t rmsnorm_q8_vjp_workspace(int64_t rows, int64_t d) { return (int64_t)vjp_groups(rows) * d * 4; }
+int64_t rmsnorm_q8_vjp_workspace(int64_t rows, int64_t d) { return (int64_t)vjp_groups(rows, d) * d * 4; }
 
 hipError_t launch_rmsnorm_q8_vjp(const NormVjpArgs& a, DT io, bool e8, hipStream_t stream) {
   if (io == DT::F32) return e8 ? norm_vjp_go<float, true>(a, stream) : norm_vjp_go<float, false>(a, stream);
