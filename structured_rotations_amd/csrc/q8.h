@@ -80,6 +80,16 @@ __device__ __forceinline__ u32x4 load16_bytes(const uint8_t* p, int n) {
   return v;
 }
 
+// v's bytes from number `by` on (0..15), zeros behind them.
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int by) {
+  if (by & 8) v = u32x4{v[2], v[3], 0, 0};
+  if (by & 4) v = u32x4{v[1], v[2], v[3], 0};
+  const int b = 8 * (by & 3);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = (uint32_t)((((uint64_t)(i < 3 ? v[i + 1] : 0) << 32) | v[i]) >> b);
+  return v;
+}
+
 // Four E4M3 codes of four values (round to nearest, ties to even; the inputs
 // are within 448 up to an fp32 rounding, which rounds to 448).
 __device__ __forceinline__ uint32_t enc4(float a, float b, float c, float d) {
@@ -286,6 +296,17 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int* t
 
 // Lane offset that is beyond any tile.
 constexpr unsigned kNoLoad = 0x7fffff00u;
+
+// A scale as it is stored (E8M0: its byte), and its value.
+template <bool E8>
+__device__ __forceinline__ uint32_t scale_bits(const void* scales, int64_t i) {
+  if constexpr (E8) return static_cast<const uint8_t*>(scales)[i];
+  else return static_cast<const uint32_t*>(scales)[i];
+}
+template <bool E8>
+__device__ __forceinline__ float scale_value(uint32_t bits) {
+  return E8 ? e8m0_value(bits) : __uint_as_float(bits);
+}
 
 // Largest / sum over the 16 lanes that share a block (one DPP row), in every
 // lane of it.

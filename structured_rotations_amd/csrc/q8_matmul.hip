@@ -14,6 +14,8 @@
 // The weight is the instruction's first operand, so a lane's four results are
 // four neighbouring n of one row m: the row's scale is one value per lane and
 // the store one vector.
+#include <algorithm>
+
 #include "q8.h"
 
 namespace harp {
@@ -76,15 +78,15 @@ __device__ __forceinline__ bf16x8_t widen(const i32x8& f, int t) {
 
 constexpr int kChunk = 8;  // steps whose row scales are brought in together
 
-// One 64 MW x (64 NT NW / 4) tile of y per workgroup of MW x NW waves, each
-// with 64 rows (m) by 16 NT columns (n) of it.  LDS holds two steps of one
+// One 16 MT MW x 16 NT NW tile of y per workgroup of MW x NW waves, each with
+// 16 MT rows (m) by 16 NT columns (n) of it.  LDS holds two steps of one
 // block of 128: while a step is computed the next one is on its way, straight
 // from global memory into LDS (kDirect; rows of whole 16-byte pieces) or
 // through registers (any length and alignment).
-template <int MW, int NW, int NT, bool E8, typename TO, bool kDirect>
+template <int MT, int MW, int NW, int NT, bool E8, typename TO, bool kDirect>
 __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g, int kb_per_split, int tiles_m,
                                                                    int tiles_n) {
-  constexpr int BM = 64 * MW, BN = 16 * NT * NW, WAVES = MW * NW;
+  constexpr int BM = 16 * MT * MW, BN = 16 * NT * NW, WAVES = MW * NW;
   constexpr int PA = BM / 8 / WAVES, PW = BN / 8 / WAVES;  // 8-row pieces of each operand a wave brings in
   static_assert(PA * 8 * WAVES == BM && PW * 8 * WAVES == BN, "");
   __shared__ __align__(16) uint8_t la[2][BM * kQBlk];
@@ -94,7 +96,7 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
   int tm, tn;
   tile_of((int)blockIdx.x, tiles_m, tiles_n, &tm, &tn);
   const int m0 = tm * BM, n0 = tn * BN;
-  const int wm = (wave / NW) * 64, wn = (wave % NW) * (16 * NT);
+  const int wm = (wave / NW) * (16 * MT), wn = (wave % NW) * (16 * NT);
   const int q = lane >> 4, i16 = lane & 15;
   const int kb0 = (int)blockIdx.y * kb_per_split, kb1 = min(g.nkb, kb0 + kb_per_split);
   // bf16 results with E8M0 scales: the instruction applies the scales
@@ -151,11 +153,11 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
     }
   };
 
-  f32x4 acc[NT][4];
+  f32x4 acc[NT][MT];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
   // Scales of the rows: a load of one step's 64 would touch 64 cache lines, so
   // they come kChunk steps at a time, 8 rows by 8 steps per wave's load, and
@@ -195,11 +197,11 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   for (int kb = kb0; kb < kb1; ++kb) {
     const int step = kb - kb0, buf = step & 1, in = step % kChunk;
-    float s[4];
-    int sb[4];
+    float s[MT];
+    int sb[MT];
     const int swb = (int)sw;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < MT; ++j) {
       const uint32_t sa = ls[step / kChunk & 1][(wm + j * 16 + i16) * kChunk + in];
       sb[j] = (int)sa;
       if constexpr (!kHwScale)
@@ -210,21 +212,21 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
       load_sw(kb + 1);
       if (in == kChunk - 1) bring_scales(kb + 1, (step / kChunk & 1) ^ 1);
     }
-    i32x8 fa[4];
+    i32x8 fa[MT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) fa[j] = frag(la[buf], wm + j * 16 + i16, i16 & 7, q);
+    for (int j = 0; j < MT; ++j) fa[j] = frag(la[buf], wm + j * 16 + i16, i16 & 7, q);
     auto weight = [&](int i) {
       const int row = (i >> 2) * 64 + (i16 >> 2) * 16 + (i & 3) * 4 + (i16 & 3);
       return frag(lw[buf], wn + row, (i16 & 3) | (i16 & 4), q);
     };
     i32x8 fw = weight(0);
-    f32x4 p[2][4];
+    f32x4 p[2][MT];
 #pragma unroll
     for (int i = 0; i <= NT; ++i) {
       i32x8 next;
       if (i + 1 < NT) next = weight(i + 1);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < MT; ++j) {
         if (i < NT) {
           if constexpr (kHwScale) {
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fa[j], acc[i][j], 0, 0, 0, swb, 0, sb[j]);
@@ -251,7 +253,7 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < MT; ++j) {
     const int m = m0 + wm + j * 16 + i16;
     if (m >= g.rows) continue;
 #pragma unroll
@@ -416,6 +418,280 @@ __global__ __launch_bounds__(512) void matmul_big_kernel(MatmulArgs g, int tiles
   }
 }
 
+// Few rows (a decoding step): the weight is read once and bounds the time, so
+// it goes straight from global memory into the fragments.  A workgroup
+// computes 16 NT columns (n) of 16 MT rows; its 8 waves share the blocks of
+// the reduction out, each a contiguous run, and add their sums through LDS: one
+// launch, no workspace.  Each wave keeps kRing blocks of both operands on
+// their way.  Row scales: a lane's load of one block's would touch 16 lines, so lane
+// (q, i16) loads block q of four for row i16 and the others ask it.
+template <int MT, int NT, bool E8, typename TO>
+__global__ __launch_bounds__(512) void matmul_few_kernel(MatmulArgs g, int per) {
+  __shared__ __align__(16) f32x4 part[8][NT * MT][64];
+  constexpr bool kHwScale = E8 && sizeof(TO) == 2, kWide = sizeof(TO) == 4;
+  constexpr int kRing = MT + NT <= 3 ? 4 : 2, kGroup = 4;  // blocks on their way; blocks whose scales come together
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, i16 = lane & 15;
+  const int n0 = (int)blockIdx.x * 16 * NT, m0 = (int)blockIdx.y * 16 * MT;
+  const int kb0 = wave * per, kb1 = min(g.nkb, kb0 + per);
+  const TileSrc rw = tile_src(g.w + (int64_t)n0 * g.ldw, (min(16 * NT, g.n - n0) - 1) * (int)g.ldw + g.k);
+  const TileSrc ra = tile_src(g.a + (int64_t)m0 * g.lda, (min(16 * MT, g.rows - m0) - 1) * (int)g.lda + g.k);
+  const int end = min(g.k, kb1 * kQBlk);
+
+  i32x8 fw[kRing][NT], fa[kRing][MT];
+  auto load = [&](int slot, int kb) {
+    // pieces past the end are not loaded; one that the end cuts is loaded from
+    // 16 bytes before it and shifted when it is used
+    unsigned v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = kb * kQBlk + q * 16 + h * 64;
+      v[h] = at < end ? (unsigned)min(at, g.k - 16) : kNoLoad;
+    }
+    auto piece = [&](TileSrc src, int row, int64_t ld, i32x8& f) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x4 w = load_16(src, v[h] + (unsigned)(row * (int)ld));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[4 * h + c] = (int)w[c];
+      }
+    };
+#pragma unroll
+    for (int t = 0; t < NT; ++t) piece(rw, 16 * t + i16, g.ldw, fw[slot][t]);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) piece(ra, 16 * t + i16, g.lda, fa[slot][t]);
+  };
+  auto cut = [&](int kb, i32x8& f) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int over = kb * kQBlk + q * 16 + h * 64 + 16 - g.k;
+      if (over > 0 && over < 16) {
+        const u32x4 w = shift_down(u32x4{(uint32_t)f[4 * h], (uint32_t)f[4 * h + 1], (uint32_t)f[4 * h + 2],
+                                         (uint32_t)f[4 * h + 3]}, over);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[4 * h + c] = (int)w[c];
+      }
+    }
+  };
+
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  const int64_t sw_row = (int64_t)(n0 / kQBlk) * g.nkb;
+  int64_t sa_row[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) sa_row[j] = (int64_t)min(m0 + 16 * j + i16, g.rows - 1) * g.nkb;
+  uint32_t sa[MT], sw;
+  auto load_scales = [&](int kb) {
+    const int at = min(kb + q, g.nkb - 1);
+    sw = scale_bits<E8>(g.w_scales, sw_row + at);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) sa[j] = scale_bits<E8>(g.a_scales, sa_row[j] + at);
+  };
+
+  if (kb0 < kb1) {
+    load_scales(kb0);
+#pragma unroll
+    for (int t = 0; t < kRing; ++t) load(t, kb0 + t);
+    const bool cuts = (g.k & 15) != 0 && kb1 == g.nkb;
+    for (int kb = kb0; kb < kb1; kb += kGroup) {
+      uint32_t s4[MT];
+      const uint32_t w4 = sw;
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+        s4[j] = kHwScale ? sa[j] : __float_as_uint(scale_value<E8>(sa[j]) * scale_value<E8>(sw));
+      load_scales(kb + kGroup);
+#pragma unroll
+      for (int t = 0; t < kGroup; ++t) {
+        constexpr int kMask = kRing - 1;
+        const int c = t & kMask;
+        if (cuts && kb + t == g.nkb - 1) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) cut(kb + t, fw[c][i]);
+#pragma unroll
+          for (int j = 0; j < MT; ++j) cut(kb + t, fa[c][j]);
+        }
+        // blocks past the run: codes zero, and a scale that may be anything
+        const bool in = kb + t < kb1;
+        const int swb = __builtin_amdgcn_readlane((int)w4, 16 * t);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const uint32_t sj = (uint32_t)__shfl((int)s4[j], 16 * t + i16);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            if constexpr (kHwScale) {
+              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[c][i], fa[c][j], acc[i][j], 0, 0, 0,
+                                                                           in ? swb : 127, 0, in ? (int)sj : 127);
+            } else {
+              f32x4 p = {0, 0, 0, 0};
+              if constexpr (kWide) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(fw[c][i], u), widen(fa[c][j], u), p, 0, 0, 0);
+              } else {
+                p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[c][i], fa[c][j], p, 0, 0, 0, 0, 0, 0);
+              }
+              const float f = in ? __uint_as_float(sj) : 0.0f;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], f, acc[i][j][e]);
+            }
+          }
+        }
+        load(c, kb + t + kRing);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) part[wave][i * MT + j][lane] = acc[i][j];
+  __syncthreads();
+  for (int u = threadIdx.x; u < NT * MT * 64; u += 512) {
+    const int l = u & 63, t = u >> 6, m = m0 + 16 * (t % MT) + (l & 15), n = n0 + 16 * (t / MT) + 4 * (l >> 4);
+    f32x4 s = part[0][t][l];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += part[w][t][l][e];
+    }
+    if (m < g.rows && n < g.n) store4<TO>(static_cast<TO*>(g.y) + (int64_t)m * g.ldy + n, g.n - n, s);
+  }
+}
+
+// Tiles that wait for memory rather than multiply: a batch of rows that is
+// small for its weight, or too few tiles for 256 x 256.  LDS holds a ring of
+// kRing steps, all but one of them on their way, and nothing is ever drained.
+// One 16 MT WM x 16 NT WN tile per workgroup of WM x WN waves.  A step's
+// scales come with it: by lane for the rows, a load that touches 64 lines but
+// is one of a step's five.
+template <int MT, int NT, int WM, int WN, bool E8, typename TO>
+__global__ __launch_bounds__(64 * WM * WN) void matmul_ring_kernel(MatmulArgs g, int kb_per_split, int tiles_m,
+                                                                   int tiles_n) {
+  constexpr bool kHwScale = E8 && sizeof(TO) == 2, kWide = sizeof(TO) == 4;
+  constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN, WAVES = WM * WN;
+  static_assert(BM <= 128 && BN <= kQBlk && NT <= 2 && WAVES >= 4, "");
+  constexpr int kScales = (BM + BN) * kQBlk, kBytes = kScales + 1024;
+  constexpr int kRing = std::min(144 * 1024 / kBytes, 12);
+  constexpr int LA = (BM / 8 + WAVES - 1) / WAVES, LW = BN / 8 / WAVES, kLoads = LA + LW + 1;  // per wave and step
+  // a step: W, A, and 64 words each from four waves: the row scales (waves 0
+  // and 1), the weight's (2), words that nobody reads (the others)
+  __shared__ __align__(16) uint8_t ring[kRing][kBytes];
+  __shared__ __align__(16) uint8_t spare[1024];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, i16 = lane & 15, lrow = lane >> 3;
+  int tm, tn;
+  tile_of((int)blockIdx.x, tiles_m, tiles_n, &tm, &tn);
+  const int m0 = tm * BM, n0 = tn * BN;
+  const int wm = wave / WN * (16 * MT), wn = wave % WN * (16 * NT);
+  const int kb0 = (int)blockIdx.y * kb_per_split, kb1 = min(g.nkb, kb0 + kb_per_split);
+  const int rows_a = min(BM, g.rows - m0), rows_w = min(BN, g.n - n0);
+  const TileSrc ra = tile_src(g.a + (int64_t)m0 * g.lda, (rows_a - 1) * (int)g.lda + g.k);
+  const TileSrc rw = tile_src(g.w + (int64_t)n0 * g.ldw, (rows_w - 1) * (int)g.ldw + g.k);
+  // NT = 2: a wave reads its weight rows in the order 8 (r / 4) + 4 i + r % 4,
+  // so that a lane's results are 8 neighbouring n; the exchange of pieces
+  // goes by bits 0, 1 and 3 of the row then, by bits 0..2 otherwise
+  const int pca = ((lane & 7) ^ lrow) * 16;
+  const int pcw = NT == 2 ? ((lane & 7) ^ (lrow & 3) ^ ((wave & 1) << 2)) * 16 : pca;
+  const unsigned va = (unsigned)((wave * 8 + lrow) * (int)g.lda + pca), vw = (unsigned)((wave * 8 + lrow) * (int)g.ldw + pcw);
+  const int last = (kb1 - 1) * kQBlk;
+  constexpr int kSB = E8 ? 1 : 4;
+  const TileSrc rs =
+      wave == 2 ? tile_src(static_cast<const uint8_t*>(g.w_scales) + (int64_t)(n0 / kQBlk) * g.nkb * kSB, g.nkb * kSB)
+                : tile_src(static_cast<const uint8_t*>(g.a_scales) + (int64_t)m0 * g.nkb * kSB, rows_a * g.nkb * kSB);
+  const unsigned vs = wave < 2 ? (unsigned)((wave * 64 + lane) * g.nkb * kSB) : wave == 2 && lane == 0 ? 0u : kNoLoad;
+  // Past the last step, and rows past the tile, the loads give zeros: their
+  // number per step is constant.
+  auto fill = [&](int kb, int slot) {
+    const int kk = min(kb * kQBlk, last);
+    const bool ia = kb < kb1 && kb * kQBlk + pca < g.k, iw = kb < kb1 && kb * kQBlk + pcw < g.k;
+#pragma unroll
+    for (int i = 0; i < LW; ++i)
+      load_lds16(rw, ring[slot] + (wave + WAVES * i) * 1024, iw ? vw + 8 * WAVES * i * (unsigned)g.ldw : kNoLoad, kk);
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      // 16 rows: two waves' worth; the others' zeros go where nobody reads
+      const bool mine = BM >= 8 * WAVES || wave < BM / 8;
+      load_lds16(ra, mine ? ring[slot] + BN * kQBlk + (wave + WAVES * i) * 1024 : spare,
+                 ia && mine ? va + 8 * WAVES * i * (unsigned)g.lda : kNoLoad, kk);
+    }
+    load_lds_word<kSB>(rs, ring[slot] + kScales + min(wave, 3) * 256, vs, min(kb, kb1 - 1) * kSB);
+  };
+
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int t = 0; t < kRing - 1; ++t) fill(kb0 + t, t);
+  int slot = 0;
+  for (int kb = kb0; kb < kb1; ++kb) {
+    // newer than this step's loads: those of kRing - 2 steps.  After the
+    // barrier everyone's have landed and the last step's slot has been read.
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"(kLoads * (kRing - 2)) : "memory");
+    const uint8_t* lw = ring[slot];
+    const uint32_t* ls = reinterpret_cast<const uint32_t*>(lw + kScales);
+    i32x8 fw[NT], fa[MT];
+    uint32_t sa[MT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      fw[i] = NT == 2 ? frag(lw, wn + (i16 >> 2) * 8 + i * 4 + (i16 & 3), (i16 & 3) | (i16 & 4), q)
+                      : frag(lw, wn + i16, i16 & 7, q);
+    const uint32_t sw = ls[128];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      fa[j] = frag(lw + BN * kQBlk, wm + j * 16 + i16, i16 & 7, q);
+      sa[j] = ls[wm + j * 16 + i16];
+    }
+    fill(kb + kRing - 1, slot == 0 ? kRing - 1 : slot - 1);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      const float f = kHwScale ? 0.0f : scale_value<E8>(sa[j]) * scale_value<E8>(sw);
+      f32x4 p[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        if constexpr (kHwScale) {
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[i], fa[j], acc[i][j], 0, 0, 0, (int)sw, 0, (int)sa[j]);
+        } else {
+          p[i] = f32x4{0, 0, 0, 0};
+          if constexpr (kWide) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              p[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(fw[i], u), widen(fa[j], u), p[i], 0, 0, 0);
+          } else {
+            p[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[i], fa[j], p[i], 0, 0, 0, 0, 0, 0);
+          }
+        }
+      }
+      if constexpr (!kHwScale) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[i][e], f, acc[i][j][e]);
+      }
+    }
+    slot = slot + 1 == kRing ? 0 : slot + 1;
+    // the barrier above must find this step's reads done
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+  // no load may be in flight into LDS when the workgroup ends
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int m = m0 + wm + j * 16 + i16;
+    if (m >= g.rows) continue;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int n = n0 + wn + q * 4 * NT + i * 4;
+      if (n >= g.n) continue;
+      if (gridDim.y > 1) store4<float>(g.partial + ((int64_t)blockIdx.y * g.rows + m) * g.n + n, g.n - n, acc[i][j]);
+      else store4<TO>(static_cast<TO*>(g.y) + (int64_t)m * g.ldy + n, g.n - n, acc[i][j]);
+    }
+  }
+}
+
 // y = the splits' partial results added in order.
 template <typename TO>
 __global__ __launch_bounds__(256) void matmul_join_kernel(MatmulArgs g, int splits) {
@@ -428,13 +704,31 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(MatmulArgs g, int spli
   }
 }
 
-// The reduction is split while the tiles leave compute units idle.
-int splits_of(int64_t rows, int64_t n, int64_t k) {
-  const int64_t tiles = ((rows + 127) / 128) * ((n + 127) / 128), nkb = q_nblk(k);
-  int64_t s = 1;
-  while (tiles * s < 256 && s * 2 <= nkb && s < 16) s *= 2;
+// Which kernel, from sizes alone (the workspace depends on it).
+enum class Way { kFew, kBatch, kMid, kMany, kBig };
+Way way_of(int64_t rows, int64_t n, int64_t k, bool wide) {
+  if (rows <= 16 && k >= 16 && n * k <= (1 << 25)) return Way::kFew;
+  const int64_t big = ((rows + 255) / 256) * ((n + 255) / 256);
+  if (!wide && rows > 128 && big >= 160) return Way::kBig;
+  if (rows <= 128 || ((rows + 63) / 64) * ((n + 63) / 64) <= 256) return Way::kBatch;
+  return ((rows + 127) / 128) * ((n + 127) / 128) <= 256 ? Way::kMid : Way::kMany;
+}
+// Rows of a tile of matmul_ring_kernel in the batch way.
+int batch_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || rows > 128 ? 64 : 128; }
+
+// The reduction is split into as many parts as the compute units can take at
+// once, of 4 blocks at least: another round costs more than the idle units.
+int split(int64_t tiles, int64_t nkb) {
+  const int64_t s = std::max<int64_t>(1, std::min(std::min<int64_t>(256 / tiles, nkb / 4), (int64_t)16));
   const int64_t per = (nkb + s - 1) / s;
   return (int)((nkb + per - 1) / per);
+}
+int splits_of(int64_t rows, int64_t n, int64_t k, bool wide) {
+  switch (way_of(rows, n, k, wide)) {
+    case Way::kBatch: return split(((rows + batch_rows(rows) - 1) / batch_rows(rows)) * ((n + 63) / 64), q_nblk(k));
+    case Way::kMid: return split(((rows + 127) / 128) * ((n + 127) / 128), q_nblk(k));
+    default: return 1;
+  }
 }
 
 // Rows of whole, aligned 16-byte pieces whose tiles stay within a descriptor's
@@ -444,22 +738,56 @@ bool direct_ok(const MatmulArgs& g) {
            (uintptr_t)g.k) & 15) == 0 && g.lda <= (1 << 22) && g.ldw <= (1 << 22);
 }
 
-template <int MW, int NW, int NT, bool E8, typename TO, bool kDirect>
+template <int MT, int MW, int NW, int NT, bool E8, typename TO, bool kDirect>
 void tile_go(const MatmulArgs& g, int splits, hipStream_t stream) {
-  constexpr int BM = 64 * MW, BN = 16 * NT * NW;
+  constexpr int BM = 16 * MT * MW, BN = 16 * NT * NW;
   const int tm = (g.rows + BM - 1) / BM, tn = (g.n + BN - 1) / BN, per = (g.nkb + splits - 1) / splits;
-  hipLaunchKernelGGL((matmul_tile_kernel<MW, NW, NT, E8, TO, kDirect>), dim3(tm * tn, splits), dim3(64 * MW * NW), 0,
+  hipLaunchKernelGGL((matmul_tile_kernel<MT, MW, NW, NT, E8, TO, kDirect>), dim3(tm * tn, splits), dim3(64 * MW * NW), 0,
                      stream, g, per, tm, tn);
+}
+
+template <int MT, int NT, bool E8, typename TO>
+void few_go(const MatmulArgs& g, hipStream_t stream) {
+  hipLaunchKernelGGL((matmul_few_kernel<MT, NT, E8, TO>), dim3((g.n + 16 * NT - 1) / (16 * NT), (g.rows + 16 * MT - 1) / (16 * MT)),
+                     dim3(512), 0, stream, g, (g.nkb + 7) / 8);
+}
+
+template <int MT, int NT, int WM, int WN, bool E8, typename TO>
+void ring_go(const MatmulArgs& g, int splits, hipStream_t stream) {
+  constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN;
+  const int tm = (g.rows + BM - 1) / BM, tn = (g.n + BN - 1) / BN, per = (g.nkb + splits - 1) / splits;
+  hipLaunchKernelGGL((matmul_ring_kernel<MT, NT, WM, WN, E8, TO>), dim3(tm * tn, splits), dim3(64 * WM * WN), 0, stream,
+                     g, per, tm, tn);
 }
 
 template <bool E8, typename TO>
 hipError_t matmul_go(const MatmulArgs& g, hipStream_t stream) {
-  const int s = splits_of(g.rows, g.n, g.k);
-  const int tm = (g.rows + 255) / 256, tn = (g.n + 255) / 256;
-  if (!direct_ok(g)) tile_go<2, 2, 4, E8, TO, false>(g, s, stream);
-  else if (sizeof(TO) == 2 && (int64_t)tm * tn >= 256)
+  constexpr bool kWide = sizeof(TO) == 4;
+  const int s = splits_of(g.rows, g.n, g.k, kWide);
+  const Way way = way_of(g.rows, g.n, g.k, kWide);
+  const bool near = g.lda <= (1 << 22) && g.ldw <= (1 << 22);
+  if (way == Way::kFew && near) {
+    few_go<1, 1, E8, TO>(g, stream);
+  } else if (!direct_ok(g)) {
+    // rows that are no whole pieces: the few-rows form reads its weight faster
+    if (s == 1 && near && g.k >= 16 && g.rows <= 16) few_go<1, 2, E8, TO>(g, stream);
+    else tile_go<4, 2, 2, 4, E8, TO, false>(g, s, stream);
+  } else if (way == Way::kBig) {
+    const int tm = (g.rows + 255) / 256, tn = (g.n + 255) / 256;
     hipLaunchKernelGGL((matmul_big_kernel<E8>), dim3(tm * tn), dim3(512), 0, stream, g, tm, tn);
-  else tile_go<2, 2, 4, E8, TO, true>(g, s, stream);
+  } else if (way == Way::kMid) {
+    ring_go<4, 2, 2, 4, E8, TO>(g, s, stream);
+  } else if (way == Way::kMany) {
+    if ((int64_t)((g.rows + 127) / 128) * ((g.n + 127) / 128) < 384) tile_go<2, 2, 2, 4, E8, TO, true>(g, s, stream);
+    else tile_go<4, 2, 2, 4, E8, TO, true>(g, s, stream);
+  } else {
+    switch (batch_rows(g.rows)) {
+      case 16: ring_go<1, 1, 1, 4, E8, TO>(g, s, stream); break;
+      case 32: ring_go<2, 1, 1, 4, E8, TO>(g, s, stream); break;
+      case 64: ring_go<4, 1, 1, 4, E8, TO>(g, s, stream); break;
+      default: ring_go<8, 1, 1, 4, E8, TO>(g, s, stream);
+    }
+  }
   if (s > 1) {
     const int64_t wg = ((int64_t)g.rows * g.n + 255) / 256;
     hipLaunchKernelGGL((matmul_join_kernel<TO>), dim3((unsigned)(wg < 4096 ? wg : 4096)), dim3(256), 0, stream, g, s);
@@ -471,7 +799,7 @@ hipError_t matmul_go(const MatmulArgs& g, hipStream_t stream) {
 
 int64_t matmul_q8_workspace(int64_t rows, int64_t n, int64_t k) {
   if (rows == 0) return 0;
-  const int s = splits_of(rows, n, k);
+  const int s = std::max(splits_of(rows, n, k, false), splits_of(rows, n, k, true));
   return s > 1 ? (int64_t)s * rows * n * 4 : 0;
 }
 

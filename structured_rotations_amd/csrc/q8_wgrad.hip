@@ -70,16 +70,6 @@ __device__ __forceinline__ void store4<uint16_t>(uint16_t* p, int n, const f32x4
       if (i < n) p[i] = (uint16_t)((i < 2 ? lo : hi) >> (16 * (i & 1)));
 }
 
-// v's bytes from number `by` on (0..15), zeros behind them.
-__device__ __forceinline__ u32x4 shift_down(u32x4 v, int by) {
-  if (by & 8) v = u32x4{v[2], v[3], 0, 0};
-  if (by & 4) v = u32x4{v[1], v[2], v[3], 0};
-  const int b = 8 * (by & 3);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = (uint32_t)((((uint64_t)(i < 3 ? v[i + 1] : 0) << 32) | v[i]) >> b);
-  return v;
-}
-
 // acc += a b.  kAcc: the accumulators are named as accumulation registers (a
 // wave that has 256 of them leaves the compiler no other place, and left to
 // itself it moves them about in the loop).  Nothing reads or writes one again

@@ -9,13 +9,12 @@ check runs first, the GPU check last, then one library call.
 """
 from __future__ import annotations
 
-import ctypes
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import _lib
-from .api import _dev, _stream, _workspace_bytes
+from .api import _workspace_bytes
 from ._lib import check, lib
 
 BLOCK = 128
@@ -42,14 +41,17 @@ def _mat(t, name, dtypes, rows=None, cols=None):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
-    r, c = t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(shape)}")
+    r, c = shape
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{name} must be {'rows' if rows is None else rows} x {'columns' if cols is None else cols}, "
                          f"got {r} x {c}")
     if c < 1:
         raise ValueError(f"{name} has no columns")
+    if t.is_contiguous():
+        return c
     if c > 1 and r > 0 and t.stride(1) != 1:
         raise ValueError(f"{name} rows must be contiguous")
     if r <= 1:
@@ -65,8 +67,8 @@ def _scales(t, name, rows, cols, block_rows, dtype=None):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype not in _SCALE or (dtype is not None and t.dtype != dtype):
         raise TypeError(f"{name} must be {dtype or 'torch.float32 or torch.float8_e8m0fnu'}, got {t.dtype}")
-    want = ((rows + block_rows - 1) // block_rows, _nblk(cols))
-    if tuple(t.shape) != want:
+    want = ((rows + block_rows - 1) // block_rows, (cols + 127) // 128)
+    if t.shape != want:
         raise ValueError(f"{name} must be {want[0]} x {want[1]} (blocks of {block_rows} x {BLOCK}), "
                          f"got {tuple(t.shape)}")
     if not t.is_contiguous():
@@ -78,18 +80,36 @@ def _vec(t, name, dtype, n):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (n,) or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {n} elements, got {tuple(t.shape)}")
 
 
-def _on_gpu(*pairs):
-    first = None
-    for name, t in pairs:
-        _dev(t, name)
+def _on_gpu(*tensors):
+    """Every tensor given (None: left out) on one GPU: its index."""
+    dev = -1
+    for t in tensors:
         if t is not None:
-            if first is not None and t.device != first:
-                raise ValueError(f"{name} is on {t.device}, the first argument on {first}")
-            first = t.device
+            d = t.get_device()
+            if d < 0:
+                raise TypeError("every argument must be a GPU tensor (the library has no CPU path)")
+            if d != dev:
+                if dev >= 0:
+                    raise ValueError(f"the arguments are on different GPUs ({dev} and {d})")
+                dev = d
+    return dev
+
+
+def _stream_of(stream, dev):
+    """The given stream's handle, or that of the current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _current_stream(dev)
+
+
+# torch's own short way to the handle, where this build has it (a decoding step
+# is a few calls of 5 us each; the Stream object alone costs 1 us)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _p(t):
@@ -102,7 +122,7 @@ def _work(workspace, need, device):
         raise ValueError("sizes out of range")
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace, _workspace_bytes(workspace)
+    return workspace, 0 if workspace is None else _workspace_bytes(workspace)
 
 
 # ------------------------------------------------------------------ coding
@@ -121,9 +141,9 @@ def harp_quantize_q8(x, block_rows: int = 1, scale_dtype: str = "f32", codes=Non
         scales = torch.empty(((rows + block_rows - 1) // block_rows, _nblk(cols)), dtype=sdt, device=x.device)
     ldc = _mat(codes, "codes", (CODES,), rows, cols)
     _scales(scales, "scales", rows, cols, block_rows, sdt)
-    _on_gpu(("x", x), ("codes", codes), ("scales", scales))
+    dev = _on_gpu(x, codes, scales)
     check(lib().harp_quantize_q8(_p(x), ldx, _IO[x.dtype], rows, cols, block_rows, _p(codes), ldc, _p(scales),
-                                 _SCALE[sdt], _stream(stream)))
+                                 _SCALE[sdt], _stream_of(stream, dev)))
     return codes, scales
 
 
@@ -180,11 +200,10 @@ def harp_rmsnorm_q8(x, residual=None, gamma=None, eps: float = 1e-6, scale_dtype
         raise ValueError("rstd goes with checkpoint=True only")
     if (gamma is None or not checkpoint) and (ckpt_codes is not None or ckpt_scales is not None):
         raise ValueError("ckpt_codes and ckpt_scales go with gamma and checkpoint=True only")
-    _on_gpu(("x", x), ("residual", residual), ("gamma", gamma), ("h", h), ("codes", codes), ("scales", scales),
-            ("rstd", rstd), ("ckpt_codes", ckpt_codes), ("ckpt_scales", ckpt_scales))
+    dev = _on_gpu(x, residual, gamma, h, codes, scales, rstd, ckpt_codes, ckpt_scales)
     check(lib().harp_rmsnorm_q8(_p(x), ldx, _p(residual), ldr, _p(gamma), eps, _p(h), ldh, _p(codes), ldc, _p(scales),
                                 _p(rstd), _p(ckpt_codes), ldk, _p(ckpt_scales), _SCALE[sdt], rows, d, _IO[io],
-                                _stream(stream)))
+                                _stream_of(stream, dev)))
     if checkpoint and gamma is None:
         ckpt_codes, ckpt_scales = codes, scales
     return RmsnormQ8(codes, scales, x if h is None else h, rstd, ckpt_codes, ckpt_scales)
@@ -223,12 +242,11 @@ def harp_rmsnorm_q8_vjp(ckpt_codes, ckpt_scales, rstd, dn, gamma=None, dres=None
             dgamma = torch.empty(d, dtype=torch.float32, device=dn.device)
         _vec(dgamma, "dgamma", torch.float32, d)
         workspace, _ = _work(workspace, harp_rmsnorm_q8_vjp_workspace(rows, d), dn.device)
-    ws_bytes = _workspace_bytes(workspace)
-    _on_gpu(("dn", dn), ("ckpt_codes", ckpt_codes), ("ckpt_scales", ckpt_scales), ("rstd", rstd), ("gamma", gamma),
-            ("dres", dres), ("dh", dh), ("dgamma", dgamma), ("workspace", workspace))
+    ws_bytes = 0 if workspace is None else _workspace_bytes(workspace)
+    dev = _on_gpu(dn, ckpt_codes, ckpt_scales, rstd, gamma, dres, dh, dgamma, workspace)
     check(lib().harp_rmsnorm_q8_vjp(_p(ckpt_codes), ldc, _p(ckpt_scales), _SCALE[ckpt_scales.dtype], _p(rstd),
                                     _p(gamma), _p(dn), lddn, _p(dres), lddres, _p(dh), lddh, _p(dgamma), rows, d,
-                                    _IO[io], _p(workspace), ws_bytes, _stream(stream)))
+                                    _IO[io], _p(workspace), ws_bytes, _stream_of(stream, dev)))
     return dh, dgamma
 
 
@@ -254,11 +272,10 @@ def harp_matmul_q8(a_codes, a_scales, w_codes, w_scales, out: str = "bf16", y=No
         y = torch.empty((rows, n), dtype=odt, device=a_codes.device)
     ldy = _mat(y, "y", (odt,), rows, n)
     workspace, ws_bytes = _work(workspace, harp_matmul_q8_workspace(rows, n, k), a_codes.device)
-    _on_gpu(("a_codes", a_codes), ("a_scales", a_scales), ("w_codes", w_codes), ("w_scales", w_scales), ("y", y),
-            ("workspace", workspace))
+    dev = _on_gpu(a_codes, a_scales, w_codes, w_scales, y, workspace)
     check(lib().harp_matmul_q8(_p(a_codes), lda, _p(a_scales), _p(w_codes), ldw, _p(w_scales),
                                _SCALE[a_scales.dtype], rows, n, k, _p(y), ldy, _IO[odt], _p(workspace), ws_bytes,
-                               _stream(stream)))
+                               _stream_of(stream, dev)))
     return y
 
 
@@ -280,7 +297,7 @@ def harp_matmul_q8_wgrad(dy, x_codes, x_scales, out: str = "f32", dw=None, works
         dw = torch.empty((n, k), dtype=odt, device=dy.device)
     lddw = _mat(dw, "dw", (odt,), n, k)
     workspace, ws_bytes = _work(workspace, harp_matmul_q8_wgrad_workspace(rows, n, k), dy.device)
-    _on_gpu(("dy", dy), ("x_codes", x_codes), ("x_scales", x_scales), ("dw", dw), ("workspace", workspace))
+    dev = _on_gpu(dy, x_codes, x_scales, dw, workspace)
     check(lib().harp_matmul_q8_wgrad(_p(dy), lddy, _p(x_codes), ldx, _p(x_scales), _SCALE[x_scales.dtype], rows, n, k,
-                                     _p(dw), lddw, _IO[odt], _p(workspace), ws_bytes, _stream(stream)))
+                                     _p(dw), lddw, _IO[odt], _p(workspace), ws_bytes, _stream_of(stream, dev)))
     return dw
