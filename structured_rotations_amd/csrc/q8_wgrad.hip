@@ -38,16 +38,14 @@ template <int W>
 __device__ __forceinline__ uint32_t frag_base(int first, int lane) {
   return (uint32_t)(seg_off<W>(8 * (lane >> 4) + ((lane & 15) >> 2), first) + (lane & 3) * 8);
 }
-// The 8 values m = 32 sub + 8q .. + 7 of column i16 of segment f.
+// Half of the 8 values m = 32 sub + 8q .. + 7 of column i16 of segment f: 4h .. + 3.
 template <int W>
-__device__ __forceinline__ bf16x8_t frag_t(const uint8_t* lds, uint32_t base, int sub, int f) {
-  s16x4 v[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) s16x4*)(lds + (base ^ (uint32_t)(f << 5)) + (32 * sub + 4 * h) * W * 2));
-  const s16x8 r = __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
-  return __builtin_bit_cast(bf16x8_t, r);
+__device__ __forceinline__ s16x4 frag_half(const uint8_t* lds, uint32_t base, int sub, int f, int h) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) s16x4*)(lds + (base ^ (uint32_t)(f << 5)) + (32 * sub + 4 * h) * W * 2));
+}
+__device__ __forceinline__ bf16x8_t frag_of(const s16x4 (&v)[2]) {
+  return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 template <typename T>
@@ -150,37 +148,32 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
     const int left = rows_left(m0);
     return tile_src(g.dy + (int64_t)(left ? m0 : mlo) * g.lddy, left ? ((left - 1) * (int)g.lddy + g.n) * 2 : 0);
   };
+  auto src_x = [&](int m0) {
+    const int left = rows_left(m0);
+    return tile_src(g.x + (int64_t)(left ? m0 : mlo) * g.ldx, left ? (left - 1) * (int)g.ldx + g.k : 0);
+  };
+  auto src_s = [&](int m0) {
+    const int left = rows_left(m0);
+    return tile_src(static_cast<const uint8_t*>(g.x_scales) + (int64_t)(left ? m0 : mlo) * g.nkb * kSB, left * g.nkb * kSB);
+  };
   auto bring_dy = [&](TileSrc src, int buf, int u) {
     const unsigned v = vdd[kRowsD == 2 ? u & 1 : 0];
     const int row = row_of_load(u) + (kRowsD == 2 ? (u & 1) * 2 : 0);
     load_lds16(src, ld[buf] + (row + wave * 8) * BN * 2, v + (unsigned)(n0 * 2 + row_of_load(u) * (int)g.lddy * 2), 0);
   };
-  auto load_dy = [&](int m0) {
-    if constexpr (kRows == kCut) {
-      const TileSrc src = src_dy(m0);
-#pragma unroll
-      for (int u = 0; u < UD; ++u) rd[u] = load_16(src, vd + (unsigned)(n0 * 2 + u * (2048 / BN) * (int)g.lddy * 2));
-    } else if constexpr (kRows == kNarrow) {
-#pragma unroll
-      for (int u = 0; u < UD; ++u) {
-        const int64_t m = m0 + drow + u * (2048 / BN);
-        rd[u] = load16_bytes(reinterpret_cast<const uint8_t*>(g.dy + m * g.lddy + n0 + dcol), m < mhi ? dn * 2 : 0);
-      }
-    }
+  auto load_dy = [&](TileSrc src, int m0, int u) {
+    const int r = u * (2048 / BN);
+    if constexpr (kRows == kCut) rd[u] = load_16(src, vd + (unsigned)(n0 * 2 + r * (int)g.lddy * 2));
+    else if constexpr (kRows == kNarrow)
+      rd[u] = load16_bytes(reinterpret_cast<const uint8_t*>(g.dy + (int64_t)(m0 + drow + r) * g.lddy + n0 + dcol),
+                           m0 + drow + r < mhi ? dn * 2 : 0);
   };
-  auto load_x = [&](int m0) {
-    const int left = rows_left(m0);
-    const int64_t at = left ? m0 : mlo;
-    const TileSrc sx = tile_src(g.x + at * g.ldx, left ? (left - 1) * (int)g.ldx + g.k : 0);
-    const TileSrc ss = tile_src(static_cast<const uint8_t*>(g.x_scales) + at * g.nkb * kSB, left * g.nkb * kSB);
-#pragma unroll
-    for (int u = 0; u < UX; ++u) {
-      const int r = u * (4096 / BK);
-      if constexpr (kRows == kNarrow)
-        rx[u] = load16_bytes(g.x + (at + xrow + r) * g.ldx + k0 + xcol, xrow + r < left ? xn : 0);
-      else rx[u] = load_16(sx, vx + (unsigned)(k0 + r * (int)g.ldx));
-      rs[u] = load_word<kSB>(ss, vs + (unsigned)(r * g.nkb * kSB));
-    }
+  auto load_x = [&](TileSrc src, TileSrc scales, int m0, int u) {
+    const int r = u * (4096 / BK);
+    if constexpr (kRows == kNarrow)
+      rx[u] = load16_bytes(g.x + (int64_t)(m0 + xrow + r) * g.ldx + k0 + xcol, m0 + xrow + r < mhi ? xn : 0);
+    else rx[u] = load_16(src, vx + (unsigned)(k0 + r * (int)g.ldx));
+    rs[u] = load_word<kSB>(scales, vs + (unsigned)(r * g.nkb * kSB));
   };
   auto keep_dy = [&](int buf, int u) {
     if constexpr (kRows != kWhole) {
@@ -190,37 +183,46 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   };
   static_assert(4096 / BK >= 16 || UX == 1 || (4096 / BK) % 8 == 0, "");
   uint32_t xat = (uint32_t)seg_off<BK>(xrow, xcol >> 4);
-  auto keep_x = [&](int u) {
-    // bits 3 and 4 of the row, which u changes, exchange segments 4 and 8 apart
-    constexpr int kUp = 4096 / BK;
-    const uint32_t at = (xat ^ (uint32_t)(((u * kUp >> 1 & 12) & (BK / 16 - 1)) << 5)) + u * kUp * BK * 2;
-    if (kRows == kCut && cut_x) rx[u] = shift_down(rx[u], cut_x);
-    u32x4 w[PARTS][2];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
+  // decodes piece u in five units: 4 codes each, then the writes
+  u32x4 xw[PARTS][2];
+  auto keep_x = [&](int u, int c) {
+    if (c < 4) {
+      if (kRows == kCut && c == 0 && cut_x) rx[u] = shift_down(rx[u], cut_x);
       if constexpr (E8 && PARTS == 1) {
-        w[0][c >> 1][2 * (c & 1)] = widen2(rx[u][c], rs[u] << 23, false);
-        w[0][c >> 1][2 * (c & 1) + 1] = widen2(rx[u][c], rs[u] << 23, true);
+        xw[0][c >> 1][2 * (c & 1)] = widen2(rx[u][c], rs[u] << 23, false);
+        xw[0][c >> 1][2 * (c & 1) + 1] = widen2(rx[u][c], rs[u] << 23, true);
       } else {
-        const float s = E8 ? e8m0_value(rs[u]) : __uint_as_float(rs[u]);
+        const float s = scale_value<E8>(rs[u]);
         float v[4];
         dec4(rx[u][c], v);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float a = v[2 * e] * s, b = v[2 * e + 1] * s;
           const uint32_t hi = pack_bf16x2_hw(a, b);
-          w[0][c >> 1][2 * (c & 1) + e] = hi;
-          if constexpr (PARTS == 2) w[PARTS - 1][c >> 1][2 * (c & 1) + e] = pack_bf16x2_hw(a - bf16_lo(hi), b - bf16_hi(hi));
+          xw[0][c >> 1][2 * (c & 1) + e] = hi;
+          if constexpr (PARTS == 2)
+            xw[PARTS - 1][c >> 1][2 * (c & 1) + e] = pack_bf16x2_hw(a - bf16_lo(hi), b - bf16_hi(hi));
         }
       }
+      return;
     }
+    // bits 3 and 4 of the row, which u changes, exchange segments 4 and 8 apart
+    constexpr int kUp = 4096 / BK;
+    const uint32_t at = (xat ^ (uint32_t)(((u * kUp >> 1 & 12) & (BK / 16 - 1)) << 5)) + u * kUp * BK * 2;
     // odd pieces write their halves in the other order: eight lanes then fill
     // 128 different bytes
 #pragma unroll
     for (int t = 0; t < PARTS; ++t) {
       const bool odd = tid & 1;
-      *reinterpret_cast<u32x4*>(lx[0][t] + at + (odd ? 16 : 0)) = odd ? w[t][1] : w[t][0];
-      *reinterpret_cast<u32x4*>(lx[0][t] + at + (odd ? 0 : 16)) = odd ? w[t][0] : w[t][1];
+      const u32x4 lo = xw[t][0], hi = xw[t][1];
+      u32x4 first, second;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        first[e] = odd ? hi[e] : lo[e];
+        second[e] = odd ? lo[e] : hi[e];
+      }
+      *reinterpret_cast<u32x4*>(lx[0][t] + at + (odd ? 16 : 0)) = first;
+      *reinterpret_cast<u32x4*>(lx[0][t] + at + (odd ? 0 : 16)) = second;
     }
   };
 
@@ -231,36 +233,35 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   settle<kAcc>();
-  bf16x8_t fx[2][R], fd[2][NJ];
+  s16x4 fr[2][NJ + R][2];  // fragments of two half steps: dy's, then x's
   // offsets of the buffer that is read; the other one is at ^ kFlip
   constexpr uint32_t kFlipD = kStep * BN * 2, kFlipX = PARTS * kStep * BK * 2;
   uint32_t fbd = frag_base<BN>(wn, lane), fbx = frag_base<BK>(wk, lane);
-  auto read_frag = [&](int set, int sub, int f) {  // fragment f of a half step: dy's first
-    if (f < NJ) fd[set][f] = frag_t<BN>(ld[0], fbd, sub, f);
-    else fx[set][f - NJ] = frag_t<BK>(lx[0][(f - NJ) / NI], fbx, sub, (f - NJ) % NI);
+  auto read_half = [&](int set, int sub, int u) {  // half u & 1 of fragment u / 2
+    const int f = u >> 1, h = u & 1;
+    if (f < NJ) fr[set][f][h] = frag_half<BN>(ld[0], fbd, sub, f, h);
+    else fr[set][f][h] = frag_half<BK>(lx[0][(f - NJ) / NI], fbx, sub, (f - NJ) % NI, h);
   };
-  constexpr int H = R / 2, kReads = (R + NJ + H - 1) / H;  // rows of instructions in half of a half step
+  // A half step is S instructions; the rest of the work goes between them, in
+  // small units, since one wave per SIMD has nothing else to fill the gaps.
+  constexpr int S = R * NJ, kReads = 2 * (R + NJ), kKeeps = (kRows == kWhole ? 0 : UD) + 5 * UX;
+  constexpr int kAsks = UX + UD, kLate = S * 3 / 4;
   auto step = [&](int m0, int buf) {
     // keeps the compiler from holding every segment's address in a register
     asm volatile("" : "+v"(fbd), "+v"(fbx), "+v"(xat));
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (r < H) {
+    for (int t = 0; t < S; ++t) {
+      if (t < S / 2) {
 #pragma unroll
-        for (int f = r * kReads; f < (r + 1) * kReads; ++f)
-          if (f < R + NJ) read_frag(1, 1, f);
+        for (int u = t * kReads / (S / 2); u < (t + 1) * kReads / (S / 2); ++u) read_half(1, 1, u);
       } else {
-        constexpr int kD = (UD + H - 1) / H, kX = (UX + H - 1) / H;
 #pragma unroll
-        for (int u = (r - H) * kD; u < (r - H + 1) * kD; ++u)
-          if (u < UD) keep_dy(buf ^ 1, u);
-#pragma unroll
-        for (int u = (r - H) * kX; u < (r - H + 1) * kX; ++u)
-          if (u < UX) keep_x(u);
+        for (int u = (t - S / 2) * kKeeps / (S / 2); u < (t + 1 - S / 2) * kKeeps / (S / 2); ++u) {
+          if (u < 5 * UX) keep_x(u / 5, u % 5);
+          else keep_dy(buf ^ 1, u - 5 * UX);
+        }
       }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        mfma<kAcc>(acc[r % NI][j], fx[0][r], fd[0][j]);
+      mfma<kAcc>(acc[t / NJ % NI][t % NJ], frag_of(fr[0][NJ + t / NJ]), frag_of(fr[0][t % NJ]));
       __builtin_amdgcn_sched_barrier(0);
     }
     // this buffer has been read by every wave, the other one is complete
@@ -268,48 +269,50 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
     fbd ^= kFlipD;
     fbx ^= kFlipX;
     xat ^= kFlipX;
-    const TileSrc src = src_dy(m0 + 2 * kStep);
-    load_x(m0 + 2 * kStep);
-    load_dy(m0 + 2 * kStep);
+    const int m2 = m0 + 2 * kStep;
+    const TileSrc sd = src_dy(m2), sx = src_x(m2), ss = src_s(m2);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if constexpr (kRows == kWhole) {
-        constexpr int kL = (UD + R - 1) / R;
+    for (int t = 0; t < S; ++t) {
 #pragma unroll
-        for (int u = r * kL; u < (r + 1) * kL; ++u)
-          if (u < UD) bring_dy(src, buf, u);
+      for (int u = t * kAsks / S; u < (t + 1) * kAsks / S; ++u) {
+        if (u < UX) load_x(sx, ss, m2, u);
+        else if (kRows == kWhole) bring_dy(sd, buf, u - UX);
+        else load_dy(sd, m2, u - UX);
       }
-      if (r < H) {
+      if (t < kLate) {
 #pragma unroll
-        for (int f = r * kReads; f < (r + 1) * kReads; ++f)
-          if (f < R + NJ) read_frag(0, 0, f);
+        for (int u = t * kReads / kLate; u < (t + 1) * kReads / kLate; ++u) read_half(0, 0, u);
       }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        mfma<kAcc>(acc[r % NI][j], fx[1][r], fd[1][j]);
+      mfma<kAcc>(acc[t / NJ % NI][t % NJ], frag_of(fr[1][NJ + t / NJ]), frag_of(fr[1][t % NJ]));
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   if (mlo < mhi) {
-    if constexpr (kRows == kWhole) {
-      const TileSrc s0 = src_dy(mlo), s1 = src_dy(mlo + kStep);
+    const int m1 = mlo + kStep;
+    const TileSrc sd0 = src_dy(mlo), sd1 = src_dy(m1);
 #pragma unroll
-      for (int u = 0; u < UD; ++u) bring_dy(s0, 0, u);
-#pragma unroll
-      for (int u = 0; u < UD; ++u) bring_dy(s1, 1, u);
+    for (int u = 0; u < UD; ++u) {
+      if constexpr (kRows == kWhole) {
+        bring_dy(sd0, 0, u);
+        bring_dy(sd1, 1, u);
+      } else {
+        load_dy(sd0, mlo, u);
+      }
     }
-    load_x(mlo);
-    load_dy(mlo);
+#pragma unroll
+    for (int u = 0; u < UX; ++u) load_x(src_x(mlo), src_s(mlo), mlo, u);
 #pragma unroll
     for (int u = 0; u < UD; ++u) keep_dy(0, u);
 #pragma unroll
-    for (int u = 0; u < UX; ++u) keep_x(u);
+    for (int u = 0; u < 5 * UX; ++u) keep_x(u / 5, u % 5);
     xat ^= kFlipX;
-    load_x(mlo + kStep);
-    load_dy(mlo + kStep);
+#pragma unroll
+    for (int u = 0; u < UX; ++u) load_x(src_x(m1), src_s(m1), m1, u);
+#pragma unroll
+    for (int u = 0; u < UD; ++u) load_dy(sd1, m1, u);
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
-    for (int f = 0; f < R + NJ; ++f) read_frag(0, 0, f);
+    for (int u = 0; u < kReads; ++u) read_half(0, 0, u);
     for (int m0 = mlo, buf = 0; m0 < mhi; m0 += kStep, buf ^= 1) step(m0, buf);
     settle<kAcc>();
     // no load may be in flight into LDS when the workgroup ends
