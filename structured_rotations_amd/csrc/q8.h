@@ -249,8 +249,12 @@ __device__ __forceinline__ TileSrc tile_src(const void* base, int bytes) {
   bytes = __builtin_amdgcn_readfirstlane(bytes);
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00027000);
 }
+__device__ __forceinline__ uint32_t lds_offset(const void* lds) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
+}
 __device__ __forceinline__ void load_lds16(TileSrc src, void* lds, unsigned lane_offset, int offset) {
-  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+  const uint32_t at = lds_offset(lds);
+  offset = __builtin_amdgcn_readfirstlane(offset);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(at), "v"(lane_offset), "s"(src), "s"(offset)
@@ -259,7 +263,8 @@ __device__ __forceinline__ void load_lds16(TileSrc src, void* lds, unsigned lane
 // The same for one word per lane: 4 bytes, or one byte widened.
 template <int kBytes>
 __device__ __forceinline__ void load_lds_word(TileSrc src, void* lds, unsigned lane_offset, int offset) {
-  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+  const uint32_t at = lds_offset(lds);
+  offset = __builtin_amdgcn_readfirstlane(offset);
   if constexpr (kBytes == 4)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                  :
@@ -281,6 +286,10 @@ __device__ __forceinline__ uint32_t load_word(TileSrc src, unsigned lane_offset)
   else return __builtin_amdgcn_raw_buffer_load_b8(src, lane_offset, 0, 0);
 }
 
+__device__ __forceinline__ void store_16(TileSrc dst, unsigned lane_offset, u32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, dst, lane_offset, 0, 0);
+}
+
 // Which tile a workgroup computes: consecutive workgroups go to the 8 dies in
 // turn, so each die takes one contiguous run of the tiles, ordered in groups
 // of 8 tiles along m, and its 32 compute units share 8 + 4 panels in its L2.
@@ -290,8 +299,9 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int* t
   constexpr int kGroup = 8;
   const int per = kGroup * tiles_n, g = t / per, first = g * kGroup;
   const int gm = min(kGroup, tiles_m - first), in = t - g * per;
-  *tm = first + in % gm;
-  *tn = in / gm;
+  // (the division is done per lane; the result is the same in all of them)
+  *tn = __builtin_amdgcn_readfirstlane(in / gm);
+  *tm = __builtin_amdgcn_readfirstlane(first + in - in / gm * gm);
 }
 
 // Lane offset that is beyond any tile.

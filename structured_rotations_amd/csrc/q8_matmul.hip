@@ -267,155 +267,224 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
   }
 }
 
-// The large form, bf16 results: one 256 x 256 tile per workgroup of 8 waves,
-// each 64 rows (m) by 128 columns (n).  Nothing in the loop waits for a load
-// that was issued less than a whole step before, and the loads are never
-// drained: LDS holds two steps in three parts (A, and the two halves W0, W1
-// of each wave's weight rows), and a part is filled again for two steps on as
-// soon as every wave has read it.  Per step k, in parts of 8 result rows:
+// The large form, bf16 results: 256 x 256 tiles, 8 waves, each 64 rows (m) by
+// 128 columns (n).  Nothing in the loop waits for a load that was issued less
+// than a whole step before, and the loads are never drained: LDS holds two
+// steps in three parts (A, and the two halves W0, W1 of each wave's weight
+// rows), and a part is filled again for two steps on as soon as every wave has
+// read it.  Per step k, in parts of 8 result rows:
 //   row 0      multiply; A of step k is in registers
 //   barrier 1  W1(k) has landed
 //   rows 1..3  multiply; fill W1(k + 1), A(k + 2)
-//   barrier 2  A(k + 1), W0(k + 1) have landed
-//   rows 4..7  multiply; fill W0(k + 2); read A(k + 1) and row 0 of W0(k + 1)
+//   barrier 2  A(k + 1), W0(k + 1) and the scales of k + 1 have landed
+//   rows 4..7  multiply; fill the scales of k + 2, W0(k + 2); read A(k + 1) and
+//              row 0 of W0(k + 1)
 // The scaling of a product runs under the matrix instructions after it.
+//
+// One workgroup per compute unit walks over tiles, and the steps run on from
+// one tile into the next: its first loads are on their way during the last
+// steps, and the stores of a tile drain during the first step of the next
+// (kStores is added to what that step's waits count on).  Bound by the matrix
+// instructions: at 16384 x 13824 x 5120 they alone, on the same operands, take
+// 674 us.
 constexpr int kBigA = 4, kBigW = 4;  // loads per wave and step: A, W (half of them W0)
+constexpr int kStores = 16;          // stores per wave and tile
+
+// Waits until at most kLoads loads (kMore more operations in a tile's first
+// step) are outstanding, then for the other waves.  The choice is made inside
+// the statement: a branch that the compiler sees lets it move the scaling of
+// products past it.
+template <int kLoads, int kMore>
+__device__ __forceinline__ void wait_barrier(int step) {
+  asm volatile(
+      "s_cmp_eq_u32 %0, 0\n\t"
+      "s_cbranch_scc1 .Lfirst%=\n\t"
+      "s_waitcnt vmcnt(%1)\n"
+      ".Lfirst%=:\n\t"
+      "s_waitcnt vmcnt(%2)\n\t"
+      "s_barrier" ::"s"(step), "i"(kLoads), "i"(kLoads + kMore)
+      : "memory", "scc");
+}
 
 template <bool E8>
-__global__ __launch_bounds__(512) void matmul_big_kernel(MatmulArgs g, int tiles_m, int tiles_n) {
-  constexpr int B = 256, NT = 8;
-  __shared__ __align__(16) uint8_t la[2][B * kQBlk];
-  __shared__ __align__(16) uint8_t lw[2][B * kQBlk];
-  __shared__ uint32_t ls[2][B * kChunk];
-  __shared__ uint32_t lsw[2][9][64];
+__global__ __launch_bounds__(512) void matmul_big_kernel(MatmulArgs g, int tiles_m, int tiles_n, bool whole_y) {
+  constexpr int B = 256, NT = 8, kHalf = B * kQBlk;  // bytes of one operand of a step
+  constexpr uint32_t kW = 2 * kHalf, kS = 4 * kHalf, kSBuf = 2048;
+  __shared__ __align__(16) uint8_t smem[kS + 2 * kSBuf];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int tm, tn;
-  tile_of((int)blockIdx.x, tiles_m, tiles_n, &tm, &tn);
-  const int m0 = tm * B, n0 = tn * B;
   const int wm = (wave >> 1) * 64, wn = (wave & 1) * 128;
   const int q = lane >> 4, i16 = lane & 15, lrow = lane >> 3;
+  const int nkb = g.nkb;
+  constexpr int kSB = E8 ? 1 : 4;
 
-  // What this lane brings in, as in matmul_tile_kernel.  Rows past the
-  // matrix's end are past the descriptor's, too.
-  const int rows_a = min(B, g.rows - m0), rows_w = min(B, g.n - n0);
-  const TileSrc ra = tile_src(g.a + (int64_t)m0 * g.lda, (rows_a - 1) * (int)g.lda + g.k);
-  const TileSrc rw = tile_src(g.w + (int64_t)n0 * g.ldw, (rows_w - 1) * (int)g.ldw + g.k);
+  // What this lane brings in: pieces of rows 8 wave + lrow (+ 64 i), as in
+  // matmul_tile_kernel; scales of row 64 wave + lane (waves 0..3) or of weight
+  // block `lane` (wave 4).  Rows past the matrix's end are past the
+  // descriptor's, too; in the last block, pieces past the row's end are not
+  // loaded.
+  const int last = (nkb - 1) * kQBlk;
   const int pca = ((lane & 7) ^ lrow) * 16, pcw = ((lane & 7) ^ (lrow & 3) ^ ((wave & 2) << 1)) * 16;
   const unsigned va = (unsigned)((wave * 8 + lrow) * (int)g.lda + pca), vw = (unsigned)((wave * 8 + lrow) * (int)g.ldw + pcw);
-  const int last = (g.nkb - 1) * kQBlk;
-  // Past the last step the loads give zeros that nobody reads: their number
-  // per step stays what the waits below count on.
-  auto fill_a = [&](int kb, int i) {
-    load_lds16(ra, la[kb & 1] + (wave + 8 * i) * 1024, kb * kQBlk + pca < g.k ? va + 64 * i * (unsigned)g.lda : kNoLoad,
-               min(kb * kQBlk, last));
+  const unsigned va_last = last + pca < g.k ? va : kNoLoad, vw_last = last + pcw < g.k ? vw : kNoLoad;
+  const unsigned vs = wave < 4 ? (unsigned)((wave * 64 + lane) * nkb * kSB)
+                               : wave == 4 && lane < 2 ? (unsigned)(lane * nkb * kSB) : kNoLoad;
+  auto a_of = [&](int m0) { return tile_src(g.a + (int64_t)m0 * g.lda, (min(B, g.rows - m0) - 1) * (int)g.lda + g.k); };
+  auto w_of = [&](int n0) { return tile_src(g.w + (int64_t)n0 * g.ldw, (min(B, g.n - n0) - 1) * (int)g.ldw + g.k); };
+  auto s_of = [&](int m0, int n0) {
+    const int blocks = (g.n - 1) / kQBlk - n0 / kQBlk + 1;
+    const void* scales = wave == 4 ? g.w_scales : g.a_scales;
+    return tile_src(static_cast<const uint8_t*>(scales) + (int64_t)(wave == 4 ? n0 / kQBlk : m0) * nkb * kSB,
+                    (wave == 4 ? min(2, blocks) : min(B, g.rows - m0)) * nkb * kSB);
   };
-  auto fill_w = [&](int kb, int i) {  // i even: W0, odd: W1
-    load_lds16(rw, lw[kb & 1] + (wave + 8 * i) * 1024, kb * kQBlk + pcw < g.k ? vw + 64 * i * (unsigned)g.ldw : kNoLoad,
-               min(kb * kQBlk, last));
+  // `to`: the LDS offset of the step's buffers, 0 or kHalf
+  auto fill_a = [&](TileSrc src, int kb, uint32_t to, int i) {
+    load_lds16(src, smem + to + (wave + 8 * i) * 1024, (kb == nkb - 1 ? va_last : va) + 64 * i * (unsigned)g.lda, kb * kQBlk);
   };
-  // Scales of kChunk steps: one load per step of the chunk before, 64 rows by
-  // kChunk steps in each of the first four, the weight's in the fifth; the
-  // rest give zeros to words that nobody reads.  (Always one, with no branch:
-  // a branch lets the compiler move the scaling of products past it.)
-  constexpr int kSB = E8 ? 1 : 4;
-  const TileSrc rs = tile_src(static_cast<const uint8_t*>(g.a_scales) + (int64_t)m0 * g.nkb * kSB, rows_a * g.nkb * kSB);
-  const int sw_row = min((n0 + wn) / kQBlk, (g.n - 1) / kQBlk);
-  const TileSrc rsw = tile_src(static_cast<const uint8_t*>(g.w_scales) + (int64_t)sw_row * g.nkb * kSB, g.nkb * kSB);
-  const unsigned vs = (unsigned)(((wave * 8 + lrow) * g.nkb + (lane & (kChunk - 1))) * kSB);
-  const unsigned vsw = lane < kChunk ? (unsigned)(lane * kSB) : kNoLoad;
-  auto fill_scales = [&](int kb, int i) {  // load i of the chunk that starts with step kb
-    const int buf = kb / kChunk & 1, at = min(kb, g.nkb - 1) * kSB;
-    load_lds_word<kSB>(i == 4 ? rsw : rs, i < 4 ? ls[buf] + (wave + 8 * i) * 64 : lsw[buf][i == 4 ? wave : 8],
-                       i < 4 ? vs + (unsigned)(64 * i * g.nkb * kSB) : i == 4 ? vsw : kNoLoad, at);
+  auto fill_w = [&](TileSrc src, int kb, uint32_t to, int i) {  // i even: W0, odd: W1
+    load_lds16(src, smem + kW + to + (wave + 8 * i) * 1024, (kb == nkb - 1 ? vw_last : vw) + 64 * i * (unsigned)g.ldw,
+               kb * kQBlk);
+  };
+  auto fill_s = [&](TileSrc src, int kb, uint32_t to) {
+    load_lds_word<kSB>(src, smem + kS + to / (kHalf / kSBuf) + wave * 256, vs, kb * kSB);
   };
 
   f32x4 acc[NT][4], p[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    p[j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i][j] = f32x4{0, 0, 0, 0};
-  }
+  for (int j = 0; j < 4; ++j) p[j] = f32x4{0, 0, 0, 0};
   i32x8 fa[4], fw;
   float s[4] = {0, 0, 0, 0};
   uint32_t sa[4], sw;
-  const int arow = wm + i16, ax = i16 & 7;
-  const int wrow = wn + (i16 >> 2) * 16 + (i16 & 3), wx = (i16 & 3) | (i16 & 4);
-  auto weight = [&](int kb, int i) { return frag(lw[kb & 1], wrow + (i >> 2) * 64 + (i & 3) * 4, wx, q); };
-  auto read_scales = [&](int kb) {
-    const int buf = kb / kChunk & 1, in = kb % kChunk;
-    sw = lsw[buf][wave][in];
+  // offsets of this lane's fragments in the buffers of the step at hand; the
+  // other step's are at ^ kHalf, a fragment's second piece is at ^ 64
+  uint32_t oa = (uint32_t)((wm + i16) * kQBlk + ((q ^ (i16 & 7)) << 4)), to = 0;
+  uint32_t ow = kW + (uint32_t)((wn + (i16 >> 2) * 16 + (i16 & 3)) * kQBlk + ((q ^ (i16 & 7)) << 4));
+  auto read = [&](uint32_t at, int off) {
+    const i32x4 x = *reinterpret_cast<const i32x4*>(smem + at + off), y = *reinterpret_cast<const i32x4*>(smem + (at ^ 64) + off);
+    return i32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+  };
+  auto weight = [&](uint32_t at, int i) { return read(at, ((i >> 2) * 64 + (i & 3) * 4) * kQBlk); };
+  auto read_scales = [&](uint32_t buf) {
+    const uint32_t* ls = reinterpret_cast<const uint32_t*>(smem + kS + buf / (kHalf / kSBuf));
+    sw = ls[256 + (wave & 1)];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sa[j] = ls[buf][(arow + j * 16) * kChunk + in];
+    for (int j = 0; j < 4; ++j) sa[j] = ls[wm + j * 16 + i16];
   };
 
-  for (int i = 0; i < kBigA; ++i) fill_a(0, i);
-  for (int i = 0; i < kBigW; i += 2) fill_w(0, i);
-  for (int i = 0; i < 5; ++i) fill_scales(0, i);
-  for (int i = 1; i < kBigW; i += 2) fill_w(0, i);
-  for (int i = 0; i < kBigA; ++i) fill_a(1, i);
-  for (int i = 0; i < kBigW; i += 2) fill_w(1, i);
-  fill_scales(0, 7);
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"(kBigA + kBigW + 1) : "memory");
+  const int tiles = tiles_m * tiles_n;
+  int tm, tn;
+  tile_of((int)blockIdx.x, tiles_m, tiles_n, &tm, &tn);
+  int m0 = tm * B, n0 = tn * B;
+  TileSrc a0 = a_of(m0), w0 = w_of(n0), s0 = s_of(m0, n0);
+  for (int t = 0; t < 2; ++t) {
+    for (int i = 0; i < kBigA; ++i) fill_a(a0, t, t * kHalf, i);
+    for (int i = 0; i < kBigW; ++i)
+      if (t == 0 || (i & 1) == 0) fill_w(w0, t, t * kHalf, i);
+    fill_s(s0, t, t * kHalf);
+  }
+  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
-  for (int j = 0; j < 4; ++j) fa[j] = frag(la[0], arow + j * 16, ax, q);
-  fw = weight(0, 0);
+  for (int j = 0; j < 4; ++j) fa[j] = read(oa, j * 16 * kQBlk);
+  fw = weight(ow, 0);
   read_scales(0);
 
-  for (int kb = 0; kb < g.nkb; ++kb) {
+  for (int tile = (int)blockIdx.x; tile < tiles; tile += (int)gridDim.x) {
+    // the next tile (the last one's: itself again, and nobody reads it)
+    tile_of(tile + (int)gridDim.x < tiles ? tile + (int)gridDim.x : tile, tiles_m, tiles_n, &tm, &tn);
+    const int m1 = tm * B, n1 = tn * B;
+    const TileSrc a1 = a_of(m1), w1 = w_of(n1), s1 = s_of(m1, n1);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const i32x8 next = i + 1 < NT ? weight(kb, i + 1) : weight(kb + 1, 0);
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    s[2] = s[3] = 0.0f;  // what the last tile left in p has been added
+    auto step = [&](int kb) {
+      const int k1 = kb + 1 < nkb ? kb + 1 : 0, k2 = kb + 2 < nkb ? kb + 2 : kb + 2 - nkb;
+      const TileSrc wn1 = kb + 1 < nkb ? w0 : w1, an2 = kb + 2 < nkb ? a0 : a1, wn2 = kb + 2 < nkb ? w0 : w1,
+                    sn2 = kb + 2 < nkb ? s0 : s1;
+      const uint32_t oan = oa ^ kHalf, own = ow ^ kHalf;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const i32x8 next = i + 1 < NT ? weight(ow, i + 1) : weight(own, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (E8) {
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fa[j], acc[i][j], 0, 0, 0, (int)sw, 0, (int)sa[j]);
+          } else {
+            p[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fa[j], f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+            // the products of two instructions ago
+            const int pj = (j + 2) & 3, pi = j >= 2 ? i : i > 0 ? i - 1 : NT - 1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[pi][pj][e] = fmaf(p[pj][e], s[pj], acc[pi][pj][e]);
+            if (i == 0 && j == 1) {
+#pragma unroll
+              for (int t = 0; t < 4; ++t) s[t] = __uint_as_float(sa[t]) * __uint_as_float(sw);
+            }
+          }
+          if (i == NT - 1) fa[j] = read(oan, j * 16 * kQBlk);
+          // one load per two instructions at most: more at a time fill the
+          // memory pipe's queue, and the wave stands still until they fit
+          if (i == 1 && (j & 1) == 0) fill_w(wn1, k1, to ^ kHalf, 1 + j);
+          if ((i == 2 || i == 3) && (j & 1) == 0) fill_a(an2, k2, to, (i - 2) * 2 + j / 2);
+          if (i == 4 && j == 1) fill_s(sn2, k2, to);
+          if ((i == 5 || i == 6) && j == 1) fill_w(wn2, k2, to, (i - 5) * 2);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        fw = next;
+        // newer than W1(k): A(k + 1), the scales, W0(k + 1) (and the stores)
+        if (i == 0) wait_barrier<kBigA + kBigW / 2 + 1, kStores>(kb);
+        // newer than W0(k + 1): (the stores,) W1(k + 1), A(k + 2)
+        if (i == 3) wait_barrier<kBigA + kBigW / 2, kStores>(kb);
+      }
+      oa = oan;
+      ow = own;
+      to ^= kHalf;
+      read_scales(to);
+    };
+    for (int kb = 0; kb < nkb; ++kb) step(kb);
+    if constexpr (!E8) {
+#pragma unroll
+      for (int j = 2; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[NT - 1][j][e] = fmaf(p[j][e], s[j], acc[NT - 1][j][e]);
+    }
+    if (whole_y) {
+      // rows of whole 16-byte pieces: always the same number of stores
+      const TileSrc ry = tile_src(static_cast<const uint16_t*>(g.y) + (int64_t)m0 * g.ldy + n0,
+                                  ((min(B, g.rows - m0) - 1) * (int)g.ldy + g.n - n0) * 2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < NT; i += 2) {
+          const int col = wn + (i >> 2) * 64 + q * 16 + (i & 3) * 4;
+          u32x4 v;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            v[2 * h] = pack_bf16x2_hw(acc[i + h][j][0], acc[i + h][j][1]);
+            v[2 * h + 1] = pack_bf16x2_hw(acc[i + h][j][2], acc[i + h][j][3]);
+          }
+          store_16(ry, n0 + col < g.n ? (unsigned)((wm + j * 16 + i16) * (int)g.ldy + col) * 2u : kNoLoad, v);
+        }
+    } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if constexpr (E8) {
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fa[j], acc[i][j], 0, 0, 0, (int)sw, 0, (int)sa[j]);
-        } else {
-          p[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fa[j], f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
-          // the products of two instructions ago
-          const int pj = (j + 2) & 3, pi = j >= 2 ? i : i > 0 ? i - 1 : NT - 1;
+        const int m = m0 + wm + j * 16 + i16;
+        if (m >= g.rows) continue;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[pi][pj][e] = fmaf(p[pj][e], s[pj], acc[pi][pj][e]);
-          if (i == 0 && j == 1) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) s[t] = __uint_as_float(sa[t]) * __uint_as_float(sw);
-          }
+        for (int i = 0; i < NT; ++i) {
+          const int n = n0 + wn + (i >> 2) * 64 + q * 16 + (i & 3) * 4;
+          if (n < g.n) store4<uint16_t>(static_cast<uint16_t*>(g.y) + (int64_t)m * g.ldy + n, g.n - n, acc[i][j]);
         }
-        if (i == NT - 1) fa[j] = frag(la[(kb + 1) & 1], arow + j * 16, ax, q);
-        // one load per two instructions at most: more at a time fill the
-        // memory pipe's queue, and the wave stands still until they fit
-        if (i == 1 && (j & 1) == 0) fill_w(kb + 1, 1 + j);
-        if ((i == 2 || i == 3) && (j & 1) == 0) fill_a(kb + 2, (i - 2) * 2 + j / 2);
-        if ((i == 4 || i == 5) && j == 1) fill_w(kb + 2, (i - 4) * 2);
-        if (i == 6 && j == 1) fill_scales((kb / kChunk + 1) * kChunk, kb % kChunk);
-        __builtin_amdgcn_sched_barrier(0);
       }
-      fw = next;
-      // newer than W1(kb): A(kb + 1), W0(kb + 1), a load of scales
-      if (i == 0) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"(kBigA + kBigW / 2 + 1) : "memory");
-      // newer than W0(kb + 1): a load of scales, W1(kb + 1), A(kb + 2)
-      if (i == 3) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"(kBigA + kBigW / 2 + 1) : "memory");
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the next step counts on kStores at most
     }
-    read_scales(kb + 1);
-  }
-  if constexpr (!E8) {
-#pragma unroll
-    for (int j = 2; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[NT - 1][j][e] = fmaf(p[j][e], s[j], acc[NT - 1][j][e]);
+    m0 = m1;
+    n0 = n1;
+    a0 = a1;
+    w0 = w1;
+    s0 = s1;
   }
   // no load may be in flight into LDS when the workgroup ends
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int m = m0 + wm + j * 16 + i16;
-    if (m >= g.rows) continue;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int n = n0 + wn + (i >> 2) * 64 + q * 16 + (i & 3) * 4;
-      if (n < g.n) store4<uint16_t>(static_cast<uint16_t*>(g.y) + (int64_t)m * g.ldy + n, g.n - n, acc[i][j]);
-    }
-  }
 }
 
 // Few rows (a decoding step): the weight is read once and bounds the time, so
@@ -709,7 +778,7 @@ enum class Way { kFew, kBatch, kMid, kMany, kBig };
 Way way_of(int64_t rows, int64_t n, int64_t k, bool wide) {
   if (rows <= 16 && k >= 16 && n * k <= (1 << 25)) return Way::kFew;
   const int64_t big = ((rows + 255) / 256) * ((n + 255) / 256);
-  if (!wide && rows > 128 && big >= 160) return Way::kBig;
+  if (!wide && rows > 128 && k > kQBlk && big >= 160) return Way::kBig;
   if (rows <= 128 || ((rows + 63) / 64) * ((n + 63) / 64) <= 256) return Way::kBatch;
   return ((rows + 127) / 128) * ((n + 127) / 128) <= 256 ? Way::kMid : Way::kMany;
 }
@@ -774,7 +843,9 @@ hipError_t matmul_go(const MatmulArgs& g, hipStream_t stream) {
     else tile_go<4, 2, 2, 4, E8, TO, false>(g, s, stream);
   } else if (way == Way::kBig) {
     const int tm = (g.rows + 255) / 256, tn = (g.n + 255) / 256;
-    hipLaunchKernelGGL((matmul_big_kernel<E8>), dim3(tm * tn), dim3(512), 0, stream, g, tm, tn);
+    const bool whole_y = ((reinterpret_cast<uintptr_t>(g.y) | (uintptr_t)(g.ldy * 2) | (uintptr_t)(g.n * 2)) & 15) == 0 &&
+                         g.ldy <= (1 << 22);
+    hipLaunchKernelGGL((matmul_big_kernel<E8>), dim3(std::min(tm * tn, 256)), dim3(512), 0, stream, g, tm, tn, whole_y);
   } else if (way == Way::kMid) {
     ring_go<4, 2, 2, 4, E8, TO>(g, s, stream);
   } else if (way == Way::kMany) {
