@@ -249,31 +249,29 @@ __device__ __forceinline__ TileSrc tile_src(const void* base, int bytes) {
   bytes = __builtin_amdgcn_readfirstlane(bytes);
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00027000);
 }
-__device__ __forceinline__ uint32_t lds_offset(const void* lds) {
-  return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
+__device__ __forceinline__ uint32_t lds_address(const void* lds) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds;
 }
-__device__ __forceinline__ void load_lds16(TileSrc src, void* lds, unsigned lane_offset, int offset) {
-  const uint32_t at = lds_offset(lds);
-  offset = __builtin_amdgcn_readfirstlane(offset);
+__device__ __forceinline__ void load_lds16(TileSrc src, uint32_t lds, unsigned lane_offset, int offset) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
-               : "s"(at), "v"(lane_offset), "s"(src), "s"(offset)
+               : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(lane_offset), "s"(src),
+                 "s"(__builtin_amdgcn_readfirstlane(offset))
                : "memory");
 }
 // The same for one word per lane: 4 bytes, or one byte widened.
 template <int kBytes>
-__device__ __forceinline__ void load_lds_word(TileSrc src, void* lds, unsigned lane_offset, int offset) {
-  const uint32_t at = lds_offset(lds);
-  offset = __builtin_amdgcn_readfirstlane(offset);
+__device__ __forceinline__ void load_lds_word(TileSrc src, uint32_t lds, unsigned lane_offset, int offset) {
+  const int at = __builtin_amdgcn_readfirstlane((int)lds), from = __builtin_amdgcn_readfirstlane(offset);
   if constexpr (kBytes == 4)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                  :
-                 : "s"(at), "v"(lane_offset), "s"(src), "s"(offset)
+                 : "s"(at), "v"(lane_offset), "s"(src), "s"(from)
                  : "memory");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
                  :
-                 : "s"(at), "v"(lane_offset), "s"(src), "s"(offset)
+                 : "s"(at), "v"(lane_offset), "s"(src), "s"(from)
                  : "memory");
 }
 // Loads of such a tile into registers.

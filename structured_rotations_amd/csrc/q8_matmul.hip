@@ -92,6 +92,7 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
   __shared__ __align__(16) uint8_t la[2][BM * kQBlk];
   __shared__ __align__(16) uint8_t lw[2][BN * kQBlk];
   __shared__ uint32_t ls[2][BM * kChunk];
+  const uint32_t lds_a = lds_address(la), lds_w = lds_address(lw), lds_s = lds_address(ls);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int tm, tn;
   tile_of((int)blockIdx.x, tiles_m, tiles_n, &tm, &tn);
@@ -134,9 +135,9 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
     if constexpr (kDirect) {
       const bool ta = kk + pca < g.k, tw = kk + pcw < g.k;
 #pragma unroll
-      for (int i = 0; i < PA; ++i) load_lds16(ra, la[buf] + (wave + WAVES * i) * 1024, ta ? va[i] : kNoLoad, kk);
+      for (int i = 0; i < PA; ++i) load_lds16(ra, lds_a + (uint32_t)(buf * BM * kQBlk + (wave + WAVES * i) * 1024), ta ? va[i] : kNoLoad, kk);
 #pragma unroll
-      for (int i = 0; i < PW; ++i) load_lds16(rw, lw[buf] + (wave + WAVES * i) * 1024, tw ? vw[i] : kNoLoad, kk);
+      for (int i = 0; i < PW; ++i) load_lds16(rw, lds_w + (uint32_t)(buf * BN * kQBlk + (wave + WAVES * i) * 1024), tw ? vw[i] : kNoLoad, kk);
     } else {
 #pragma unroll
       for (int i = 0; i < PA; ++i) {
@@ -173,7 +174,7 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
       const int r = (wave + WAVES * i) * 8 + lrow;
       const bool in = r < rows_a && kb + k1 < kb1;
       if constexpr (kDirect) {
-        load_lds_word<kSB>(rs, ls[buf] + (wave + WAVES * i) * 64, in ? (unsigned)((r * g.nkb + k1) * kSB) : kNoLoad,
+        load_lds_word<kSB>(rs, lds_s + (uint32_t)((buf * BM * kChunk + (wave + WAVES * i) * 64) * 4), in ? (unsigned)((r * g.nkb + k1) * kSB) : kNoLoad,
                            kb * kSB);
       } else {
         const int64_t at = (int64_t)r * g.nkb + kb + k1;
@@ -311,6 +312,7 @@ __global__ __launch_bounds__(512) void matmul_big_kernel(MatmulArgs g, int tiles
   constexpr int B = 256, NT = 8, kHalf = B * kQBlk;  // bytes of one operand of a step
   constexpr uint32_t kW = 2 * kHalf, kS = 4 * kHalf, kSBuf = 2048;
   __shared__ __align__(16) uint8_t smem[kS + 2 * kSBuf];
+  const uint32_t lds = lds_address(smem);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = (wave >> 1) * 64, wn = (wave & 1) * 128;
   const int q = lane >> 4, i16 = lane & 15, lrow = lane >> 3;
@@ -338,14 +340,14 @@ __global__ __launch_bounds__(512) void matmul_big_kernel(MatmulArgs g, int tiles
   };
   // `to`: the LDS offset of the step's buffers, 0 or kHalf
   auto fill_a = [&](TileSrc src, int kb, uint32_t to, int i) {
-    load_lds16(src, smem + to + (wave + 8 * i) * 1024, (kb == nkb - 1 ? va_last : va) + 64 * i * (unsigned)g.lda, kb * kQBlk);
+    load_lds16(src, lds + to + (uint32_t)(wave + 8 * i) * 1024, (kb == nkb - 1 ? va_last : va) + 64 * i * (unsigned)g.lda, kb * kQBlk);
   };
   auto fill_w = [&](TileSrc src, int kb, uint32_t to, int i) {  // i even: W0, odd: W1
-    load_lds16(src, smem + kW + to + (wave + 8 * i) * 1024, (kb == nkb - 1 ? vw_last : vw) + 64 * i * (unsigned)g.ldw,
+    load_lds16(src, lds + kW + to + (uint32_t)(wave + 8 * i) * 1024, (kb == nkb - 1 ? vw_last : vw) + 64 * i * (unsigned)g.ldw,
                kb * kQBlk);
   };
   auto fill_s = [&](TileSrc src, int kb, uint32_t to) {
-    load_lds_word<kSB>(src, smem + kS + to / (kHalf / kSBuf) + wave * 256, vs, kb * kSB);
+    load_lds_word<kSB>(src, lds + kS + to / (kHalf / kSBuf) + (uint32_t)wave * 256, vs, kb * kSB);
   };
 
   f32x4 acc[NT][4], p[4];
@@ -648,6 +650,7 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_ring_kernel(MatmulArgs g,
   // and 1), the weight's (2), words that nobody reads (the others)
   __shared__ __align__(16) uint8_t ring[kRing][kBytes];
   __shared__ __align__(16) uint8_t spare[1024];
+  const uint32_t lds_ring = lds_address(ring), lds_spare = lds_address(spare);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, i16 = lane & 15, lrow = lane >> 3;
   int tm, tn;
@@ -674,18 +677,19 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_ring_kernel(MatmulArgs g,
   // number per step is constant.
   auto fill = [&](int kb, int slot) {
     const int kk = min(kb * kQBlk, last);
+    const uint32_t at = lds_ring + (uint32_t)(slot * kBytes);
     const bool ia = kb < kb1 && kb * kQBlk + pca < g.k, iw = kb < kb1 && kb * kQBlk + pcw < g.k;
 #pragma unroll
     for (int i = 0; i < LW; ++i)
-      load_lds16(rw, ring[slot] + (wave + WAVES * i) * 1024, iw ? vw + 8 * WAVES * i * (unsigned)g.ldw : kNoLoad, kk);
+      load_lds16(rw, at + (uint32_t)(wave + WAVES * i) * 1024, iw ? vw + 8 * WAVES * i * (unsigned)g.ldw : kNoLoad, kk);
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
       // 16 rows: two waves' worth; the others' zeros go where nobody reads
       const bool mine = BM >= 8 * WAVES || wave < BM / 8;
-      load_lds16(ra, mine ? ring[slot] + BN * kQBlk + (wave + WAVES * i) * 1024 : spare,
+      load_lds16(ra, mine ? at + (uint32_t)(BN * kQBlk + (wave + WAVES * i) * 1024) : lds_spare,
                  ia && mine ? va + 8 * WAVES * i * (unsigned)g.lda : kNoLoad, kk);
     }
-    load_lds_word<kSB>(rs, ring[slot] + kScales + min(wave, 3) * 256, vs, min(kb, kb1 - 1) * kSB);
+    load_lds_word<kSB>(rs, at + (uint32_t)(kScales + min(wave, 3) * 256), vs, min(kb, kb1 - 1) * kSB);
   };
 
   f32x4 acc[NT][MT];

@@ -103,6 +103,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   constexpr int BK = 32 * NI, BN = 32 * NJ, R = NI * PARTS;
   constexpr int UD = kStep * BN / 8 / 256, UX = kStep * BK / 16 / 256;  // pieces per thread: 8 of dy, 16 of x
   __shared__ __align__(16) uint8_t ld[2][kStep * BN * 2];
+  const uint32_t lds_d = lds_address(ld);
   __shared__ __align__(16) uint8_t lx[2][PARTS][kStep * BK * 2];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int tn, tk;
@@ -159,7 +160,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   auto bring_dy = [&](TileSrc src, int buf, int u) {
     const unsigned v = vdd[kRowsD == 2 ? u & 1 : 0];
     const int row = row_of_load(u) + (kRowsD == 2 ? (u & 1) * 2 : 0);
-    load_lds16(src, ld[buf] + (row + wave * 8) * BN * 2, v + (unsigned)(n0 * 2 + row_of_load(u) * (int)g.lddy * 2), 0);
+    load_lds16(src, lds_d + (uint32_t)((buf * kStep + row + wave * 8) * BN * 2), v + (unsigned)(n0 * 2 + row_of_load(u) * (int)g.lddy * 2), 0);
   };
   auto load_dy = [&](TileSrc src, int m0, int u) {
     const int r = u * (2048 / BN);
