@@ -13,6 +13,8 @@
 // Both operands are stored along the other axis than the one summed over:
 // they stay that way in LDS ([m][n], [m][k]) and the transposing LDS read
 // (ds_read_b64_tr_b16) gives a lane its neighbouring m.
+#include <type_traits>
+
 #include "q8.h"
 
 namespace harp {
@@ -140,8 +142,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   constexpr int kSB = E8 ? 1 : 4;
   const unsigned vs = xn > 0 ? (unsigned)(xrow * g.nkb + (k0 + xcol) / kQBlk) * kSB : kNoLoad;
 
-  u32x4 rd[UD], rx[UX];  // the next step's rows, as they come
-  uint32_t rs[UX];
+  // rows of the next steps, as they come: of one step for the large tile, whose
+  // steps are long, of two for the small one
+  constexpr int kSets = kRows == kCut && NI * NJ * 4 <= 64 ? 2 : 1;
+  u32x4 rd[kSets][UD], rx[kSets][UX];
+  uint32_t rs[kSets][UX];
   // descriptors of a step's rows; they begin with the row, not the tile, so
   // that a shifted piece of the first columns is inside
   auto rows_left = [&](int m0) { return max(0, min(mhi - m0, kStep)); };
@@ -162,40 +167,40 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
     const int row = row_of_load(u) + (kRowsD == 2 ? (u & 1) * 2 : 0);
     load_lds16(src, lds_d + (uint32_t)((buf * kStep + row + wave * 8) * BN * 2), v + (unsigned)(n0 * 2 + row_of_load(u) * (int)g.lddy * 2), 0);
   };
-  auto load_dy = [&](TileSrc src, int m0, int u) {
+  auto load_dy = [&](int set, TileSrc src, int m0, int u) {
     const int r = u * (2048 / BN);
-    if constexpr (kRows == kCut) rd[u] = load_16(src, vd + (unsigned)(n0 * 2 + r * (int)g.lddy * 2));
+    if constexpr (kRows == kCut) rd[set][u] = load_16(src, vd + (unsigned)(n0 * 2 + r * (int)g.lddy * 2));
     else if constexpr (kRows == kNarrow)
-      rd[u] = load16_bytes(reinterpret_cast<const uint8_t*>(g.dy + (int64_t)(m0 + drow + r) * g.lddy + n0 + dcol),
+      rd[set][u] = load16_bytes(reinterpret_cast<const uint8_t*>(g.dy + (int64_t)(m0 + drow + r) * g.lddy + n0 + dcol),
                            m0 + drow + r < mhi ? dn * 2 : 0);
   };
-  auto load_x = [&](TileSrc src, TileSrc scales, int m0, int u) {
+  auto load_x = [&](int set, TileSrc src, TileSrc scales, int m0, int u) {
     const int r = u * (4096 / BK);
     if constexpr (kRows == kNarrow)
-      rx[u] = load16_bytes(g.x + (int64_t)(m0 + xrow + r) * g.ldx + k0 + xcol, m0 + xrow + r < mhi ? xn : 0);
-    else rx[u] = load_16(src, vx + (unsigned)(k0 + r * (int)g.ldx));
-    rs[u] = load_word<kSB>(scales, vs + (unsigned)(r * g.nkb * kSB));
+      rx[set][u] = load16_bytes(g.x + (int64_t)(m0 + xrow + r) * g.ldx + k0 + xcol, m0 + xrow + r < mhi ? xn : 0);
+    else rx[set][u] = load_16(src, vx + (unsigned)(k0 + r * (int)g.ldx));
+    rs[set][u] = load_word<kSB>(scales, vs + (unsigned)(r * g.nkb * kSB));
   };
-  auto keep_dy = [&](int buf, int u) {
+  auto keep_dy = [&](int set, int buf, int u) {
     if constexpr (kRows != kWhole) {
-      if (cut_d) rd[u] = shift_down(rd[u], cut_d);
-      *reinterpret_cast<u32x4*>(ld[buf] + seg_off<BN>(drow + u * (2048 / BN), dcol >> 4) + (dcol & 8) * 2) = rd[u];
+      if (cut_d) rd[set][u] = shift_down(rd[set][u], cut_d);
+      *reinterpret_cast<u32x4*>(ld[buf] + seg_off<BN>(drow + u * (2048 / BN), dcol >> 4) + (dcol & 8) * 2) = rd[set][u];
     }
   };
   static_assert(4096 / BK >= 16 || UX == 1 || (4096 / BK) % 8 == 0, "");
   uint32_t xat = (uint32_t)seg_off<BK>(xrow, xcol >> 4);
   // decodes piece u in five units: 4 codes each, then the writes
   u32x4 xw[PARTS][2];
-  auto keep_x = [&](int u, int c) {
+  auto keep_x = [&](int set, int u, int c) {
     if (c < 4) {
-      if (kRows == kCut && c == 0 && cut_x) rx[u] = shift_down(rx[u], cut_x);
+      if (kRows == kCut && c == 0 && cut_x) rx[set][u] = shift_down(rx[set][u], cut_x);
       if constexpr (E8 && PARTS == 1) {
-        xw[0][c >> 1][2 * (c & 1)] = widen2(rx[u][c], rs[u] << 23, false);
-        xw[0][c >> 1][2 * (c & 1) + 1] = widen2(rx[u][c], rs[u] << 23, true);
+        xw[0][c >> 1][2 * (c & 1)] = widen2(rx[set][u][c], rs[set][u] << 23, false);
+        xw[0][c >> 1][2 * (c & 1) + 1] = widen2(rx[set][u][c], rs[set][u] << 23, true);
       } else {
-        const float s = scale_value<E8>(rs[u]);
+        const float s = scale_value<E8>(rs[set][u]);
         float v[4];
-        dec4(rx[u][c], v);
+        dec4(rx[set][u][c], v);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float a = v[2 * e] * s, b = v[2 * e + 1] * s;
@@ -247,7 +252,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   // small units, since one wave per SIMD has nothing else to fill the gaps.
   constexpr int S = R * NJ, kReads = 2 * (R + NJ), kKeeps = (kRows == kWhole ? 0 : UD) + 5 * UX;
   constexpr int kAsks = UX + UD, kLate = S * 3 / 4;
-  auto step = [&](int m0, int buf) {
+  // the rows of step k are in set k % kSets until they are decoded
+  auto step = [&](auto parity, int m0, int buf) {
+    constexpr int set = kSets == 2 ? 1 - decltype(parity)::value : 0;
     // keeps the compiler from holding every segment's address in a register
     asm volatile("" : "+v"(fbd), "+v"(fbx), "+v"(xat));
 #pragma unroll
@@ -258,27 +265,28 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
       } else {
 #pragma unroll
         for (int u = (t - S / 2) * kKeeps / (S / 2); u < (t + 1 - S / 2) * kKeeps / (S / 2); ++u) {
-          if (u < 5 * UX) keep_x(u / 5, u % 5);
-          else keep_dy(buf ^ 1, u - 5 * UX);
+          if (u < 5 * UX) keep_x(set, u / 5, u % 5);
+          else keep_dy(set, buf ^ 1, u - 5 * UX);
         }
       }
       mfma<kAcc>(acc[t / NJ % NI][t % NJ], frag_of(fr[0][NJ + t / NJ]), frag_of(fr[0][t % NJ]));
       __builtin_amdgcn_sched_barrier(0);
     }
     // this buffer has been read by every wave, the other one is complete
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if constexpr (kRows == kWhole) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     fbd ^= kFlipD;
     fbx ^= kFlipX;
     xat ^= kFlipX;
-    const int m2 = m0 + 2 * kStep;
+    const int m2 = m0 + (kSets + 1) * kStep;
     const TileSrc sd = src_dy(m2), sx = src_x(m2), ss = src_s(m2);
 #pragma unroll
     for (int t = 0; t < S; ++t) {
 #pragma unroll
       for (int u = t * kAsks / S; u < (t + 1) * kAsks / S; ++u) {
-        if (u < UX) load_x(sx, ss, m2, u);
+        if (u < UX) load_x(set, sx, ss, m2, u);
         else if (kRows == kWhole) bring_dy(sd, buf, u - UX);
-        else load_dy(sd, m2, u - UX);
+        else load_dy(set, sd, m2, u - UX);
       }
       if (t < kLate) {
 #pragma unroll
@@ -290,31 +298,44 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   };
   if (mlo < mhi) {
     const int m1 = mlo + kStep;
-    const TileSrc sd0 = src_dy(mlo), sd1 = src_dy(m1);
+    [[maybe_unused]] const TileSrc sd0 = src_dy(mlo), sd1 = src_dy(m1);
 #pragma unroll
     for (int u = 0; u < UD; ++u) {
       if constexpr (kRows == kWhole) {
         bring_dy(sd0, 0, u);
         bring_dy(sd1, 1, u);
       } else {
-        load_dy(sd0, mlo, u);
+        load_dy(0, sd0, mlo, u);
       }
     }
 #pragma unroll
-    for (int u = 0; u < UX; ++u) load_x(src_x(mlo), src_s(mlo), mlo, u);
+    for (int u = 0; u < UX; ++u) load_x(0, src_x(mlo), src_s(mlo), mlo, u);
 #pragma unroll
-    for (int u = 0; u < UD; ++u) keep_dy(0, u);
+    for (int u = 0; u < UD; ++u) keep_dy(0, 0, u);
 #pragma unroll
-    for (int u = 0; u < 5 * UX; ++u) keep_x(u / 5, u % 5);
+    for (int u = 0; u < 5 * UX; ++u) keep_x(0, u / 5, u % 5);
     xat ^= kFlipX;
 #pragma unroll
-    for (int u = 0; u < UX; ++u) load_x(src_x(m1), src_s(m1), m1, u);
+    for (int k = 1; k <= kSets; ++k) {
+      const int mk = mlo + k * kStep;
 #pragma unroll
-    for (int u = 0; u < UD; ++u) load_dy(sd1, m1, u);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      for (int u = 0; u < UX; ++u) load_x(k % kSets, src_x(mk), src_s(mk), mk, u);
+#pragma unroll
+      for (int u = 0; u < UD; ++u) load_dy(k % kSets, src_dy(mk), mk, u);
+    }
+    if constexpr (kRows == kWhole) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
     for (int u = 0; u < kReads; ++u) read_half(0, 0, u);
-    for (int m0 = mlo, buf = 0; m0 < mhi; m0 += kStep, buf ^= 1) step(m0, buf);
+    int buf = 0;
+    for (int m0 = mlo; m0 < mhi; m0 += kSets * kStep) {
+      step(std::integral_constant<int, 0>{}, m0, buf);
+      buf ^= 1;
+      if constexpr (kSets == 2) {  // past the last row: a step of zeros
+        step(std::integral_constant<int, 1>{}, m0 + kStep, buf);
+        buf ^= 1;
+      }
+    }
     settle<kAcc>();
     // no load may be in flight into LDS when the workgroup ends
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -384,7 +405,6 @@ hipError_t wgrad_go(const WgradArgs& g, hipStream_t stream) {
   if (narrow) wgrad_tile_go<4 / PARTS, 4, E8, PARTS, TO, kNarrow>(g, s, stream);
   else if (s.big && whole) wgrad_tile_go<8 / PARTS, 8, E8, PARTS, TO, kWhole>(g, s, stream);
   else if (s.big) wgrad_tile_go<8 / PARTS, 8, E8, PARTS, TO, kCut>(g, s, stream);
-  else if (whole) wgrad_tile_go<4 / PARTS, 4, E8, PARTS, TO, kWhole>(g, s, stream);
   else wgrad_tile_go<4 / PARTS, 4, E8, PARTS, TO, kCut>(g, s, stream);
   if (s.splits > 1) {
     const int64_t wg = ((int64_t)g.n * g.k + 255) / 256;
