@@ -288,6 +288,13 @@ __device__ __forceinline__ void store_16(TileSrc dst, unsigned lane_offset, u32x
   __builtin_amdgcn_raw_buffer_store_b128(v, dst, lane_offset, 0, 0);
 }
 
+// How a product's rows are brought in.  kWhole: 16-byte aligned rows of whole
+// 16-byte pieces, straight into LDS.  kCut: any alignment and length of 16
+// bytes or more, through registers; the piece that a row's end cuts is loaded
+// from 16 bytes before the end and shifted.  kNarrow: shorter rows, or strides
+// beyond a descriptor, by elements.
+enum Rows { kWhole, kCut, kNarrow };
+
 // Which tile a workgroup computes: consecutive workgroups go to the 8 dies in
 // turn, so each die takes one contiguous run of the tiles, ordered in groups
 // of 8 tiles along m, and its 32 compute units share 8 + 4 panels in its L2.

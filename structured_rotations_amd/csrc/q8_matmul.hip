@@ -80,10 +80,8 @@ constexpr int kChunk = 8;  // steps whose row scales are brought in together
 
 // One 16 MT MW x 16 NT NW tile of y per workgroup of MW x NW waves, each with
 // 16 MT rows (m) by 16 NT columns (n) of it.  LDS holds two steps of one
-// block of 128: while a step is computed the next one is on its way, straight
-// from global memory into LDS (kDirect; rows of whole 16-byte pieces) or
-// through registers (any length and alignment).
-template <int MT, int MW, int NW, int NT, bool E8, typename TO, bool kDirect>
+// block of 128: while a step is computed the next one is on its way.
+template <int MT, int MW, int NW, int NT, bool E8, typename TO, Rows kRows>
 __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g, int kb_per_split, int tiles_m,
                                                                    int tiles_n) {
   constexpr int BM = 16 * MT * MW, BN = 16 * NT * NW, WAVES = MW * NW;
@@ -116,7 +114,7 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
   const int pcw = ((lane & 7) ^ (lrow & 3) ^ ((wave & 2) << 1)) * 16;
   TileSrc ra, rw;
   unsigned va[PA], vw[PW];
-  if constexpr (kDirect) {
+  if constexpr (kRows != kNarrow) {
     ra = tile_src(abase, (rows_a - 1) * (int)g.lda + g.k);
     rw = tile_src(wbase, (rows_w - 1) * (int)g.ldw + g.k);
 #pragma unroll
@@ -130,27 +128,41 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
       vw[i] = r < rows_w ? (unsigned)(r * (int)g.ldw + pcw) : kNoLoad;
     }
   }
+  // asks for a step; what comes through registers is kept after the products
+  u32x4 xa[PA], xw[PW];
   auto bring = [&](int kb, int buf) {
-    const int kk = kb * kQBlk;
-    if constexpr (kDirect) {
-      const bool ta = kk + pca < g.k, tw = kk + pcw < g.k;
+    const int kk = kb * kQBlk, na = g.k - kk - pca, nw = g.k - kk - pcw;
+    // kCut: a piece with n bytes left is loaded from 16 - n bytes before
+    const unsigned ca = kRows == kCut && na > 0 && na < 16 ? 16 - na : 0, cw = kRows == kCut && nw > 0 && nw < 16 ? 16 - nw : 0;
 #pragma unroll
-      for (int i = 0; i < PA; ++i) load_lds16(ra, lds_a + (uint32_t)(buf * BM * kQBlk + (wave + WAVES * i) * 1024), ta ? va[i] : kNoLoad, kk);
+    for (int i = 0; i < PA; ++i) {
+      const int r = (wave + WAVES * i) * 8 + lrow;
+      if constexpr (kRows == kWhole)
+        load_lds16(ra, lds_a + (uint32_t)(buf * BM * kQBlk + (wave + WAVES * i) * 1024), na > 0 ? va[i] : kNoLoad, kk);
+      else if constexpr (kRows == kCut) xa[i] = load_16(ra, na > 0 ? va[i] + kk - ca : kNoLoad);
+      else xa[i] = load16_bytes(abase + (int64_t)r * g.lda + kk + pca, r < rows_a ? na : 0);
+    }
 #pragma unroll
-      for (int i = 0; i < PW; ++i) load_lds16(rw, lds_w + (uint32_t)(buf * BN * kQBlk + (wave + WAVES * i) * 1024), tw ? vw[i] : kNoLoad, kk);
-    } else {
+    for (int i = 0; i < PW; ++i) {
+      const int r = (wave + WAVES * i) * 8 + lrow;
+      if constexpr (kRows == kWhole)
+        load_lds16(rw, lds_w + (uint32_t)(buf * BN * kQBlk + (wave + WAVES * i) * 1024), nw > 0 ? vw[i] : kNoLoad, kk);
+      else if constexpr (kRows == kCut) xw[i] = load_16(rw, nw > 0 ? vw[i] + kk - cw : kNoLoad);
+      else xw[i] = load16_bytes(wbase + (int64_t)r * g.ldw + kk + pcw, r < rows_w ? nw : 0);
+    }
+  };
+  auto keep = [&](int kb, int buf) {
+    if constexpr (kRows == kWhole) return;
+    const int na = g.k - kb * kQBlk - pca, nw = g.k - kb * kQBlk - pcw;
 #pragma unroll
-      for (int i = 0; i < PA; ++i) {
-        const int r = (wave + WAVES * i) * 8 + lrow;
-        *reinterpret_cast<u32x4*>(la[buf] + (wave + WAVES * i) * 1024 + lane * 16) =
-            load16_bytes(abase + (int64_t)r * g.lda + kk + pca, r < rows_a ? g.k - kk - pca : 0);
-      }
+    for (int i = 0; i < PA; ++i) {
+      if (kRows == kCut && na > 0 && na < 16) xa[i] = shift_down(xa[i], 16 - na);
+      *reinterpret_cast<u32x4*>(la[buf] + (wave + WAVES * i) * 1024 + lane * 16) = xa[i];
+    }
 #pragma unroll
-      for (int i = 0; i < PW; ++i) {
-        const int r = (wave + WAVES * i) * 8 + lrow;
-        *reinterpret_cast<u32x4*>(lw[buf] + (wave + WAVES * i) * 1024 + lane * 16) =
-            load16_bytes(wbase + (int64_t)r * g.ldw + kk + pcw, r < rows_w ? g.k - kk - pcw : 0);
-      }
+    for (int i = 0; i < PW; ++i) {
+      if (kRows == kCut && nw > 0 && nw < 16) xw[i] = shift_down(xw[i], 16 - nw);
+      *reinterpret_cast<u32x4*>(lw[buf] + (wave + WAVES * i) * 1024 + lane * 16) = xw[i];
     }
   };
 
@@ -166,14 +178,14 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
   constexpr int kSB = E8 ? 1 : 4;
   const uint8_t* sbase = static_cast<const uint8_t*>(g.a_scales) + (int64_t)m0 * g.nkb * kSB;
   TileSrc rs;
-  if constexpr (kDirect) rs = tile_src(sbase, rows_a * g.nkb * kSB);
+  if constexpr (kRows != kNarrow) rs = tile_src(sbase, rows_a * g.nkb * kSB);
   auto bring_scales = [&](int kb, int buf) {
     const int k1 = lane & (kChunk - 1);
 #pragma unroll
     for (int i = 0; i < PA; ++i) {
       const int r = (wave + WAVES * i) * 8 + lrow;
       const bool in = r < rows_a && kb + k1 < kb1;
-      if constexpr (kDirect) {
+      if constexpr (kRows != kNarrow) {
         load_lds_word<kSB>(rs, lds_s + (uint32_t)((buf * BM * kChunk + (wave + WAVES * i) * 64) * 4), in ? (unsigned)((r * g.nkb + k1) * kSB) : kNoLoad,
                            kb * kSB);
       } else {
@@ -192,6 +204,7 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
   };
 
   bring(kb0, 0);
+  keep(kb0, 0);
   bring_scales(kb0, 0);
   load_sw(kb0);
   // every wave's own loads have landed before the barrier lets others read
@@ -250,6 +263,7 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
       }
       fw = next;
     }
+    if (kb + 1 < kb1) keep(kb + 1, buf ^ 1);
     // this step's reads are done and the next step's loads have landed
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
@@ -491,25 +505,25 @@ __global__ __launch_bounds__(512) void matmul_big_kernel(MatmulArgs g, int tiles
 
 // Few rows (a decoding step): the weight is read once and bounds the time, so
 // it goes straight from global memory into the fragments.  A workgroup
-// computes 16 NT columns (n) of 16 MT rows; its 8 waves share the blocks of
+// computes 16 NT columns (n) of 16 rows; its 8 waves share the blocks of
 // the reduction out, each a contiguous run, and add their sums through LDS: one
 // launch, no workspace.  Each wave keeps kRing blocks of both operands on
 // their way.  Row scales: a lane's load of one block's would touch 16 lines, so lane
 // (q, i16) loads block q of four for row i16 and the others ask it.
-template <int MT, int NT, bool E8, typename TO>
+template <int NT, bool E8, typename TO>
 __global__ __launch_bounds__(512) void matmul_few_kernel(MatmulArgs g, int per) {
-  __shared__ __align__(16) f32x4 part[8][NT * MT][64];
+  __shared__ __align__(16) f32x4 part[8][NT][64];
   constexpr bool kHwScale = E8 && sizeof(TO) == 2, kWide = sizeof(TO) == 4;
-  constexpr int kRing = MT + NT <= 3 ? 4 : 2, kGroup = 4;  // blocks on their way; blocks whose scales come together
+  constexpr int kRing = 4;  // blocks on their way, and whose scales come together
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, i16 = lane & 15;
-  const int n0 = (int)blockIdx.x * 16 * NT, m0 = (int)blockIdx.y * 16 * MT;
+  const int n0 = (int)blockIdx.x * 16 * NT, m0 = (int)blockIdx.y * 16;
   const int kb0 = wave * per, kb1 = min(g.nkb, kb0 + per);
   const TileSrc rw = tile_src(g.w + (int64_t)n0 * g.ldw, (min(16 * NT, g.n - n0) - 1) * (int)g.ldw + g.k);
-  const TileSrc ra = tile_src(g.a + (int64_t)m0 * g.lda, (min(16 * MT, g.rows - m0) - 1) * (int)g.lda + g.k);
+  const TileSrc ra = tile_src(g.a + (int64_t)m0 * g.lda, (min(16, g.rows - m0) - 1) * (int)g.lda + g.k);
   const int end = min(g.k, kb1 * kQBlk);
 
-  i32x8 fw[kRing][NT], fa[kRing][MT];
+  i32x8 fw[kRing][NT], fa[kRing];
   auto load = [&](int slot, int kb) {
     // pieces past the end are not loaded; one that the end cuts is loaded from
     // 16 bytes before it and shifted when it is used
@@ -529,8 +543,7 @@ __global__ __launch_bounds__(512) void matmul_few_kernel(MatmulArgs g, int per) 
     };
 #pragma unroll
     for (int t = 0; t < NT; ++t) piece(rw, 16 * t + i16, g.ldw, fw[slot][t]);
-#pragma unroll
-    for (int t = 0; t < MT; ++t) piece(ra, 16 * t + i16, g.lda, fa[slot][t]);
+    piece(ra, i16, g.lda, fa[slot]);
   };
   auto cut = [&](int kb, i32x8& f) {
 #pragma unroll
@@ -545,21 +558,16 @@ __global__ __launch_bounds__(512) void matmul_few_kernel(MatmulArgs g, int per) 
     }
   };
 
-  f32x4 acc[NT][MT];
+  f32x4 acc[NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0, 0, 0, 0};
   const int64_t sw_row = (int64_t)(n0 / kQBlk) * g.nkb;
-  int64_t sa_row[MT];
-#pragma unroll
-  for (int j = 0; j < MT; ++j) sa_row[j] = (int64_t)min(m0 + 16 * j + i16, g.rows - 1) * g.nkb;
-  uint32_t sa[MT], sw;
+  const int64_t sa_row = (int64_t)min(m0 + i16, g.rows - 1) * g.nkb;
+  uint32_t sa, sw;
   auto load_scales = [&](int kb) {
     const int at = min(kb + q, g.nkb - 1);
     sw = scale_bits<E8>(g.w_scales, sw_row + at);
-#pragma unroll
-    for (int j = 0; j < MT; ++j) sa[j] = scale_bits<E8>(g.a_scales, sa_row[j] + at);
+    sa = scale_bits<E8>(g.a_scales, sa_row + at);
   };
 
   if (kb0 < kb1) {
@@ -567,60 +575,49 @@ __global__ __launch_bounds__(512) void matmul_few_kernel(MatmulArgs g, int per) 
 #pragma unroll
     for (int t = 0; t < kRing; ++t) load(t, kb0 + t);
     const bool cuts = (g.k & 15) != 0 && kb1 == g.nkb;
-    for (int kb = kb0; kb < kb1; kb += kGroup) {
-      uint32_t s4[MT];
+    for (int kb = kb0; kb < kb1; kb += kRing) {
       const uint32_t w4 = sw;
+      const uint32_t s4 = kHwScale ? sa : __float_as_uint(scale_value<E8>(sa) * scale_value<E8>(sw));
+      load_scales(kb + kRing);
 #pragma unroll
-      for (int j = 0; j < MT; ++j)
-        s4[j] = kHwScale ? sa[j] : __float_as_uint(scale_value<E8>(sa[j]) * scale_value<E8>(sw));
-      load_scales(kb + kGroup);
-#pragma unroll
-      for (int t = 0; t < kGroup; ++t) {
-        constexpr int kMask = kRing - 1;
-        const int c = t & kMask;
+      for (int t = 0; t < kRing; ++t) {
         if (cuts && kb + t == g.nkb - 1) {
 #pragma unroll
-          for (int i = 0; i < NT; ++i) cut(kb + t, fw[c][i]);
-#pragma unroll
-          for (int j = 0; j < MT; ++j) cut(kb + t, fa[c][j]);
+          for (int i = 0; i < NT; ++i) cut(kb + t, fw[t][i]);
+          cut(kb + t, fa[t]);
         }
         // blocks past the run: codes zero, and a scale that may be anything
         const bool in = kb + t < kb1;
         const int swb = __builtin_amdgcn_readlane((int)w4, 16 * t);
+        const uint32_t sj = (uint32_t)__shfl((int)s4, 16 * t + i16);
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          const uint32_t sj = (uint32_t)__shfl((int)s4[j], 16 * t + i16);
+        for (int i = 0; i < NT; ++i) {
+          if constexpr (kHwScale) {
+            acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[t][i], fa[t], acc[i], 0, 0, 0, in ? swb : 127, 0,
+                                                                      in ? (int)sj : 127);
+          } else {
+            f32x4 p = {0, 0, 0, 0};
+            if constexpr (kWide) {
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            if constexpr (kHwScale) {
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[c][i], fa[c][j], acc[i][j], 0, 0, 0,
-                                                                           in ? swb : 127, 0, in ? (int)sj : 127);
+              for (int u = 0; u < 4; ++u)
+                p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(fw[t][i], u), widen(fa[t], u), p, 0, 0, 0);
             } else {
-              f32x4 p = {0, 0, 0, 0};
-              if constexpr (kWide) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                  p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(fw[c][i], u), widen(fa[c][j], u), p, 0, 0, 0);
-              } else {
-                p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[c][i], fa[c][j], p, 0, 0, 0, 0, 0, 0);
-              }
-              const float f = in ? __uint_as_float(sj) : 0.0f;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], f, acc[i][j][e]);
+              p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[t][i], fa[t], p, 0, 0, 0, 0, 0, 0);
             }
+            const float f = in ? __uint_as_float(sj) : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(p[e], f, acc[i][e]);
           }
         }
-        load(c, kb + t + kRing);
+        load(t, kb + kRing + t);
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) part[wave][i * MT + j][lane] = acc[i][j];
+  for (int i = 0; i < NT; ++i) part[wave][i][lane] = acc[i];
   __syncthreads();
-  for (int u = threadIdx.x; u < NT * MT * 64; u += 512) {
-    const int l = u & 63, t = u >> 6, m = m0 + 16 * (t % MT) + (l & 15), n = n0 + 16 * (t / MT) + 4 * (l >> 4);
+  for (int u = threadIdx.x; u < NT * 64; u += 512) {
+    const int l = u & 63, t = u >> 6, m = m0 + (l & 15), n = n0 + 16 * t + 4 * (l >> 4);
     f32x4 s = part[0][t][l];
 #pragma unroll
     for (int w = 1; w < 8; ++w) {
@@ -811,18 +808,18 @@ bool direct_ok(const MatmulArgs& g) {
            (uintptr_t)g.k) & 15) == 0 && g.lda <= (1 << 22) && g.ldw <= (1 << 22);
 }
 
-template <int MT, int MW, int NW, int NT, bool E8, typename TO, bool kDirect>
+template <int MT, int MW, int NW, int NT, bool E8, typename TO, Rows kRows>
 void tile_go(const MatmulArgs& g, int splits, hipStream_t stream) {
   constexpr int BM = 16 * MT * MW, BN = 16 * NT * NW;
   const int tm = (g.rows + BM - 1) / BM, tn = (g.n + BN - 1) / BN, per = (g.nkb + splits - 1) / splits;
-  hipLaunchKernelGGL((matmul_tile_kernel<MT, MW, NW, NT, E8, TO, kDirect>), dim3(tm * tn, splits), dim3(64 * MW * NW), 0,
+  hipLaunchKernelGGL((matmul_tile_kernel<MT, MW, NW, NT, E8, TO, kRows>), dim3(tm * tn, splits), dim3(64 * MW * NW), 0,
                      stream, g, per, tm, tn);
 }
 
-template <int MT, int NT, bool E8, typename TO>
+template <int NT, bool E8, typename TO>
 void few_go(const MatmulArgs& g, hipStream_t stream) {
-  hipLaunchKernelGGL((matmul_few_kernel<MT, NT, E8, TO>), dim3((g.n + 16 * NT - 1) / (16 * NT), (g.rows + 16 * MT - 1) / (16 * MT)),
-                     dim3(512), 0, stream, g, (g.nkb + 7) / 8);
+  hipLaunchKernelGGL((matmul_few_kernel<NT, E8, TO>), dim3((g.n + 16 * NT - 1) / (16 * NT), (g.rows + 15) / 16), dim3(512), 0,
+                     stream, g, (g.nkb + 7) / 8);
 }
 
 template <int MT, int NT, int WM, int WN, bool E8, typename TO>
@@ -840,11 +837,12 @@ hipError_t matmul_go(const MatmulArgs& g, hipStream_t stream) {
   const Way way = way_of(g.rows, g.n, g.k, kWide);
   const bool near = g.lda <= (1 << 22) && g.ldw <= (1 << 22);
   if (way == Way::kFew && near) {
-    few_go<1, 1, E8, TO>(g, stream);
+    few_go<1, E8, TO>(g, stream);
   } else if (!direct_ok(g)) {
     // rows that are no whole pieces: the few-rows form reads its weight faster
-    if (s == 1 && near && g.k >= 16 && g.rows <= 16) few_go<1, 2, E8, TO>(g, stream);
-    else tile_go<4, 2, 2, 4, E8, TO, false>(g, s, stream);
+    if (s == 1 && near && g.k >= 16 && g.rows <= 16) few_go<2, E8, TO>(g, stream);
+    else if (near && g.k >= 16) tile_go<4, 2, 2, 4, E8, TO, kCut>(g, s, stream);
+    else tile_go<4, 2, 2, 4, E8, TO, kNarrow>(g, s, stream);
   } else if (way == Way::kBig) {
     const int tm = (g.rows + 255) / 256, tn = (g.n + 255) / 256;
     const bool whole_y = ((reinterpret_cast<uintptr_t>(g.y) | (uintptr_t)(g.ldy * 2) | (uintptr_t)(g.n * 2)) & 15) == 0 &&
@@ -853,8 +851,8 @@ hipError_t matmul_go(const MatmulArgs& g, hipStream_t stream) {
   } else if (way == Way::kMid) {
     ring_go<4, 2, 2, 4, E8, TO>(g, s, stream);
   } else if (way == Way::kMany) {
-    if ((int64_t)((g.rows + 127) / 128) * ((g.n + 127) / 128) < 384) tile_go<2, 2, 2, 4, E8, TO, true>(g, s, stream);
-    else tile_go<4, 2, 2, 4, E8, TO, true>(g, s, stream);
+    if ((int64_t)((g.rows + 127) / 128) * ((g.n + 127) / 128) < 384) tile_go<2, 2, 2, 4, E8, TO, kWhole>(g, s, stream);
+    else tile_go<4, 2, 2, 4, E8, TO, kWhole>(g, s, stream);
   } else {
     switch (batch_rows(g.rows)) {
       case 16: ring_go<1, 1, 1, 4, E8, TO>(g, s, stream); break;

@@ -85,12 +85,6 @@ __device__ __forceinline__ void settle() {
   if constexpr (kAcc) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
 }
 
-// How rows are brought in.  kWhole: 16-byte aligned rows of whole 16-byte
-// pieces; dy straight into LDS.  kCut: any alignment and length (8 columns of
-// dy and 16 of x at least); the piece that a row's end cuts is loaded from 16
-// bytes before the end and shifted.  kNarrow: fewer columns, by elements.
-enum Rows { kWhole, kCut, kNarrow };
-
 // One tile of dw per workgroup of 4 waves, each 16 NI (k) by 16 NJ (n) of it;
 // PARTS: bf16 parts of x.  Per step of 64 rows a wave multiplies from
 // registers (the fragments of half a step), while it
