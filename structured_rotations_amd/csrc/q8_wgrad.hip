@@ -5,10 +5,12 @@
 //
 // The scale changes along the reduction, so x is decoded before the product.
 // A code has 4 significant bits: times a power of two (E8M0) it is exact in
-// bf16 and so is every product.  Times an fp32 scale it has up to 28 bits;
-// x = hi + lo in bf16 keeps 16 of them (two products), which fp32 results
-// take; bf16 results take the rounded x alone, whose error (2^-9 of each
-// term) is below the result's own rounding.
+// bf16 and so is every product.  Times an fp32 scale it has up to 28 bits, and
+// x is a sum of bf16 parts, one product each: three parts (24 bits) for fp32
+// results, one for bf16 results, which adds an error as large as the result's
+// own rounding (in all 1.4 times it; a second part takes 56 us instead of 40
+// at 1500 x 4099 x 1037).  Up to one step of rows, where writing dw bounds the
+// time, bf16 results take two parts.
 //
 // Both operands are stored along the other axis than the one summed over:
 // they stay that way in LDS ([m][n], [m][k]) and the transposing LDS read
@@ -100,7 +102,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   constexpr int UD = kStep * BN / 8 / 256, UX = kStep * BK / 16 / 256;  // pieces per thread: 8 of dy, 16 of x
   __shared__ __align__(16) uint8_t ld[2][kStep * BN * 2];
   const uint32_t lds_d = lds_address(ld);
-  __shared__ __align__(16) uint8_t lx[2][PARTS][kStep * BK * 2];
+  __shared__ __align__(16) uint8_t lx[PARTS][2][kStep * BK * 2];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int tn, tk;
   tile_of((int)blockIdx.x, tiles_n, tiles_k, &tn, &tk);
@@ -197,11 +199,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
         dec4(rx[set][u][c], v);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float a = v[2 * e] * s, b = v[2 * e + 1] * s;
-          const uint32_t hi = pack_bf16x2_hw(a, b);
-          xw[0][c >> 1][2 * (c & 1) + e] = hi;
-          if constexpr (PARTS == 2)
-            xw[PARTS - 1][c >> 1][2 * (c & 1) + e] = pack_bf16x2_hw(a - bf16_lo(hi), b - bf16_hi(hi));
+          float a = v[2 * e] * s, b = v[2 * e + 1] * s;
+#pragma unroll
+          for (int t = 0; t < PARTS; ++t) {  // what the parts before left is exact
+            const uint32_t w = pack_bf16x2_hw(a, b);
+            xw[t][c >> 1][2 * (c & 1) + e] = w;
+            a -= bf16_lo(w);
+            b -= bf16_hi(w);
+          }
         }
       }
       return;
@@ -221,8 +226,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
         first[e] = odd ? hi[e] : lo[e];
         second[e] = odd ? lo[e] : hi[e];
       }
-      *reinterpret_cast<u32x4*>(lx[0][t] + at + (odd ? 16 : 0)) = first;
-      *reinterpret_cast<u32x4*>(lx[0][t] + at + (odd ? 0 : 16)) = second;
+      *reinterpret_cast<u32x4*>(lx[t][0] + at + (odd ? 16 : 0)) = first;
+      *reinterpret_cast<u32x4*>(lx[t][0] + at + (odd ? 0 : 16)) = second;
     }
   };
 
@@ -235,12 +240,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   settle<kAcc>();
   s16x4 fr[2][NJ + R][2];  // fragments of two half steps: dy's, then x's
   // offsets of the buffer that is read; the other one is at ^ kFlip
-  constexpr uint32_t kFlipD = kStep * BN * 2, kFlipX = PARTS * kStep * BK * 2;
+  constexpr uint32_t kFlipD = kStep * BN * 2, kFlipX = kStep * BK * 2;
   uint32_t fbd = frag_base<BN>(wn, lane), fbx = frag_base<BK>(wk, lane);
   auto read_half = [&](int set, int sub, int u) {  // half u & 1 of fragment u / 2
     const int f = u >> 1, h = u & 1;
     if (f < NJ) fr[set][f][h] = frag_half<BN>(ld[0], fbd, sub, f, h);
-    else fr[set][f][h] = frag_half<BK>(lx[0][(f - NJ) / NI], fbx, sub, (f - NJ) % NI, h);
+    else fr[set][f][h] = frag_half<BK>(lx[(f - NJ) / NI][0], fbx, sub, (f - NJ) % NI, h);
   };
   // A half step is S instructions; the rest of the work goes between them, in
   // small units, since one wave per SIMD has nothing else to fill the gaps.
@@ -360,8 +365,8 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(WgradArgs g, int splits
 }
 
 // The tile and the number of splits of the rows: 256 x 256 tiles when there
-// are enough of them for the compute units, else 128 x 128.  (Two parts of x:
-// half as wide in k.)  The rows are split while tiles leave compute units
+// are enough of them for the compute units, else 128 x 128.  (More parts of x:
+// narrower in k.)  The rows are split while tiles leave compute units
 // idle and every split keeps 4 steps.
 struct WgradShape {
   bool big;
@@ -396,10 +401,11 @@ hipError_t wgrad_go(const WgradArgs& g, hipStream_t stream) {
                        (uintptr_t)g.ldx | (uintptr_t)(g.n * 2) | (uintptr_t)g.k) & 15) == 0;
   // a descriptor holds 64 rows in 2 GiB
   const bool narrow = g.n < 8 || g.k < 16 || g.lddy > (1 << 22) || g.ldx > (1 << 22);
-  if (narrow) wgrad_tile_go<4 / PARTS, 4, E8, PARTS, TO, kNarrow>(g, s, stream);
-  else if (s.big && whole) wgrad_tile_go<8 / PARTS, 8, E8, PARTS, TO, kWhole>(g, s, stream);
-  else if (s.big) wgrad_tile_go<8 / PARTS, 8, E8, PARTS, TO, kCut>(g, s, stream);
-  else wgrad_tile_go<4 / PARTS, 4, E8, PARTS, TO, kCut>(g, s, stream);
+  constexpr int kBigK = PARTS == 1 ? 8 : PARTS == 2 ? 4 : 2, kSmallK = PARTS == 1 ? 4 : 2;
+  if (narrow) wgrad_tile_go<kSmallK, 4, E8, PARTS, TO, kNarrow>(g, s, stream);
+  else if (s.big && whole) wgrad_tile_go<kBigK, 8, E8, PARTS, TO, kWhole>(g, s, stream);
+  else if (s.big) wgrad_tile_go<kBigK, 8, E8, PARTS, TO, kCut>(g, s, stream);
+  else wgrad_tile_go<kSmallK, 4, E8, PARTS, TO, kCut>(g, s, stream);
   if (s.splits > 1) {
     const int64_t wg = ((int64_t)g.n * g.k + 255) / 256;
     hipLaunchKernelGGL((wgrad_join_kernel<TO>), dim3((unsigned)(wg < 4096 ? wg : 4096)), dim3(256), 0, stream, g,
@@ -416,8 +422,9 @@ int64_t matmul_q8_wgrad_workspace(int64_t rows, int64_t n, int64_t k) {
 }
 
 hipError_t launch_matmul_q8_wgrad(const WgradArgs& g, bool e8, DT out, hipStream_t stream) {
-  if (out == DT::F32) return e8 ? wgrad_go<true, 1, float>(g, stream) : wgrad_go<false, 2, float>(g, stream);
-  return e8 ? wgrad_go<true, 1, uint16_t>(g, stream) : wgrad_go<false, 1, uint16_t>(g, stream);
+  if (out == DT::F32) return e8 ? wgrad_go<true, 1, float>(g, stream) : wgrad_go<false, 3, float>(g, stream);
+  if (e8) return wgrad_go<true, 1, uint16_t>(g, stream);
+  return g.rows <= kStep ? wgrad_go<false, 2, uint16_t>(g, stream) : wgrad_go<false, 1, uint16_t>(g, stream);
 }
 
 }  // namespace harp
