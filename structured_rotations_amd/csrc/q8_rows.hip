@@ -95,15 +95,32 @@ __device__ __forceinline__ float block_sum(float v, float (&part)[2][16], int se
   return row16_sum(l < nw ? part[set][l] : 0.0f);
 }
 
-// Rows up to 8192 leave registers for the next row.
-template <int NCH>
-constexpr bool kAhead = NCH <= 2;
+// How a row is held.  One workgroup, or (rows of one block, kShort: the norms
+// of attention heads) 16 lanes, 16 rows in a workgroup of 256.
+template <bool kShort>
+struct RowMap {
+  int tid, threads;
+  int64_t first, step;
+  __device__ __forceinline__ RowMap() {
+    tid = kShort ? threadIdx.x & 15 : threadIdx.x;
+    threads = kShort ? 16 : blockDim.x;
+    first = kShort ? (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4) : blockIdx.x;
+    step = kShort ? (int64_t)gridDim.x * 16 : gridDim.x;
+  }
+};
+template <bool kShort>
+__device__ __forceinline__ float row_sum(float v, float (&part)[2][16], int set) {
+  if constexpr (kShort) return row16_sum(v);
+  else return block_sum(v, part, set);
+}
 
 // A workgroup walks over rows; a row stays in registers between the sum of
-// squares and the coding (NCH chunks of 8 per thread), and (kAhead) the next
-// row is on its way meanwhile.
-template <typename T, int NCH, bool E8>
-__global__ __launch_bounds__(kAhead<NCH> ? 512 : 1024) void rmsnorm_q8_kernel(NormArgs a) {
+// squares and the coding (NCH chunks of 8 per thread), and (kAhead: rows up to
+// 8192, which leave registers for it) the next row is on its way meanwhile.
+template <typename T, int NCH, bool E8, bool kShort = false>
+__global__ __launch_bounds__(NCH <= 2 ? 512 : 1024) void rmsnorm_q8_kernel(NormArgs a) {
+  constexpr bool kAhead = NCH <= 2;
+  const RowMap<kShort> map;
   __shared__ float part[2][16];
   const int nblk = (a.d + kQBlk - 1) / kQBlk;
   const T* gamma = static_cast<const T*>(a.gamma);
@@ -111,7 +128,7 @@ __global__ __launch_bounds__(kAhead<NCH> ? 512 : 1024) void rmsnorm_q8_kernel(No
   Raw8<T> x[NCH], res[NCH];
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    col[c] = ((int)threadIdx.x + c * (int)blockDim.x) * 8;
+    col[c] = (map.tid + c * map.threads) * 8;
     n[c] = a.d - col[c];
     x[c].fill(0);
     res[c].fill(0);
@@ -125,10 +142,10 @@ __global__ __launch_bounds__(kAhead<NCH> ? 512 : 1024) void rmsnorm_q8_kernel(No
       if (a.residual) res[c].load(static_cast<const T*>(a.residual) + r * a.ldr + col[c], n[c]);
     }
   };
-  if (kAhead<NCH>) load(blockIdx.x);
+  if (kAhead) load(map.first);
   int set = 0;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, set ^= 1) {
-    if (!kAhead<NCH>) load(r);
+  for (int64_t r = map.first; r < a.rows; r += map.step, set ^= 1) {
+    if (!kAhead) load(r);
     float v[NCH][8], ss = 0.0f;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
@@ -139,10 +156,10 @@ __global__ __launch_bounds__(kAhead<NCH> ? 512 : 1024) void rmsnorm_q8_kernel(No
       }
       if (a.h && n[c] > 0) store8_of<T>(static_cast<T*>(a.h) + r * a.ldh + col[c], n[c], v[c]);
     }
-    if (kAhead<NCH>) load(r + gridDim.x);
-    ss = block_sum(ss, part, set);
+    if (kAhead) load(r + map.step);
+    ss = row_sum<kShort>(ss, part, set);
     const float rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
-    if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
+    if (a.rstd && map.tid == 0) a.rstd[r] = rstd;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int blk = col[c] / kQBlk;
@@ -176,11 +193,13 @@ __global__ __launch_bounds__(kAhead<NCH> ? 512 : 1024) void rmsnorm_q8_kernel(No
 // A workgroup walks over rows, keeping gamma and its share of dgamma's sum
 // for its columns in registers, and the row as it came: the values are made
 // from it once for the sum and once for dh, which takes fewer registers than
-// keeping them.  The next row is on its way meanwhile (kAhead; longer rows
-// read gamma and dres when they are used instead).  The partial sums of the
+// keeping them.  The next row is on its way meanwhile (kAhead: rows up to 8192;
+// longer ones read gamma and dres when they are used instead).  The partial sums of the
 // workgroups are added in order by the second kernel.
-template <typename T, int NCH, bool E8>
-__global__ __launch_bounds__(1024) void rmsnorm_q8_vjp_kernel(NormVjpArgs a) {
+template <typename T, int NCH, bool E8, bool kShort = false>
+__global__ __launch_bounds__(kShort ? 256 : 1024) void rmsnorm_q8_vjp_kernel(NormVjpArgs a) {
+  constexpr bool kAhead = NCH == 1;
+  const RowMap<kShort> map;
   __shared__ float part[2][16];
   const int nblk = (a.d + kQBlk - 1) / kQBlk;
   int col[NCH], n[NCH];
@@ -188,7 +207,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_q8_vjp_kernel(NormVjpArgs a) {
   float dg[NCH][8];
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    col[c] = ((int)threadIdx.x + c * (int)blockDim.x) * 8;
+    col[c] = (map.tid + c * map.threads) * 8;
     n[c] = a.d - col[c];
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[c][j] = 0.0f;
@@ -197,7 +216,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_q8_vjp_kernel(NormVjpArgs a) {
     g[c].fill(0x3f800000u);
     if (a.gamma && n[c] > 0) g[c].load(static_cast<const T*>(a.gamma) + col[c], n[c]);
   };
-  if (kAhead<NCH>)
+  if (kAhead)
 #pragma unroll
     for (int c = 0; c < NCH; ++c) load_g(c);
   struct Row {
@@ -215,7 +234,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_q8_vjp_kernel(NormVjpArgs a) {
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       w.dn[c].fill(0);
-      if (kAhead<NCH>) load_dr(w, r, c);
+      if (kAhead) load_dr(w, r, c);
       w.cd[c].w[0] = w.cd[c].w[1] = 0;
       w.sc[c] = 0.0f;
       if (r >= a.rows || n[c] <= 0) continue;
@@ -224,17 +243,17 @@ __global__ __launch_bounds__(1024) void rmsnorm_q8_vjp_kernel(NormVjpArgs a) {
       w.sc[c] = load_scale<E8>(a.scales, r * nblk + col[c] / kQBlk);
     }
   };
-  if (kAhead<NCH>) load(now, blockIdx.x);
+  if (kAhead) load(now, map.first);
   int set = 0;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, set ^= 1) {
-    if (kAhead<NCH>) load(next, r + gridDim.x);
+  for (int64_t r = map.first; r < a.rows; r += map.step, set ^= 1) {
+    if (kAhead) load(next, r + map.step);
     else load(now, r);
     float dot = 0.0f;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       float xn[8];
       now.cd[c].values(xn);
-      if (!kAhead<NCH>) load_g(c);
+      if (!kAhead) load_g(c);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         xn[j] = j < n[c] ? xn[j] * now.sc[c] : 0.0f;  // 0 past the row's end, whatever the scale
@@ -243,13 +262,13 @@ __global__ __launch_bounds__(1024) void rmsnorm_q8_vjp_kernel(NormVjpArgs a) {
         dot += u * g[c][j] * xn[j];
       }
     }
-    const float mean = block_sum(dot, part, set) / (float)a.d;
+    const float mean = row_sum<kShort>(dot, part, set) / (float)a.d;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       if (n[c] <= 0) continue;
       float xn[8], o[8];
       now.cd[c].values(xn);
-      if (!kAhead<NCH>) {
+      if (!kAhead) {
         load_g(c);
         load_dr(now, r, c);
       }
@@ -258,9 +277,20 @@ __global__ __launch_bounds__(1024) void rmsnorm_q8_vjp_kernel(NormVjpArgs a) {
         o[j] = now.dr[c][j] + now.rstd * (now.dn[c][j] * g[c][j] - xn[j] * now.sc[c] * mean);
       store8_of<T>(static_cast<T*>(a.dh) + r * a.lddh + col[c], n[c], o);
     }
-    if (kAhead<NCH>) now = next;
+    if (kAhead) now = next;
   }
-  if (a.partial) {
+  if constexpr (kShort) {
+    // the 16 rows' shares in order
+    __shared__ float share[16][129];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) share[threadIdx.x >> 4][map.tid * 8 + j] = dg[0][j];
+    __syncthreads();
+    if (a.partial && (int)threadIdx.x < a.d) {
+      float t = 0.0f;
+      for (int i = 0; i < 16; ++i) t += share[i][threadIdx.x];
+      a.partial[(int64_t)blockIdx.x * a.d + threadIdx.x] = t;
+    }
+  } else if (a.partial) {
 #pragma unroll
     for (int c = 0; c < NCH; ++c)
       if (n[c] > 0) store8_of<float>(a.partial + (int64_t)blockIdx.x * a.d + col[c], n[c], dg[c]);
@@ -297,6 +327,11 @@ int row_threads(int d, int nch) { return ((d + 7) / 8 + nch * 64 - 1) / (nch * 6
 // 4, and one row alone is faster with 8).
 template <typename T, bool E8>
 hipError_t norm_go(const NormArgs& a, hipStream_t stream) {
+  if (a.d <= kQBlk) {
+    const dim3 grid((unsigned)std::min((a.rows + 15) / 16, (int64_t)2048));
+    hipLaunchKernelGGL((rmsnorm_q8_kernel<T, 1, E8, true>), grid, dim3(256), 0, stream, a);
+    return hipGetLastError();
+  }
   const int nch = a.d <= 4096 ? 1 : a.d <= 8192 ? 2 : 4, threads = row_threads(a.d, nch);
   // about as many workgroups as fit the compute units at once
   const int64_t fit = 256 * (int64_t)std::max(1, 1024 / threads);
@@ -310,17 +345,21 @@ hipError_t norm_go(const NormArgs& a, hipStream_t stream) {
 // Workgroups of the backward pass: each writes a row of partial sums, so no
 // more than keep the compute units busy (16384 x 5120: 512 of 640 threads
 // 127 us, 1024 135 us; two chunks per thread 186 us, for want of registers).
-int vjp_threads(int64_t d) { return row_threads((int)d, d <= 8192 ? 1 : 4); }
+int vjp_chunks(int64_t d) { return d <= 8192 ? 1 : d <= 16384 ? 2 : 4; }
 int vjp_groups(int64_t rows, int64_t d) {
-  return (int)std::min(rows, 256 * (int64_t)std::min(8, std::max(2, 1024 / vjp_threads(d))));
+  if (d <= kQBlk) return (int)std::min((rows + 15) / 16, (int64_t)2048);
+  const int threads = row_threads((int)d, vjp_chunks(d));
+  return (int)std::min(rows, 256 * (int64_t)std::min(8, std::max(2, 1024 / threads)));
 }
 
 template <typename T, bool E8>
 hipError_t norm_vjp_go(const NormVjpArgs& a, hipStream_t stream) {
-  const int groups = vjp_groups(a.rows, a.d), threads = vjp_threads(a.d);
+  const int groups = vjp_groups(a.rows, a.d), nch = vjp_chunks(a.d), threads = row_threads(a.d, nch);
   if (groups > 0) {
     const dim3 grid(groups);
-    if (a.d <= 8192) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 1, E8>), grid, dim3(threads), 0, stream, a);
+    if (a.d <= kQBlk) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 1, E8, true>), grid, dim3(256), 0, stream, a);
+    else if (nch == 1) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 1, E8>), grid, dim3(threads), 0, stream, a);
+    else if (nch == 2) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 2, E8>), grid, dim3(threads), 0, stream, a);
     else hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 4, E8>), grid, dim3(threads), 0, stream, a);
   }
   if (a.dgamma)

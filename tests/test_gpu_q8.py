@@ -193,7 +193,8 @@ def check_coded(codes, scales, want, kind):
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,d,gamma,residual,ckpt", [
     (1, 4096, False, True, False), (5, 1, True, True, True), (3, 130, True, False, True), (70, 4099, True, True, True),
-    (33, 5120, False, True, True), (2, 20001, True, True, True), (2, 32768, False, False, True), (9, 512, True, True, False)])
+    (33, 5120, False, True, True), (2, 20001, True, True, True), (1000, 64, True, True, True), (35, 128, True, False, True),
+    (2, 9001, True, True, True), (2, 32768, False, False, True), (9, 512, True, True, False)])
 def test_rmsnorm(rows, d, gamma, residual, ckpt, io, kind):
     say("rmsnorm", rows, d, gamma, residual, ckpt, io, kind)
     rng = np.random.default_rng(rows + d)
@@ -260,7 +261,8 @@ def coded(rng, x, kind):
 @pytest.mark.parametrize("kind", ["f32", "e8m0"])
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,d,gamma,dres", [(1, 4096, True, True), (1, 1, True, False), (1500, 130, True, True),
-                                               (37, 4099, False, True), (3, 20001, True, True), (2, 32768, True, False)])
+                                               (37, 4099, False, True), (3, 20001, True, True), (40000, 64, True, True),
+                                               (33, 128, True, False), (5, 9001, True, True), (2, 32768, True, False)])
 def test_rmsnorm_vjp(rows, d, gamma, dres, io, kind):
     say("rmsnorm_vjp", rows, d, gamma, dres, io, kind)
     rng = np.random.default_rng(rows + 3 * d)
