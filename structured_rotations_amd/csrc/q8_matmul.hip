@@ -846,7 +846,7 @@ hipError_t matmul_go(const MatmulArgs& g, hipStream_t stream) {
   } else if (way == Way::kBig) {
     const int tm = (g.rows + 255) / 256, tn = (g.n + 255) / 256;
     const bool whole_y = ((reinterpret_cast<uintptr_t>(g.y) | (uintptr_t)(g.ldy * 2) | (uintptr_t)(g.n * 2)) & 15) == 0 &&
-                         g.ldy <= (1 << 22);
+                         g.ldy <= (1 << 21);  // 256 rows of 2-byte results end before kNoLoad
     hipLaunchKernelGGL((matmul_big_kernel<E8>), dim3(std::min(tm * tn, 256)), dim3(512), 0, stream, g, tm, tn, whole_y);
   } else if (way == Way::kMid) {
     ring_go<4, 2, 2, 4, E8, TO>(g, s, stream);

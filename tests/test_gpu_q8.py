@@ -453,6 +453,19 @@ def test_matmul_far_offsets():
     check_codes(codes_np(q)[keep], x[keep], 1, "f32")
 
 
+@pytest.mark.parametrize("ldy", [1 << 21, 1 << 22])
+def test_matmul_far_result_rows(ldy):
+    # a 256-row tile of results over 1 and 2 GiB
+    say("matmul far result rows", ldy)
+    rng = np.random.default_rng(26)
+    rows, n, k = 256, 160 * 256, 256
+    (ac, as_), (wc, ws) = operands(rng, rows, n, k, "f32")
+    y = torch.empty((rows - 1) * ldy + n, dtype=torch.bfloat16, device="cuda").as_strided((rows, n), (ldy, 1))
+    H.harp_matmul_q8(to_codes(ac), to_scales(as_, "f32"), to_codes(wc), to_scales(ws, "f32"), y=y)
+    torch.cuda.synchronize()
+    assert rel_rows(np64(y), Q.matmul(ac, as_, wc, ws)) <= TOL["bf16"]
+
+
 WGRAD = [(1, 1, 1), (1, 300, 130), (31, 128, 128), (32, 64, 640), (33, 129, 127), (100, 500, 272), (257, 260, 515),
          (1000, 384, 256), (1500, 1030, 400), (5000, 64, 80), (4097, 16, 130)]
 
