@@ -147,15 +147,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   // that a shifted piece of the first columns is inside
   auto rows_left = [&](int m0) { return max(0, min(mhi - m0, kStep)); };
   auto src_dy = [&](int m0) {
-    const int left = rows_left(m0);
+    const int left = kRows == kNarrow ? 0 : rows_left(m0);
     return tile_src(g.dy + (int64_t)(left ? m0 : mlo) * g.lddy, left ? ((left - 1) * (int)g.lddy + g.n) * 2 : 0);
   };
   auto src_x = [&](int m0) {
-    const int left = rows_left(m0);
+    const int left = kRows == kNarrow ? 0 : rows_left(m0);
     return tile_src(g.x + (int64_t)(left ? m0 : mlo) * g.ldx, left ? (left - 1) * (int)g.ldx + g.k : 0);
   };
   auto src_s = [&](int m0) {
-    const int left = rows_left(m0);
+    const int left = kRows == kNarrow ? 0 : rows_left(m0);
     return tile_src(static_cast<const uint8_t*>(g.x_scales) + (int64_t)(left ? m0 : mlo) * g.nkb * kSB, left * g.nkb * kSB);
   };
   auto bring_dy = [&](TileSrc src, int buf, int u) {
@@ -175,6 +175,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
     if constexpr (kRows == kNarrow)
       rx[set][u] = load16_bytes(g.x + (int64_t)(m0 + xrow + r) * g.ldx + k0 + xcol, m0 + xrow + r < mhi ? xn : 0);
     else rx[set][u] = load_16(src, vx + (unsigned)(k0 + r * (int)g.ldx));
+    if constexpr (kRows == kNarrow) {
+      const bool in = m0 + xrow + r < mhi && xn > 0;
+      rs[set][u] = 0;
+      if (in) rs[set][u] = scale_bits<E8>(g.x_scales, (int64_t)(m0 + xrow + r) * g.nkb + (k0 + xcol) / kQBlk);
+      return;
+    }
     rs[set][u] = load_word<kSB>(scales, vs + (unsigned)(r * g.nkb * kSB));
   };
   auto keep_dy = [&](int set, int buf, int u) {

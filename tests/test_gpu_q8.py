@@ -466,6 +466,25 @@ def test_matmul_far_result_rows(ldy):
     assert rel_rows(np64(y), Q.matmul(ac, as_, wc, ws)) <= TOL["bf16"]
 
 
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+def test_wgrad_far_rows(kind):
+    # rows more than 2^22 values apart
+    say("wgrad far rows", kind)
+    rng = np.random.default_rng(32)
+    rows, n, k, ld = 70, 144, 272, (1 << 22) + 16
+    xc, xs = Q.quantize(rng.standard_normal((rows, k)), 1, kind)
+    dy = torch.from_numpy(rng.standard_normal((rows, n)).astype(np.float32)).to(torch.bfloat16)
+    fx = torch.empty((rows - 1) * ld + k, dtype=torch.float8_e4m3fn, device="cuda").as_strided((rows, k), (ld, 1))
+    fd = torch.empty((rows - 1) * ld + n, dtype=torch.bfloat16, device="cuda").as_strided((rows, n), (ld, 1))
+    fx.copy_(to_codes(xc))
+    fd.copy_(dy.cuda())
+    want = Q.wgrad(np64(dy), xc, xs)
+    for a, b in ((fd, fx), (dy.cuda(), fx), (fd, to_codes(xc))):
+        dw = H.harp_matmul_q8_wgrad(a, b, to_scales(xs, kind), "f32")
+        torch.cuda.synchronize()
+        assert rel_rows(np64(dw), want) <= TOL["f32"]
+
+
 WGRAD = [(1, 1, 1), (1, 300, 130), (31, 128, 128), (32, 64, 640), (33, 129, 127), (100, 500, 272), (257, 260, 515),
          (1000, 384, 256), (1500, 1030, 400), (5000, 64, 80), (4097, 16, 130)]
 
