@@ -81,6 +81,10 @@ constexpr int kChunk = 8;  // steps whose row scales are brought in together
 // One 16 MT MW x 16 NT NW tile of y per workgroup of MW x NW waves, each with
 // 16 MT rows (m) by 16 NT columns (n) of it.  LDS holds two steps of one
 // block of 128: while a step is computed the next one is on its way.
+// 64 x 64 per wave; 32 x 64 (MT = 2) below 384 tiles of 128 x 128, where twice
+// the workgroups even the load out: 777 x 5120 x 4112, fp32 results, 59 us
+// against 70, while at 432 tiles (bf16) 68 against 53.  fp32 results multiply
+// on the bf16 instructions: 96 conversions go with every 32 of them.
 template <int MT, int MW, int NW, int NT, bool E8, typename TO, Rows kRows>
 __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g, int kb_per_split, int tiles_m,
                                                                    int tiles_n) {
@@ -301,7 +305,10 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
 // steps, and the stores of a tile drain during the first step of the next
 // (kStores is added to what that step's waits count on).  Bound by the matrix
 // instructions: at 16384 x 13824 x 5120 they alone, on the same operands, take
-// 674 us.
+// 674 us; the whole 1003 to 1037 us with fp32 scales (2.3 PFLOP/s; every
+// block's product is scaled on the vector unit, a multiply-add per result and
+// block) and 895 to 924 us with E8M0, which the instruction applies itself
+// (2.6 PFLOP/s, a per-tensor library product's rate).
 constexpr int kBigA = 4, kBigW = 4;  // loads per wave and step: A, W (half of them W0)
 constexpr int kStores = 16;          // stores per wave and tile
 
@@ -508,7 +515,9 @@ __global__ __launch_bounds__(512) void matmul_big_kernel(MatmulArgs g, int tiles
 // computes 16 NT columns (n) of 16 rows; its 8 waves share the blocks of
 // the reduction out, each a contiguous run, and add their sums through LDS: one
 // launch, no workspace.  Each wave keeps kRing blocks of both operands on
-// their way.  Row scales: a lane's load of one block's would touch 16 lines, so lane
+// their way.  1 x 4096 x 4096: 5.9 us of the call's 8 (the ring form 13);
+// 13824 x 5120 takes 18 to 22 us here and 14 to 15 in the ring form, where the
+// weight streams better: hence up to 2^25 codes.  Row scales: a lane's load of one block's would touch 16 lines, so lane
 // (q, i16) loads block q of four for row i16 and the others ask it.
 template <int NT, bool E8, typename TO>
 __global__ __launch_bounds__(512) void matmul_few_kernel(MatmulArgs g, int per) {
@@ -633,7 +642,7 @@ __global__ __launch_bounds__(512) void matmul_few_kernel(MatmulArgs g, int per) 
 // kRing steps, all but one of them on their way, and nothing is ever drained.
 // One 16 MT WM x 16 NT WN tile per workgroup of WM x WN waves.  A step's
 // scales come with it: by lane for the rows, a load that touches 64 lines but
-// is one of a step's five.
+// is one of a step's five.  64 x 13824 x 5120: 17 us (4.3 TB/s of codes).
 template <int MT, int NT, int WM, int WN, bool E8, typename TO>
 __global__ __launch_bounds__(64 * WM * WN) void matmul_ring_kernel(MatmulArgs g, int kb_per_split, int tiles_m,
                                                                    int tiles_n) {
@@ -774,7 +783,13 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(MatmulArgs g, int spli
   }
 }
 
-// Which kernel, from sizes alone (the workspace depends on it).
+// Which kernel, from sizes alone (the workspace depends on it).  Both sides at
+// the borders:
+//   few    weights of up to 2^25 codes, see matmul_few_kernel
+//   big    from 160 tiles: 1024 x 13824 x 5120 (216) 77 us, kMany 106
+//   batch  64 x 64 tiles that all fit at once: 256 x 4096 x 4096 15 us, kMid 30
+//   mid    128 x 128 tiles that all fit: 1024 x 4096 x 4096 25 us, kMany 44;
+//          at 432 tiles, two rounds, 71 against kMany's 53
 enum class Way { kFew, kBatch, kMid, kMany, kBig };
 Way way_of(int64_t rows, int64_t n, int64_t k, bool wide) {
   if (rows <= 16 && k >= 16 && n * k <= (1 << 25)) return Way::kFew;
@@ -787,7 +802,8 @@ Way way_of(int64_t rows, int64_t n, int64_t k, bool wide) {
 int batch_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || rows > 128 ? 64 : 128; }
 
 // The reduction is split into as many parts as the compute units can take at
-// once, of 4 blocks at least: another round costs more than the idle units.
+// once, of 4 blocks at least: another round costs more than the idle units
+// (64 x 13824 x 5120: whole 19 us, in two 24 us and 4 to join).
 int split(int64_t tiles, int64_t nkb) {
   const int64_t s = std::max<int64_t>(1, std::min(std::min<int64_t>(256 / tiles, nkb / 4), (int64_t)16));
   const int64_t per = (nkb + s - 1) / s;

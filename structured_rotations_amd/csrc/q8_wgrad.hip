@@ -94,7 +94,10 @@ __device__ __forceinline__ void settle() {
 //                 step's rows, which are in registers, into the other buffer
 //   second half   (after a barrier) reads the next step's first fragments and
 //                 asks for the rows of the step after that.
-// Global loads have a whole step to arrive.
+// Global loads have a whole step to arrive.  Bound by the matrix instructions:
+// 16384 x 4096 x 4096, E8M0, 414 to 426 us, 1.3 PFLOP/s, 0.84 of a plain bf16
+// product's (4 by 4 fragments per wave, with twice the LDS reads per
+// instruction: 608 us).
 template <int NI, int NJ, bool E8, int PARTS, typename TO, Rows kRows>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) void wgrad_tile_kernel(
     WgradArgs g, int m_per_split, int tiles_n, int tiles_k) {
@@ -370,23 +373,32 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(WgradArgs g, int splits
   }
 }
 
-// The tile and the number of splits of the rows: 256 x 256 tiles when there
-// are enough of them for the compute units, else 128 x 128.  (More parts of x:
-// narrower in k.)  The rows are split while tiles leave compute units
-// idle and every split keeps 4 steps.
+// Tiles along k of the two kinds, in segments of 32: (more parts of x: narrower).
+constexpr int kBigK(int parts) { return parts == 1 ? 8 : parts == 2 ? 4 : 2; }
+constexpr int kSmallK(int parts) { return parts == 1 ? 4 : 2; }
+
+// The rows are split while 128 x 128 tiles leave compute units idle and every
+// split keeps 4 steps (the workspace depends on sizes alone).  Without a split
+// the tile is the large one (8 fragments of dy by kBigK of x per wave) if its
+// rounds over the 256 compute units take less time than the small one's (4 by
+// kSmallK): per round 2.7 times the small one's with one part, 1.8 with three.
+// 4096 rows, n = 4096, one part: k = 2048 small 80 us, large 103 (one round of
+// the large against two); k = 2304 119 and 104 (against three), 3328 148 and
+// 105; 16384 x 4096 x 4096 608 and 421.  Three parts: k = 2048 219 and 198,
+// 2560 274 and 287.
 struct WgradShape {
   bool big;
   int splits, m_per_split;
 };
-WgradShape wgrad_shape(int64_t rows, int64_t n, int64_t k) {
-  WgradShape s;
-  s.big = ((n + 255) / 256) * ((k + 255) / 256) >= 192;
-  const int64_t b = s.big ? 256 : 128;
-  const int64_t tiles = ((n + b - 1) / b) * ((k + b - 1) / b), steps = (rows + kStep - 1) / kStep;
+WgradShape wgrad_shape(int64_t rows, int64_t n, int64_t k, int parts) {
+  auto tiles = [&](int64_t bn, int64_t bk) { return ((n + bn - 1) / bn) * ((k + bk - 1) / bk); };
+  auto rounds = [&](int64_t bn, int64_t bk) { return (tiles(bn, bk) + 255) / 256; };
+  const int64_t t = tiles(128, 128), steps = (rows + kStep - 1) / kStep;
   int64_t p = 1;
-  if (!s.big)
-    while (tiles * p < 256 && p * 2 * 4 <= steps && p < 64) p *= 2;
+  while (t * p < 256 && p * 2 * 4 <= steps && p < 64) p *= 2;
   const int64_t per = (steps + p - 1) / p;
+  WgradShape s;
+  s.big = t >= 256 && (parts == 1 ? 8 : 6) * rounds(256, 32 * kBigK(parts)) <= 3 * rounds(128, 32 * kSmallK(parts));
   s.m_per_split = (int)(per * kStep);
   s.splits = per > 0 ? (int)((steps + per - 1) / per) : 1;
   return s;
@@ -402,16 +414,15 @@ void wgrad_tile_go(const WgradArgs& g, const WgradShape& s, hipStream_t stream) 
 
 template <bool E8, int PARTS, typename TO>
 hipError_t wgrad_go(const WgradArgs& g, hipStream_t stream) {
-  const WgradShape s = wgrad_shape(g.rows, g.n, g.k);
+  const WgradShape s = wgrad_shape(g.rows, g.n, g.k, PARTS);
   const bool whole = ((reinterpret_cast<uintptr_t>(g.dy) | reinterpret_cast<uintptr_t>(g.x) | (uintptr_t)(g.lddy * 2) |
                        (uintptr_t)g.ldx | (uintptr_t)(g.n * 2) | (uintptr_t)g.k) & 15) == 0;
   // a descriptor holds 64 rows in 2 GiB
   const bool narrow = g.n < 8 || g.k < 16 || g.lddy > (1 << 22) || g.ldx > (1 << 22);
-  constexpr int kBigK = PARTS == 1 ? 8 : PARTS == 2 ? 4 : 2, kSmallK = PARTS == 1 ? 4 : 2;
-  if (narrow) wgrad_tile_go<kSmallK, 4, E8, PARTS, TO, kNarrow>(g, s, stream);
-  else if (s.big && whole) wgrad_tile_go<kBigK, 8, E8, PARTS, TO, kWhole>(g, s, stream);
-  else if (s.big) wgrad_tile_go<kBigK, 8, E8, PARTS, TO, kCut>(g, s, stream);
-  else wgrad_tile_go<kSmallK, 4, E8, PARTS, TO, kCut>(g, s, stream);
+  if (narrow) wgrad_tile_go<kSmallK(PARTS), 4, E8, PARTS, TO, kNarrow>(g, s, stream);
+  else if (s.big && whole) wgrad_tile_go<kBigK(PARTS), 8, E8, PARTS, TO, kWhole>(g, s, stream);
+  else if (s.big) wgrad_tile_go<kBigK(PARTS), 8, E8, PARTS, TO, kCut>(g, s, stream);
+  else wgrad_tile_go<kSmallK(PARTS), 4, E8, PARTS, TO, kCut>(g, s, stream);
   if (s.splits > 1) {
     const int64_t wg = ((int64_t)g.n * g.k + 255) / 256;
     hipLaunchKernelGGL((wgrad_join_kernel<TO>), dim3((unsigned)(wg < 4096 ? wg : 4096)), dim3(256), 0, stream, g,
@@ -423,7 +434,7 @@ hipError_t wgrad_go(const WgradArgs& g, hipStream_t stream) {
 }  // namespace
 
 int64_t matmul_q8_wgrad_workspace(int64_t rows, int64_t n, int64_t k) {
-  const int s = wgrad_shape(rows, n, k).splits;
+  const int s = wgrad_shape(rows, n, k, 1).splits;
   return s > 1 ? (int64_t)s * n * k * 4 : 0;
 }
 

@@ -116,13 +116,30 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _work(workspace, need, device):
-    """The caller's workspace, or one allocated here when needed."""
+def _out_mat(t, name, dtype, rows, cols, like):
+    """The caller's result matrix, checked, or a new one beside `like`: it and
+    its leading dimension."""
+    if t is None:
+        return torch.empty((rows, cols), dtype=dtype, device=like.device), cols
+    return t, _mat(t, name, (dtype,), rows, cols)
+
+
+def _out_scales(t, name, rows, cols, block_rows, dtype, like):
+    if t is None:
+        return torch.empty(((rows + block_rows - 1) // block_rows, _nblk(cols)), dtype=dtype, device=like.device)
+    _scales(t, name, rows, cols, block_rows, dtype)
+    return t
+
+
+def _work(workspace, need, like):
+    """The caller's workspace, or one allocated here when needed, and its bytes."""
     if need < 0:
         raise ValueError("sizes out of range")
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace, 0 if workspace is None else _workspace_bytes(workspace)
+    if workspace is not None:
+        return workspace, _workspace_bytes(workspace)
+    if need == 0:
+        return None, 0
+    return torch.empty(need, dtype=torch.uint8, device=like.device), need
 
 
 # ------------------------------------------------------------------ coding
@@ -135,12 +152,8 @@ def harp_quantize_q8(x, block_rows: int = 1, scale_dtype: str = "f32", codes=Non
     if block_rows not in (1, BLOCK):
         raise ValueError(f"block_rows must be 1 or {BLOCK}, got {block_rows}")
     sdt = _named(_SCALE_NAME, scale_dtype, "scale_dtype")
-    if codes is None:
-        codes = torch.empty((rows, cols), dtype=CODES, device=x.device)
-    if scales is None:
-        scales = torch.empty(((rows + block_rows - 1) // block_rows, _nblk(cols)), dtype=sdt, device=x.device)
-    ldc = _mat(codes, "codes", (CODES,), rows, cols)
-    _scales(scales, "scales", rows, cols, block_rows, sdt)
+    codes, ldc = _out_mat(codes, "codes", CODES, rows, cols, x)
+    scales = _out_scales(scales, "scales", rows, cols, block_rows, sdt, x)
     dev = _on_gpu(x, codes, scales)
     check(lib().harp_quantize_q8(_p(x), ldx, _IO[x.dtype], rows, cols, block_rows, _p(codes), ldc, _p(scales),
                                  _SCALE[sdt], _stream_of(stream, dev)))
@@ -175,27 +188,20 @@ def harp_rmsnorm_q8(x, residual=None, gamma=None, eps: float = 1e-6, scale_dtype
     if residual is None:
         if h is not None:
             raise ValueError("h goes with a residual only")
-    elif h is None:
-        h = torch.empty((rows, d), dtype=io, device=x.device)
-    ldh = _mat(h, "h", (io,), rows, d) if h is not None else d
-    if codes is None:
-        codes = torch.empty((rows, d), dtype=CODES, device=x.device)
-    if scales is None:
-        scales = torch.empty((rows, _nblk(d)), dtype=sdt, device=x.device)
-    ldc = _mat(codes, "codes", (CODES,), rows, d)
-    _scales(scales, "scales", rows, d, 1, sdt)
+        ldh = d
+    else:
+        h, ldh = _out_mat(h, "h", io, rows, d, x)
+    codes, ldc = _out_mat(codes, "codes", CODES, rows, d, x)
+    scales = _out_scales(scales, "scales", rows, d, 1, sdt, x)
     ldk = d
     if checkpoint:
         if rstd is None:
             rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-        _vec(rstd, "rstd", torch.float32, rows)
+        else:
+            _vec(rstd, "rstd", torch.float32, rows)
         if gamma is not None:
-            if ckpt_codes is None:
-                ckpt_codes = torch.empty((rows, d), dtype=CODES, device=x.device)
-            if ckpt_scales is None:
-                ckpt_scales = torch.empty((rows, _nblk(d)), dtype=sdt, device=x.device)
-            ldk = _mat(ckpt_codes, "ckpt_codes", (CODES,), rows, d)
-            _scales(ckpt_scales, "ckpt_scales", rows, d, 1, sdt)
+            ckpt_codes, ldk = _out_mat(ckpt_codes, "ckpt_codes", CODES, rows, d, x)
+            ckpt_scales = _out_scales(ckpt_scales, "ckpt_scales", rows, d, 1, sdt, x)
     elif rstd is not None:
         raise ValueError("rstd goes with checkpoint=True only")
     if (gamma is None or not checkpoint) and (ckpt_codes is not None or ckpt_scales is not None):
@@ -229,9 +235,7 @@ def harp_rmsnorm_q8_vjp(ckpt_codes, ckpt_scales, rstd, dn, gamma=None, dres=None
     if gamma is not None:
         _vec(gamma, "gamma", io, d)
     lddres = _mat(dres, "dres", (io,), rows, d) if dres is not None else d
-    if dh is None:
-        dh = torch.empty((rows, d), dtype=io, device=dn.device)
-    lddh = _mat(dh, "dh", (io,), rows, d)
+    dh, lddh = _out_mat(dh, "dh", io, rows, d, dn)
     if want_dgamma is None:
         want_dgamma = gamma is not None or dgamma is not None
     if not want_dgamma:
@@ -240,9 +244,10 @@ def harp_rmsnorm_q8_vjp(ckpt_codes, ckpt_scales, rstd, dn, gamma=None, dres=None
     else:
         if dgamma is None:
             dgamma = torch.empty(d, dtype=torch.float32, device=dn.device)
-        _vec(dgamma, "dgamma", torch.float32, d)
-        workspace, _ = _work(workspace, harp_rmsnorm_q8_vjp_workspace(rows, d), dn.device)
-    ws_bytes = 0 if workspace is None else _workspace_bytes(workspace)
+        else:
+            _vec(dgamma, "dgamma", torch.float32, d)
+    need = lib().harp_rmsnorm_q8_vjp_workspace(rows, d) if want_dgamma else 0
+    workspace, ws_bytes = _work(workspace, need, dn)
     dev = _on_gpu(dn, ckpt_codes, ckpt_scales, rstd, gamma, dres, dh, dgamma, workspace)
     check(lib().harp_rmsnorm_q8_vjp(_p(ckpt_codes), ldc, _p(ckpt_scales), _SCALE[ckpt_scales.dtype], _p(rstd),
                                     _p(gamma), _p(dn), lddn, _p(dres), lddres, _p(dh), lddh, _p(dgamma), rows, d,
@@ -268,10 +273,8 @@ def harp_matmul_q8(a_codes, a_scales, w_codes, w_scales, out: str = "bf16", y=No
     _scales(a_scales, "a_scales", rows, k, 1)
     _scales(w_scales, "w_scales", n, k, BLOCK, a_scales.dtype)
     odt = _named(_IO_NAME, out, "out")
-    if y is None:
-        y = torch.empty((rows, n), dtype=odt, device=a_codes.device)
-    ldy = _mat(y, "y", (odt,), rows, n)
-    workspace, ws_bytes = _work(workspace, harp_matmul_q8_workspace(rows, n, k), a_codes.device)
+    y, ldy = _out_mat(y, "y", odt, rows, n, a_codes)
+    workspace, ws_bytes = _work(workspace, lib().harp_matmul_q8_workspace(rows, n, k), a_codes)
     dev = _on_gpu(a_codes, a_scales, w_codes, w_scales, y, workspace)
     check(lib().harp_matmul_q8(_p(a_codes), lda, _p(a_scales), _p(w_codes), ldw, _p(w_scales),
                                _SCALE[a_scales.dtype], rows, n, k, _p(y), ldy, _IO[odt], _p(workspace), ws_bytes,
@@ -293,10 +296,8 @@ def harp_matmul_q8_wgrad(dy, x_codes, x_scales, out: str = "f32", dw=None, works
     k = x_codes.shape[1]
     _scales(x_scales, "x_scales", rows, k, 1)
     odt = _named(_IO_NAME, out, "out")
-    if dw is None:
-        dw = torch.empty((n, k), dtype=odt, device=dy.device)
-    lddw = _mat(dw, "dw", (odt,), n, k)
-    workspace, ws_bytes = _work(workspace, harp_matmul_q8_wgrad_workspace(rows, n, k), dy.device)
+    dw, lddw = _out_mat(dw, "dw", odt, n, k, dy)
+    workspace, ws_bytes = _work(workspace, lib().harp_matmul_q8_wgrad_workspace(rows, n, k), dy)
     dev = _on_gpu(dy, x_codes, x_scales, dw, workspace)
     check(lib().harp_matmul_q8_wgrad(_p(dy), lddy, _p(x_codes), ldx, _p(x_scales), _SCALE[x_scales.dtype], rows, n, k,
                                      _p(dw), lddw, _IO[odt], _p(workspace), ws_bytes, _stream_of(stream, dev)))
