@@ -217,6 +217,9 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
     const int step = kb - kb0, buf = step & 1, in = step % kChunk;
     float s[MT];
     int sb[MT];
+    // the weight's scale becomes a number here and not, with a wait for every
+    // load, in the step that asks for it
+    if constexpr (!kHwScale) asm volatile("" : "+v"(sw));
     const int swb = (int)sw;
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
