@@ -97,23 +97,26 @@ __device__ __forceinline__ float block_sum(float v, float (&part)[2][16], int se
   return row16_sum(l < nw ? part[set][l] : 0.0f);
 }
 
-// How a row is held.  One workgroup, or (rows of one block, kShort: the norms
-// of attention heads) 16 lanes, 16 rows in a workgroup of 256.
-template <bool kShort>
+// How a row is held.  One workgroup (kLanes 0), or, rows of one or two blocks
+// (the norms of attention heads), 16 or 32 lanes of a workgroup of 256.
+template <int kLanes>
 struct RowMap {
-  int tid, threads;
+  static constexpr int kRows = kLanes ? 256 / kLanes : 1;
+  int tid, threads, row;
   int64_t first, step;
   __device__ __forceinline__ RowMap() {
-    tid = kShort ? threadIdx.x & 15 : threadIdx.x;
-    threads = kShort ? 16 : blockDim.x;
-    first = kShort ? (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4) : blockIdx.x;
-    step = kShort ? (int64_t)gridDim.x * 16 : gridDim.x;
+    tid = kLanes ? threadIdx.x & (kLanes - 1) : threadIdx.x;
+    threads = kLanes ? kLanes : blockDim.x;
+    row = kLanes ? (int)threadIdx.x / kLanes : 0;
+    first = (int64_t)blockIdx.x * kRows + row;
+    step = (int64_t)gridDim.x * kRows;
   }
 };
-template <bool kShort>
+template <int kLanes>
 __device__ __forceinline__ float row_sum(float v, float (&part)[2][16], int set) {
-  if constexpr (kShort) return row16_sum(v);
-  else return block_sum(v, part, set);
+  if constexpr (kLanes == 0) return block_sum(v, part, set);
+  v = row16_sum(v);
+  return kLanes == 32 ? v + __shfl_xor(v, 16) : v;
 }
 
 // A workgroup walks over rows; a row stays in registers between the sum of
@@ -121,12 +124,13 @@ __device__ __forceinline__ float row_sum(float v, float (&part)[2][16], int set)
 // 8192, which leave registers for it) the next row is on its way meanwhile.
 // 16384 x 5120 bf16, residual, checkpoint: 674 MB in 134 us, 5.0 TB/s (175 us
 // without the next row's loads); 4096 x 16384: 93 us.  One row of 4096: 2.8 us
-// of the call's 7.4, the rest is the launch.  Rows of 64 (kShort), 100000 of
-// them: 14 us, against 46 us with a workgroup per row.
-template <typename T, int NCH, bool E8, bool kShort = false>
+// of the call's 7.4, the rest is the launch.  Rows of 64 (16 lanes each), 100000 of
+// them: 14 us, against 46 us with a workgroup per row; 60000 of 160 (32 lanes):
+// 20 us, against 39.
+template <typename T, int NCH, bool E8, int kLanes = 0>
 __global__ __launch_bounds__(NCH <= 2 ? 512 : 1024) void rmsnorm_q8_kernel(NormArgs a) {
   constexpr bool kAhead = NCH <= 2;
-  const RowMap<kShort> map;
+  const RowMap<kLanes> map;
   __shared__ float part[2][16];
   const int nblk = (a.d + kQBlk - 1) / kQBlk;
   const T* gamma = static_cast<const T*>(a.gamma);
@@ -163,7 +167,7 @@ __global__ __launch_bounds__(NCH <= 2 ? 512 : 1024) void rmsnorm_q8_kernel(NormA
       if (a.h && n[c] > 0) store8_of<T>(static_cast<T*>(a.h) + r * a.ldh + col[c], n[c], v[c]);
     }
     if (kAhead) load(r + map.step);
-    ss = row_sum<kShort>(ss, part, set);
+    ss = row_sum<kLanes>(ss, part, set);
     const float rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
     if (a.rstd && map.tid == 0) a.rstd[r] = rstd;
 #pragma unroll
@@ -203,12 +207,13 @@ __global__ __launch_bounds__(NCH <= 2 ? 512 : 1024) void rmsnorm_q8_kernel(NormA
 // longer ones read gamma and dres when they are used instead).  The partial sums of the
 // workgroups are added in order by the second kernel (6 us at 16384 x 5120; atomics would
 // change the result from run to run).  16384 x 5120 bf16 with dres, both kernels: 126 us,
-// 4.7 TB/s; 4096 x 16384: 111 us; 100000 x 64: 23 us (a workgroup per row 51).
+// 4.7 TB/s; 4096 x 16384: 111 us; 100000 x 64: 23 us (a workgroup per row 51), 60000 x 160:
+// 26 us (36).
 // Rows beyond 16384 spill: 273 us at 2234 x 30000, 3.4 times what the bytes take.
-template <typename T, int NCH, bool E8, bool kShort = false>
-__global__ __launch_bounds__(kShort ? 256 : 1024) void rmsnorm_q8_vjp_kernel(NormVjpArgs a) {
+template <typename T, int NCH, bool E8, int kLanes = 0>
+__global__ __launch_bounds__(kLanes ? 256 : 1024) void rmsnorm_q8_vjp_kernel(NormVjpArgs a) {
   constexpr bool kAhead = NCH == 1;
-  const RowMap<kShort> map;
+  const RowMap<kLanes> map;
   __shared__ float part[2][16];
   const int nblk = (a.d + kQBlk - 1) / kQBlk;
   int col[NCH], n[NCH];
@@ -271,7 +276,7 @@ __global__ __launch_bounds__(kShort ? 256 : 1024) void rmsnorm_q8_vjp_kernel(Nor
         dot += u * g[c][j] * xn[j];
       }
     }
-    const float mean = row_sum<kShort>(dot, part, set) / (float)a.d;
+    const float mean = row_sum<kLanes>(dot, part, set) / (float)a.d;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       if (n[c] <= 0) continue;
@@ -288,15 +293,15 @@ __global__ __launch_bounds__(kShort ? 256 : 1024) void rmsnorm_q8_vjp_kernel(Nor
     }
     if (kAhead) now = next;
   }
-  if constexpr (kShort) {
-    // the 16 rows' shares in order
-    __shared__ float share[16][129];
+  if constexpr (kLanes > 0) {
+    // the rows' shares in order
+    __shared__ float share[256 / kLanes][kLanes * 8 + 1];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) share[threadIdx.x >> 4][map.tid * 8 + j] = dg[0][j];
+    for (int j = 0; j < 8; ++j) share[map.row][map.tid * 8 + j] = dg[0][j];
     __syncthreads();
     if (a.partial && (int)threadIdx.x < a.d) {
       float t = 0.0f;
-      for (int i = 0; i < 16; ++i) t += share[i][threadIdx.x];
+      for (int i = 0; i < 256 / kLanes; ++i) t += share[i][threadIdx.x];
       a.partial[(int64_t)blockIdx.x * a.d + threadIdx.x] = t;
     }
   } else if (a.partial) {
@@ -331,14 +336,21 @@ __global__ __launch_bounds__(1024) void dgamma_kernel(const float* __restrict__ 
 // Threads for a row of d values with nch chunks of 8 each: whole waves.
 int row_threads(int d, int nch) { return ((d + 7) / 8 + nch * 64 - 1) / (nch * 64) * 64; }
 
+// Workgroups for rows of one or two blocks.
+int short_groups(int64_t rows, int64_t d) {
+  const int64_t per = d <= kQBlk ? 16 : 8;
+  return (int)std::min((rows + per - 1) / per, (int64_t)2048);
+}
+
 // Chunks per thread of the norm: two from 4096 on (16384 x 5120 bf16 with a
 // checkpoint: one chunk 165 us, two 134 us; a row of 4096 is then 8 waves or
 // 4, and one row alone is faster with 8).
 template <typename T, bool E8>
 hipError_t norm_go(const NormArgs& a, hipStream_t stream) {
-  if (a.d <= kQBlk) {
-    const dim3 grid((unsigned)std::min((a.rows + 15) / 16, (int64_t)2048));
-    hipLaunchKernelGGL((rmsnorm_q8_kernel<T, 1, E8, true>), grid, dim3(256), 0, stream, a);
+  if (a.d <= 2 * kQBlk) {
+    const dim3 grid(short_groups(a.rows, a.d));
+    if (a.d <= kQBlk) hipLaunchKernelGGL((rmsnorm_q8_kernel<T, 1, E8, 16>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((rmsnorm_q8_kernel<T, 1, E8, 32>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
   }
   const int nch = a.d <= 4096 ? 1 : a.d <= 8192 ? 2 : 4, threads = row_threads(a.d, nch);
@@ -356,7 +368,7 @@ hipError_t norm_go(const NormArgs& a, hipStream_t stream) {
 // 127 us, 1024 135 us; two chunks per thread 186 us, for want of registers).
 int vjp_chunks(int64_t d) { return d <= 8192 ? 1 : d <= 16384 ? 2 : 4; }
 int vjp_groups(int64_t rows, int64_t d) {
-  if (d <= kQBlk) return (int)std::min((rows + 15) / 16, (int64_t)2048);
+  if (d <= 2 * kQBlk) return short_groups(rows, d);
   const int threads = row_threads((int)d, vjp_chunks(d));
   return (int)std::min(rows, 256 * (int64_t)std::min(8, std::max(2, 1024 / threads)));
 }
@@ -366,7 +378,8 @@ hipError_t norm_vjp_go(const NormVjpArgs& a, hipStream_t stream) {
   const int groups = vjp_groups(a.rows, a.d), nch = vjp_chunks(a.d), threads = row_threads(a.d, nch);
   if (groups > 0) {
     const dim3 grid(groups);
-    if (a.d <= kQBlk) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 1, E8, true>), grid, dim3(256), 0, stream, a);
+    if (a.d <= kQBlk) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 1, E8, 16>), grid, dim3(256), 0, stream, a);
+    else if (a.d <= 2 * kQBlk) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 1, E8, 32>), grid, dim3(256), 0, stream, a);
     else if (nch == 1) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 1, E8>), grid, dim3(threads), 0, stream, a);
     else if (nch == 2) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 2, E8>), grid, dim3(threads), 0, stream, a);
     else hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 4, E8>), grid, dim3(threads), 0, stream, a);

@@ -194,7 +194,8 @@ def check_coded(codes, scales, want, kind):
 @pytest.mark.parametrize("rows,d,gamma,residual,ckpt", [
     (1, 4096, False, True, False), (5, 1, True, True, True), (3, 130, True, False, True), (70, 4099, True, True, True),
     (33, 5120, False, True, True), (2, 20001, True, True, True), (1000, 64, True, True, True), (35, 128, True, False, True),
-    (2, 9001, True, True, True), (2, 32768, False, False, True), (9, 512, True, True, False)])
+    (2, 9001, True, True, True), (2, 32768, False, False, True), (9, 512, True, True, False),
+    (17001, 200, True, True, True), (9, 256, False, True, True), (3, 129, True, False, False)])
 def test_rmsnorm(rows, d, gamma, residual, ckpt, io, kind):
     say("rmsnorm", rows, d, gamma, residual, ckpt, io, kind)
     rng = np.random.default_rng(rows + d)
@@ -262,7 +263,8 @@ def coded(rng, x, kind):
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,d,gamma,dres", [(1, 4096, True, True), (1, 1, True, False), (1500, 130, True, True),
                                                (37, 4099, False, True), (3, 20001, True, True), (40000, 64, True, True),
-                                               (33, 128, True, False), (5, 9001, True, True), (2, 32768, True, False)])
+                                               (33, 128, True, False), (5, 9001, True, True), (2, 32768, True, False),
+                                               (17001, 200, True, True), (9, 256, True, False), (3, 129, False, True)])
 def test_rmsnorm_vjp(rows, d, gamma, dres, io, kind):
     say("rmsnorm_vjp", rows, d, gamma, dres, io, kind)
     rng = np.random.default_rng(rows + 3 * d)
@@ -487,11 +489,13 @@ def test_wgrad_far_rows(kind):
 
 WGRAD = [(1, 1, 1), (1, 300, 130), (31, 128, 128), (32, 64, 640), (33, 129, 127), (100, 500, 272), (257, 260, 515),
          (1000, 384, 256), (1500, 1030, 400), (5000, 64, 80), (4097, 16, 130)]
+# more than 256 tiles: the large tile for some formats, the small one for others
+WGRAD_LARGE = [(100, 4096, 2048), (70, 2111, 4200), (65, 2048, 2304)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "e8m0"])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,n,k", WGRAD)
+@pytest.mark.parametrize("rows,n,k", WGRAD + WGRAD_LARGE)
 def test_wgrad(rows, n, k, out, kind):
     say("wgrad", rows, n, k, out, kind)
     rng = np.random.default_rng(rows + 5 * n + 11 * k)
