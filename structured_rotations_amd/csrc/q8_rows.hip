@@ -207,8 +207,8 @@ __global__ __launch_bounds__(NCH <= 2 ? 512 : 1024) void rmsnorm_q8_kernel(NormA
 // longer ones read gamma and dres when they are used instead).  The partial sums of the
 // workgroups are added in order by the second kernel (6 us at 16384 x 5120; atomics would
 // change the result from run to run).  16384 x 5120 bf16 with dres, both kernels: 126 us,
-// 4.7 TB/s; 4096 x 16384: 111 us; 100000 x 64: 23 us (a workgroup per row 51), 60000 x 160:
-// 26 us (36).
+// 4.7 TB/s; 4096 x 16384: 111 us; 100000 x 64: 17 us (a workgroup per row 51), 60000 x 160:
+// 19 us (36).
 // Rows beyond 16384 spill: 273 us at 2234 x 30000, 3.4 times what the bytes take.
 template <typename T, int NCH, bool E8, int kLanes = 0>
 __global__ __launch_bounds__(kLanes ? 256 : 1024) void rmsnorm_q8_vjp_kernel(NormVjpArgs a) {
@@ -363,23 +363,37 @@ hipError_t norm_go(const NormArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Workgroups of the backward pass: each writes a row of partial sums, so no
-// more than keep the compute units busy (16384 x 5120: 512 of 640 threads
-// 127 us, 1024 135 us; two chunks per thread 186 us, for want of registers).
+// Chunks per thread of the backward pass (16384 x 5120: two 186 us against 127,
+// for want of registers).
 int vjp_chunks(int64_t d) { return d <= 8192 ? 1 : d <= 16384 ? 2 : 4; }
+// Lanes of a row, 0: a workgroup.  Up to 64 rows of two blocks take a workgroup
+// each (16 rows of 256: 4.84 us against 5.01; 256 rows: 5.99 against 5.25).
+int vjp_lanes(int64_t rows, int64_t d) { return d <= kQBlk ? 16 : d <= 2 * kQBlk && rows > 64 ? 32 : 0; }
+// Workgroups of the backward pass.  Each writes a row of partial sums, which the
+// second kernel reads with d / 16 workgroups, so no more than keep the compute
+// units busy: about 512 threads each (1000 values x 30000 rows: 42 us, with 1024
+// threads 48), 1024 where rows are no whole pieces of 8 and take more
+// instructions (999 x 30000: 86 us, with 512 threads 124), with 8 or 4 rows
+// for each workgroup (1000 x 2048: 11.4 us, 21.6 with one).  16384 x 5120: 512
+// workgroups 127 us, 1024 135 us.  Rows of one or two blocks, 16 or 8 at a time:
+// 512 (200 x 30000: 14 us, 2048 workgroups 21).
 int vjp_groups(int64_t rows, int64_t d) {
-  if (d <= 2 * kQBlk) return short_groups(rows, d);
+  if (vjp_lanes(rows, d)) return std::min(short_groups(rows, d), 512);
   const int threads = row_threads((int)d, vjp_chunks(d));
-  return (int)std::min(rows, 256 * (int64_t)std::min(8, std::max(2, 1024 / threads)));
+  const bool whole = d % 8 == 0;
+  const int per_unit = whole ? (512 + threads - 1) / threads : 1024 / threads;
+  const int64_t most = 256 * (int64_t)std::min(8, std::max(2, per_unit));
+  return (int)std::min(rows, std::max<int64_t>(512, std::min(rows / (whole ? 8 : 4), most)));
 }
 
 template <typename T, bool E8>
 hipError_t norm_vjp_go(const NormVjpArgs& a, hipStream_t stream) {
   const int groups = vjp_groups(a.rows, a.d), nch = vjp_chunks(a.d), threads = row_threads(a.d, nch);
+  const int lanes = vjp_lanes(a.rows, a.d);
   if (groups > 0) {
     const dim3 grid(groups);
-    if (a.d <= kQBlk) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 1, E8, 16>), grid, dim3(256), 0, stream, a);
-    else if (a.d <= 2 * kQBlk) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 1, E8, 32>), grid, dim3(256), 0, stream, a);
+    if (lanes == 16) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 1, E8, 16>), grid, dim3(256), 0, stream, a);
+    else if (lanes == 32) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 1, E8, 32>), grid, dim3(256), 0, stream, a);
     else if (nch == 1) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 1, E8>), grid, dim3(threads), 0, stream, a);
     else if (nch == 2) hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 2, E8>), grid, dim3(threads), 0, stream, a);
     else hipLaunchKernelGGL((rmsnorm_q8_vjp_kernel<T, 4, E8>), grid, dim3(threads), 0, stream, a);
