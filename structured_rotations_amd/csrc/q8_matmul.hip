@@ -422,7 +422,10 @@ __global__ __launch_bounds__(512) void matmul_big_kernel(MatmulArgs g, int tiles
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    s[2] = s[3] = 0.0f;  // what the last tile left in p has been added
+    // what the last tile left in p has been added; the first step adds it again
+    // times s, and a NaN in it would come through a zero s
+    p[2] = p[3] = f32x4{0, 0, 0, 0};
+    s[2] = s[3] = 0.0f;
     auto step = [&](int kb) {
       const int k1 = kb + 1 < nkb ? kb + 1 : 0, k2 = kb + 2 < nkb ? kb + 2 : kb + 2 - nkb;
       const TileSrc wn1 = kb + 1 < nkb ? w0 : w1, an2 = kb + 2 < nkb ? a0 : a1, wn2 = kb + 2 < nkb ? w0 : w1,
