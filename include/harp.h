@@ -427,10 +427,12 @@ harp_status harp_matmul_q8(const uint8_t* a, int64_t lda, const void* a_scales,
  * dy rows x n (BF16, row stride lddy), x coded rows x k (1 x 128 blocks), dw
  * n x k, F32 or BF16 (rounded once), overwritten.  Sums in fp32, in a fixed
  * order.  With E8M0 scales every product is exact.  With fp32 scales x is
- * multiplied as a sum of bf16 parts: of three (24 significant bits) for F32 dw;
- * for BF16 dw of two up to 64 rows and of one, x rounded once, above. workspace:
- * harp_matmul_q8_wgrad_workspace() bytes (may be 0; -1 for sizes out of
- * range), 16-byte aligned.  n, k >= 1; rows == 0 writes zeros. */
+ * multiplied as a sum of bf16 parts of its own sign: of three (24 significant
+ * bits) for F32 dw; for BF16 dw of two up to 64 rows and of one, x rounded once,
+ * above (a value beyond 3.39e38 rounds to an infinity there).  Infinities in dy
+ * or x, and products that overflow, give what the formula gives.
+ * workspace: harp_matmul_q8_wgrad_workspace() bytes (may be 0; -1 for sizes out
+ * of range), 16-byte aligned.  n, k >= 1; rows == 0 writes zeros. */
 int64_t harp_matmul_q8_wgrad_workspace(int64_t rows, int64_t n, int64_t k);
 harp_status harp_matmul_q8_wgrad(const void* dy, int64_t lddy, const uint8_t* x,
                                  int64_t ldx, const void* x_scales,

@@ -87,6 +87,31 @@ __device__ __forceinline__ void settle() {
   if constexpr (kAcc) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
 }
 
+// Two values as PARTS bf16 parts each, handed to put(part, pair).  Parts are
+// cut off towards zero and the last one is rounded, so all have the value's
+// sign and none overflows; what a cut leaves is exact, and three parts hold all
+// 24 bits.  Every part is multiplied by dy on its own, and dy may be infinite or
+// its first product overflow: a later part of the other sign, or 0, would make a
+// NaN of that.  So what is left of a value v is brought between +-2^-126 (v
+// itself if that is nearer to 0) and v, which adds at most 2^-126 times dy to an
+// exact value; also after an infinity, whose rest is NaN, which the median
+// leaves out.
+template <int PARTS, typename F>
+__device__ __forceinline__ void split_parts(float va, float vb, F put) {
+  if constexpr (PARTS == 1) return put(0, pack_bf16x2_hw(va, vb));
+  const float least_a = __builtin_amdgcn_fmed3f(va, 0x1p-126f, -0x1p-126f);
+  const float least_b = __builtin_amdgcn_fmed3f(vb, 0x1p-126f, -0x1p-126f);
+  float a = va, b = vb;
+#pragma unroll
+  for (int t = 0; t < PARTS - 1; ++t) {
+    const uint32_t w = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
+    put(t, w);
+    a = __builtin_amdgcn_fmed3f(a - bf16_lo(w), least_a, va);
+    b = __builtin_amdgcn_fmed3f(b - bf16_hi(w), least_b, vb);
+  }
+  put(PARTS - 1, pack_bf16x2_hw(a, b));
+}
+
 // One tile of dw per workgroup of 4 waves, each 16 NI (k) by 16 NJ (n) of it;
 // PARTS: bf16 parts of x.  Per step of 64 rows a wave multiplies from
 // registers (the fragments of half a step), while it
@@ -207,16 +232,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
         float v[4];
         dec4(rx[set][u][c], v);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float a = v[2 * e] * s, b = v[2 * e + 1] * s;
-#pragma unroll
-          for (int t = 0; t < PARTS; ++t) {  // what the parts before left is exact
-            const uint32_t w = pack_bf16x2_hw(a, b);
-            xw[t][c >> 1][2 * (c & 1) + e] = w;
-            a -= bf16_lo(w);
-            b -= bf16_hi(w);
-          }
-        }
+        for (int e = 0; e < 2; ++e) split_parts<PARTS>(v[2 * e] * s, v[2 * e + 1] * s, [&](int t, uint32_t w) {
+          xw[t][c >> 1][2 * (c & 1) + e] = w;
+        });
       }
       return;
     }

@@ -9,7 +9,7 @@ import torch
 
 import structured_rotations_amd as H
 from oracle import q8_oracle as Q
-from tests.test_gpu_q8 import TOL, np64, operands, rel_rows, say, to_codes, to_scales
+from tests.test_gpu_q8 import IO, TOL, np64, operands, rel_rows, say, to_codes, to_scales
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,57 @@ def test_matmul_nan_stays_in_its_tile(kind):
     cols = np.r_[0:1024, 1152:n]
     want = Q.matmul(ac[ok], as_[ok], wc, np.where(np.isnan(ws), 0, ws))
     assert rel_rows(got[np.ix_(ok, cols)], want[:, cols]) <= TOL["bf16"]
+
+
+# --------------------------------------------------------- weight gradient
+def same_specials(got, want, out):
+    """NaNs and infinities where the formula in fp64, rounded to the result's type, has them."""
+    want = np64(torch.from_numpy(want).float().to(IO[out]))
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(got == np.inf, want == np.inf) and np.array_equal(got == -np.inf, want == -np.inf)
+
+
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,n,k", [(40, 144, 272), (200, 144, 272), (90, 77, 301), (70, 4096, 2304)])
+def test_wgrad_infinite_gradients(rows, n, k, out, kind):
+    say("wgrad infinities", rows, n, k, out, kind)
+    rng = np.random.default_rng(61)
+    xc, xs = Q.quantize(rng.standard_normal((rows, k)), 1, kind)
+    dy = torch.from_numpy(rng.standard_normal((rows, n)).astype(np.float32)).to(torch.bfloat16)
+    dy[5, 7], dy[6, 20], dy[38, 30], dy[39, 30] = float("inf"), float("-inf"), float("inf"), float("inf")
+    xc[5, 3] = 0                                                  # inf * 0: a NaN by the formula, too
+    with np.errstate(invalid="ignore"):
+        want = Q.wgrad(np64(dy), xc, xs)
+    got = np64(H.harp_matmul_q8_wgrad(dy.cuda(), to_codes(xc), to_scales(xs, kind), out))
+    assert np.isnan(want).sum() >= 1 and np.isinf(want).sum() >= 2 * k - 2
+    same_specials(got, want, out)
+    ok = np.setdiff1d(np.arange(n), (7, 20, 30))
+    assert rel_rows(got[ok], want[ok]) <= TOL[out] * (1.5 if out == "bf16" and kind == "f32" else 1.0)
+
+
+@pytest.mark.parametrize("out,rows", [("f32", 40), ("f32", 200), ("bf16", 40)])
+def test_wgrad_ends_of_the_range(out, rows):
+    # values next to fp32's largest, infinite scales, and products that leave the range in the first part of a value
+    say("wgrad range", out, rows)
+    rng = np.random.default_rng(62)
+    n, k = 48, 400
+    xc, xs = Q.quantize(rng.standard_normal((rows, k)), 1, "f32")
+    dy = np.zeros((rows, n), dtype=np.float32)
+    dy[:, :16] = rng.standard_normal((rows, 16)) * 2.0 ** -30
+    xs[:, 0] = 3.4e38 / 448
+    xc[3, :128] = 0x7e                                            # 3.4e38
+    dy[11, 20] = 2.0 ** 126
+    xs[11, 1] = 0.3
+    xc[11, 128:256] = rng.integers(0x58, 0x7f, 128)               # 16 .. 448, times 0.3: no bf16 values
+    xs[12, 2] = np.inf
+    xc[12, 256:384] = np.where(rng.random(128) < 0.5, 0x38, 0xb8)
+    dy[12, 5], dy[12, 30] = 1.0, -1.0
+    dyt = torch.from_numpy(dy).to(torch.bfloat16)
+    with np.errstate(invalid="ignore"):
+        want = Q.wgrad(np64(dyt), xc, xs)
+    got = np64(H.harp_matmul_q8_wgrad(dyt.cuda(), to_codes(xc), to_scales(xs, "f32"), out))
+    same_specials(got, want, out)
+    keep = np.r_[0:5, 6:16]
+    assert rel_rows(got[keep, :256], want[keep, :256]) <= TOL[out]
+    assert (want[20, 128:256] > 3.41e38).all() and np.isfinite(want[:5, :256]).all()
