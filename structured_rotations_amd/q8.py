@@ -6,6 +6,11 @@ and one scale per block of 128 columns, torch.float32 or (powers of two)
 torch.float8_e8m0fnu.  Rows are coded in blocks of 1 x 128, weights in blocks
 of 128 x 128.  Argument marshalling only, with the rules of api.py: every
 check runs first, the GPU check last, then one library call.
+
+stream: the stream that the work goes to (None: the current one).  The caller
+makes it wait for the inputs, and the readers of the results for it; memory is
+safe either way: results and workspaces made here belong to that stream, and
+every tensor may be dropped as soon as the call returns.
 """
 from __future__ import annotations
 
@@ -16,6 +21,7 @@ import torch
 from . import _lib
 from .api import _workspace_bytes
 from ._lib import check, lib
+from ._streams import new, stream_of
 
 BLOCK = 128
 CODES = torch.float8_e4m3fn
@@ -99,39 +105,26 @@ def _on_gpu(*tensors):
     return dev
 
 
-def _stream_of(stream, dev):
-    """The given stream's handle, or that of the current stream."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _current_stream(dev)
-
-
-# torch's own short way to the handle, where this build has it (a decoding step
-# is a few calls of 5 us each; the Stream object alone costs 1 us)
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _out_mat(t, name, dtype, rows, cols, like):
+def _out_mat(t, name, dtype, rows, cols, like, stream):
     """The caller's result matrix, checked, or a new one beside `like`: it and
     its leading dimension."""
     if t is None:
-        return torch.empty((rows, cols), dtype=dtype, device=like.device), cols
+        return new((rows, cols), dtype, like, stream), cols
     return t, _mat(t, name, (dtype,), rows, cols)
 
 
-def _out_scales(t, name, rows, cols, block_rows, dtype, like):
+def _out_scales(t, name, rows, cols, block_rows, dtype, like, stream):
     if t is None:
-        return torch.empty(((rows + block_rows - 1) // block_rows, _nblk(cols)), dtype=dtype, device=like.device)
+        return new(((rows + block_rows - 1) // block_rows, _nblk(cols)), dtype, like, stream)
     _scales(t, name, rows, cols, block_rows, dtype)
     return t
 
 
-def _work(workspace, need, like):
+def _work(workspace, need, like, stream):
     """The caller's workspace, or one allocated here when needed, and its bytes."""
     if need < 0:
         raise ValueError("sizes out of range")
@@ -139,7 +132,7 @@ def _work(workspace, need, like):
         return workspace, _workspace_bytes(workspace)
     if need == 0:
         return None, 0
-    return torch.empty(need, dtype=torch.uint8, device=like.device), need
+    return new(need, torch.uint8, like, stream), need
 
 
 # ------------------------------------------------------------------ coding
@@ -152,11 +145,12 @@ def harp_quantize_q8(x, block_rows: int = 1, scale_dtype: str = "f32", codes=Non
     if block_rows not in (1, BLOCK):
         raise ValueError(f"block_rows must be 1 or {BLOCK}, got {block_rows}")
     sdt = _named(_SCALE_NAME, scale_dtype, "scale_dtype")
-    codes, ldc = _out_mat(codes, "codes", CODES, rows, cols, x)
-    scales = _out_scales(scales, "scales", rows, cols, block_rows, sdt, x)
-    dev = _on_gpu(x, codes, scales)
+    codes, ldc = _out_mat(codes, "codes", CODES, rows, cols, x, stream)
+    scales = _out_scales(scales, "scales", rows, cols, block_rows, sdt, x, stream)
+    tensors = (x, codes, scales)
+    dev = _on_gpu(*tensors)
     check(lib().harp_quantize_q8(_p(x), ldx, _IO[x.dtype], rows, cols, block_rows, _p(codes), ldc, _p(scales),
-                                 _SCALE[sdt], _stream_of(stream, dev)))
+                                 _SCALE[sdt], stream_of(stream, dev, tensors)))
     return codes, scales
 
 
@@ -190,26 +184,27 @@ def harp_rmsnorm_q8(x, residual=None, gamma=None, eps: float = 1e-6, scale_dtype
             raise ValueError("h goes with a residual only")
         ldh = d
     else:
-        h, ldh = _out_mat(h, "h", io, rows, d, x)
-    codes, ldc = _out_mat(codes, "codes", CODES, rows, d, x)
-    scales = _out_scales(scales, "scales", rows, d, 1, sdt, x)
+        h, ldh = _out_mat(h, "h", io, rows, d, x, stream)
+    codes, ldc = _out_mat(codes, "codes", CODES, rows, d, x, stream)
+    scales = _out_scales(scales, "scales", rows, d, 1, sdt, x, stream)
     ldk = d
     if checkpoint:
         if rstd is None:
-            rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+            rstd = new(rows, torch.float32, x, stream)
         else:
             _vec(rstd, "rstd", torch.float32, rows)
         if gamma is not None:
-            ckpt_codes, ldk = _out_mat(ckpt_codes, "ckpt_codes", CODES, rows, d, x)
-            ckpt_scales = _out_scales(ckpt_scales, "ckpt_scales", rows, d, 1, sdt, x)
+            ckpt_codes, ldk = _out_mat(ckpt_codes, "ckpt_codes", CODES, rows, d, x, stream)
+            ckpt_scales = _out_scales(ckpt_scales, "ckpt_scales", rows, d, 1, sdt, x, stream)
     elif rstd is not None:
         raise ValueError("rstd goes with checkpoint=True only")
     if (gamma is None or not checkpoint) and (ckpt_codes is not None or ckpt_scales is not None):
         raise ValueError("ckpt_codes and ckpt_scales go with gamma and checkpoint=True only")
-    dev = _on_gpu(x, residual, gamma, h, codes, scales, rstd, ckpt_codes, ckpt_scales)
+    tensors = (x, residual, gamma, h, codes, scales, rstd, ckpt_codes, ckpt_scales)
+    dev = _on_gpu(*tensors)
     check(lib().harp_rmsnorm_q8(_p(x), ldx, _p(residual), ldr, _p(gamma), eps, _p(h), ldh, _p(codes), ldc, _p(scales),
                                 _p(rstd), _p(ckpt_codes), ldk, _p(ckpt_scales), _SCALE[sdt], rows, d, _IO[io],
-                                _stream_of(stream, dev)))
+                                stream_of(stream, dev, tensors)))
     if checkpoint and gamma is None:
         ckpt_codes, ckpt_scales = codes, scales
     return RmsnormQ8(codes, scales, x if h is None else h, rstd, ckpt_codes, ckpt_scales)
@@ -235,7 +230,7 @@ def harp_rmsnorm_q8_vjp(ckpt_codes, ckpt_scales, rstd, dn, gamma=None, dres=None
     if gamma is not None:
         _vec(gamma, "gamma", io, d)
     lddres = _mat(dres, "dres", (io,), rows, d) if dres is not None else d
-    dh, lddh = _out_mat(dh, "dh", io, rows, d, dn)
+    dh, lddh = _out_mat(dh, "dh", io, rows, d, dn, stream)
     if want_dgamma is None:
         want_dgamma = gamma is not None or dgamma is not None
     if not want_dgamma:
@@ -243,15 +238,16 @@ def harp_rmsnorm_q8_vjp(ckpt_codes, ckpt_scales, rstd, dn, gamma=None, dres=None
             raise ValueError("dgamma goes with want_dgamma")
     else:
         if dgamma is None:
-            dgamma = torch.empty(d, dtype=torch.float32, device=dn.device)
+            dgamma = new(d, torch.float32, dn, stream)
         else:
             _vec(dgamma, "dgamma", torch.float32, d)
     need = lib().harp_rmsnorm_q8_vjp_workspace(rows, d) if want_dgamma else 0
-    workspace, ws_bytes = _work(workspace, need, dn)
-    dev = _on_gpu(dn, ckpt_codes, ckpt_scales, rstd, gamma, dres, dh, dgamma, workspace)
+    workspace, ws_bytes = _work(workspace, need, dn, stream)
+    tensors = (dn, ckpt_codes, ckpt_scales, rstd, gamma, dres, dh, dgamma, workspace)
+    dev = _on_gpu(*tensors)
     check(lib().harp_rmsnorm_q8_vjp(_p(ckpt_codes), ldc, _p(ckpt_scales), _SCALE[ckpt_scales.dtype], _p(rstd),
                                     _p(gamma), _p(dn), lddn, _p(dres), lddres, _p(dh), lddh, _p(dgamma), rows, d,
-                                    _IO[io], _p(workspace), ws_bytes, _stream_of(stream, dev)))
+                                    _IO[io], _p(workspace), ws_bytes, stream_of(stream, dev, tensors)))
     return dh, dgamma
 
 
@@ -273,12 +269,13 @@ def harp_matmul_q8(a_codes, a_scales, w_codes, w_scales, out: str = "bf16", y=No
     _scales(a_scales, "a_scales", rows, k, 1)
     _scales(w_scales, "w_scales", n, k, BLOCK, a_scales.dtype)
     odt = _named(_IO_NAME, out, "out")
-    y, ldy = _out_mat(y, "y", odt, rows, n, a_codes)
-    workspace, ws_bytes = _work(workspace, lib().harp_matmul_q8_workspace(rows, n, k), a_codes)
-    dev = _on_gpu(a_codes, a_scales, w_codes, w_scales, y, workspace)
+    y, ldy = _out_mat(y, "y", odt, rows, n, a_codes, stream)
+    workspace, ws_bytes = _work(workspace, lib().harp_matmul_q8_workspace(rows, n, k), a_codes, stream)
+    tensors = (a_codes, a_scales, w_codes, w_scales, y, workspace)
+    dev = _on_gpu(*tensors)
     check(lib().harp_matmul_q8(_p(a_codes), lda, _p(a_scales), _p(w_codes), ldw, _p(w_scales),
                                _SCALE[a_scales.dtype], rows, n, k, _p(y), ldy, _IO[odt], _p(workspace), ws_bytes,
-                               _stream_of(stream, dev)))
+                               stream_of(stream, dev, tensors)))
     return y
 
 
@@ -296,9 +293,10 @@ def harp_matmul_q8_wgrad(dy, x_codes, x_scales, out: str = "f32", dw=None, works
     k = x_codes.shape[1]
     _scales(x_scales, "x_scales", rows, k, 1)
     odt = _named(_IO_NAME, out, "out")
-    dw, lddw = _out_mat(dw, "dw", odt, n, k, dy)
-    workspace, ws_bytes = _work(workspace, lib().harp_matmul_q8_wgrad_workspace(rows, n, k), dy)
-    dev = _on_gpu(dy, x_codes, x_scales, dw, workspace)
+    dw, lddw = _out_mat(dw, "dw", odt, n, k, dy, stream)
+    workspace, ws_bytes = _work(workspace, lib().harp_matmul_q8_wgrad_workspace(rows, n, k), dy, stream)
+    tensors = (dy, x_codes, x_scales, dw, workspace)
+    dev = _on_gpu(*tensors)
     check(lib().harp_matmul_q8_wgrad(_p(dy), lddy, _p(x_codes), ldx, _p(x_scales), _SCALE[x_scales.dtype], rows, n, k,
-                                     _p(dw), lddw, _IO[odt], _p(workspace), ws_bytes, _stream_of(stream, dev)))
+                                     _p(dw), lddw, _IO[odt], _p(workspace), ws_bytes, stream_of(stream, dev, tensors)))
     return dw

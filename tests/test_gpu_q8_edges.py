@@ -92,3 +92,29 @@ def test_wgrad_ends_of_the_range(out, rows):
     keep = np.r_[0:5, 6:16]
     assert rel_rows(got[keep, :256], want[keep, :256]) <= TOL[out]
     assert (want[20, 128:256] > 3.41e38).all() and np.isfinite(want[:5, :256]).all()
+
+
+# ----------------------------------------------------------------- streams
+def test_memory_of_a_call_on_another_stream():
+    # while the call's stream is busy, the current stream gets none of the call's memory, dropped or not
+    say("memory of another stream")
+    rng = np.random.default_rng(71)
+    rows, n, k = 128, 128, 4096
+    (ac, as_), (wc, ws) = operands(rng, rows, n, k, "f32")
+    args = to_codes(ac), to_scales(as_, "f32"), to_codes(wc), to_scales(ws, "f32")
+    need = H.harp_matmul_q8_workspace(rows, n, k)
+    assert need > 0
+    want = H.harp_matmul_q8(*args, "f32")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)                         # about 10 ms
+        y = H.harp_matmul_q8(*args, "f32", stream=side)
+        dropped = H.harp_matmul_q8(*args, "f32", stream=side).data_ptr()
+        others = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        others += [torch.full((rows, n), float("nan"), device="cuda") for _ in range(4)]
+        assert dropped not in [t.data_ptr() for t in others]
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(y, want)
+        assert all(torch.all(t == 255) for t in others[:4]) and all(torch.isnan(t).all() for t in others[4:])

@@ -1,0 +1,105 @@
+"""Host-side tests (no GPU needed) of what a call with an explicit stream does
+with memory: everything it makes is allocated on that stream, and the allocator
+is told that the stream and the current one use the call's tensors.
+
+Meta tensors take the GPU ones' place, and recorders the library's and torch's.
+"""
+import contextlib
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from structured_rotations_amd import q8
+
+E4 = torch.float8_e4m3fn
+
+
+_empty = torch.empty
+
+
+def meta(*shape, dtype=torch.float32):
+    return _empty(shape, dtype=dtype, device="meta")
+
+
+class _Lib:
+    """The real library's size helpers; every entry point succeeds."""
+
+    def __init__(self, real):
+        self._real = real
+
+    def __getattr__(self, name):
+        return getattr(self._real, name) if name.endswith("_workspace") else lambda *a: 0
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    log = SimpleNamespace(active=None, made=[], recorded=[])
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, log.active = log.active, stream
+        yield
+        log.active = before
+
+    def logged(*a, **k):
+        t = _empty(*a, **k)
+        log.made.append((t, log.active))
+        return t
+
+    real = q8.lib()
+    here = SimpleNamespace(cuda_stream=7)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: here)
+    monkeypatch.setattr(torch, "empty", logged)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: log.recorded.append((t, s)))
+    monkeypatch.setattr(q8, "lib", lambda: _Lib(real))
+    monkeypatch.setattr(q8, "_on_gpu", lambda *t: 0)
+    log.here = here
+    return log
+
+
+def quantize(stream):
+    x = meta(200, 300)
+    return (x,), q8.harp_quantize_q8(x, stream=stream), 2
+
+
+def norm(stream):
+    x, g = meta(200, 300), meta(300)
+    return (x, g), q8.harp_rmsnorm_q8(x, x, g, checkpoint=True, stream=stream), 6
+
+
+def norm_vjp(stream):
+    dn, c, s, r = meta(200, 300), meta(200, 300, dtype=E4), meta(200, 3), meta(200)
+    return (dn, c, s, r), q8.harp_rmsnorm_q8_vjp(c, s, r, dn, want_dgamma=True, stream=stream), 3
+
+
+def matmul(stream):
+    a, sa, w, sw = meta(128, 4096, dtype=E4), meta(128, 32), meta(128, 4096, dtype=E4), meta(1, 32)
+    return (a, sa, w, sw), (q8.harp_matmul_q8(a, sa, w, sw, stream=stream),), 2
+
+
+def wgrad(stream):
+    dy, x, s = meta(4096, 128, dtype=torch.bfloat16), meta(4096, 128, dtype=E4), meta(4096, 1)
+    return (dy, x, s), (q8.harp_matmul_q8_wgrad(dy, x, s, stream=stream),), 2
+
+
+CALLS = [quantize, norm, norm_vjp, matmul, wgrad]
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_an_explicit_stream_allocates_and_is_recorded(calls, call):
+    s = SimpleNamespace(cuda_stream=99)
+    inputs, outputs, made = call(s)
+    assert len(calls.made) == made                                # results, and a workspace where one is needed
+    assert all(active is s for _, active in calls.made)
+    told = {(id(t), st.cuda_stream) for t, st in calls.recorded}
+    for t in [*inputs, *outputs, *(t for t, _ in calls.made)]:
+        assert (id(t), 99) in told and (id(t), 7) in told
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_the_current_stream_needs_no_record(calls, call):
+    call(calls.here)
+    assert not calls.recorded
+    assert all(active is calls.here for _, active in calls.made)
