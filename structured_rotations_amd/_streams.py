@@ -1,15 +1,18 @@
-"""Streams and memory of a call: which stream allocates what the call makes,
-and which streams the allocator has to wait for before it gives the memory of
-the call's tensors to others.
+"""Streams, devices and memory of a call: which GPU it goes to, which stream
+allocates what it makes, and which streams the allocator has to wait for before
+it gives the memory of the call's tensors to others.
 """
 from __future__ import annotations
 
 import torch
 
+from ._lib import check
+
 # torch's own short way to the handle, where this build has it (a decoding step
 # is a few calls of 5 us each; the Stream object alone costs 1 us)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def new(shape, dtype, like, stream):
@@ -28,6 +31,8 @@ def stream_of(stream, dev, tensors):
     that both streams use them."""
     if stream is None:
         return _current_stream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"the stream is on GPU {stream.device.index}, the arguments on GPU {dev}")
     here = torch.cuda.current_stream(dev)
     if stream.cuda_stream != here.cuda_stream:
         for t in tensors:
@@ -35,3 +40,15 @@ def stream_of(stream, dev, tensors):
                 t.record_stream(stream)
                 t.record_stream(here)
     return stream.cuda_stream
+
+
+def launch(fn, stream, dev, tensors, *args):
+    """fn(*args, stream handle) on GPU dev, which holds every tensor: the
+    library launches on the current GPU, and handle 0 is that one's default
+    stream."""
+    handle = stream_of(stream, dev, tensors)
+    if dev == _current_device():
+        check(fn(*args, handle))
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args, handle))

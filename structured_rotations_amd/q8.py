@@ -20,8 +20,8 @@ import torch
 
 from . import _lib
 from .api import _workspace_bytes
-from ._lib import check, lib
-from ._streams import new, stream_of
+from ._lib import lib
+from ._streams import launch, new
 
 BLOCK = 128
 CODES = torch.float8_e4m3fn
@@ -149,8 +149,8 @@ def harp_quantize_q8(x, block_rows: int = 1, scale_dtype: str = "f32", codes=Non
     scales = _out_scales(scales, "scales", rows, cols, block_rows, sdt, x, stream)
     tensors = (x, codes, scales)
     dev = _on_gpu(*tensors)
-    check(lib().harp_quantize_q8(_p(x), ldx, _IO[x.dtype], rows, cols, block_rows, _p(codes), ldc, _p(scales),
-                                 _SCALE[sdt], stream_of(stream, dev, tensors)))
+    launch(lib().harp_quantize_q8, stream, dev, tensors, _p(x), ldx, _IO[x.dtype], rows, cols, block_rows, _p(codes),
+           ldc, _p(scales), _SCALE[sdt])
     return codes, scales
 
 
@@ -202,9 +202,8 @@ def harp_rmsnorm_q8(x, residual=None, gamma=None, eps: float = 1e-6, scale_dtype
         raise ValueError("ckpt_codes and ckpt_scales go with gamma and checkpoint=True only")
     tensors = (x, residual, gamma, h, codes, scales, rstd, ckpt_codes, ckpt_scales)
     dev = _on_gpu(*tensors)
-    check(lib().harp_rmsnorm_q8(_p(x), ldx, _p(residual), ldr, _p(gamma), eps, _p(h), ldh, _p(codes), ldc, _p(scales),
-                                _p(rstd), _p(ckpt_codes), ldk, _p(ckpt_scales), _SCALE[sdt], rows, d, _IO[io],
-                                stream_of(stream, dev, tensors)))
+    launch(lib().harp_rmsnorm_q8, stream, dev, tensors, _p(x), ldx, _p(residual), ldr, _p(gamma), eps, _p(h), ldh,
+           _p(codes), ldc, _p(scales), _p(rstd), _p(ckpt_codes), ldk, _p(ckpt_scales), _SCALE[sdt], rows, d, _IO[io])
     if checkpoint and gamma is None:
         ckpt_codes, ckpt_scales = codes, scales
     return RmsnormQ8(codes, scales, x if h is None else h, rstd, ckpt_codes, ckpt_scales)
@@ -245,9 +244,9 @@ def harp_rmsnorm_q8_vjp(ckpt_codes, ckpt_scales, rstd, dn, gamma=None, dres=None
     workspace, ws_bytes = _work(workspace, need, dn, stream)
     tensors = (dn, ckpt_codes, ckpt_scales, rstd, gamma, dres, dh, dgamma, workspace)
     dev = _on_gpu(*tensors)
-    check(lib().harp_rmsnorm_q8_vjp(_p(ckpt_codes), ldc, _p(ckpt_scales), _SCALE[ckpt_scales.dtype], _p(rstd),
-                                    _p(gamma), _p(dn), lddn, _p(dres), lddres, _p(dh), lddh, _p(dgamma), rows, d,
-                                    _IO[io], _p(workspace), ws_bytes, stream_of(stream, dev, tensors)))
+    launch(lib().harp_rmsnorm_q8_vjp, stream, dev, tensors, _p(ckpt_codes), ldc, _p(ckpt_scales),
+           _SCALE[ckpt_scales.dtype], _p(rstd), _p(gamma), _p(dn), lddn, _p(dres), lddres, _p(dh), lddh, _p(dgamma),
+           rows, d, _IO[io], _p(workspace), ws_bytes)
     return dh, dgamma
 
 
@@ -273,9 +272,8 @@ def harp_matmul_q8(a_codes, a_scales, w_codes, w_scales, out: str = "bf16", y=No
     workspace, ws_bytes = _work(workspace, lib().harp_matmul_q8_workspace(rows, n, k), a_codes, stream)
     tensors = (a_codes, a_scales, w_codes, w_scales, y, workspace)
     dev = _on_gpu(*tensors)
-    check(lib().harp_matmul_q8(_p(a_codes), lda, _p(a_scales), _p(w_codes), ldw, _p(w_scales),
-                               _SCALE[a_scales.dtype], rows, n, k, _p(y), ldy, _IO[odt], _p(workspace), ws_bytes,
-                               stream_of(stream, dev, tensors)))
+    launch(lib().harp_matmul_q8, stream, dev, tensors, _p(a_codes), lda, _p(a_scales), _p(w_codes), ldw, _p(w_scales),
+           _SCALE[a_scales.dtype], rows, n, k, _p(y), ldy, _IO[odt], _p(workspace), ws_bytes)
     return y
 
 
@@ -297,6 +295,6 @@ def harp_matmul_q8_wgrad(dy, x_codes, x_scales, out: str = "f32", dw=None, works
     workspace, ws_bytes = _work(workspace, lib().harp_matmul_q8_wgrad_workspace(rows, n, k), dy, stream)
     tensors = (dy, x_codes, x_scales, dw, workspace)
     dev = _on_gpu(*tensors)
-    check(lib().harp_matmul_q8_wgrad(_p(dy), lddy, _p(x_codes), ldx, _p(x_scales), _SCALE[x_scales.dtype], rows, n, k,
-                                     _p(dw), lddw, _IO[odt], _p(workspace), ws_bytes, stream_of(stream, dev, tensors)))
+    launch(lib().harp_matmul_q8_wgrad, stream, dev, tensors, _p(dy), lddy, _p(x_codes), ldx, _p(x_scales),
+           _SCALE[x_scales.dtype], rows, n, k, _p(dw), lddw, _IO[odt], _p(workspace), ws_bytes)
     return dw

@@ -1,6 +1,7 @@
 """Host-side tests (no GPU needed) of what a call with an explicit stream does
 with memory: everything it makes is allocated on that stream, and the allocator
-is told that the stream and the current one use the call's tensors.
+is told that the stream and the current one use the call's tensors; and of the
+GPU that a call goes to.
 
 Meta tensors take the GPU ones' place, and recorders the library's and torch's.
 """
@@ -10,7 +11,7 @@ from types import SimpleNamespace
 import pytest
 import torch
 
-from structured_rotations_amd import q8
+from structured_rotations_amd import _streams, q8
 
 E4 = torch.float8_e4m3fn
 
@@ -22,19 +23,29 @@ def meta(*shape, dtype=torch.float32):
     return _empty(shape, dtype=dtype, device="meta")
 
 
+def fake_stream(handle, gpu=0):
+    return SimpleNamespace(cuda_stream=handle, device=torch.device("cuda", gpu))
+
+
 class _Lib:
     """The real library's size helpers; every entry point succeeds."""
 
-    def __init__(self, real):
-        self._real = real
+    def __init__(self, real, log):
+        self._real, self._log = real, log
 
     def __getattr__(self, name):
-        return getattr(self._real, name) if name.endswith("_workspace") else lambda *a: 0
+        if name.endswith("_workspace"):
+            return getattr(self._real, name)
+
+        def entry(*a):
+            self._log.launched.append((self._log.gpu, a[-1]))
+            return 0
+        return entry
 
 
 @pytest.fixture
 def calls(monkeypatch):
-    log = SimpleNamespace(active=None, made=[], recorded=[])
+    log = SimpleNamespace(active=None, made=[], recorded=[], launched=[], gpu=0, tensors_on=0)
 
     @contextlib.contextmanager
     def on(stream):
@@ -47,14 +58,23 @@ def calls(monkeypatch):
         log.made.append((t, log.active))
         return t
 
+    @contextlib.contextmanager
+    def device(gpu):
+        before, log.gpu = log.gpu, gpu
+        yield
+        log.gpu = before
+
     real = q8.lib()
-    here = SimpleNamespace(cuda_stream=7)
+    here = fake_stream(7)
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: here)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(_streams, "_current_device", lambda: log.gpu, raising=False)
+    monkeypatch.setattr(_streams, "_current_stream", lambda dev: 100 + dev)
     monkeypatch.setattr(torch, "empty", logged)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: log.recorded.append((t, s)))
-    monkeypatch.setattr(q8, "lib", lambda: _Lib(real))
-    monkeypatch.setattr(q8, "_on_gpu", lambda *t: 0)
+    monkeypatch.setattr(q8, "lib", lambda: _Lib(real, log))
+    monkeypatch.setattr(q8, "_on_gpu", lambda *t: log.tensors_on)
     log.here = here
     return log
 
@@ -89,7 +109,7 @@ CALLS = [quantize, norm, norm_vjp, matmul, wgrad]
 
 @pytest.mark.parametrize("call", CALLS)
 def test_an_explicit_stream_allocates_and_is_recorded(calls, call):
-    s = SimpleNamespace(cuda_stream=99)
+    s = fake_stream(99)
     inputs, outputs, made = call(s)
     assert len(calls.made) == made                                # results, and a workspace where one is needed
     assert all(active is s for _, active in calls.made)
@@ -103,3 +123,21 @@ def test_the_current_stream_needs_no_record(calls, call):
     call(calls.here)
     assert not calls.recorded
     assert all(active is calls.here for _, active in calls.made)
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_call_goes_to_its_tensors_gpu(calls, call):
+    calls.tensors_on = 1                                          # while GPU 0 is the current one
+    call(None)
+    call(fake_stream(99, 1))
+    calls.tensors_on = 0
+    call(None)
+    assert calls.launched == [(1, 101), (1, 99), (0, 100)] and calls.gpu == 0
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_stream_of_another_gpu_is_refused(calls, call):
+    calls.tensors_on = 1
+    with pytest.raises(ValueError, match="stream is on GPU 0"):
+        call(fake_stream(99, 0))
+    assert not calls.launched
