@@ -25,6 +25,14 @@ def new(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def new_like(like, stream):
+    """torch.empty_like, allocated as new() does."""
+    if stream is None or like.device.type == "cpu":
+        return torch.empty_like(like)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(like)
+
+
 def stream_of(stream, dev, tensors):
     """The given stream's handle, or that of the current stream.  Any of the
     call's tensors may be dropped when the call returns: the allocator is told

@@ -2,7 +2,9 @@
 
 Argument marshalling only: every computation runs in the gfx950 kernels of
 libharp.so.  torch supplies device memory and the current HIP stream; every
-tensor argument must already live on the GPU (there is no CPU path).
+tensor argument must already live on the GPU (there is no CPU path).  stream
+names another one: what a call makes is then allocated on it, and every tensor
+may be dropped as soon as the call returns.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import torch
 
 from . import _lib
 from ._lib import Schedule, check, lib
+from ._streams import new, new_like, stream_of
 
 _DT = {torch.float32: _lib.HARP_F32, torch.bfloat16: _lib.HARP_BF16, torch.int8: _lib.HARP_I8,
        torch.float64: _lib.HARP_F64}
@@ -29,9 +32,12 @@ def _dev(t, name):
         raise TypeError(f"{name} must be a GPU tensor (the library has no CPU path)")
 
 
-def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _on_gpu(**named):
+    """The tensors given (None: left out), all on the GPU, and its index."""
+    for name, t in named.items():
+        _dev(t, name)
+    tensors = [t for t in named.values() if t is not None]
+    return tensors, tensors[0].get_device()
 
 
 def _flat(t, name, dtype, count):
@@ -105,19 +111,18 @@ def harp_materialize_blocks(schedule, d: int, theta: torch.Tensor, gauss: torch.
         _flat(gauss, "gauss", torch.float64, harp_gauss_count(schedule, d))
     tdt = _BLK_NAME[block_dtype]
     if blocks_out is None:
-        blocks_out = torch.empty(harp_block_count(schedule, d), dtype=tdt, device=theta.device)
+        blocks_out = new(harp_block_count(schedule, d), tdt, theta, stream)
     if block_dtype == "i8" and scales_out is None:
-        scales_out = torch.empty(harp_group_count(schedule, d), dtype=torch.float32, device=theta.device)
+        scales_out = new(harp_group_count(schedule, d), torch.float32, theta, stream)
     _flat(blocks_out, "blocks_out", tdt, harp_block_count(schedule, d))
     if block_dtype == "i8":
         _flat(scales_out, "scales_out", torch.float32, harp_group_count(schedule, d))
     elif scales_out is not None:
         raise ValueError("scales_out goes with int8 blocks only")
-    for n, t in (("theta", theta), ("gauss", gauss), ("blocks_out", blocks_out), ("scales_out", scales_out)):
-        _dev(t, n)
+    tensors, dev = _on_gpu(theta=theta, gauss=gauss, blocks_out=blocks_out, scales_out=scales_out)
     check(lib().harp_materialize_blocks(ctypes.byref(Schedule.of(schedule)), d, _ptr(theta),
                                         _ptr(gauss), _DT[tdt],
-                                        _ptr(blocks_out), _ptr(scales_out), _stream(stream)))
+                                        _ptr(blocks_out), _ptr(scales_out), stream_of(stream, dev, tensors)))
     return blocks_out, (scales_out if block_dtype == "i8" else None)
 
 
@@ -127,15 +132,14 @@ def harp_quantize_theta(schedule, d: int, theta: torch.Tensor, codes_out: torch.
     Returns (codes, scales)."""
     _flat(theta, "theta", torch.float64, harp_theta_count(schedule, d))
     if codes_out is None:
-        codes_out = torch.empty(harp_theta_count(schedule, d), dtype=torch.int8, device=theta.device)
+        codes_out = new(harp_theta_count(schedule, d), torch.int8, theta, stream)
     if scales_out is None:
-        scales_out = torch.empty(len(tuple(schedule)), dtype=torch.float32, device=theta.device)
+        scales_out = new(len(tuple(schedule)), torch.float32, theta, stream)
     _flat(codes_out, "codes_out", torch.int8, harp_theta_count(schedule, d))
     _flat(scales_out, "scales_out", torch.float32, len(tuple(schedule)))
-    for n, t in (("theta", theta), ("codes_out", codes_out), ("scales_out", scales_out)):
-        _dev(t, n)
+    tensors, dev = _on_gpu(theta=theta, codes_out=codes_out, scales_out=scales_out)
     check(lib().harp_quantize_theta(ctypes.byref(Schedule.of(schedule)), d, _ptr(theta), _ptr(codes_out),
-                                    _ptr(scales_out), _stream(stream)))
+                                    _ptr(scales_out), stream_of(stream, dev, tensors)))
     return codes_out, scales_out
 
 
@@ -151,20 +155,19 @@ def harp_materialize_blocks_q8(schedule, d: int, theta_codes: torch.Tensor, thet
         _flat(gauss, "gauss", torch.float64, harp_gauss_count(schedule, d))
     tdt = _BLK_NAME[block_dtype]
     if blocks_out is None:
-        blocks_out = torch.empty(harp_block_count(schedule, d), dtype=tdt, device=theta_codes.device)
+        blocks_out = new(harp_block_count(schedule, d), tdt, theta_codes, stream)
     if block_dtype == "i8" and scales_out is None:
-        scales_out = torch.empty(harp_group_count(schedule, d), dtype=torch.float32, device=theta_codes.device)
+        scales_out = new(harp_group_count(schedule, d), torch.float32, theta_codes, stream)
     _flat(blocks_out, "blocks_out", tdt, harp_block_count(schedule, d))
     if block_dtype == "i8":
         _flat(scales_out, "scales_out", torch.float32, harp_group_count(schedule, d))
     elif scales_out is not None:
         raise ValueError("scales_out goes with int8 blocks only")
-    for n, t in (("theta_codes", theta_codes), ("theta_scales", theta_scales), ("gauss", gauss),
-                 ("blocks_out", blocks_out), ("scales_out", scales_out)):
-        _dev(t, n)
+    tensors, dev = _on_gpu(theta_codes=theta_codes, theta_scales=theta_scales, gauss=gauss, blocks_out=blocks_out,
+                           scales_out=scales_out)
     check(lib().harp_materialize_blocks_q8(ctypes.byref(Schedule.of(schedule)), d, _ptr(theta_codes),
                                            _ptr(theta_scales), _ptr(gauss), _DT[tdt], _ptr(blocks_out),
-                                           _ptr(scales_out), _stream(stream)))
+                                           _ptr(scales_out), stream_of(stream, dev, tensors)))
     return blocks_out, (scales_out if block_dtype == "i8" else None)
 
 
@@ -173,11 +176,11 @@ def harp_materialize_blocks_q8(schedule, d: int, theta_codes: torch.Tensor, thet
 # is on the GPU last, then calls the library once: nothing is launched for a
 # call that fails a check.
 
-def _out_like(out, x, d, name):
+def _out_like(out, x, d, name, stream):
     """The output of a row transform: x's row count and dtype (the library is
     given one row count and one I/O dtype for both)."""
     if out is None:
-        return torch.empty_like(x)
+        return new_like(x, stream)
     rows, _ = _rows_ld(out, d, name)
     if rows != x.shape[0] or out.dtype != x.dtype:
         raise ValueError(f"{name} must match the input in rows and dtype: {tuple(out.shape)} {out.dtype} "
@@ -188,12 +191,11 @@ def _out_like(out, x, d, name):
 def _apply(fn, schedule, d, blocks, scales, signs, x, y, stream):
     _block_params(schedule, d, blocks, scales, signs)
     rows, ldx = _rows_ld(x, d, "x")
-    y = _out_like(y, x, d, "y")
+    y = _out_like(y, x, d, "y", stream)
     _, ldy = _rows_ld(y, d, "y")
-    for n, t in (("blocks", blocks), ("scales", scales), ("signs", signs), ("x", x), ("y", y)):
-        _dev(t, n)
+    tensors, dev = _on_gpu(blocks=blocks, scales=scales, signs=signs, x=x, y=y)
     check(fn(ctypes.byref(Schedule.of(schedule)), d, _ptr(blocks), _DT[blocks.dtype], _ptr(scales),
-             _ptr(signs), _ptr(x), ldx, _ptr(y), ldy, rows, _DT[x.dtype], _stream(stream)))
+             _ptr(signs), _ptr(x), ldx, _ptr(y), ldy, rows, _DT[x.dtype], stream_of(stream, dev, tensors)))
     return y
 
 
@@ -228,20 +230,18 @@ def harp_apply_decode(schedule, d: int, blocks, scales, signs, x, y=None, invers
     (allocated here when None and needed)."""
     _block_params(schedule, d, blocks, scales, signs)
     rows, ldx = _rows_ld(x, d, "x")
-    y = _out_like(y, x, d, "y")
+    y = _out_like(y, x, d, "y", stream)
     _, ldy = _rows_ld(y, d, "y")
     sch = Schedule.of(schedule)
     if workspace is None:
         need = int(lib().harp_apply_decode_workspace(ctypes.byref(sch), d, _DT[blocks.dtype], rows))
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            workspace = new(need, torch.uint8, x, stream)
     ws_bytes = _workspace_bytes(workspace)
-    for n, t in (("blocks", blocks), ("scales", scales), ("signs", signs), ("x", x), ("y", y),
-                 ("workspace", workspace)):
-        _dev(t, n)
+    tensors, dev = _on_gpu(blocks=blocks, scales=scales, signs=signs, x=x, y=y, workspace=workspace)
     check(lib().harp_apply_decode(ctypes.byref(sch), d, _ptr(blocks), _DT[blocks.dtype], _ptr(scales),
                                   _ptr(signs), _ptr(x), ldx, _ptr(y), ldy, rows, _DT[x.dtype], int(inverse),
-                                  _ptr(workspace), ws_bytes, _stream(stream)))
+                                  _ptr(workspace), ws_bytes, stream_of(stream, dev, tensors)))
     return y
 
 
@@ -253,13 +253,12 @@ def harp_apply_decode_noalloc(schedule, d: int, blocks, scales, signs, x, y, inv
     rows, ldx = _rows_ld(x, d, "x")
     if y is None:
         raise ValueError("y is required (this entry point allocates nothing)")
-    y = _out_like(y, x, d, "y")
+    y = _out_like(y, x, d, "y", stream)
     _, ldy = _rows_ld(y, d, "y")
-    for n, t in (("blocks", blocks), ("scales", scales), ("signs", signs), ("x", x), ("y", y)):
-        _dev(t, n)
+    tensors, dev = _on_gpu(blocks=blocks, scales=scales, signs=signs, x=x, y=y)
     check(lib().harp_apply_decode_noalloc(ctypes.byref(Schedule.of(schedule)), d, _ptr(blocks), _DT[blocks.dtype],
                                           _ptr(scales), _ptr(signs), _ptr(x), ldx, _ptr(y), ldy, rows,
-                                          _DT[x.dtype], int(inverse), _stream(stream)))
+                                          _DT[x.dtype], int(inverse), stream_of(stream, dev, tensors)))
     return y
 
 
@@ -276,28 +275,27 @@ def harp_apply_vjp(schedule, d: int, blocks, scales, signs, x, dy, dx=None, want
     rows, ldx = _rows_ld(x, d, "x")
     if dy is None:
         raise ValueError("dy is required")
-    dy = _out_like(dy, x, d, "dy")
+    dy = _out_like(dy, x, d, "dy", stream)
     _, lddy = _rows_ld(dy, d, "dy")
     if dx is None and want_dx:
-        dx = torch.empty_like(x)
+        dx = new_like(x, stream)
     lddx = 0
     if dx is not None:
-        dx = _out_like(dx, x, d, "dx")
+        dx = _out_like(dx, x, d, "dx", stream)
         _, lddx = _rows_ld(dx, d, "dx")
     if dblocks is None:
-        dblocks = torch.empty(harp_block_count(schedule, d), dtype=torch.float32, device=x.device)
+        dblocks = new(harp_block_count(schedule, d), torch.float32, x, stream)
     _flat(dblocks, "dblocks", torch.float32, harp_block_count(schedule, d))
     sch = Schedule.of(schedule)
     if workspace is None:
         need = int(lib().harp_apply_vjp_workspace(ctypes.byref(sch), d, rows))
-        workspace = torch.empty(max(need, 4), dtype=torch.uint8, device=x.device)
+        workspace = new(max(need, 4), torch.uint8, x, stream)
     ws_bytes = _workspace_bytes(workspace)
-    for n, t in (("blocks", blocks), ("scales", scales), ("signs", signs), ("x", x), ("dy", dy),
-                 ("dx", dx), ("dblocks", dblocks), ("workspace", workspace)):
-        _dev(t, n)
+    tensors, dev = _on_gpu(blocks=blocks, scales=scales, signs=signs, x=x, dy=dy, dx=dx, dblocks=dblocks,
+                           workspace=workspace)
     check(lib().harp_apply_vjp(ctypes.byref(sch), d, _ptr(blocks), _DT[blocks.dtype], _ptr(scales), _ptr(signs),
                                _ptr(x), ldx, _ptr(dy), lddy, _ptr(dx), lddx, rows, _DT[x.dtype], _ptr(dblocks),
-                               _ptr(workspace), ws_bytes, _stream(stream)))
+                               _ptr(workspace), ws_bytes, stream_of(stream, dev, tensors)))
     return dx, dblocks
 
 
@@ -308,12 +306,11 @@ def harp_theta_vjp(schedule, d: int, theta: torch.Tensor, gauss, dblocks, dtheta
         _flat(gauss, "gauss", torch.float64, harp_gauss_count(schedule, d))
     _flat(dblocks, "dblocks", torch.float32, harp_block_count(schedule, d))
     if dtheta is None:
-        dtheta = torch.empty_like(theta)
+        dtheta = new_like(theta, stream)
     _flat(dtheta, "dtheta", torch.float64, harp_theta_count(schedule, d))
-    for n, t in (("theta", theta), ("gauss", gauss), ("dblocks", dblocks), ("dtheta", dtheta)):
-        _dev(t, n)
+    tensors, dev = _on_gpu(theta=theta, gauss=gauss, dblocks=dblocks, dtheta=dtheta)
     check(lib().harp_theta_vjp(ctypes.byref(Schedule.of(schedule)), d, _ptr(theta), _ptr(gauss), _ptr(dblocks),
-                               _ptr(dtheta), _stream(stream)))
+                               _ptr(dtheta), stream_of(stream, dev, tensors)))
     return dtheta
 
 
@@ -335,7 +332,7 @@ def harp_rotate_weight(su, blocks_u, scales_u, signs_u, sv, blocks_v, scales_v, 
         raise TypeError("blocks_u and blocks_v must share a dtype")
     _, ldw = _rows_ld(w, d_in, "w")
     if w_out is None:
-        w_out = torch.empty_like(w)
+        w_out = new_like(w, stream)
     if tuple(w_out.shape) != tuple(w.shape) or w_out.dtype != w.dtype:
         raise ValueError(f"w_out must match w in shape and dtype: {tuple(w_out.shape)} {w_out.dtype} "
                          f"for {tuple(w.shape)} {w.dtype}")
@@ -343,17 +340,15 @@ def harp_rotate_weight(su, blocks_u, scales_u, signs_u, sv, blocks_v, scales_v, 
     if workspace is None and fp32_intermediates:
         need = harp_rotate_weight_workspace(d_out, d_in)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=w.device)
+            workspace = new(need, torch.uint8, w, stream)
     ws_bytes = _workspace_bytes(workspace)
-    for n, t in (("blocks_u", blocks_u), ("blocks_v", blocks_v), ("scales_u", scales_u), ("scales_v", scales_v),
-                 ("signs_u", signs_u), ("signs_v", signs_v), ("w", w), ("w_out", w_out),
-                 ("workspace", workspace)):
-        _dev(t, n)
+    tensors, dev = _on_gpu(blocks_u=blocks_u, blocks_v=blocks_v, scales_u=scales_u, scales_v=scales_v,
+                           signs_u=signs_u, signs_v=signs_v, w=w, w_out=w_out, workspace=workspace)
     check(lib().harp_rotate_weight(
         ctypes.byref(Schedule.of(su)), _ptr(blocks_u), _ptr(scales_u), _ptr(signs_u),
         ctypes.byref(Schedule.of(sv)), _ptr(blocks_v), _ptr(scales_v), _ptr(signs_v),
         _DT[blocks_u.dtype], _ptr(w), ldw, _ptr(w_out), ldo, d_out, d_in, _DT[w.dtype], int(bool(inverse)),
-        _ptr(workspace), ws_bytes, _stream(stream)))
+        _ptr(workspace), ws_bytes, stream_of(stream, dev, tensors)))
     return w_out
 
 
@@ -363,10 +358,10 @@ def rht_compose(schedule, d: int, signs, x, y=None, inverse: bool = False, strea
             signs.shape[1] != d or not signs.is_contiguous():
         raise ValueError("signs must be a contiguous int8 tensor of shape (k, d)")
     rows, ldx = _rows_ld(x, d, "x")
-    y = _out_like(y, x, d, "y")
+    y = _out_like(y, x, d, "y", stream)
     _, ldy = _rows_ld(y, d, "y")
-    for n, t in (("signs", signs), ("x", x), ("y", y)):
-        _dev(t, n)
+    tensors, dev = _on_gpu(signs=signs, x=x, y=y)
     check(lib().rht_compose(ctypes.byref(Schedule.of(schedule)), d, _ptr(signs), signs.shape[0],
-                            _ptr(x), ldx, _ptr(y), ldy, rows, _DT[x.dtype], int(bool(inverse)), _stream(stream)))
+                            _ptr(x), ldx, _ptr(y), ldy, rows, _DT[x.dtype], int(bool(inverse)),
+                            stream_of(stream, dev, tensors)))
     return y

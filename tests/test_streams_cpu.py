@@ -11,7 +11,7 @@ from types import SimpleNamespace
 import pytest
 import torch
 
-from structured_rotations_amd import _streams, q8
+from structured_rotations_amd import _streams, api, q8
 
 E4 = torch.float8_e4m3fn
 
@@ -34,7 +34,7 @@ class _Lib:
         self._real, self._log = real, log
 
     def __getattr__(self, name):
-        if name.endswith("_workspace"):
+        if name.endswith(("_workspace", "_count")):
             return getattr(self._real, name)
 
         def entry(*a):
@@ -58,6 +58,9 @@ def calls(monkeypatch):
         log.made.append((t, log.active))
         return t
 
+    def like(t):
+        return logged(t.shape, dtype=t.dtype, device=t.device)
+
     @contextlib.contextmanager
     def device(gpu):
         before, log.gpu = log.gpu, gpu
@@ -72,9 +75,13 @@ def calls(monkeypatch):
     monkeypatch.setattr(_streams, "_current_device", lambda: log.gpu, raising=False)
     monkeypatch.setattr(_streams, "_current_stream", lambda dev: 100 + dev)
     monkeypatch.setattr(torch, "empty", logged)
+    monkeypatch.setattr(torch, "empty_like", like)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: log.recorded.append((t, s)))
-    monkeypatch.setattr(q8, "lib", lambda: _Lib(real, log))
+    for binding in (q8, api):
+        monkeypatch.setattr(binding, "lib", lambda: _Lib(real, log))
     monkeypatch.setattr(q8, "_on_gpu", lambda *t: log.tensors_on)
+    monkeypatch.setattr(api, "_on_gpu", lambda **t: ([v for v in t.values() if v is not None], log.tensors_on),
+                        raising=False)
     log.here = here
     return log
 
@@ -104,14 +111,56 @@ def wgrad(stream):
     return (dy, x, s), (q8.harp_matmul_q8_wgrad(dy, x, s, stream=stream),), 2
 
 
-CALLS = [quantize, norm, norm_vjp, matmul, wgrad]
+SCH, D = (8, 8, 8), 512
+
+
+def blocks():
+    return meta(api.harp_block_count(SCH, D))
+
+
+def materialize(stream):
+    th = meta(api.harp_theta_count(SCH, D), dtype=torch.float64)
+    out = api.harp_materialize_blocks(SCH, D, th, None, "i8", stream=stream)
+    codes = api.harp_quantize_theta(SCH, D, th, stream=stream)
+    more = api.harp_materialize_blocks_q8(SCH, D, *codes, None, "i8", stream=stream)
+    return (th,), (*out, *codes, *more), 6
+
+
+def apply(stream):
+    b, x = blocks(), meta(5, D)
+    return (b, x), (api.harp_apply(SCH, D, b, None, None, x, stream=stream),
+                    api.harp_apply_inverse(SCH, D, b, None, None, x, stream=stream),
+                    api.harp_apply_decode(SCH, D, b, None, None, x, stream=stream)), None
+
+
+def apply_vjp(stream):
+    b, x, dy = blocks(), meta(5, D), meta(5, D)
+    return (b, x, dy), api.harp_apply_vjp(SCH, D, b, None, None, x, dy, stream=stream), 3
+
+
+def theta_vjp(stream):
+    th, db = meta(api.harp_theta_count(SCH, D), dtype=torch.float64), blocks()
+    return (th, db), (api.harp_theta_vjp(SCH, D, th, None, db, stream=stream),), 1
+
+
+def rotate(stream):
+    b, w = blocks(), meta(D, D)
+    return (b, w), (api.harp_rotate_weight(SCH, b, None, None, SCH, b, None, None, w, stream=stream),), 2
+
+
+def rht(stream):
+    signs, x = meta(2, D, dtype=torch.int8), meta(5, D)
+    return (signs, x), (api.rht_compose(SCH, D, signs, x, stream=stream),), 1
+
+
+CALLS = [quantize, norm, norm_vjp, matmul, wgrad, materialize, apply, apply_vjp, theta_vjp, rotate, rht]
 
 
 @pytest.mark.parametrize("call", CALLS)
 def test_an_explicit_stream_allocates_and_is_recorded(calls, call):
     s = fake_stream(99)
     inputs, outputs, made = call(s)
-    assert len(calls.made) == made                                # results, and a workspace where one is needed
+    assert made is None or len(calls.made) == made                # results, and a workspace where one is needed
     assert all(active is s for _, active in calls.made)
     told = {(id(t), st.cuda_stream) for t, st in calls.recorded}
     for t in [*inputs, *outputs, *(t for t, _ in calls.made)]:
@@ -125,7 +174,7 @@ def test_the_current_stream_needs_no_record(calls, call):
     assert all(active is calls.here for _, active in calls.made)
 
 
-@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("call", CALLS[:5])
 def test_a_call_goes_to_its_tensors_gpu(calls, call):
     calls.tensors_on = 1                                          # while GPU 0 is the current one
     call(None)
@@ -135,7 +184,7 @@ def test_a_call_goes_to_its_tensors_gpu(calls, call):
     assert calls.launched == [(1, 101), (1, 99), (0, 100)] and calls.gpu == 0
 
 
-@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("call", CALLS[:5])
 def test_a_stream_of_another_gpu_is_refused(calls, call):
     calls.tensors_on = 1
     with pytest.raises(ValueError, match="stream is on GPU 0"):
