@@ -13,8 +13,8 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import Schedule, check, lib
-from ._streams import new, new_like, stream_of
+from ._lib import Schedule, lib
+from ._streams import launch, new, new_like
 
 _DT = {torch.float32: _lib.HARP_F32, torch.bfloat16: _lib.HARP_BF16, torch.int8: _lib.HARP_I8,
        torch.float64: _lib.HARP_F64}
@@ -33,11 +33,14 @@ def _dev(t, name):
 
 
 def _on_gpu(**named):
-    """The tensors given (None: left out), all on the GPU, and its index."""
+    """The tensors given (None: left out), all on one GPU, and its index."""
     for name, t in named.items():
         _dev(t, name)
     tensors = [t for t in named.values() if t is not None]
-    return tensors, tensors[0].get_device()
+    gpus = {t.get_device() for t in tensors}
+    if len(gpus) > 1:
+        raise ValueError(f"the arguments are on different GPUs ({', '.join(map(str, sorted(gpus)))})")
+    return tensors, gpus.pop()
 
 
 def _flat(t, name, dtype, count):
@@ -120,9 +123,8 @@ def harp_materialize_blocks(schedule, d: int, theta: torch.Tensor, gauss: torch.
     elif scales_out is not None:
         raise ValueError("scales_out goes with int8 blocks only")
     tensors, dev = _on_gpu(theta=theta, gauss=gauss, blocks_out=blocks_out, scales_out=scales_out)
-    check(lib().harp_materialize_blocks(ctypes.byref(Schedule.of(schedule)), d, _ptr(theta),
-                                        _ptr(gauss), _DT[tdt],
-                                        _ptr(blocks_out), _ptr(scales_out), stream_of(stream, dev, tensors)))
+    launch(lib().harp_materialize_blocks, stream, dev, tensors, ctypes.byref(Schedule.of(schedule)), d, _ptr(theta),
+           _ptr(gauss), _DT[tdt], _ptr(blocks_out), _ptr(scales_out))
     return blocks_out, (scales_out if block_dtype == "i8" else None)
 
 
@@ -138,8 +140,8 @@ def harp_quantize_theta(schedule, d: int, theta: torch.Tensor, codes_out: torch.
     _flat(codes_out, "codes_out", torch.int8, harp_theta_count(schedule, d))
     _flat(scales_out, "scales_out", torch.float32, len(tuple(schedule)))
     tensors, dev = _on_gpu(theta=theta, codes_out=codes_out, scales_out=scales_out)
-    check(lib().harp_quantize_theta(ctypes.byref(Schedule.of(schedule)), d, _ptr(theta), _ptr(codes_out),
-                                    _ptr(scales_out), stream_of(stream, dev, tensors)))
+    launch(lib().harp_quantize_theta, stream, dev, tensors, ctypes.byref(Schedule.of(schedule)), d, _ptr(theta),
+           _ptr(codes_out), _ptr(scales_out))
     return codes_out, scales_out
 
 
@@ -165,9 +167,8 @@ def harp_materialize_blocks_q8(schedule, d: int, theta_codes: torch.Tensor, thet
         raise ValueError("scales_out goes with int8 blocks only")
     tensors, dev = _on_gpu(theta_codes=theta_codes, theta_scales=theta_scales, gauss=gauss, blocks_out=blocks_out,
                            scales_out=scales_out)
-    check(lib().harp_materialize_blocks_q8(ctypes.byref(Schedule.of(schedule)), d, _ptr(theta_codes),
-                                           _ptr(theta_scales), _ptr(gauss), _DT[tdt], _ptr(blocks_out),
-                                           _ptr(scales_out), stream_of(stream, dev, tensors)))
+    launch(lib().harp_materialize_blocks_q8, stream, dev, tensors, ctypes.byref(Schedule.of(schedule)), d,
+           _ptr(theta_codes), _ptr(theta_scales), _ptr(gauss), _DT[tdt], _ptr(blocks_out), _ptr(scales_out))
     return blocks_out, (scales_out if block_dtype == "i8" else None)
 
 
@@ -194,8 +195,8 @@ def _apply(fn, schedule, d, blocks, scales, signs, x, y, stream):
     y = _out_like(y, x, d, "y", stream)
     _, ldy = _rows_ld(y, d, "y")
     tensors, dev = _on_gpu(blocks=blocks, scales=scales, signs=signs, x=x, y=y)
-    check(fn(ctypes.byref(Schedule.of(schedule)), d, _ptr(blocks), _DT[blocks.dtype], _ptr(scales),
-             _ptr(signs), _ptr(x), ldx, _ptr(y), ldy, rows, _DT[x.dtype], stream_of(stream, dev, tensors)))
+    launch(fn, stream, dev, tensors, ctypes.byref(Schedule.of(schedule)), d, _ptr(blocks), _DT[blocks.dtype],
+           _ptr(scales), _ptr(signs), _ptr(x), ldx, _ptr(y), ldy, rows, _DT[x.dtype])
     return y
 
 
@@ -239,9 +240,9 @@ def harp_apply_decode(schedule, d: int, blocks, scales, signs, x, y=None, invers
             workspace = new(need, torch.uint8, x, stream)
     ws_bytes = _workspace_bytes(workspace)
     tensors, dev = _on_gpu(blocks=blocks, scales=scales, signs=signs, x=x, y=y, workspace=workspace)
-    check(lib().harp_apply_decode(ctypes.byref(sch), d, _ptr(blocks), _DT[blocks.dtype], _ptr(scales),
-                                  _ptr(signs), _ptr(x), ldx, _ptr(y), ldy, rows, _DT[x.dtype], int(inverse),
-                                  _ptr(workspace), ws_bytes, stream_of(stream, dev, tensors)))
+    launch(lib().harp_apply_decode, stream, dev, tensors, ctypes.byref(sch), d, _ptr(blocks), _DT[blocks.dtype],
+           _ptr(scales), _ptr(signs), _ptr(x), ldx, _ptr(y), ldy, rows, _DT[x.dtype], int(inverse), _ptr(workspace),
+           ws_bytes)
     return y
 
 
@@ -256,9 +257,8 @@ def harp_apply_decode_noalloc(schedule, d: int, blocks, scales, signs, x, y, inv
     y = _out_like(y, x, d, "y", stream)
     _, ldy = _rows_ld(y, d, "y")
     tensors, dev = _on_gpu(blocks=blocks, scales=scales, signs=signs, x=x, y=y)
-    check(lib().harp_apply_decode_noalloc(ctypes.byref(Schedule.of(schedule)), d, _ptr(blocks), _DT[blocks.dtype],
-                                          _ptr(scales), _ptr(signs), _ptr(x), ldx, _ptr(y), ldy, rows,
-                                          _DT[x.dtype], int(inverse), stream_of(stream, dev, tensors)))
+    launch(lib().harp_apply_decode_noalloc, stream, dev, tensors, ctypes.byref(Schedule.of(schedule)), d, _ptr(blocks),
+           _DT[blocks.dtype], _ptr(scales), _ptr(signs), _ptr(x), ldx, _ptr(y), ldy, rows, _DT[x.dtype], int(inverse))
     return y
 
 
@@ -293,9 +293,9 @@ def harp_apply_vjp(schedule, d: int, blocks, scales, signs, x, dy, dx=None, want
     ws_bytes = _workspace_bytes(workspace)
     tensors, dev = _on_gpu(blocks=blocks, scales=scales, signs=signs, x=x, dy=dy, dx=dx, dblocks=dblocks,
                            workspace=workspace)
-    check(lib().harp_apply_vjp(ctypes.byref(sch), d, _ptr(blocks), _DT[blocks.dtype], _ptr(scales), _ptr(signs),
-                               _ptr(x), ldx, _ptr(dy), lddy, _ptr(dx), lddx, rows, _DT[x.dtype], _ptr(dblocks),
-                               _ptr(workspace), ws_bytes, stream_of(stream, dev, tensors)))
+    launch(lib().harp_apply_vjp, stream, dev, tensors, ctypes.byref(sch), d, _ptr(blocks), _DT[blocks.dtype],
+           _ptr(scales), _ptr(signs), _ptr(x), ldx, _ptr(dy), lddy, _ptr(dx), lddx, rows, _DT[x.dtype], _ptr(dblocks),
+           _ptr(workspace), ws_bytes)
     return dx, dblocks
 
 
@@ -309,8 +309,8 @@ def harp_theta_vjp(schedule, d: int, theta: torch.Tensor, gauss, dblocks, dtheta
         dtheta = new_like(theta, stream)
     _flat(dtheta, "dtheta", torch.float64, harp_theta_count(schedule, d))
     tensors, dev = _on_gpu(theta=theta, gauss=gauss, dblocks=dblocks, dtheta=dtheta)
-    check(lib().harp_theta_vjp(ctypes.byref(Schedule.of(schedule)), d, _ptr(theta), _ptr(gauss), _ptr(dblocks),
-                               _ptr(dtheta), stream_of(stream, dev, tensors)))
+    launch(lib().harp_theta_vjp, stream, dev, tensors, ctypes.byref(Schedule.of(schedule)), d, _ptr(theta),
+           _ptr(gauss), _ptr(dblocks), _ptr(dtheta))
     return dtheta
 
 
@@ -344,11 +344,10 @@ def harp_rotate_weight(su, blocks_u, scales_u, signs_u, sv, blocks_v, scales_v, 
     ws_bytes = _workspace_bytes(workspace)
     tensors, dev = _on_gpu(blocks_u=blocks_u, blocks_v=blocks_v, scales_u=scales_u, scales_v=scales_v,
                            signs_u=signs_u, signs_v=signs_v, w=w, w_out=w_out, workspace=workspace)
-    check(lib().harp_rotate_weight(
-        ctypes.byref(Schedule.of(su)), _ptr(blocks_u), _ptr(scales_u), _ptr(signs_u),
-        ctypes.byref(Schedule.of(sv)), _ptr(blocks_v), _ptr(scales_v), _ptr(signs_v),
-        _DT[blocks_u.dtype], _ptr(w), ldw, _ptr(w_out), ldo, d_out, d_in, _DT[w.dtype], int(bool(inverse)),
-        _ptr(workspace), ws_bytes, stream_of(stream, dev, tensors)))
+    launch(lib().harp_rotate_weight, stream, dev, tensors, ctypes.byref(Schedule.of(su)), _ptr(blocks_u),
+           _ptr(scales_u), _ptr(signs_u), ctypes.byref(Schedule.of(sv)), _ptr(blocks_v), _ptr(scales_v), _ptr(signs_v),
+           _DT[blocks_u.dtype], _ptr(w), ldw, _ptr(w_out), ldo, d_out, d_in, _DT[w.dtype], int(bool(inverse)),
+           _ptr(workspace), ws_bytes)
     return w_out
 
 
@@ -361,7 +360,6 @@ def rht_compose(schedule, d: int, signs, x, y=None, inverse: bool = False, strea
     y = _out_like(y, x, d, "y", stream)
     _, ldy = _rows_ld(y, d, "y")
     tensors, dev = _on_gpu(signs=signs, x=x, y=y)
-    check(lib().rht_compose(ctypes.byref(Schedule.of(schedule)), d, _ptr(signs), signs.shape[0],
-                            _ptr(x), ldx, _ptr(y), ldy, rows, _DT[x.dtype], int(bool(inverse)),
-                            stream_of(stream, dev, tensors)))
+    launch(lib().rht_compose, stream, dev, tensors, ctypes.byref(Schedule.of(schedule)), d, _ptr(signs),
+           signs.shape[0], _ptr(x), ldx, _ptr(y), ldy, rows, _DT[x.dtype], int(bool(inverse)))
     return y
