@@ -145,7 +145,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   // in bit 1 only.
   constexpr int kRowsD = 512 / BN;  // rows of dy per load of a wave
   unsigned vdd[2];
-  {
+  if constexpr (kRows == kWhole) {
     const int lr = lane / (BN / 8), pp = lane % (BN / 8);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -161,10 +161,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   const int drow = tid / (BN / 8), xrow = tid / (BK / 16);
   const int dn = g.n - n0 - dcol, xn = g.k - k0 - xcol;
   const int cut_d = kRows == kCut && dn > 0 && dn < 8 ? 16 - 2 * dn : 0, cut_x = kRows == kCut && xn > 0 && xn < 16 ? 16 - xn : 0;
-  const unsigned vd = dn > 0 ? (unsigned)((drow * (int)g.lddy + dcol) * 2 - cut_d) : kNoLoad;
-  const unsigned vx = xn > 0 ? (unsigned)(xrow * (int)g.ldx + xcol - cut_x) : kNoLoad;
   constexpr int kSB = E8 ? 1 : 4;
-  const unsigned vs = xn > 0 ? (unsigned)(xrow * g.nkb + (k0 + xcol) / kQBlk) * kSB : kNoLoad;
+  unsigned vd, vx, vs;
+  if constexpr (kRows != kNarrow) {
+    vd = dn > 0 ? (unsigned)((drow * (int)g.lddy + dcol) * 2 - cut_d) : kNoLoad;
+    vx = xn > 0 ? (unsigned)(xrow * (int)g.ldx + xcol - cut_x) : kNoLoad;
+    vs = xn > 0 ? (unsigned)(xrow * g.nkb + (k0 + xcol) / kQBlk) * kSB : kNoLoad;
+  }
 
   // rows of the next steps, as they come: of one step for the large tile, whose
   // steps are long, of two for the small one
@@ -196,20 +199,19 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
     if constexpr (kRows == kCut) rd[set][u] = load_16(src, vd + (unsigned)(n0 * 2 + r * (int)g.lddy * 2));
     else if constexpr (kRows == kNarrow)
       rd[set][u] = load16_bytes(reinterpret_cast<const uint8_t*>(g.dy + (int64_t)(m0 + drow + r) * g.lddy + n0 + dcol),
-                           m0 + drow + r < mhi ? dn * 2 : 0);
+                                m0 + drow + r < mhi ? min(dn, 8) * 2 : 0);  // dn is up to 2^30
   };
   auto load_x = [&](int set, TileSrc src, TileSrc scales, int m0, int u) {
     const int r = u * (4096 / BK);
-    if constexpr (kRows == kNarrow)
-      rx[set][u] = load16_bytes(g.x + (int64_t)(m0 + xrow + r) * g.ldx + k0 + xcol, m0 + xrow + r < mhi ? xn : 0);
-    else rx[set][u] = load_16(src, vx + (unsigned)(k0 + r * (int)g.ldx));
     if constexpr (kRows == kNarrow) {
+      rx[set][u] = load16_bytes(g.x + (int64_t)(m0 + xrow + r) * g.ldx + k0 + xcol, m0 + xrow + r < mhi ? xn : 0);
       const bool in = m0 + xrow + r < mhi && xn > 0;
       rs[set][u] = 0;
       if (in) rs[set][u] = scale_bits<E8>(g.x_scales, (int64_t)(m0 + xrow + r) * g.nkb + (k0 + xcol) / kQBlk);
-      return;
+    } else {
+      rx[set][u] = load_16(src, vx + (unsigned)(k0 + r * (int)g.ldx));
+      rs[set][u] = load_word<kSB>(scales, vs + (unsigned)(r * g.nkb * kSB));
     }
-    rs[set][u] = load_word<kSB>(scales, vs + (unsigned)(r * g.nkb * kSB));
   };
   auto keep_dy = [&](int set, int buf, int u) {
     if constexpr (kRows != kWhole) {

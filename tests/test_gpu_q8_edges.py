@@ -118,3 +118,18 @@ def test_memory_of_a_call_on_another_stream():
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(y, want)
         assert all(torch.all(t == 255) for t in others[:4]) and all(torch.isnan(t).all() for t in others[4:])
+
+
+# ---------------------------------------------------------- largest sizes
+BIG = 1 << 30
+
+
+def test_wgrad_of_the_most_rows():
+    # dw has 2^30 rows of one value: dy times one power of two, exact
+    say("wgrad n = 2^30")
+    dy = (torch.arange(BIG, device="cuda", dtype=torch.int32) % 251 + 1).to(torch.bfloat16).view(1, BIG)
+    x = torch.full((1, 1), 0x38, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    scale = torch.full((1, 1), 0x7d, dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu)
+    dw = H.harp_matmul_q8_wgrad(dy, x, scale, "f32")
+    torch.cuda.synchronize()
+    assert torch.equal(dw.view(-1), dy.view(-1).float() * 0.25)
