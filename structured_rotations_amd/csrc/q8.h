@@ -309,6 +309,11 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int* t
   *tm = __builtin_amdgcn_readfirstlane(first + in - in / gm * gm);
 }
 
+// Tiles of one launch: its threads along x have to be less than 2^32, or it is
+// refused or leaves out tiles; 2^30 columns by tiles of 64 and 256 threads are
+// more.
+constexpr int kTilesPerLaunch = 1 << 23;
+
 // Lane offset that is beyond any tile.
 constexpr unsigned kNoLoad = 0x7fffff00u;
 

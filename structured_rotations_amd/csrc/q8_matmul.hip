@@ -651,7 +651,7 @@ __global__ __launch_bounds__(512) void matmul_few_kernel(MatmulArgs g, int per) 
 // is one of a step's five.  64 x 13824 x 5120: 17 us (4.3 TB/s of codes).
 template <int MT, int NT, int WM, int WN, bool E8, typename TO>
 __global__ __launch_bounds__(64 * WM * WN) void matmul_ring_kernel(MatmulArgs g, int kb_per_split, int tiles_m,
-                                                                   int tiles_n) {
+                                                                   int tiles_n, int first_tile) {
   constexpr bool kHwScale = E8 && sizeof(TO) == 2, kWide = sizeof(TO) == 4;
   constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN, WAVES = WM * WN;
   static_assert(BM <= 128 && BN <= kQBlk && NT <= 2 && WAVES >= 4, "");
@@ -666,7 +666,7 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_ring_kernel(MatmulArgs g,
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, i16 = lane & 15, lrow = lane >> 3;
   int tm, tn;
-  tile_of((int)blockIdx.x, tiles_m, tiles_n, &tm, &tn);
+  tile_of(first_tile + (int)blockIdx.x, tiles_m, tiles_n, &tm, &tn);
   const int m0 = tm * BM, n0 = tn * BN;
   const int wm = wave / WN * (16 * MT), wn = wave % WN * (16 * NT);
   const int kb0 = (int)blockIdx.y * kb_per_split, kb1 = min(g.nkb, kb0 + kb_per_split);
@@ -848,8 +848,9 @@ template <int MT, int NT, int WM, int WN, bool E8, typename TO>
 void ring_go(const MatmulArgs& g, int splits, hipStream_t stream) {
   constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN;
   const int tm = (g.rows + BM - 1) / BM, tn = (g.n + BN - 1) / BN, per = (g.nkb + splits - 1) / splits;
-  hipLaunchKernelGGL((matmul_ring_kernel<MT, NT, WM, WN, E8, TO>), dim3(tm * tn, splits), dim3(64 * WM * WN), 0, stream,
-                     g, per, tm, tn);
+  for (int first = 0; first < tm * tn; first += kTilesPerLaunch)
+    hipLaunchKernelGGL((matmul_ring_kernel<MT, NT, WM, WN, E8, TO>), dim3(std::min(tm * tn - first, kTilesPerLaunch), splits),
+                       dim3(64 * WM * WN), 0, stream, g, per, tm, tn, first);
 }
 
 template <bool E8, typename TO>
@@ -862,7 +863,8 @@ hipError_t matmul_go(const MatmulArgs& g, hipStream_t stream) {
     few_go<1, E8, TO>(g, stream);
   } else if (!direct_ok(g)) {
     // rows that are no whole pieces: the few-rows form reads its weight faster
-    if (s == 1 && near && g.k >= 16 && g.rows <= 16) few_go<2, E8, TO>(g, stream);
+    // (its 512 threads per 32 columns make one launch up to 2^27)
+    if (s == 1 && near && g.k >= 16 && g.rows <= 16 && g.n <= (1 << 27)) few_go<2, E8, TO>(g, stream);
     else if (near && g.k >= 16) tile_go<4, 2, 2, 4, E8, TO, kCut>(g, s, stream);
     else tile_go<4, 2, 2, 4, E8, TO, kNarrow>(g, s, stream);
   } else if (way == Way::kBig) {

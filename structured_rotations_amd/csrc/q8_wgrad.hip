@@ -15,6 +15,7 @@
 // Both operands are stored along the other axis than the one summed over:
 // they stay that way in LDS ([m][n], [m][k]) and the transposing LDS read
 // (ds_read_b64_tr_b16) gives a lane its neighbouring m.
+#include <algorithm>
 #include <type_traits>
 
 #include "q8.h"
@@ -125,7 +126,7 @@ __device__ __forceinline__ void split_parts(float va, float vb, F put) {
 // instruction: 608 us).
 template <int NI, int NJ, bool E8, int PARTS, typename TO, Rows kRows>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) void wgrad_tile_kernel(
-    WgradArgs g, int m_per_split, int tiles_n, int tiles_k) {
+    WgradArgs g, int m_per_split, int tiles_n, int tiles_k, int first_tile) {
   constexpr int BK = 32 * NI, BN = 32 * NJ, R = NI * PARTS;
   constexpr int UD = kStep * BN / 8 / 256, UX = kStep * BK / 16 / 256;  // pieces per thread: 8 of dy, 16 of x
   __shared__ __align__(16) uint8_t ld[2][kStep * BN * 2];
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   __shared__ __align__(16) uint8_t lx[PARTS][2][kStep * BK * 2];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int tn, tk;
-  tile_of((int)blockIdx.x, tiles_n, tiles_k, &tn, &tk);
+  tile_of(first_tile + (int)blockIdx.x, tiles_n, tiles_k, &tn, &tk);
   const int k0 = tk * BK, n0 = tn * BN;
   const int wk = (wave & 1) * NI, wn = (wave >> 1) * NJ;  // in segments of 16
   const int mlo = (int)blockIdx.y * m_per_split, mhi = min(g.rows, mlo + m_per_split);
@@ -428,8 +429,10 @@ template <int NI, int NJ, bool E8, int PARTS, typename TO, Rows kRows>
 void wgrad_tile_go(const WgradArgs& g, const WgradShape& s, hipStream_t stream) {
   constexpr int BK = 32 * NI, BN = 32 * NJ;
   const int tn = (g.n + BN - 1) / BN, tk = (g.k + BK - 1) / BK;
-  hipLaunchKernelGGL((wgrad_tile_kernel<NI, NJ, E8, PARTS, TO, kRows>), dim3(tn * tk, s.splits), dim3(256), 0, stream,
-                     g, s.m_per_split, tn, tk);
+  for (int first = 0; first < tn * tk; first += kTilesPerLaunch)
+    hipLaunchKernelGGL((wgrad_tile_kernel<NI, NJ, E8, PARTS, TO, kRows>),
+                       dim3(std::min(tn * tk - first, kTilesPerLaunch), s.splits), dim3(256), 0, stream, g,
+                       s.m_per_split, tn, tk, first);
 }
 
 template <bool E8, int PARTS, typename TO>

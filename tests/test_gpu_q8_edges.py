@@ -9,7 +9,7 @@ import torch
 
 import structured_rotations_amd as H
 from oracle import q8_oracle as Q
-from tests.test_gpu_q8 import IO, TOL, np64, operands, rel_rows, say, to_codes, to_scales
+from tests.test_gpu_q8 import IO, SCALE, TOL, np64, operands, rel_rows, say, to_codes, to_scales
 
 pytestmark = pytest.mark.gpu
 
@@ -133,3 +133,36 @@ def test_wgrad_of_the_most_rows():
     dw = H.harp_matmul_q8_wgrad(dy, x, scale, "f32")
     torch.cuda.synchronize()
     assert torch.equal(dw.view(-1), dy.view(-1).float() * 0.25)
+
+
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+def test_wgrad_of_the_longest_rows(kind):
+    # one row of 2^30 values times 2: exact, fp32 scales with few bits
+    say("wgrad k = 2^30", kind)
+    codes = (torch.arange(BIG, device="cuda", dtype=torch.int32) % 119 + 8).to(torch.uint8).view(1, BIG)
+    scale = torch.full((1, BIG // 128), 0.25, device="cuda")
+    dw = H.harp_matmul_q8_wgrad(torch.full((1, 1), 2.0, dtype=torch.bfloat16, device="cuda"),
+                                codes.view(torch.float8_e4m3fn), scale if kind == "f32" else scale.to(SCALE[kind]), "f32")
+    torch.cuda.synchronize()
+    table = torch.from_numpy(Q.E4M3 * 0.5).float().cuda()
+    for i in range(0, BIG, BIG // 8):
+        want = table[codes[0, i:i + BIG // 8].int()]
+        assert torch.all((dw[0, i:i + BIG // 8] - want).abs() <= 1e-6 * want)
+
+
+@pytest.mark.parametrize("n,k", [(BIG, 16), ((1 << 28) + 4096, 17)])
+def test_matmul_of_the_most_columns(n, k):
+    # one row by n weight rows that repeat: results repeat, too
+    say("matmul n", n, k)
+    rng = np.random.default_rng(81)
+    part = 1 << 12
+    (ac, as_), (wc, _) = Q.quantize(rng.standard_normal((1, k))), Q.quantize(rng.standard_normal((part, k)), 128)
+    ones = np.ones((part // 128, 1), np.float32)
+    w = torch.empty(n, k, dtype=torch.uint8, device="cuda")
+    w.view(n // part, part, k).copy_(torch.from_numpy(wc).cuda())
+    y = H.harp_matmul_q8(to_codes(ac), to_scales(as_, "f32"), w.view(torch.float8_e4m3fn),
+                         torch.ones(n // 128, 1, device="cuda"), "bf16")
+    torch.cuda.synchronize()
+    y = y.view(n // part, part)
+    assert rel_rows(np64(y[:1]), Q.matmul(ac, as_, wc, ones)) <= TOL["bf16"]
+    assert torch.all(y == y[:1])
