@@ -369,7 +369,8 @@ harp_status harp_quantize_q8(const void* x, int64_t ldx, harp_dtype x_dtype,
 /* Residual addition, root-mean-square norm and coding of each row:
  *   h = x + residual (residual NULL: h = x),  r = 1 / sqrt(mean(h^2) + eps),
  *   codes, scales = 1 x 128 coding of  h * r * gamma  (gamma NULL: all ones).
- * h and r are fp32 inside; h_out (needs a residual; NULL: not written)
+ * h and r are fp32 inside (r also of rows whose squares are not in fp32's range;
+ * h * gamma has to be); h_out (needs a residual; NULL: not written)
  * receives h rounded once.  rstd (NULL: not written): r, one fp32 per row.
  * ckpt_codes, ckpt_scales (both or neither, only with gamma): the coding of
  * h * r, what harp_rmsnorm_q8_vjp reads; without gamma `codes` is that.

@@ -85,9 +85,10 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const T* __restrict_
 
 // ------------------------------------------------------------------ norm
 // Sum over the workgroup, in a fixed order, in every thread.  `part` holds
-// two sets of 16 slots, used in turn: a wave reaches the next use of a set
-// only after a barrier that follows everyone's reads of it.
-__device__ __forceinline__ float block_sum(float v, float (&part)[2][16], int set) {
+// sets of 16 slots, used in turn: a wave reaches the next use of a set only
+// after a barrier that follows everyone's reads of it.
+template <int kSets>
+__device__ __forceinline__ float block_sum(float v, float (&part)[kSets][16], int set) {
   v = wave_sum(v);
   const int nw = (int)blockDim.x >> 6;
   if (nw == 1) return v;
@@ -112,8 +113,8 @@ struct RowMap {
     step = (int64_t)gridDim.x * kRows;
   }
 };
-template <int kLanes>
-__device__ __forceinline__ float row_sum(float v, float (&part)[2][16], int set) {
+template <int kLanes, int kSets>
+__device__ __forceinline__ float row_sum(float v, float (&part)[kSets][16], int set) {
   if constexpr (kLanes == 0) return block_sum(v, part, set);
   v = row16_sum(v);
   return kLanes == 32 ? v + __shfl_xor(v, 16) : v;
@@ -131,7 +132,7 @@ template <typename T, int NCH, bool E8, int kLanes = 0>
 __global__ __launch_bounds__(NCH <= 2 ? 512 : 1024) void rmsnorm_q8_kernel(NormArgs a) {
   constexpr bool kAhead = NCH <= 2;
   const RowMap<kLanes> map;
-  __shared__ float part[2][16];
+  __shared__ float part[3][16];
   const int nblk = (a.d + kQBlk - 1) / kQBlk;
   const T* gamma = static_cast<const T*>(a.gamma);
   int col[NCH], n[NCH];
@@ -153,6 +154,7 @@ __global__ __launch_bounds__(NCH <= 2 ? 512 : 1024) void rmsnorm_q8_kernel(NormA
     }
   };
   if (kAhead) load(map.first);
+  const float least = a.eps < 0x1p-100f ? 0x1p-80f : 0.0f;
   int set = 0;
   for (int64_t r = map.first; r < a.rows; r += map.step, set ^= 1) {
     if (!kAhead) load(r);
@@ -168,7 +170,20 @@ __global__ __launch_bounds__(NCH <= 2 ? 512 : 1024) void rmsnorm_q8_kernel(NormA
     }
     if (kAhead) load(r + map.step);
     ss = row_sum<kLanes>(ss, part, set);
-    const float rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
+    float rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
+    // Squares beyond fp32's range (rows around 2^64 / sqrt(d) and more, or, if
+    // eps does not outweigh them, below 2^-40): again with the sum in other
+    // units.  The sum is the same in every thread of the row.
+    if (!(ss >= least && ss < __uint_as_float(0x7f800000u))) {
+      const float unit = ss < least ? 0x1p80f : 0x1p-80f;
+      ss = 0.0f;
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss += (v[c][j] * unit) * (v[c][j] * unit);
+      ss = row_sum<kLanes>(ss, part, 2);
+      rstd = unit / sqrtf(ss / (float)a.d + a.eps * unit * unit);
+    }
     if (a.rstd && map.tid == 0) a.rstd[r] = rstd;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {

@@ -9,7 +9,7 @@ import torch
 
 import structured_rotations_amd as H
 from oracle import q8_oracle as Q
-from tests.test_gpu_q8 import IO, SCALE, TOL, np64, operands, rel_rows, say, to_codes, to_scales
+from tests.test_gpu_q8 import IO, SCALE, SLACK, TOL, check_coded, np64, operands, rel_rows, say, to_codes, to_scales
 
 pytestmark = pytest.mark.gpu
 
@@ -94,6 +94,27 @@ def test_wgrad_ends_of_the_range(out, rows):
     assert (want[20, 128:256] > 3.41e38).all() and np.isfinite(want[:5, :256]).all()
 
 
+# -------------------------------------------------------------------- norm
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 200, 300, 4099, 5120, 20001])
+@pytest.mark.parametrize("eps", [0.0, 1e-5])
+def test_rmsnorm_far_from_one(d, io, kind, eps):
+    # rows whose squares leave fp32's range at either end
+    say("rmsnorm range", d, io, kind, eps)
+    rng = np.random.default_rng(d)
+    mult = np.array([1.0, 2e37, 1e25, 1e19, 1e18, 1.0] + ([1e-18, 1e-25, 1e-33] if eps == 0 else [1e-9]))
+    x = rng.standard_normal((len(mult), d)) * mult[:, None]
+    x = torch.from_numpy(x.astype(np.float32)).to(IO[io])
+    g = torch.from_numpy((1 + 0.2 * rng.standard_normal(d)).astype(np.float32)).to(IO[io])
+    out = H.harp_rmsnorm_q8(x.cuda(), None, g.cuda(), eps, kind, checkpoint=True)
+    torch.cuda.synchronize()
+    n, _, r, xn = Q.rmsnorm(np64(x), None, np64(g), eps)
+    assert np.all(np.abs(np64(out.rstd) - r) <= SLACK * r)
+    check_coded(out.codes, out.scales, n, kind)
+    check_coded(out.ckpt_codes, out.ckpt_scales, xn, kind)
+
+
 # ----------------------------------------------------------------- streams
 def test_memory_of_a_call_on_another_stream():
     # while the call's stream is busy, the current stream gets none of the call's memory, dropped or not
@@ -142,7 +163,7 @@ def test_wgrad_of_the_longest_rows(kind):
     codes = (torch.arange(BIG, device="cuda", dtype=torch.int32) % 119 + 8).to(torch.uint8).view(1, BIG)
     scale = torch.full((1, BIG // 128), 0.25, device="cuda")
     dw = H.harp_matmul_q8_wgrad(torch.full((1, 1), 2.0, dtype=torch.bfloat16, device="cuda"),
-                                codes.view(torch.float8_e4m3fn), scale if kind == "f32" else scale.to(SCALE[kind]), "f32")
+                                codes.view(torch.float8_e4m3fn), scale.to(SCALE[kind]), "f32")
     torch.cuda.synchronize()
     table = torch.from_numpy(Q.E4M3 * 0.5).float().cuda()
     for i in range(0, BIG, BIG // 8):
