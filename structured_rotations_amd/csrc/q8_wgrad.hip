@@ -76,16 +76,29 @@ __device__ __forceinline__ void store4<uint16_t>(uint16_t* p, int n, const f32x4
 // acc += a b.  kAcc: the accumulators are named as accumulation registers (a
 // wave that has 256 of them leaves the compiler no other place, and left to
 // itself it moves them about in the loop).  Nothing reads or writes one again
-// before 32 more instructions or settle().
+// before 32 more instructions or settle().  The factors come from LDS reads, for
+// which the compiler waits; a vector instruction that wrote one would have to be
+// two wait states earlier, and the built code has none.
 template <bool kAcc>
 __device__ __forceinline__ void mfma(f32x4& acc, bf16x8_t a, bf16x8_t b) {
   if constexpr (kAcc) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
   else acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
 }
-// Lets the last results arrive.
-template <bool kAcc>
-__device__ __forceinline__ void settle() {
-  if constexpr (kAcc) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+// Lets the accumulators' last writes arrive: the zeros' and the matrix
+// instructions'.  They are operands on both sides of the wait: nothing else
+// keeps the compiler, which sees no matrix instruction here, from moving an
+// access to one across it.
+template <bool kAcc, int NI, int NJ>
+__device__ __forceinline__ void settle(f32x4 (&acc)[NI][NJ]) {
+  if constexpr (!kAcc) return;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) asm volatile("" : "+a"(acc[i][j]));
+    if (t == 0) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  }
 }
 
 // Two values as PARTS bf16 parts each, handed to put(part, pair).  Parts are
@@ -267,7 +280,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  settle<kAcc>();
   s16x4 fr[2][NJ + R][2];  // fragments of two half steps: dy's, then x's
   // offsets of the buffer that is read; the other one is at ^ kFlip
   constexpr uint32_t kFlipD = kStep * BN * 2, kFlipX = kStep * BK * 2;
@@ -357,6 +369,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
 #pragma unroll
     for (int u = 0; u < kReads; ++u) read_half(0, 0, u);
     int buf = 0;
+    settle<kAcc>(acc);
     for (int m0 = mlo; m0 < mhi; m0 += kSets * kStep) {
       step(std::integral_constant<int, 0>{}, m0, buf);
       buf ^= 1;
@@ -365,7 +378,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
         buf ^= 1;
       }
     }
-    settle<kAcc>();
+    settle<kAcc>(acc);
     // no load may be in flight into LDS when the workgroup ends
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
