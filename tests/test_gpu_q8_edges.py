@@ -9,7 +9,8 @@ import torch
 
 import structured_rotations_amd as H
 from oracle import q8_oracle as Q
-from tests.test_gpu_q8 import IO, SCALE, SLACK, TOL, check_coded, np64, operands, rel_rows, say, to_codes, to_scales
+from tests.test_gpu_q8 import (IO, SCALE, SLACK, TOL, check_coded, empty_padded, np64, operands, padded, rel_rows, say,
+                               to_codes, to_scales)
 
 pytestmark = pytest.mark.gpu
 
@@ -38,6 +39,56 @@ def test_matmul_nan_stays_in_its_tile(kind):
     cols = np.r_[0:1024, 1152:n]
     want = Q.matmul(ac[ok], as_[ok], wc, np.where(np.isnan(ws), 0, ws))
     assert rel_rows(got[np.ix_(ok, cols)], want[:, cols]) <= TOL["bf16"]
+
+
+# where NaNs reach, per form of the product: rows, n, k that choose it (fp32 results never take the 256 x 256 form)
+FORMS = [(3, 300, 400), (40, 300, 400), (200, 300, 400), (3, 300, 395), (40, 300, 395), (200, 300, 395),
+         (40, 300, 2048), (1024, 2048, 400), (2304, 2304, 400), (4352, 2560, 400)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,n,k", FORMS)
+def test_matmul_special_values_by_form(rows, n, k, out, kind):
+    # a NaN code, NaN scales of both operands, zero blocks: own row or columns only
+    say("matmul special by form", rows, n, k, out, kind)
+    rng = np.random.default_rng(52)
+    (ac, as_), (wc, ws) = operands(rng, rows, n, k, kind)
+    ac[1, k - 1] = 0x7f
+    as_[2, 0] = np.nan
+    wc[n - 1, 130] = 0xff
+    ws[1, 2] = np.nan
+    y = H.harp_matmul_q8(to_codes(ac), to_scales(as_, kind), to_codes(wc), to_scales(ws, kind), out)
+    torch.cuda.synchronize()
+    want = Q.matmul(ac, as_, wc, ws)
+    got = np64(y)
+    mask = np.zeros((rows, n), dtype=bool)
+    mask[[1, 2]] = True
+    mask[:, 128:256] = True
+    mask[:, n - 1] = True
+    assert np.array_equal(np.isnan(want), mask) and np.array_equal(np.isnan(got), mask)
+    ok = [r for r in range(rows) if r not in (1, 2)]
+    cols = np.r_[0:128, 256:n - 1]
+    assert rel_rows(got[np.ix_(ok, cols)], want[np.ix_(ok, cols)]) <= TOL[out]
+
+
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+def test_matmul_strided_operands_of_large_tiles(kind):
+    # the 256 x 256 form: operands and results with rows apart, whole 16-byte pieces or not
+    say("matmul strides, large", kind)
+    rng = np.random.default_rng(53)
+    rows, n, k = 4100, 2576, 272
+    (ac, as_), (wc, ws) = operands(rng, rows, n, k, kind)
+    want = Q.matmul(ac, as_, wc, ws)
+    for pad, off in ((16, 16), (48, 0), (3, 5)):
+        y, buf = empty_padded(rows, n, torch.bfloat16, pad, off)
+        H.harp_matmul_q8(padded(to_codes(ac), pad, off), to_scales(as_, kind), padded(to_codes(wc), pad, off),
+                         to_scales(ws, kind), y=y)
+        torch.cuda.synchronize()
+        assert rel_rows(np64(y), want) <= TOL["bf16"]
+        outside = torch.ones(buf.numel() // 2, dtype=torch.bool, device="cuda")
+        outside[off:].as_strided((rows, n), (n + pad, 1)).fill_(False)
+        assert torch.all(buf.view(torch.int16)[outside] == 0x5555)
 
 
 # --------------------------------------------------------- weight gradient
@@ -92,6 +143,70 @@ def test_wgrad_ends_of_the_range(out, rows):
     keep = np.r_[0:5, 6:16]
     assert rel_rows(got[keep, :256], want[keep, :256]) <= TOL[out]
     assert (want[20, 128:256] > 3.41e38).all() and np.isfinite(want[:5, :256]).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,n,k", [(40, 144, 272), (200, 144, 272), (200, 141, 275), (70, 4096, 2304),
+                                      (70, 4099, 2305)])
+def test_wgrad_nan_scales(rows, n, k, out, kind):
+    # a NaN gradient reaches its result row, a NaN code its column, a NaN scale its block of 128 columns
+    say("wgrad nan", rows, n, k, out, kind)
+    rng = np.random.default_rng(63)
+    xc, xs = Q.quantize(rng.standard_normal((rows, k)), 1, kind)
+    dy = torch.from_numpy(rng.standard_normal((rows, n)).astype(np.float32)).to(torch.bfloat16)
+    dy[5, 7] = float("nan")
+    xc[9, 3] = 0xff
+    xs[rows - 1, 1] = np.nan
+    want = Q.wgrad(np64(dy), xc, xs)
+    got = np64(H.harp_matmul_q8_wgrad(dy.cuda(), to_codes(xc), to_scales(xs, kind), out))
+    mask = np.zeros((n, k), dtype=bool)
+    mask[7] = True
+    mask[:, 3] = True
+    mask[:, 128:256] = True
+    assert np.array_equal(np.isnan(got), mask)
+    rest = np.ix_(np.setdiff1d(np.arange(n), 7), np.setdiff1d(np.arange(k), np.r_[3, 128:256]))
+    assert rel_rows(got[rest], want[rest]) <= TOL[out] * (1.5 if out == "bf16" and kind == "f32" else 1.0)
+
+
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,n,k", [(50, 144, 272), (200, 144, 272), (70, 4096, 2304)])
+def test_wgrad_strided_operands(rows, n, k, out, kind):
+    say("wgrad strides", rows, n, k, out, kind)
+    rng = np.random.default_rng(64)
+    xc, xs = Q.quantize(rng.standard_normal((rows, k)), 1, kind)
+    dy = torch.from_numpy(rng.standard_normal((rows, n)).astype(np.float32)).to(torch.bfloat16)
+    want = Q.wgrad(np64(dy), xc, xs)
+    for pad, off in ((1, 3), (16, 0), (16, 16), (8, 8)):
+        dw, buf = empty_padded(n, k, IO[out], pad, off)
+        H.harp_matmul_q8_wgrad(padded(dy.cuda(), pad, off), padded(to_codes(xc), pad, off), to_scales(xs, kind), out,
+                               dw=dw)
+        torch.cuda.synchronize()
+        assert rel_rows(np64(dw), want) <= TOL[out] * (1.5 if out == "bf16" and kind == "f32" else 1.0)
+        word = torch.int32 if out == "f32" else torch.int16
+        outside = torch.ones(buf.numel() // word.itemsize, dtype=torch.bool, device="cuda")
+        outside[off:].as_strided((n, k), (k + pad, 1)).fill_(False)
+        assert torch.all(buf.view(word)[outside] == (0x55555555 if out == "f32" else 0x5555))
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [40, 200])
+def test_wgrad_ends_of_the_powers(rows, out):
+    # E8M0 scales of either end, and dy that brings the products back
+    say("wgrad e8m0 ends", rows, out)
+    rng = np.random.default_rng(65)
+    n, k = 48, 400
+    xc, xs = Q.quantize(rng.standard_normal((rows, k)), 1, "e8m0")
+    xs[:, 0] = 2.0 ** -110
+    xs[:, 1] = 2.0 ** 110
+    xs[:, 2] = 2.0 ** 118
+    dy = torch.from_numpy((rng.standard_normal((rows, n)) * 2.0 ** -20).astype(np.float32)).to(torch.bfloat16)
+    want = Q.wgrad(np64(dy), xc, xs)
+    got = np64(H.harp_matmul_q8_wgrad(dy.cuda(), to_codes(xc), to_scales(xs, "e8m0"), out))
+    for j in range(4):
+        at = np.s_[:, 128 * j:128 * j + 128]
+        assert rel_rows(got[at], want[at]) <= TOL[out]
 
 
 # -------------------------------------------------------------------- norm
