@@ -355,7 +355,8 @@ harp_status rht_compose(const harp_schedule* s, int64_t d, const int8_t* signs,
  * Sizes: rows, n, k and cols at most 2^30; row strides at least the row
  * length.  Any length and alignment is computed; the products' fastest loads
  * need 16-byte aligned bases and row strides and lengths of whole 16 bytes.
- * Outputs must not overlap inputs except where said.
+ * Outputs must not overlap inputs or each other except where said; rows of
+ * several matrices may lie side by side in one buffer (the same distance apart).
  * ---------------------------------------------------------------------- */
 
 /* Codes and scales of rows x cols values (F32 or BF16), in blocks of

@@ -58,14 +58,23 @@ harp_status check(const Mat& m) {
   return HARP_OK;
 }
 
-// An output against an input: no common byte, unless `same` allows the same
-// buffer with the same leading dimension.
+// An output against another argument: no common byte, unless `same` allows the
+// same buffer with the same leading dimension.  Rows may lie side by side in one
+// buffer: matrices whose rows are the same distance apart (a single row goes with
+// any distance) have no common byte if a row of one fits between the other's.
+// Other matrices have to be apart as a whole.
 harp_status check_apart(const Mat& out, const Mat& in, bool same) {
   if (out.p == nullptr || in.p == nullptr) return HARP_OK;
   if (same && out.p == in.p && out.eb == in.eb && out.ld == in.ld) return HARP_OK;
-  if (out.at() < in.at() + in.bytes() && in.at() < out.at() + out.bytes())
-    return fail(HARP_ERR_INVALID_ARG, "%s overlaps %s", out.name, in.name);
-  return HARP_OK;
+  if (out.at() >= in.at() + in.bytes() || in.at() >= out.at() + out.bytes()) return HARP_OK;
+  const uint64_t lo = (uint64_t)out.ld * out.eb, li = (uint64_t)in.ld * in.eb;
+  if ((out.rows > 1 || in.rows > 1) && (out.rows == 1 || in.rows == 1 || lo == li)) {
+    const uint64_t step = out.rows > 1 ? lo : li;
+    // where a row of `in` begins after the beginning of one of `out`
+    const uint64_t d = (in.at() >= out.at() ? in.at() - out.at() : step - (out.at() - in.at()) % step) % step;
+    if (d >= (uint64_t)out.cols * out.eb && step - d >= (uint64_t)in.cols * in.eb) return HARP_OK;
+  }
+  return fail(HARP_ERR_INVALID_ARG, "%s overlaps %s", out.name, in.name);
 }
 
 // Sizes fit an int with room for a tile beyond the last row or column.

@@ -256,6 +256,38 @@ def test_memory_of_a_call_on_another_stream():
         assert all(torch.all(t == 255) for t in others[:4]) and all(torch.isnan(t).all() for t in others[4:])
 
 
+# ------------------------------------------------- arguments in one buffer
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_arguments_side_by_side_in_one_buffer(io):
+    # columns of one buffer as input and output, and as two outputs: no common byte
+    say("side by side", io)
+    rng = np.random.default_rng(91)
+    rows, d, n = 37, 272, 400
+    x, res = (torch.from_numpy(rng.standard_normal((rows, d)).astype(np.float32)).to(IO[io]).cuda() for _ in range(2))
+    g = torch.from_numpy((1 + 0.2 * rng.standard_normal(d)).astype(np.float32)).to(IO[io]).cuda()
+    want = H.harp_rmsnorm_q8(x, res, g, checkpoint=True)
+    buf = torch.empty(rows, 3 * d + 5, dtype=IO[io], device="cuda")
+    xb, rb, hb = buf[:, 5:5 + d], buf[:, 5 + d:5 + 2 * d], buf[:, 5 + 2 * d:]
+    xb.copy_(x)
+    rb.copy_(res)
+    codes = torch.empty(rows, 2 * d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    got = H.harp_rmsnorm_q8(xb, rb, g, checkpoint=True, h=hb, codes=codes[:, d:], ckpt_codes=codes[:, :d])
+    for a, b in ((got.codes, want.codes), (got.ckpt_codes, want.ckpt_codes)):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.view(torch.uint8))
+    assert torch.equal(hb, want.h) and torch.equal(xb, x) and torch.equal(rb, res)
+    dh, dg = H.harp_rmsnorm_q8_vjp(want.ckpt_codes, want.ckpt_scales, want.rstd, xb, g, rb, dh=hb)
+    want_dh, want_dg = H.harp_rmsnorm_q8_vjp(want.ckpt_codes, want.ckpt_scales, want.rstd, x, g, res)
+    assert torch.equal(dh, want_dh) and torch.equal(dg, want_dg) and torch.equal(xb, x)
+    wc, ws = H.harp_quantize_q8(torch.from_numpy(rng.standard_normal((n, d)).astype(np.float32)).cuda(), 128)
+    both = torch.empty(rows, d + 2 * n, dtype=torch.uint8, device="cuda")
+    ab = both[:, 2 * n:].view(torch.float8_e4m3fn)
+    ab.copy_(want.codes)
+    yb = both.view(torch.bfloat16)[:, :n]
+    H.harp_matmul_q8(ab, want.scales, wc, ws, y=yb)
+    assert torch.equal(yb, H.harp_matmul_q8(want.codes, want.scales, wc, ws))
+    assert torch.equal(ab.contiguous().view(torch.uint8), want.codes.view(torch.uint8))
+
+
 # ---------------------------------------------------------- largest sizes
 BIG = 1 << 30
 

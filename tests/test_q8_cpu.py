@@ -177,6 +177,30 @@ def test_wgrad_rejects_on_host(lib, kw, status):
     assert lib.harp_last_error().decode()
 
 
+# x and residual side by side in rows of 4000 bytes, 1024 bytes each; h may lie in the 1952 bytes behind them, or be
+# the residual
+@pytest.mark.parametrize("at,free", [(2048, True), (2500, True), (2976, True), (4000 + 2048, True), (-4000 + 2976, True),
+                                     (1024, True), (2980, False), (2044, False), (512, False), (4000, False),
+                                     (8000 + 512, False), (-4, False)])
+def test_rows_side_by_side(lib, at, free):
+    # rstd over scales is refused last: the message says whether h was let through
+    base = 0x1000000
+    kw = dict(x=P(base), ldx=1000, res=P(base + 1024), ldr=1000, h=P(base + at), rstd=V)
+    assert norm(lib, ldh=1000, **kw) == BAD
+    assert lib.harp_last_error().decode().startswith("rstd overlaps" if free else "h_out overlaps")
+    assert norm(lib, ldh=999, **kw) == BAD                        # other distances: apart as a whole only
+    assert lib.harp_last_error().decode().startswith("h_out overlaps")
+
+
+def test_a_single_row_beside_others(lib):
+    # gamma (1024 bytes) within the rows' 4000 bytes, codes (256 of 4000) over it or not
+    base = 0x1000000
+    for at, free in ((0, True), (1024, False), (1024 + 2976, True), (800, False), (745, False), (744, True)):
+        assert norm(lib, x=Y, gamma=P(base + 1000), res=None, codes=P(base + at), ldc=4000, rstd=V) == BAD
+        got = lib.harp_last_error().decode()
+        assert got.startswith("rstd overlaps" if free else "codes overlaps gamma"), (at, got)
+
+
 def test_products_reject_short_workspaces(lib):
     for call, size in ((matmul, lambda: lib.harp_matmul_q8_workspace(200, 300, 4096)),
                        (wgrad, lambda: lib.harp_matmul_q8_wgrad_workspace(4000, 300, 256))):
