@@ -411,7 +411,9 @@ harp_status harp_rmsnorm_q8_vjp(const uint8_t* codes, int64_t ldc,
  * 128 x 128 blocks, scales of both in scale_dtype,
  *   y[i][j] = sum over blocks b of k of
  *             a_scale[i][b] w_scale[j / 128][b] sum over b of a[i][.] w[j][.],
- * summed in fp32; y is F32 or BF16 (rounded once), row stride ldy.
+ * summed in fp32; y is F32 or BF16 (rounded once), row stride ldy.  With F32
+ * scales or F32 y a block's two scales are multiplied in fp32 first, and their
+ * product has to be in its range.
  * workspace: harp_matmul_q8_workspace() bytes (may be 0; -1 for sizes out of
  * range), 16-byte aligned.  n, k >= 1; rows == 0 returns HARP_OK without a
  * launch.  With W's transpose and coded gradient rows this is also the

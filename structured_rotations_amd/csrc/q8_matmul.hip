@@ -308,7 +308,7 @@ __global__ __launch_bounds__(64 * MW * NW) void matmul_tile_kernel(MatmulArgs g,
 // steps, and the stores of a tile drain during the first step of the next
 // (kStores is added to what that step's waits count on).  Bound by the matrix
 // instructions: at 16384 x 13824 x 5120 they alone, on the same operands, take
-// 674 us; the whole 1003 to 1037 us with fp32 scales (2.3 PFLOP/s; every
+// 674 us; the whole 1003 to 1039 us with fp32 scales (2.3 PFLOP/s; every
 // block's product is scaled on the vector unit, a multiply-add per result and
 // block) and 895 to 924 us with E8M0, which the instruction applies itself
 // (2.6 PFLOP/s, a per-tensor library product's rate).
@@ -521,7 +521,7 @@ __global__ __launch_bounds__(512) void matmul_big_kernel(MatmulArgs g, int tiles
 // computes 16 NT columns (n) of 16 rows; its 8 waves share the blocks of
 // the reduction out, each a contiguous run, and add their sums through LDS: one
 // launch, no workspace.  Each wave keeps kRing blocks of both operands on
-// their way.  1 x 4096 x 4096: 5.9 us of the call's 8 (the ring form 13);
+// their way.  1 x 4096 x 4096: 6 to 7 us of the call's 8 (the ring form 13);
 // 13824 x 5120 takes 18 to 22 us here and 14 to 15 in the ring form, where the
 // weight streams better: hence up to 2^25 codes.  Row scales: a lane's load of one block's would touch 16 lines, so lane
 // (q, i16) loads block q of four for row i16 and the others ask it.

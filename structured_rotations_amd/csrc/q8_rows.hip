@@ -14,8 +14,9 @@ namespace {
 
 // ---------------------------------------------------------------- coding
 // Rows: a workgroup of 256 threads covers 2^sh blocks by 16 >> sh rows at a
-// time and walks down the rows.  16384 x 4096 bf16: 38 us, 5.3 TB/s, a large
-// copy's rate.
+// time and walks down the rows.  16384 x 4096 bf16: 38 to 40 us over buffers in
+// turn, as a copy of as many bytes (39); one buffer again and again stays in the
+// cache, 33 us (a copy 29).
 template <typename T, bool E8>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* __restrict__ x, int64_t ldx, int64_t rows,
                                                             int cols, int nblk, int sh, uint8_t* __restrict__ codes,
@@ -43,7 +44,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* __restrict_
 
 // Weights: one 128 x 128 block per workgroup, 64 values per thread in
 // registers between the maximum and the coding, so the weight is read once.
-// 13824 x 5120 bf16: 42 us, 5.1 TB/s.
+// 13824 x 5120 bf16: 42 us (a copy 41).
 template <typename T, bool E8>
 __global__ __launch_bounds__(256) void quantize_tile_kernel(const T* __restrict__ x, int64_t ldx, int64_t rows,
                                                             int cols, int nblk, uint8_t* __restrict__ codes,
@@ -123,11 +124,12 @@ __device__ __forceinline__ float row_sum(float v, float (&part)[kSets][16], int 
 // A workgroup walks over rows; a row stays in registers between the sum of
 // squares and the coding (NCH chunks of 8 per thread), and (kAhead: rows up to
 // 8192, which leave registers for it) the next row is on its way meanwhile.
-// 16384 x 5120 bf16, residual, checkpoint: 674 MB in 134 us, 5.0 TB/s (175 us
-// without the next row's loads); 4096 x 16384: 93 us.  One row of 4096: 2.8 us
-// of the call's 7.4, the rest is the launch.  Rows of 64 (16 lanes each), 100000 of
-// them: 14 us, against 46 us with a workgroup per row; 60000 of 160 (32 lanes):
-// 20 us, against 39.
+// 16384 x 5120 bf16, residual, checkpoint: 674 MB in 135 us, 5.0 TB/s (a copy 125;
+// 175 us without the next row's loads); 4096 x 16384: 90 us, with gamma and its
+// second coding 114.  One row of 4096: 2.8 us of the call's 8, the rest is the
+// launch and the host's checks.  Rows of 64 (16 lanes each), 100000 of them: 11 us
+// with E8M0 scales and one coding to 17 with fp32 scales and two, against 46 us
+// with a workgroup per row; 60000 of 160 (32 lanes): 19 us, against 39.
 template <typename T, int NCH, bool E8, int kLanes = 0>
 __global__ __launch_bounds__(NCH <= 2 ? 512 : 1024) void rmsnorm_q8_kernel(NormArgs a) {
   constexpr bool kAhead = NCH <= 2;
@@ -222,9 +224,10 @@ __global__ __launch_bounds__(NCH <= 2 ? 512 : 1024) void rmsnorm_q8_kernel(NormA
 // longer ones read gamma and dres when they are used instead).  The partial sums of the
 // workgroups are added in order by the second kernel (6 us at 16384 x 5120; atomics would
 // change the result from run to run).  16384 x 5120 bf16 with dres, both kernels: 126 us,
-// 4.7 TB/s; 4096 x 16384: 111 us; 100000 x 64: 17 us (a workgroup per row 51), 60000 x 160:
-// 19 us (36).
-// Rows beyond 16384 spill: 273 us at 2234 x 30000, 3.4 times what the bytes take.
+// 4.7 TB/s (a copy 110); 4096 x 16384: 111 us; 100000 x 64: 16 us (a workgroup per row 51),
+// 60000 x 160: 19 us (36).
+// Rows beyond 16384 spill, dgamma's share and four chunks of the row in registers: 305 us
+// at 2234 x 30000, 3.5 times what its 469 MB take.
 template <typename T, int NCH, bool E8, int kLanes = 0>
 __global__ __launch_bounds__(kLanes ? 256 : 1024) void rmsnorm_q8_vjp_kernel(NormVjpArgs a) {
   constexpr bool kAhead = NCH == 1;

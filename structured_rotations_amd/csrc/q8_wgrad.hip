@@ -8,9 +8,11 @@
 // bf16 and so is every product.  Times an fp32 scale it has up to 28 bits, and
 // x is a sum of bf16 parts, one product each: three parts (24 bits) for fp32
 // results, one for bf16 results, which adds an error as large as the result's
-// own rounding (in all 1.4 times it; a second part takes 56 us instead of 40
-// at 1500 x 4099 x 1037).  Up to one step of rows, where writing dw bounds the
-// time, bf16 results take two parts.
+// own rounding (in all 2.35e-3 of the result where that alone is 1.66e-3; x's
+// codes are off by 2^-5 of it).  Two parts take 69 us instead of 40 at
+// 1500 x 4099 x 1037 and 1158 instead of 465 at 16384 x 4096 x 4096; who wants
+// them asks for an fp32 result.  Up to one step of rows, where writing dw bounds
+// the time, bf16 results take two parts.
 //
 // Both operands are stored along the other axis than the one summed over:
 // they stay that way in LDS ([m][n], [m][k]) and the transposing LDS read
@@ -416,10 +418,12 @@ constexpr int kSmallK(int parts) { return parts == 1 ? 4 : 2; }
 // the tile is the large one (8 fragments of dy by kBigK of x per wave) if its
 // rounds over the 256 compute units take less time than the small one's (4 by
 // kSmallK): per round 2.7 times the small one's with one part, 1.8 with three.
-// 4096 rows, n = 4096, one part: k = 2048 small 80 us, large 103 (one round of
-// the large against two); k = 2304 119 and 104 (against three), 3328 148 and
-// 105; 16384 x 4096 x 4096 608 and 421.  Three parts: k = 2048 219 and 198,
-// 2560 274 and 287.
+// 4096 rows, n = 4096, one part: k = 2048 small 78 us, large 103 (one round of
+// the large against two); k = 2304 118 and 104 (against three), 3328 147 and
+// 107; 16384 x 4096 x 4096 608 and 421.  Three parts: k = 2048 222 and 204,
+// 2560 278 and 304.  For few rows, which the stores of dw bound, the rule is not
+// as good: 64 x 8192 x 4096, fp32 results, E8M0 40 and 46 (large taken), three
+// parts 57 and 66; bf16 results 31 and 28.
 struct WgradShape {
   bool big;
   int splits, m_per_split;
