@@ -446,6 +446,140 @@ harp_status harp_matmul_q8_wgrad(const void* dy, int64_t lddy, const uint8_t* x,
                                  size_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Rotated attention with a cache in 4 bits: heads are normed, given their
+ * position and rotated in one pass, their keys and values are kept in 4 bits
+ * as they are written, and attention reads the 4-bit cache
+ * [TS §1-§3, RHT: the rotation's purpose is low-bit storage of what it mixes].
+ *
+ * Heads.  An array of `tokens` x `heads` x d values, F32 or BF16, is given by
+ * its first element, the distance of tokens and that of heads (elements; a
+ * head's d values are contiguous), so that the queries, keys and values that
+ * lie side by side in a projection's output are used as they are.  Either a
+ * token's heads lie within the distance of tokens, or a head's tokens within
+ * the distance of heads.  Any alignment to elements is computed; 16-byte
+ * aligned heads are fastest.  tokens at most 2^30, heads at most 65535.
+ * ---------------------------------------------------------------------- */
+
+/* Norm, position and rotation of the heads of queries and keys.  For a head x
+ * of a token at position p:
+ *   u = gamma * x / sqrt(mean(x^2) + eps)           (gamma NULL: all ones)
+ *   of the first 2 `pairs` values, pair j is turned by the angle p freqs[j]:
+ *     (a, b) -> (a cos - b sin, a sin + b cos),
+ *     (a, b) = (u[j], u[j + pairs]), or, interleaved != 0, (u[2j], u[2j + 1])
+ *   signs given:  y = H_d (signs * u)  with the normalised Sylvester H_d.
+ * Queries and keys that share signs keep their products q . k.
+ * gamma_q, gamma_k: d values of io_dtype.  positions: one per token, int32 or
+ * int64 (wide_positions != 0), of magnitude up to 2^31.  freqs: `pairs` fp64
+ * values, radians per position (at most 8 in magnitude).  signs: d int8, +1 or -1.
+ * Computed in fp32 (squares beyond its range included, as in harp_rmsnorm_q8),
+ * angles in fp64 until they are reduced; y is rounded once.
+ * d: a multiple of 8 up to 512, with signs a power of two; pairs: a multiple
+ * of 8, 2 pairs <= d (0: no turn).  k NULL (k_heads 0): queries only.  q_out
+ * may be q and k_out k, with the same distances; other overlaps are refused.
+ * tokens == 0 returns HARP_OK without a launch. */
+harp_status harp_qk_norm_rope(const void* q, int64_t q_token, int64_t q_head, int64_t q_heads, const void* k,
+                              int64_t k_token, int64_t k_head, int64_t k_heads, int64_t tokens, int64_t d,
+                              harp_dtype io_dtype, const void* positions, int32_t wide_positions,
+                              const double* freqs, int64_t pairs, int32_t interleaved, const void* gamma_q,
+                              const void* gamma_k, float eps, const int8_t* signs, void* q_out, int64_t qo_token,
+                              int64_t qo_head, void* k_out, int64_t ko_token, int64_t ko_head, hipStream_t stream);
+
+/* Its reverse mode, from the same inputs and the gradients dyq, dyk of q_out
+ * and k_out:  with n = x r, r = 1 / sqrt(mean(x^2) + eps), and g = dy rotated
+ * back and turned back,
+ *   dx = r (gamma * g - n mean(gamma * g * n)),
+ *   dgamma = sum over tokens and heads of g * n   (fp32, d values, overwritten).
+ * dq may be dyq (dk dyk) or q (k), with the same distances.  dgamma_q,
+ * dgamma_k: each may be NULL (not computed).  Sums in fp32, in a fixed order.
+ * workspace: harp_qk_norm_rope_vjp_workspace() bytes (-1: sizes out of range),
+ * 4-byte aligned, needed with a dgamma only.  tokens == 0 writes zeros to the
+ * dgammas. */
+int64_t harp_qk_norm_rope_vjp_workspace(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t d);
+harp_status harp_qk_norm_rope_vjp(const void* q, int64_t q_token, int64_t q_head, int64_t q_heads, const void* k,
+                                  int64_t k_token, int64_t k_head, int64_t k_heads, int64_t tokens, int64_t d,
+                                  harp_dtype io_dtype, const void* positions, int32_t wide_positions,
+                                  const double* freqs, int64_t pairs, int32_t interleaved, const void* gamma_q,
+                                  const void* gamma_k, float eps, const int8_t* signs, const void* dyq,
+                                  int64_t dyq_token, int64_t dyq_head, const void* dyk, int64_t dyk_token,
+                                  int64_t dyk_head, void* dq, int64_t dq_token, int64_t dq_head, void* dk,
+                                  int64_t dk_token, int64_t dk_head, float* dgamma_q, float* dgamma_k,
+                                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The cache.  Keys and values are kept in pages of page_size tokens.  Of each,
+ *   codes:  [pages][kv_heads][page_size][d / 2] bytes, two E2M1 codes each (the
+ *           even column in the lower half; 0 .5 1 1.5 2 3 4 6 and a sign bit),
+ *   scales: [pages][kv_heads][page_size][d / 32] bytes, E8M0: 2^(byte - 127),
+ *           255 = NaN,
+ * contiguous within a page; pages are `..._page` bytes apart (of any order of
+ * layers and of keys and values in one buffer).  Bases and distances are
+ * multiples of 16.  d is a multiple of 32 up to 256, page_size a power of two
+ * from 16 to 2^20.
+ *
+ * Coding rule, for each 32 values along the head: scale = the smallest power
+ * of two with max|v| <= 6 scale, at least 2^-120; code = v / scale rounded to
+ * nearest, ties to even, with v's sign.  A block that holds a NaN, an infinity
+ * or a magnitude of 1.75 * 2^127 or more has scale 255, codes 0, and is NaN.
+ *
+ * The plan.  A call concerns `sequences` sequences.  lengths[b]: how many tokens
+ * sequence b has, those of the call included.  starts (sequences + 1 values,
+ * not decreasing, from 0): rows starts[b] .. starts[b + 1] - 1 of the call's
+ * arrays are the last tokens of sequence b.  table[b][i] (i < width, rows
+ * ld_table apart): the page that holds its tokens i page_size and on.  All
+ * int32, on the device.  Entries of the table behind a sequence's length are
+ * not read.  Sequences may share pages; two of one call must not write the
+ * same place.  Whatever the three arrays hold, nothing outside the cache, the
+ * table and the rows is read or written: rows from starts[sequences] on are
+ * left as they are (read but not used); a row before its sequence's beginning
+ * is not written to the cache, reads as zeros and sees no key; a place whose
+ * page is outside 0 .. pages - 1 or beyond the table is not written, and reads
+ * as NaN.
+ * sequences, width at most 2^24, kv_heads at most 65535, tokens x q_heads and
+ * sequences x kv_heads at most 2^30. */
+
+/* Writes the call's keys and values (tokens x kv_heads x d, io_dtype). */
+harp_status harp_kv4_write(const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                           int64_t v_head, int64_t tokens, harp_dtype io_dtype, uint8_t* k_codes, int64_t kc_page,
+                           uint8_t* k_scales, int64_t ks_page, uint8_t* v_codes, int64_t vc_page, uint8_t* v_scales,
+                           int64_t vs_page, int64_t pages, int64_t kv_heads, int64_t page_size, int64_t d,
+                           const int32_t* starts, const int32_t* lengths, const int32_t* table, int64_t ld_table,
+                           int64_t sequences, int64_t width, hipStream_t stream);
+
+/* Reads the call's keys and values back, as the values that the cache stands
+ * for (exact in BF16 and F32). */
+harp_status harp_kv4_read(const uint8_t* k_codes, int64_t kc_page, const uint8_t* k_scales, int64_t ks_page,
+                          const uint8_t* v_codes, int64_t vc_page, const uint8_t* v_scales, int64_t vs_page,
+                          int64_t pages, int64_t kv_heads, int64_t page_size, int64_t d, const int32_t* starts,
+                          const int32_t* lengths, const int32_t* table, int64_t ld_table, int64_t sequences,
+                          int64_t width, void* k, int64_t k_token, int64_t k_head, void* v, int64_t v_token,
+                          int64_t v_head, int64_t tokens, harp_dtype io_dtype, hipStream_t stream);
+
+/* Attention of the call's queries (tokens x q_heads x d, BF16; q_heads a
+ * multiple of kv_heads, head h uses key head h / (q_heads / kv_heads)) over the
+ * cache.  The token at position p of its sequence sees the keys j with
+ *   j < lengths[b],  j <= p (causal != 0),  j > p - window (window > 0):
+ *   z_j = scale q . k_j,  out = sum exp(z_j) v_j / sum exp(z_j),
+ *   lse = ln sum exp(z_j)   (fp32, tokens x q_heads, contiguous; NULL: none).
+ * A row that sees no key: out = 0, lse = -infinity.  A key that a row does not
+ * see has no effect on it, whatever the cache holds there, with one exception:
+ * scales of 253 and 254 whose values exceed BF16's range (harp_kv4_write makes
+ * none) within a sequence's length.  scale > 0, finite.  Sums in fp32; the
+ * weights exp(z_j - max) are rounded to BF16 for the product with the values.
+ * The result of a call does not depend on the order in which its parts are
+ * computed.  out: BF16, must not overlap any input.
+ * workspace: harp_kv4_attention_workspace() bytes (may be 0; -1: sizes out of
+ * range), 16-byte aligned. */
+int64_t harp_kv4_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d,
+                                     int64_t page_size, int64_t sequences, int64_t width);
+harp_status harp_kv4_attention(const void* q, int64_t q_token, int64_t q_head, int64_t tokens, int64_t q_heads,
+                               const uint8_t* k_codes, int64_t kc_page, const uint8_t* k_scales, int64_t ks_page,
+                               const uint8_t* v_codes, int64_t vc_page, const uint8_t* v_scales, int64_t vs_page,
+                               int64_t pages, int64_t kv_heads, int64_t page_size, int64_t d, const int32_t* starts,
+                               const int32_t* lengths, const int32_t* table, int64_t ld_table, int64_t sequences,
+                               int64_t width, float scale, int32_t causal, int64_t window, void* out,
+                               int64_t out_token, int64_t out_head, float* lse, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Diagnostics (host).
  * ---------------------------------------------------------------------- */
 const char* harp_status_str(harp_status st);

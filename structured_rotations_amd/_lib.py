@@ -59,6 +59,9 @@ class HarpError(RuntimeError):
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
+_HEADS = (_P, _I64, _I64)                                  # an array of heads and its two distances
+_CACHE = (_P, _I64) * 4 + (_I64,) * 4
+_PLAN = (_P, _P, _P, _I64, _I64, _I64)
 _SIG = {
     "harp_theta_count": (_I64, [ctypes.POINTER(Schedule), _I64]),
     "harp_gauss_count": (_I64, [ctypes.POINTER(Schedule), _I64]),
@@ -95,6 +98,17 @@ _SIG = {
     "harp_matmul_q8_wgrad_workspace": (_I64, [_I64, _I64, _I64]),
     "harp_matmul_q8_wgrad": (_I32, [_P, _I64, _P, _I64, _P, _I32, _I64, _I64, _I64, _P, _I64, _I32, _P,
                                     ctypes.c_size_t, _P]),
+    "harp_qk_norm_rope": (_I32, [*_HEADS, _I64, *_HEADS, _I64, _I64, _I64, _I32, _P, _I32, _P, _I64, _I32, _P, _P,
+                                 ctypes.c_float, _P, *_HEADS, *_HEADS, _P]),
+    "harp_qk_norm_rope_vjp_workspace": (_I64, [_I64, _I64, _I64, _I64]),
+    "harp_qk_norm_rope_vjp": (_I32, [*_HEADS, _I64, *_HEADS, _I64, _I64, _I64, _I32, _P, _I32, _P, _I64, _I32, _P, _P,
+                                     ctypes.c_float, _P, *_HEADS, *_HEADS, *_HEADS, *_HEADS, _P, _P, _P,
+                                     ctypes.c_size_t, _P]),
+    "harp_kv4_write": (_I32, [*_HEADS, *_HEADS, _I64, _I32, *_CACHE, *_PLAN, _P]),
+    "harp_kv4_read": (_I32, [*_CACHE, *_PLAN, *_HEADS, *_HEADS, _I64, _I32, _P]),
+    "harp_kv4_attention_workspace": (_I64, [_I64] * 7),
+    "harp_kv4_attention": (_I32, [*_HEADS, _I64, _I64, *_CACHE, *_PLAN, ctypes.c_float, _I32, _I64, *_HEADS, _P, _P,
+                                  ctypes.c_size_t, _P]),
     "harp_status_str": (ctypes.c_char_p, [_I32]),
     "harp_last_error": (ctypes.c_char_p, []),
     "harp_version": (ctypes.c_char_p, []),

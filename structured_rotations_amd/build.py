@@ -26,7 +26,8 @@ LIB = os.path.join(PKG, "libharp.so")
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 HIP_SOURCES = ["api.hip", "apply_tile.hip", "apply_mfma.hip", "apply_valu.hip", "apply_fast.hip", "rht.hip", "rotate_cols.hip", "col_dense.hip", "materialize.hip", "decode.hip", "vjp.hip",
-               "q8_api.hip", "q8_rows.hip", "q8_matmul.hip", "q8_wgrad.hip"]
+               "q8_api.hip", "q8_rows.hip", "q8_matmul.hip", "q8_wgrad.hip",
+               "kv4_api.hip", "qk_rows.hip", "kv4_rows.hip", "kv4_attention.hip"]
 CXX_SOURCES = ["plan.cpp"]
 
 DEVICE_FLAGS = [

@@ -1,0 +1,566 @@
+// Attention over a cache in 4 bits.
+//
+// For one key head, the rows of a sequence are its call's tokens times the
+// query heads that share the key head.  With S = K Q^T (keys by rows) and
+// O^T = V^T P^T, the matrix instructions' layouts fit one another: what a lane
+// holds of S, for one row of Q and its keys, is what it has to give of P, and
+// both products have a lane's row of Q in common, so the softmax needs no
+// exchange but the maximum.  The order of keys within a step is free; it is
+// the one in which S comes out.
+//
+// K's and V's codes become bf16 exactly (E2M1 times a power of two) by one
+// conversion instruction for two values, scale included.  A lane's piece of K
+// is as it is in memory; V has to be transposed: a lane takes the same columns
+// of 8 keys and pairs them by byte permutations.
+//
+// Scores, maxima, sums and accumulators are fp32.  The weights are rounded to
+// bf16 for the product with V: each is off by at most 2^-9 of itself, the result
+// by about as much as its own rounding to bf16 adds.
+#include <algorithm>
+#include <cmath>
+
+#include "kv4.h"
+#include "q8.h"
+
+namespace harp {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ bf16x8_t as_frag(const uint32_t (&w)[4]) {
+  bf16x8_t r;
+  __builtin_memcpy(&r, w, 16);
+  return r;
+}
+__device__ __forceinline__ f32x4 mfma16(const bf16x8_t& a, const bf16x8_t& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+// Byte kByte's two codes, times 2^(e - 127), e in the exponent's place.
+template <int kByte>
+__device__ __forceinline__ uint32_t widen4(uint32_t codes, uint32_t e) {
+  const bf16x2_t v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, __uint_as_float(e), kByte);
+  uint32_t w;
+  __builtin_memcpy(&w, &v, 4);
+  return w;
+}
+// Largest over the lanes that are 16 and 32 apart, in every one of them.
+__device__ __forceinline__ float max_of_groups(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float sum_of_groups(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) |
+                   (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32);
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// The rows of one workgroup's tile, all of one sequence, and the keys that
+// they see: row r (0 ..) of the sequence's is token r / group, head r % group.
+struct TileRows {
+  int seq, first_token, tokens, len;  // the call's array; the sequence's length
+  int64_t row0, rows;                 // the tile's first row; the sequence's
+  __device__ __forceinline__ int pos(int64_t token) const { return (int)((int64_t)len - tokens + token); }
+};
+// Tiles of kRows rows: sequence b's begin at starts[b] group / kRows + b, which
+// leaves it as many as it needs, whatever its neighbours have.
+__device__ __forceinline__ bool tile_rows(const Attn4Args& a, int64_t tile, int tile_size, TileRows* t) {
+  const auto first = [&](int b) { return (int64_t)a.plan.starts[b] * a.group / tile_size + b; };
+  const int b = __builtin_amdgcn_readfirstlane(last_at_most(a.plan.sequences, tile, first));
+  const int s0 = min(max(a.plan.starts[b], 0), a.tokens), s1 = min(max(a.plan.starts[b + 1], s0), a.tokens);
+  t->seq = b;
+  t->first_token = s0;
+  t->tokens = s1 - s0;
+  t->len = max(a.plan.lengths[b], 0);
+  t->rows = (int64_t)t->tokens * a.group;
+  t->row0 = (tile - first(b)) * tile_size;
+  return t->row0 >= 0 && t->row0 < t->rows;
+}
+// The keys lo .. hi - 1 that the token at position pos sees.  Beyond what the
+// table has room for (`cap` keys), one place stands for all the others: it has
+// no page, and so is NaN.
+struct Sees {
+  int lo, hi;
+};
+__device__ __forceinline__ Sees sees(const Attn4Args& a, int len, int pos, int64_t cap) {
+  if (pos < 0) return {0, 0};
+  int64_t hi = a.causal ? (int64_t)pos + 1 : len, lo = a.window ? max(0, pos - a.window + 1) : 0;
+  return {(int)min(lo, cap), (int)min(hi, cap + 1)};
+}
+
+// ------------------------------------------------------------- few rows
+// A wave takes 32 keys at a time, every fourth of its workgroup's, with its
+// loads straight into the layouts of the matrix instructions, one step ahead.
+template <int ND>
+struct Step4 {
+  static constexpr int kUnit = ND % 4 == 0 ? 4 : ND % 2 == 0 ? 2 : 1;  // words of K per load
+  static constexpr int kUnits = ND / kUnit;
+  static constexpr int kWords = ND / 4, kHalf = (ND >> 1) & 1, kByte = ND & 1;  // how V's columns go to 16 lanes
+  uint32_t k[2][ND];
+  uint32_t ks[2][kUnits];
+  uint32_t v[8][kWords + kHalf + kByte];
+  uint32_t vs[2][ND + 1];
+};
+
+template <int ND, int NQ>
+__global__ __launch_bounds__(256) void kv4_attention_kernel(Attn4Args a, int splits, int64_t unit0) {
+  using Step = Step4<ND>;
+  constexpr int kRow = ND * 16, kTileRows = 16 * NQ, kAcc = 2 * ND, kD = ND * 32;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
+  // one workgroup: a part of the keys of a key head of a tile of rows
+  const int64_t unit = unit0 + blockIdx.x, rest = unit / splits, tile = rest / a.cache.heads;
+  const int split = (int)(unit - rest * splits), kvh = (int)(rest - tile * a.cache.heads);
+  TileRows t;
+  if (!tile_rows(a, tile, kTileRows, &t)) return;
+  const int ps_log2 = a.cache.page_log2;
+  const int64_t cap = (int64_t)a.plan.width << ps_log2;
+  const int64_t row1 = min(t.row0 + kTileRows, t.rows);
+
+  // keys of the tile, and this workgroup's share of them in steps of 32
+  const int tok0 = (int)(t.row0 / a.group), tok1 = (int)((row1 - 1) / a.group);
+  const Sees s0 = sees(a, t.len, t.pos(tok0), cap), s1 = sees(a, t.len, t.pos(tok1), cap);
+  const int hi_all = max(s0.hi, s1.hi), lo_all = t.pos(tok0) < 0 ? 0 : s0.lo;
+  const int base = lo_all & ~31;
+  const int steps = hi_all > lo_all ? (int)(((int64_t)hi_all - base + 31) >> 5) : 0;
+  const int per = ((steps + splits * 4 - 1) / (splits * 4)) * 4;
+  const int step0 = min(steps, split * per), step1 = min(steps, step0 + per);
+
+  // this lane's row of each tile of 16: its queries, its keys
+  Sees row_sees[NQ];
+  bf16x8_t q[NQ][ND];
+  int hi_min = hi_all, lo_max = lo_all;
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const int64_t r = t.row0 + n * 16 + c16;
+    const bool has = r < t.rows;
+    const int tok = has ? (int)(r / a.group) : 0, gh = has ? (int)(r - (int64_t)tok * a.group) : 0;
+    row_sees[n] = has ? sees(a, t.len, t.pos(tok), cap) : Sees{0, 0};
+    if (has) {
+      hi_min = min(hi_min, row_sees[n].hi);
+      lo_max = max(lo_max, row_sees[n].lo);
+    }
+    const uint16_t* p = a.q + (int64_t)(t.first_token + tok) * a.q_token + (int64_t)(kvh * a.group + gh) * a.q_head;
+#pragma unroll
+    for (int s = 0; s < ND; ++s) {
+      const int u = s / Step::kUnit, in = s % Step::kUnit;
+      const int col = (u * 4 + g) * Step::kUnit * 8 + in * 8;
+      Raw8<uint16_t> w;
+      w.fill(0);
+      if (has) w.load(p + col, 8);
+      q[n][s] = as_frag(w.w);
+    }
+  }
+  // what the rows that see most and least leave to be masked
+#pragma unroll
+  for (int o = 1; o < 16; o *= 2) {
+    hi_min = min(hi_min, __shfl_xor(hi_min, o));
+    lo_max = max(lo_max, __shfl_xor(lo_max, o));
+  }
+  hi_min = __builtin_amdgcn_readfirstlane(hi_min);
+  lo_max = __builtin_amdgcn_readfirstlane(lo_max);
+
+  f32x4 acc[NQ][kAcc];
+  float m[NQ], l[NQ];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    m[n] = -INFINITY;
+    l[n] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kAcc; ++i) acc[n][i] = f32x4{0, 0, 0, 0};
+  }
+  const float to_log2 = a.scale * kLog2e;
+
+  // Pages of this wave's next 32 steps, two to a step, in the lanes.
+  int pages = -1;
+  auto look_up = [&](int step) {
+    const int64_t key = (int64_t)base + ((int64_t)step + (lane >> 1) * 4) * 32 + (lane & 1) * 16;
+    pages = key < hi_all ? page_of(a.cache, a.plan, t.seq, key >> ps_log2) : -1;
+  };
+  auto load = [&](Step& w, int step, int at) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int page = __builtin_amdgcn_readlane(pages, 2 * at + s);
+      const uint32_t key = (uint32_t)base + (uint32_t)step * 32 + s * 16;
+      const int in_page = (int)(key & ((1u << ps_log2) - 1));
+      const int64_t row = ((int64_t)kvh << ps_log2) + in_page, pg = page < 0 ? 0 : page;
+      const uint8_t* kc = a.cache.k.codes + pg * a.cache.k.codes_page + row * kRow;
+      const uint8_t* ks = a.cache.k.scales + pg * a.cache.k.scales_page + row * ND;
+      const uint8_t* vc = a.cache.v.codes + pg * a.cache.v.codes_page + row * kRow;
+      const uint8_t* vs = a.cache.v.scales + pg * a.cache.v.scales_page + row * ND;
+#pragma unroll
+      for (int u = 0; u < Step::kUnits; ++u) {
+        const uint8_t* p = kc + c16 * kRow + (u * 4 + g) * Step::kUnit * 4;
+        if constexpr (Step::kUnit == 4) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w.k[s][u * 4 + i] = x[i];
+        } else if constexpr (Step::kUnit == 2) {
+          const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+          w.k[s][u * 2] = x[0];
+          w.k[s][u * 2 + 1] = x[1];
+        } else {
+          w.k[s][u] = *reinterpret_cast<const uint32_t*>(p);
+        }
+        const uint32_t e = ks[c16 * ND + (u * 4 + g) * Step::kUnit / 4];
+        w.ks[s][u] = page < 0 ? 255u : e;  // no page: NaN
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* p = vc + (4 * g + i) * kRow;
+#pragma unroll
+        for (int j = 0; j < Step::kWords; ++j)
+          w.v[4 * s + i][j] = *reinterpret_cast<const uint32_t*>(p + 64 * j + 4 * c16);
+        if constexpr (Step::kHalf)
+          w.v[4 * s + i][Step::kWords] = *reinterpret_cast<const uint16_t*>(p + 64 * Step::kWords + 2 * c16);
+        if constexpr (Step::kByte) w.v[4 * s + i][Step::kWords + Step::kHalf] = p[kRow - 16 + c16];
+      }
+#pragma unroll
+      for (int i = 0; i < ND; ++i) {
+        const uint32_t e = reinterpret_cast<const uint32_t*>(vs + 4 * g * ND)[i];
+        w.vs[s][i] = page < 0 ? 0u : e;  // another page's: nothing that is not finite
+      }
+      w.vs[s][ND] = 0;
+    }
+  };
+
+  auto compute = [&](const Step& w, int step) {
+    const int k0 = (int)((uint32_t)base + (uint32_t)step * 32);
+    // scores: rows of keys, columns of queries
+    f32x4 z[NQ][2];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) z[n][0] = z[n][1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < ND; ++i) {
+        const uint32_t e = w.ks[s][i / Step::kUnit] << 23;
+        const uint32_t f[4] = {widen4<0>(w.k[s][i], e), widen4<1>(w.k[s][i], e), widen4<2>(w.k[s][i], e),
+                               widen4<3>(w.k[s][i], e)};
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) z[n][s] = mfma16(as_frag(f), q[n][i], z[n][s]);
+      }
+    if (k0 < lo_max || k0 + 32 > hi_min) {  // some row does not see all of these keys
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const int lo = row_sees[n].lo - k0, hi = row_sees[n].hi - k0;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int j = 16 * s + 4 * g + r;
+            z[n][s][r] = j >= lo && j < hi ? z[n][s][r] : -INFINITY;
+          }
+      }
+    }
+    bf16x8_t p[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      float top = z[n][0][0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = fmaxf(top, z[n][i >> 2][i & 3]);
+      top *= to_log2;
+      if (__any(top > m[n])) {
+        const float now = fmaxf(m[n], max_of_groups(top));
+        const float shrink = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[n] - now);
+        m[n] = now;
+        l[n] *= shrink;
+#pragma unroll
+        for (int i = 0; i < kAcc; ++i) acc[n][i] *= shrink;
+      }
+      const float less = m[n] == -INFINITY ? 0.0f : m[n];
+      float e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        e[i] = __builtin_amdgcn_exp2f(fmaf(z[n][i >> 2][i & 3], to_log2, -less));
+        l[n] += e[i];
+      }
+      const uint32_t f[4] = {pack_bf16x2_hw(e[0], e[1]), pack_bf16x2_hw(e[2], e[3]), pack_bf16x2_hw(e[4], e[5]),
+                             pack_bf16x2_hw(e[6], e[7])};
+      p[n] = as_frag(f);
+    }
+    // V's columns by parts: 8 columns to a lane (words), 4 (halves), 2 (bytes)
+    const bool edge = k0 < lo_all || k0 + 32 > hi_all;
+#pragma unroll
+    for (int part = 0; part < Step::kWords + Step::kHalf + Step::kByte; ++part) {
+      const bool word = part < Step::kWords, half = !word && part == Step::kWords && Step::kHalf;
+      const int bytes = word ? 4 : half ? 2 : 1;
+      const int tile0 = word ? part * 8 : Step::kWords * 8 + (half ? 0 : Step::kHalf * 4);
+      const int blk0 = word ? part * 4 : half ? Step::kWords * 4 : ND - 1;
+      const int blk = word ? c16 >> 2 : half ? c16 >> 3 : 0;
+      uint32_t e[8], most = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = ND * (i & 3) + blk0;  // byte of the four keys' scales, less the lane's block
+        const uint64_t two = (uint64_t)w.vs[i >> 2][at / 4] | (uint64_t)w.vs[i >> 2][at / 4 + 1] << 32;
+        e[i] = (uint32_t)(two >> (8 * (at % 4 + blk))) & 0xff;
+        most = max(most, e[i]);
+      }
+      uint32_t nan_keys = 0;
+      if (edge) {  // what lies outside may hold anything
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int j = k0 + 16 * (i >> 2) + 4 * g + (i & 3);
+          e[i] = j >= lo_all && j < hi_all ? e[i] : 0;
+        }
+      }
+      const bool some_nan = __any(most == 255);
+      if (some_nan) {
+        // NaN times a weight of 0 would reach rows that do not see the key: such a block
+        // counts as 0 here, and below is put where the row does see it
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (e[i] == 255) {
+            nan_keys |= 1u << i;
+            e[i] = 0;
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] <<= 23;
+      auto column = [&](auto byte_c) {
+        constexpr int byte = decltype(byte_c)::value;
+        uint32_t even[4], odd[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x = widen4<byte>(w.v[2 * j][part], e[2 * j]);
+          const uint32_t y = widen4<byte>(w.v[2 * j + 1][part], e[2 * j + 1]);
+          even[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+          odd[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+        }
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          acc[n][tile0 + 2 * byte] = mfma16(as_frag(even), p[n], acc[n][tile0 + 2 * byte]);
+          acc[n][tile0 + 2 * byte + 1] = mfma16(as_frag(odd), p[n], acc[n][tile0 + 2 * byte + 1]);
+        }
+      };
+      column(std::integral_constant<int, 0>{});
+      if (bytes > 1) column(std::integral_constant<int, 1>{});
+      if (bytes > 2) {
+        column(std::integral_constant<int, 2>{});
+        column(std::integral_constant<int, 3>{});
+      }
+      if (some_nan) {
+        // lane c16 of the columns is rho = 4 g' + r of the results' lanes
+        for (int i = 0; i < 8; ++i)
+          for (int gg = 0; gg < 4; ++gg) {
+            const uint32_t who = (uint32_t)(__ballot(nan_keys >> i & 1) >> (16 * gg)) & 0xffff;
+            if (who == 0) continue;
+            const int j = k0 + 16 * (i >> 2) + 4 * gg + (i & 3);
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+              const bool seen = j >= row_sees[n].lo && j < row_sees[n].hi;
+#pragma unroll
+              for (int x = 0; x < 2 * bytes; ++x)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  if (seen && (who >> (4 * g + r) & 1)) acc[n][tile0 + x][r] = __uint_as_float(0x7fc00000u);
+            }
+          }
+      }
+    }
+  };
+
+  if (step0 + wave < step1) {
+    Step w0, w1;
+    int step = step0 + wave, at = 0;
+    look_up(step);
+    load(w0, step, at);
+    while (true) {
+      int next = step + 4;
+      if (next < step1) {
+        if (++at == 32) {
+          at = 0;
+          look_up(next);
+        }
+        load(w1, next, at);
+      }
+      compute(w0, step);
+      step = next;
+      if (step >= step1) break;
+      next = step + 4;
+      if (next < step1) {
+        if (++at == 32) {
+          at = 0;
+          look_up(next);
+        }
+        load(w0, next, at);
+      }
+      compute(w1, step);
+      step = next;
+      if (step >= step1) break;
+    }
+  }
+
+  // The waves' parts, one tile of 16 rows after the other, in order.
+  constexpr int kPad = kD + 4;
+  __shared__ float share[4][16][kPad];
+  __shared__ float stat[4][16][2];
+  const int64_t all_rows = (int64_t)a.tokens * a.q_heads;
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    l[n] = sum_of_groups(l[n]);
+    __syncthreads();
+    if (g == 0) {
+      stat[wave][c16][0] = m[n];
+      stat[wave][c16][1] = l[n];
+    }
+#pragma unroll
+    for (int i = 0; i < kAcc; ++i) {
+      const bool word = i < Step::kWords * 8, half = !word && i < Step::kWords * 8 + Step::kHalf * 4;
+      const int wide = word ? 8 : half ? 4 : 2;
+      const int first = word ? i / 8 * 128 : Step::kWords * 128 + (half ? 0 : Step::kHalf * 64);
+      const int in = word ? i % 8 : half ? i - Step::kWords * 8 : i - Step::kWords * 8 - Step::kHalf * 4;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) share[wave][c16][first + (4 * g + r) * wide + in] = acc[n][i][r];
+    }
+    __syncthreads();
+    // a row's 8 columns per thread
+    for (int u = threadIdx.x; u < 16 * kD / 8; u += 256) {
+      const int rr = u / (kD / 8), col = (u - rr * (kD / 8)) * 8;
+      const int64_t r = t.row0 + n * 16 + rr;
+      if (r >= t.rows) continue;
+      float top = stat[0][rr][0];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) top = fmaxf(top, stat[w][rr][0]);
+      const float less = top == -INFINITY ? 0.0f : top;
+      float sum = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = __builtin_amdgcn_exp2f(stat[w][rr][0] - less);
+        const float lw = stat[w][rr][1];
+        if (lw == 0.0f) continue;  // nothing seen
+        sum += f * lw;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] += f * share[w][rr][col + i];
+      }
+      const int tok = (int)(r / a.group), gh = (int)(r - (int64_t)tok * a.group);
+      const int64_t token = t.first_token + tok, head = (int64_t)kvh * a.group + gh;
+      const int64_t row = token * a.q_heads + head;
+      if (splits > 1) {
+        float* p = a.partial + ((int64_t)split * all_rows + row) * kD + col;
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) *reinterpret_cast<f32x4*>(p + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
+        if (col == 0) {
+          float* st = a.partial + (int64_t)splits * all_rows * kD + ((int64_t)split * all_rows + row) * 2;
+          st[0] = top;
+          st[1] = sum;
+        }
+      } else {
+        const Sees s = sees(a, t.len, t.pos(tok), cap);
+        // no key: 0; keys of weight 0 only (all scores -infinity): 0 / 0
+        const float inv = s.hi > s.lo ? 1.0f / sum : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = s.hi > s.lo ? o[i] * inv : 0.0f;
+        store8(a.out + token * a.out_token + head * a.out_head + col, o);
+        if (a.lse && col == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+      }
+    }
+  }
+}
+
+// The parts of a row, added in order: a wave per row.
+__global__ __launch_bounds__(256) void kv4_join_kernel(Attn4Args a, int splits) {
+  const int64_t all_rows = (int64_t)a.tokens * a.q_heads;
+  const int lane = threadIdx.x & 63, d = a.cache.d;
+  for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < all_rows; row += (int64_t)gridDim.x * 4) {
+    const int token = (int)(row / a.q_heads), head = (int)(row - (int64_t)token * a.q_heads);
+    const int b = sequence_of(a.plan, token);
+    const int s0 = min(max(a.plan.starts[b], 0), a.tokens), s1 = min(max(a.plan.starts[b + 1], s0), a.tokens);
+    if (token < s0 || token >= s1) continue;
+    const int len = max(a.plan.lengths[b], 0);
+    const int64_t cap = (int64_t)a.plan.width << a.cache.page_log2;
+    const Sees s = sees(a, len, (int)((int64_t)len - (s1 - token)), cap);
+    const float* st = a.partial + (int64_t)splits * all_rows * d + row * 2;
+    float top = -INFINITY;
+    for (int i = lane; i < splits; i += 64) top = fmaxf(top, st[(int64_t)i * all_rows * 2]);
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
+    const float less = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    f32x4 o = {0, 0, 0, 0};
+    const float* p = a.partial + row * d + 4 * lane;
+    for (int i = 0; i < splits; ++i) {
+      const float l = st[(int64_t)i * all_rows * 2 + 1];
+      if (l == 0.0f) continue;
+      const float f = __builtin_amdgcn_exp2f(st[(int64_t)i * all_rows * 2] - less);
+      sum += f * l;
+      if (4 * lane < d) o += f * *reinterpret_cast<const f32x4*>(p + (int64_t)i * all_rows * d);
+    }
+    const float inv = s.hi > s.lo ? 1.0f / sum : 0.0f;
+    if (s.hi <= s.lo) o = f32x4{0, 0, 0, 0};
+    if (4 * lane < d) {
+      uint16_t* out = a.out + (int64_t)token * a.out_token + (int64_t)head * a.out_head + 4 * lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store1(out + i, o[i] * inv);
+    }
+    if (a.lse && lane == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+  }
+}
+
+// How a call is cut: 16 or 32 rows to a tile, and the keys in parts until the
+// chip has work enough, of 256 keys at least.
+struct Cut {
+  int tiles16, splits;  // tiles of 16 rows to a workgroup
+  int64_t tiles;
+};
+Cut cut_of(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t page_size, int64_t sequences, int64_t width) {
+  const int64_t group = q_heads / kv_heads, rows = tokens * group;
+  Cut c;
+  c.tiles16 = rows > 16 * sequences ? 2 : 1;
+  const int64_t size = 16 * c.tiles16;
+  c.tiles = rows / size + sequences;
+  const int64_t busy = std::max<int64_t>(1, std::min(c.tiles, std::max(rows / size, std::min(sequences, tokens))) * kv_heads);
+  const int64_t most = std::max<int64_t>(1, (width * page_size + 255) / 256);
+  c.splits = (int)std::min<int64_t>(std::min<int64_t>(most, 256), std::max<int64_t>(1, 1024 / busy));
+  return c;
+}
+
+template <int ND>
+hipError_t go(const Attn4Args& a, const Cut& c, hipStream_t stream) {
+  const int64_t units = c.tiles * a.cache.heads * c.splits;
+  constexpr int64_t kMost = 1 << 23;  // workgroups of a launch: 2^32 threads are refused
+  for (int64_t u = 0; u < units; u += kMost) {
+    const dim3 grid((unsigned)std::min(kMost, units - u));
+    if (c.tiles16 == 1) hipLaunchKernelGGL((kv4_attention_kernel<ND, 1>), grid, dim3(256), 0, stream, a, c.splits, u);
+    else hipLaunchKernelGGL((kv4_attention_kernel<ND, 2>), grid, dim3(256), 0, stream, a, c.splits, u);
+  }
+  if (c.splits > 1) {
+    const int64_t rows = (int64_t)a.tokens * a.q_heads;
+    hipLaunchKernelGGL(kv4_join_kernel, dim3((unsigned)std::min((rows + 3) / 4, kMost)), dim3(256), 0, stream, a,
+                       c.splits);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t kv4_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t page_size,
+                                int64_t sequences, int64_t width) {
+  if (tokens == 0 || sequences == 0) return 0;
+  const Cut c = cut_of(tokens, q_heads, kv_heads, page_size, sequences, width);
+  return c.splits == 1 ? 0 : tokens * q_heads * c.splits * (d + 2) * 4;
+}
+
+hipError_t launch_kv4_attention(const Attn4Args& a, hipStream_t stream) {
+  const Cut c = cut_of(a.tokens, a.q_heads, a.cache.heads, 1LL << a.cache.page_log2, a.plan.sequences, a.plan.width);
+  switch (a.cache.d / 32) {
+    case 1: return go<1>(a, c, stream);
+    case 2: return go<2>(a, c, stream);
+    case 3: return go<3>(a, c, stream);
+    case 4: return go<4>(a, c, stream);
+    case 5: return go<5>(a, c, stream);
+    case 6: return go<6>(a, c, stream);
+    case 7: return go<7>(a, c, stream);
+    default: return go<8>(a, c, stream);
+  }
+}
+
+}  // namespace harp
