@@ -56,9 +56,19 @@ __device__ __forceinline__ float sum_of_groups(float v) {
   a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
-__device__ __forceinline__ int64_t uniform64(int64_t v) {
-  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) |
-                   (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32);
+// An address that all lanes have in common, kept in scalar registers: loads add
+// the lane's offset themselves, where the compiler would add it before the loop
+// and the address to that, lane by lane.
+template <typename T>
+using Global = const __attribute__((address_space(1))) T*;
+__device__ __forceinline__ Global<uint8_t> common(const uint8_t* p) {
+  uint64_t at = reinterpret_cast<uint64_t>(p);
+  asm("" : "+s"(at));
+  return reinterpret_cast<Global<uint8_t>>(at);
+}
+template <typename T>
+__device__ __forceinline__ T load_at(Global<uint8_t> base, uint32_t lane_offset, int offset) {
+  return *reinterpret_cast<Global<T>>(base + lane_offset + offset);
 }
 
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -108,14 +118,20 @@ struct Step4 {
   uint32_t k[2][ND];
   uint32_t ks[2][kUnits];
   uint32_t v[8][kWords + kHalf + kByte];
-  uint32_t vs[2][ND + 1];
+  uint32_t vs[2][ND];
 };
 
+// Workgroups a compute unit is to have room for, which bounds the registers:
+// loads in flight are what these kernels live by (64 sequences of up to 8192, d
+// = 128: one wave per SIMD and what the compiler takes, 112 us; three, 90 us).
+constexpr int room_for(int nd, int nq) { return nq == 1 && nd <= 4 ? 3 : nd * nq <= 8 ? 2 : 1; }
+
 template <int ND, int NQ>
-__global__ __launch_bounds__(256) void kv4_attention_kernel(Attn4Args a, int splits, int64_t unit0) {
+__global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(Attn4Args a, int splits, int64_t unit0) {
   using Step = Step4<ND>;
   constexpr int kRow = ND * 16, kTileRows = 16 * NQ, kAcc = 2 * ND, kD = ND * 32;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // one workgroup: a part of the keys of a key head of a tile of rows
   const int64_t unit = unit0 + blockIdx.x, rest = unit / splits, tile = rest / a.cache.heads;
   const int split = (int)(unit - rest * splits), kvh = (int)(rest - tile * a.cache.heads);
@@ -185,52 +201,57 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Attn4Args a, int spl
     const int64_t key = (int64_t)base + ((int64_t)step + (lane >> 1) * 4) * 32 + (lane & 1) * 16;
     pages = key < hi_all ? page_of(a.cache, a.plan, t.seq, key >> ps_log2) : -1;
   };
+  // Lane's places in 16 keys' rows: unsigned 32-bit, so that loads take a base
+  // common to the lanes and an offset.
+  const uint32_t k_off = c16 * kRow + g * Step::kUnit * 4, ks_off = c16 * ND + g * Step::kUnit / 4;
+  const uint32_t v_off = 4 * g * kRow, vs_off = 4 * g * ND;
   auto load = [&](Step& w, int step, int at) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int page = __builtin_amdgcn_readlane(pages, 2 * at + s);
       const uint32_t key = (uint32_t)base + (uint32_t)step * 32 + s * 16;
-      const int in_page = (int)(key & ((1u << ps_log2) - 1));
+      const uint32_t in_page = key & ((1u << ps_log2) - 1);
       const int64_t row = ((int64_t)kvh << ps_log2) + in_page, pg = page < 0 ? 0 : page;
-      const uint8_t* kc = a.cache.k.codes + pg * a.cache.k.codes_page + row * kRow;
-      const uint8_t* ks = a.cache.k.scales + pg * a.cache.k.scales_page + row * ND;
-      const uint8_t* vc = a.cache.v.codes + pg * a.cache.v.codes_page + row * kRow;
-      const uint8_t* vs = a.cache.v.scales + pg * a.cache.v.scales_page + row * ND;
+      const auto kc = common(a.cache.k.codes + pg * a.cache.k.codes_page + row * kRow);
+      const auto ks = common(a.cache.k.scales + pg * a.cache.k.scales_page + row * ND);
+      const auto vc = common(a.cache.v.codes + pg * a.cache.v.codes_page + row * kRow);
+      const auto vs = common(a.cache.v.scales + pg * a.cache.v.scales_page + row * ND);
 #pragma unroll
       for (int u = 0; u < Step::kUnits; ++u) {
-        const uint8_t* p = kc + c16 * kRow + (u * 4 + g) * Step::kUnit * 4;
         if constexpr (Step::kUnit == 4) {
-          const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+          const u32x4 x = load_at<u32x4>(kc, k_off, u * 64);
 #pragma unroll
           for (int i = 0; i < 4; ++i) w.k[s][u * 4 + i] = x[i];
         } else if constexpr (Step::kUnit == 2) {
-          const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+          const u32x2 x = load_at<u32x2>(kc, k_off, u * 32);
           w.k[s][u * 2] = x[0];
           w.k[s][u * 2 + 1] = x[1];
         } else {
-          w.k[s][u] = *reinterpret_cast<const uint32_t*>(p);
+          w.k[s][u] = load_at<uint32_t>(kc, k_off, u * 16);
         }
-        const uint32_t e = ks[c16 * ND + (u * 4 + g) * Step::kUnit / 4];
+        const uint32_t e = load_at<uint8_t>(ks, ks_off, u * Step::kUnit);
         w.ks[s][u] = page < 0 ? 255u : e;  // no page: NaN
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint8_t* p = vc + (4 * g + i) * kRow;
 #pragma unroll
-        for (int j = 0; j < Step::kWords; ++j)
-          w.v[4 * s + i][j] = *reinterpret_cast<const uint32_t*>(p + 64 * j + 4 * c16);
+        for (int j = 0; j < Step::kWords; ++j) w.v[4 * s + i][j] = load_at<uint32_t>(vc, v_off + 4 * c16, i * kRow + 64 * j);
         if constexpr (Step::kHalf)
-          w.v[4 * s + i][Step::kWords] = *reinterpret_cast<const uint16_t*>(p + 64 * Step::kWords + 2 * c16);
-        if constexpr (Step::kByte) w.v[4 * s + i][Step::kWords + Step::kHalf] = p[kRow - 16 + c16];
+          w.v[4 * s + i][Step::kWords] = load_at<uint16_t>(vc, v_off + 2 * c16, i * kRow + 64 * Step::kWords);
+        if constexpr (Step::kByte)
+          w.v[4 * s + i][Step::kWords + Step::kHalf] = load_at<uint8_t>(vc, v_off + c16, i * kRow + kRow - 16);
       }
 #pragma unroll
       for (int i = 0; i < ND; ++i) {
-        const uint32_t e = reinterpret_cast<const uint32_t*>(vs + 4 * g * ND)[i];
+        const uint32_t e = load_at<uint32_t>(vs, vs_off, 4 * i);
         w.vs[s][i] = page < 0 ? 0u : e;  // another page's: nothing that is not finite
       }
-      w.vs[s][ND] = 0;
     }
   };
+
+  uint32_t poison[NQ];  // blocks of the row's result that are NaN
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) poison[n] = 0;
 
   auto compute = [&](const Step& w, int step) {
     const int k0 = (int)((uint32_t)base + (uint32_t)step * 32);
@@ -239,9 +260,9 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Attn4Args a, int spl
 #pragma unroll
     for (int n = 0; n < NQ; ++n) z[n][0] = z[n][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int i = 0; i < ND; ++i)
 #pragma unroll
-      for (int i = 0; i < ND; ++i) {
+      for (int s = 0; s < 2; ++s) {
         const uint32_t e = w.ks[s][i / Step::kUnit] << 23;
         const uint32_t f[4] = {widen4<0>(w.k[s][i], e), widen4<1>(w.k[s][i], e), widen4<2>(w.k[s][i], e),
                                widen4<3>(w.k[s][i], e)};
@@ -249,6 +270,7 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Attn4Args a, int spl
         for (int n = 0; n < NQ; ++n) z[n][s] = mfma16(as_frag(f), q[n][i], z[n][s]);
       }
     if (k0 < lo_max || k0 + 32 > hi_min) {  // some row does not see all of these keys
+      asm volatile("");                     // a branch, no 16 comparisons at every step
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         const int lo = row_sees[n].lo - k0, hi = row_sees[n].hi - k0;
@@ -296,35 +318,49 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Attn4Args a, int spl
       const int tile0 = word ? part * 8 : Step::kWords * 8 + (half ? 0 : Step::kHalf * 4);
       const int blk0 = word ? part * 4 : half ? Step::kWords * 4 : ND - 1;
       const int blk = word ? c16 >> 2 : half ? c16 >> 3 : 0;
+      // the scale of the lane's block, one byte of the four keys' scales, as a number's highest byte
       uint32_t e[8], most = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int at = ND * (i & 3) + blk0;  // byte of the four keys' scales, less the lane's block
-        const uint64_t two = (uint64_t)w.vs[i >> 2][at / 4] | (uint64_t)w.vs[i >> 2][at / 4 + 1] << 32;
-        e[i] = (uint32_t)(two >> (8 * (at % 4 + blk))) & 0xff;
+        const int at = ND * (i & 3) + blk0, in = at / 4, span = word ? 4 : half ? 2 : 1;
+        const uint32_t lo = w.vs[i >> 2][in], hi = at % 4 + span > 4 ? w.vs[i >> 2][in + 1 < ND ? in + 1 : in] : lo;
+        e[i] = __builtin_amdgcn_perm(hi, lo, (uint32_t)(at % 4 + blk) << 24 | 0x0c0c0cu);
         most = max(most, e[i]);
       }
-      uint32_t nan_keys = 0;
       if (edge) {  // what lies outside may hold anything
+        asm volatile("");
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int j = k0 + 16 * (i >> 2) + 4 * g + (i & 3);
           e[i] = j >= lo_all && j < hi_all ? e[i] : 0;
         }
       }
-      const bool some_nan = __any(most == 255);
-      if (some_nan) {
-        // NaN times a weight of 0 would reach rows that do not see the key: such a block
-        // counts as 0 here, and below is put where the row does see it
+      if (__any(most >= 0xff000000u)) {
+        // NaN times a weight of 0 would reach rows that do not see the key: such a block counts as 0, and is noted for
+        // the rows that do see it
+        uint32_t nan_keys = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (e[i] == 255) {
+          if (e[i] >= 0xff000000u) {
             nan_keys |= 1u << i;
             e[i] = 0;
           }
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t who = (uint32_t)(__ballot(nan_keys >> (i & 7) & 1) >> (16 * (i >> 3))) & 0xffff;
+          if (who == 0) continue;
+          const int j = k0 + 16 * ((i & 7) >> 2) + 4 * (i >> 3) + (i & 3);
+          uint32_t blocks = who ? 1 : 0;
+          if (word)
+            blocks = (who & 0xf ? 1 : 0) | (who & 0xf0 ? 2 : 0) | (who & 0xf00 ? 4 : 0) | (who & 0xf000 ? 8 : 0);
+          else if (half) blocks = (who & 0xff ? 1 : 0) | (who & 0xff00 ? 2 : 0);
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+            if (j >= row_sees[n].lo && j < row_sees[n].hi) poison[n] |= blocks << blk0;
+        }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] <<= 23;
+      for (int i = 0; i < 8; ++i) e[i] >>= 1;  // into the exponent's place
       auto column = [&](auto byte_c) {
         constexpr int byte = decltype(byte_c)::value;
         uint32_t even[4], odd[4];
@@ -346,24 +382,6 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Attn4Args a, int spl
       if (bytes > 2) {
         column(std::integral_constant<int, 2>{});
         column(std::integral_constant<int, 3>{});
-      }
-      if (some_nan) {
-        // lane c16 of the columns is rho = 4 g' + r of the results' lanes
-        for (int i = 0; i < 8; ++i)
-          for (int gg = 0; gg < 4; ++gg) {
-            const uint32_t who = (uint32_t)(__ballot(nan_keys >> i & 1) >> (16 * gg)) & 0xffff;
-            if (who == 0) continue;
-            const int j = k0 + 16 * (i >> 2) + 4 * gg + (i & 3);
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-              const bool seen = j >= row_sees[n].lo && j < row_sees[n].hi;
-#pragma unroll
-              for (int x = 0; x < 2 * bytes; ++x)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  if (seen && (who >> (4 * g + r) & 1)) acc[n][tile0 + x][r] = __uint_as_float(0x7fc00000u);
-            }
-          }
       }
     }
   };
@@ -418,8 +436,11 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Attn4Args a, int spl
       const int wide = word ? 8 : half ? 4 : 2;
       const int first = word ? i / 8 * 128 : Step::kWords * 128 + (half ? 0 : Step::kHalf * 64);
       const int in = word ? i % 8 : half ? i - Step::kWords * 8 : i - Step::kWords * 8 - Step::kHalf * 4;
+      const int blk = first / 32 + (word ? g : half ? g >> 1 : 0);  // of the lane's four values
+      const bool nan = poison[n] >> blk & 1;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) share[wave][c16][first + (4 * g + r) * wide + in] = acc[n][i][r];
+      for (int r = 0; r < 4; ++r)
+        share[wave][c16][first + (4 * g + r) * wide + in] = nan ? __uint_as_float(0x7fc00000u) : acc[n][i][r];
     }
     __syncthreads();
     // a row's 8 columns per thread
@@ -436,7 +457,7 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Attn4Args a, int spl
       for (int w = 0; w < 4; ++w) {
         const float f = __builtin_amdgcn_exp2f(stat[w][rr][0] - less);
         const float lw = stat[w][rr][1];
-        if (lw == 0.0f) continue;  // nothing seen
+        if (lw == 0.0f) continue;  // nothing seen, or weights of 0 only
         sum += f * lw;
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] += f * share[w][rr][col + i];
@@ -449,9 +470,10 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Attn4Args a, int spl
 #pragma unroll
         for (int i = 0; i < 8; i += 4) *reinterpret_cast<f32x4*>(p + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
         if (col == 0) {
+          const Sees s = sees(a, t.len, t.pos(tok), cap);
           float* st = a.partial + (int64_t)splits * all_rows * kD + ((int64_t)split * all_rows + row) * 2;
           st[0] = top;
-          st[1] = sum;
+          st[1] = s.hi > s.lo ? sum : -1.0f;  // a row that sees no key in any part
         }
       } else {
         const Sees s = sees(a, t.len, t.pos(tok), cap);
@@ -466,44 +488,73 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Attn4Args a, int spl
   }
 }
 
-// The parts of a row, added in order: a wave per row.
-__global__ __launch_bounds__(256) void kv4_join_kernel(Attn4Args a, int splits) {
+// The parts of a row, added in a fixed order.  A thread takes 4 columns of a
+// row and every `slices`th part, its loads independent of one another; the
+// slices are added through LDS.  stats: each part's maximum and sum.
+struct Part {
+  float top, sum;
+  f32x4 o;
+  __device__ __forceinline__ void add(float t, float l, f32x4 x) {
+    if (l == 0.0f) return;  // nothing seen, or weights of 0 only
+    const float now = fmaxf(top, t), less = now == -INFINITY ? 0.0f : now;
+    const float f = __builtin_amdgcn_exp2f(top - less), h = __builtin_amdgcn_exp2f(t - less);
+    sum = sum * f + l * h;
+    o = o * f + x * h;
+    top = now;
+  }
+};
+__global__ __launch_bounds__(256) void kv4_join_kernel(Attn4Args a, int splits, int slices) {
+  __shared__ Part share[256];
   const int64_t all_rows = (int64_t)a.tokens * a.q_heads;
-  const int lane = threadIdx.x & 63, d = a.cache.d;
-  for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < all_rows; row += (int64_t)gridDim.x * 4) {
-    const int token = (int)(row / a.q_heads), head = (int)(row - (int64_t)token * a.q_heads);
-    const int b = sequence_of(a.plan, token);
-    const int s0 = min(max(a.plan.starts[b], 0), a.tokens), s1 = min(max(a.plan.starts[b + 1], s0), a.tokens);
-    if (token < s0 || token >= s1) continue;
-    const int len = max(a.plan.lengths[b], 0);
-    const int64_t cap = (int64_t)a.plan.width << a.cache.page_log2;
-    const Sees s = sees(a, len, (int)((int64_t)len - (s1 - token)), cap);
-    const float* st = a.partial + (int64_t)splits * all_rows * d + row * 2;
-    float top = -INFINITY;
-    for (int i = lane; i < splits; i += 64) top = fmaxf(top, st[(int64_t)i * all_rows * 2]);
+  const int d = a.cache.d, lanes = d / 4, items = 256 / slices;
+  const int slice = threadIdx.x / items, mine = threadIdx.x - slice * items;
+  const float* stats = a.partial + (int64_t)splits * all_rows * d;
+  // rows behind the last sequence have no parts
+  const int64_t rows = (int64_t)min(max(a.plan.starts[a.plan.sequences], 0), a.tokens) * a.q_heads;
+  for (int64_t first = (int64_t)blockIdx.x * items; first < rows * lanes; first += (int64_t)gridDim.x * items) {
+    const int64_t item = first + mine, row = item / lanes;
+    const int col = 4 * (int)(item - row * lanes);
+    Part p = {-INFINITY, 0.0f, {0, 0, 0, 0}};
+    bool none = false;
+    if (row < rows) {
+      const float* from = a.partial + row * d + col;
+      for (int i0 = slice; i0 < splits; i0 += 8 * slices) {
+        f32x2 st[8];
+        f32x4 x[8];
 #pragma unroll
-    for (int o = 1; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
-    const float less = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f;
-    f32x4 o = {0, 0, 0, 0};
-    const float* p = a.partial + row * d + 4 * lane;
-    for (int i = 0; i < splits; ++i) {
-      const float l = st[(int64_t)i * all_rows * 2 + 1];
-      if (l == 0.0f) continue;
-      const float f = __builtin_amdgcn_exp2f(st[(int64_t)i * all_rows * 2] - less);
-      sum += f * l;
-      if (4 * lane < d) o += f * *reinterpret_cast<const f32x4*>(p + (int64_t)i * all_rows * d);
-    }
-    const float inv = s.hi > s.lo ? 1.0f / sum : 0.0f;
-    if (s.hi <= s.lo) o = f32x4{0, 0, 0, 0};
-    if (4 * lane < d) {
-      uint16_t* out = a.out + (int64_t)token * a.out_token + (int64_t)head * a.out_head + 4 * lane;
+        for (int i = 0; i < 8; ++i) {
+          const int64_t at = (int64_t)min(i0 + i * slices, splits - 1) * all_rows;
+          st[i] = *reinterpret_cast<const f32x2*>(stats + (at + row) * 2);
+          x[i] = *reinterpret_cast<const f32x4*>(from + at * d);
+        }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) store1(out + i, o[i] * inv);
+        for (int i = 0; i < 8; ++i)
+          if (i0 + i * slices < splits) {
+            none |= st[i][1] < 0.0f;
+            p.add(st[i][0], st[i][1], x[i]);
+          }
+      }
     }
-    if (a.lse && lane == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+    if (slices > 1) {
+      __syncthreads();  // the last items' are done with
+      share[threadIdx.x] = p;
+      __syncthreads();
+      if (slice == 0)
+        for (int i = 1; i < slices; ++i) p.add(share[i * items + mine].top, share[i * items + mine].sum, share[i * items + mine].o);
+    }
+    if (slice == 0 && row < rows) {
+      const int token = (int)(row / a.q_heads), head = (int)(row - (int64_t)token * a.q_heads);
+      const float inv = none ? 0.0f : 1.0f / p.sum;
+      if (none) p.o = f32x4{0, 0, 0, 0};
+      uint16_t* out = a.out + (int64_t)token * a.out_token + (int64_t)head * a.out_head + col;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store1(out + i, p.o[i] * inv);
+      if (a.lse && col == 0) a.lse[row] = none || p.sum == 0.0f ? -INFINITY : (p.top + __builtin_amdgcn_logf(p.sum)) * kLn2;
+    }
   }
 }
+
+constexpr int kMostSplits = 256;
 
 // How a call is cut: 16 or 32 rows to a tile, and the keys in parts until the
 // chip has work enough, of 256 keys at least.
@@ -518,8 +569,9 @@ Cut cut_of(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t page_size,
   const int64_t size = 16 * c.tiles16;
   c.tiles = rows / size + sequences;
   const int64_t busy = std::max<int64_t>(1, std::min(c.tiles, std::max(rows / size, std::min(sequences, tokens))) * kv_heads);
-  const int64_t most = std::max<int64_t>(1, (width * page_size + 255) / 256);
-  c.splits = (int)std::min<int64_t>(std::min<int64_t>(most, 256), std::max<int64_t>(1, 1024 / busy));
+  const int64_t keys = width * page_size, most = std::max<int64_t>(1, (keys + 127) / 128);
+  const int64_t fill = (768 + busy - 1) / busy, even = busy >= 256 ? (keys + 2047) / 2048 : 1;
+  c.splits = (int)std::min({most, std::max(fill, even), (int64_t)kMostSplits});
   return c;
 }
 
@@ -534,8 +586,11 @@ hipError_t go(const Attn4Args& a, const Cut& c, hipStream_t stream) {
   }
   if (c.splits > 1) {
     const int64_t rows = (int64_t)a.tokens * a.q_heads;
-    hipLaunchKernelGGL(kv4_join_kernel, dim3((unsigned)std::min((rows + 3) / 4, kMost)), dim3(256), 0, stream, a,
-                       c.splits);
+    int slices = 1;
+    while (slices < 32 && slices * 8 < c.splits) slices *= 2;
+    const int64_t items = rows * (ND * 8), per = 256 / slices;
+    hipLaunchKernelGGL(kv4_join_kernel, dim3((unsigned)std::min((items + per - 1) / per, kMost)), dim3(256), 0, stream,
+                       a, c.splits, slices);
   }
   return hipGetLastError();
 }
