@@ -26,6 +26,7 @@ namespace harp {
 namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ bf16x8_t as_frag(const uint32_t (&w)[4]) {
   bf16x8_t r;
@@ -56,6 +57,15 @@ __device__ __forceinline__ float sum_of_groups(float v) {
   a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
+__device__ __forceinline__ float max_of_halves(float v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float sum_of_halves(float v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
 // An address that all lanes have in common, kept in scalar registers: loads add
 // the lane's offset themselves, where the compiler would add it before the loop
 // and the address to that, lane by lane.
@@ -107,6 +117,42 @@ __device__ __forceinline__ Sees sees(const Attn4Args& a, int len, int pos, int64
   return {(int)min(lo, cap), (int)min(hi, cap + 1)};
 }
 
+// The keys that a workgroup's rows see, lo .. hi - 1, and its part of them, in
+// steps of kStep keys from `base` on.
+struct KeyRange {
+  int lo, hi, base, step0, step1;
+};
+template <int kStep>
+__device__ __forceinline__ KeyRange key_range(const Attn4Args& a, const TileRows& t, int tile_size, int64_t cap, int split,
+                                              int splits, int unit) {
+  const int64_t row1 = min(t.row0 + tile_size, t.rows);
+  const int tok0 = (int)(t.row0 / a.group), tok1 = (int)((row1 - 1) / a.group);
+  const Sees s0 = sees(a, t.len, t.pos(tok0), cap), s1 = sees(a, t.len, t.pos(tok1), cap);
+  KeyRange r;
+  r.hi = max(s0.hi, s1.hi);
+  r.lo = t.pos(tok0) < 0 ? 0 : s0.lo;
+  r.base = r.lo & ~(kStep - 1);
+  const int steps = r.hi > r.lo ? (int)(((int64_t)r.hi - r.base + kStep - 1) / kStep) : 0;
+  const int per = ((steps + splits * unit - 1) / (splits * unit)) * unit;
+  r.step0 = min(steps, split * per);
+  r.step1 = min(steps, r.step0 + per);
+  return r;
+}
+
+// The scale of four keys' blocks, of which `vs` holds all scales: the block of
+// a lane is blk0 + blk (blk < kSpan).  As a word's highest byte.
+template <int ND, int kSpan>
+__device__ __forceinline__ uint32_t scale_of(const uint32_t (&vs)[ND], int key, int blk0, int blk) {
+  const int at = ND * key + blk0, in = at / 4;
+  const uint32_t lo = vs[in], hi = at % 4 + kSpan > 4 ? vs[in + 1 < ND ? in + 1 : in] : lo;
+  return __builtin_amdgcn_perm(hi, lo, (uint32_t)(at % 4 + blk) << 24 | 0x0c0c0cu);
+}
+constexpr uint32_t kNanScale = 0xff000000u;  // of such words, and above
+
+// Weights go by a reference that a score may pass by this much (in powers of
+// two) before the sums are brought to a new one, which is then rarely needed.
+constexpr float kSlack = 8.0f;
+
 // ------------------------------------------------------------- few rows
 // A wave takes 32 keys at a time, every fourth of its workgroup's, with its
 // loads straight into the layouts of the matrix instructions, one step ahead.
@@ -139,16 +185,8 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
   if (!tile_rows(a, tile, kTileRows, &t)) return;
   const int ps_log2 = a.cache.page_log2;
   const int64_t cap = (int64_t)a.plan.width << ps_log2;
-  const int64_t row1 = min(t.row0 + kTileRows, t.rows);
-
-  // keys of the tile, and this workgroup's share of them in steps of 32
-  const int tok0 = (int)(t.row0 / a.group), tok1 = (int)((row1 - 1) / a.group);
-  const Sees s0 = sees(a, t.len, t.pos(tok0), cap), s1 = sees(a, t.len, t.pos(tok1), cap);
-  const int hi_all = max(s0.hi, s1.hi), lo_all = t.pos(tok0) < 0 ? 0 : s0.lo;
-  const int base = lo_all & ~31;
-  const int steps = hi_all > lo_all ? (int)(((int64_t)hi_all - base + 31) >> 5) : 0;
-  const int per = ((steps + splits * 4 - 1) / (splits * 4)) * 4;
-  const int step0 = min(steps, split * per), step1 = min(steps, step0 + per);
+  const KeyRange keys = key_range<32>(a, t, kTileRows, cap, split, splits, 4);
+  const int hi_all = keys.hi, lo_all = keys.lo, base = keys.base, step0 = keys.step0, step1 = keys.step1;
 
   // this lane's row of each tile of 16: its queries, its keys
   Sees row_sees[NQ];
@@ -290,7 +328,7 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
 #pragma unroll
       for (int i = 1; i < 8; ++i) top = fmaxf(top, z[n][i >> 2][i & 3]);
       top *= to_log2;
-      if (__any(top > m[n])) {
+      if (__any(top > m[n] + kSlack)) {
         const float now = fmaxf(m[n], max_of_groups(top));
         const float shrink = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[n] - now);
         m[n] = now;
@@ -322,9 +360,9 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
       uint32_t e[8], most = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int at = ND * (i & 3) + blk0, in = at / 4, span = word ? 4 : half ? 2 : 1;
-        const uint32_t lo = w.vs[i >> 2][in], hi = at % 4 + span > 4 ? w.vs[i >> 2][in + 1 < ND ? in + 1 : in] : lo;
-        e[i] = __builtin_amdgcn_perm(hi, lo, (uint32_t)(at % 4 + blk) << 24 | 0x0c0c0cu);
+        e[i] = word   ? scale_of<ND, 4>(w.vs[i >> 2], i & 3, blk0, blk)
+               : half ? scale_of<ND, 2>(w.vs[i >> 2], i & 3, blk0, blk)
+                      : scale_of<ND, 1>(w.vs[i >> 2], i & 3, blk0, blk);
         most = max(most, e[i]);
       }
       if (edge) {  // what lies outside may hold anything
@@ -335,13 +373,13 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
           e[i] = j >= lo_all && j < hi_all ? e[i] : 0;
         }
       }
-      if (__any(most >= 0xff000000u)) {
+      if (__any(most >= kNanScale)) {
         // NaN times a weight of 0 would reach rows that do not see the key: such a block counts as 0, and is noted for
         // the rows that do see it
         uint32_t nan_keys = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (e[i] >= 0xff000000u) {
+          if (e[i] >= kNanScale) {
             nan_keys |= 1u << i;
             e[i] = 0;
           }
@@ -488,6 +526,354 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
   }
 }
 
+// ------------------------------------------------------------ many rows
+// A workgroup takes 128 rows, 32 to a wave, and 64 keys at a time.  K's and V's
+// codes are widened once for its four waves: each wave widens a quarter of the
+// next 64 keys, straight from memory into the fragments of the 32 x 32 x 16
+// instruction, and writes them to LDS as they are read, 16 bytes a lane one
+// after the other, while the products of the present 64 keys run.
+template <int ND>
+struct Quarter4 {
+  static constexpr int kScales = ND % 4 == 0 ? ND / 4 : ND <= 2 ? 1 : ND;  // of a lane's ND words of K
+  static constexpr int kFours = ND / 4, kTwo = (ND >> 1) & 1, kOne = ND & 1;  // how V's columns go to 32 lanes
+  uint32_t k[ND], ks[kScales];
+  uint32_t v[8][kFours + kTwo + kOne];
+  uint32_t vs[2][ND];
+};
+
+template <int ND>
+__global__ __launch_bounds__(256, ND <= 4 ? 2 : 1) void kv4_prompt_kernel(Attn4Args a, int splits, int64_t unit0,
+                                                                          int64_t tiles) {
+  using Q4 = Quarter4<ND>;
+  constexpr int kRow = ND * 16, kRows = 128, kFrag = 1024, kSide = 4 * ND * kFrag;
+  __shared__ __attribute__((aligned(16))) uint8_t frags[2][2 * kSide];  // K, V
+  __shared__ uint32_t nan_any[2][4], nan_blocks[2][64];
+  const int lane = threadIdx.x & 63, c32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // the last rows of a sequence, which see most keys, first
+  const int64_t unit = unit0 + blockIdx.x, rest = unit / splits, tile = tiles - 1 - rest / a.cache.heads;
+  const int split = (int)(unit - rest * splits), kvh = (int)(rest % a.cache.heads);
+  TileRows t;
+  if (!tile_rows(a, tile, kRows, &t)) return;
+  const int ps_log2 = a.cache.page_log2;
+  const int64_t cap = (int64_t)a.plan.width << ps_log2;
+  const KeyRange keys = key_range<64>(a, t, kRows, cap, split, splits, 1);
+
+  // this lane's row: its queries, its keys
+  const int64_t r = t.row0 + wave * 32 + c32;
+  const bool has = r < t.rows;
+  const int tok = has ? (int)(r / a.group) : 0, gh = has ? (int)(r - (int64_t)tok * a.group) : 0;
+  const Sees my = has ? sees(a, t.len, t.pos(tok), cap) : Sees{0, 0};
+  int hi_min = has ? my.hi : keys.hi, lo_max = has ? my.lo : keys.lo, hi_max = my.hi;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    hi_min = min(hi_min, __shfl_xor(hi_min, o));
+    lo_max = max(lo_max, __shfl_xor(lo_max, o));
+    hi_max = max(hi_max, __shfl_xor(hi_max, o));
+  }
+  hi_min = __builtin_amdgcn_readfirstlane(hi_min);
+  lo_max = __builtin_amdgcn_readfirstlane(lo_max);
+  hi_max = __builtin_amdgcn_readfirstlane(hi_max);
+  bf16x8_t q[2 * ND];
+  {
+    const uint16_t* p = a.q + (int64_t)(t.first_token + tok) * a.q_token + (int64_t)(kvh * a.group + gh) * a.q_head;
+#pragma unroll
+    for (int s = 0; s < 2 * ND; ++s) {
+      Raw8<uint16_t> w;
+      w.fill(0);
+      if (has) w.load(p + (s / ND * 2 + h) * 8 * ND + s % ND * 8, 8);
+      q[s] = as_frag(w.w);
+    }
+  }
+
+  f32x16 acc[ND];
+#pragma unroll
+  for (int i = 0; i < ND; ++i)
+#pragma unroll
+    for (int x = 0; x < 16; ++x) acc[i][x] = 0.0f;
+  float m = -INFINITY, l = 0.0f;
+  uint32_t poison = 0;
+  const float to_log2 = a.scale * kLog2e;
+
+  // Pages of 16 steps, four to a step, in the lanes.
+  int pages = -1;
+  auto look_up = [&](int step) {
+    const int64_t key = (int64_t)keys.base + (int64_t)step * 64 + lane * 16;
+    pages = key < keys.hi ? page_of(a.cache, a.plan, t.seq, key >> ps_log2) : -1;
+  };
+  auto load = [&](Q4& w, int step, int at) {
+    const uint32_t key0 = (uint32_t)keys.base + (uint32_t)step * 64, in_mask = (1u << ps_log2) - 1;
+    {  // K: keys 32 (wave / 2) .., a quarter of each row's ND words by lane half and wave
+      const int sub = (wave & 2) + (c32 >> 4);
+      const int page = __shfl(pages, 4 * at + sub);
+      const int64_t pg = page < 0 ? 0 : page;
+      const int64_t row = ((int64_t)kvh << ps_log2) + ((key0 + sub * 16) & in_mask) + (c32 & 15);
+      const uint8_t* p = a.cache.k.codes + pg * a.cache.k.codes_page + row * kRow + ((wave & 1) * 2 + h) * 4 * ND;
+      if constexpr (ND % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < ND; i += 4) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(p + 4 * i);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w.k[i + j] = x[j];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < ND; ++i) w.k[i] = reinterpret_cast<const uint32_t*>(p)[i];
+      }
+      const uint8_t* e = a.cache.k.scales + pg * a.cache.k.scales_page + row * ND;
+#pragma unroll
+      for (int i = 0; i < Q4::kScales; ++i) {
+        const int word = ((wave & 1) * 2 + h) * ND + i * (ND / Q4::kScales);
+        w.ks[i] = page < 0 ? 255u : e[word / 4];  // no page: NaN
+      }
+    }
+    {  // V: 16 keys, all columns
+      const int page = __builtin_amdgcn_readlane(pages, 4 * at + wave);
+      const int64_t pg = page < 0 ? 0 : page;
+      const int64_t row = ((int64_t)kvh << ps_log2) + ((key0 + wave * 16) & in_mask);
+      const auto vc = common(a.cache.v.codes + pg * a.cache.v.codes_page + row * kRow);
+      const auto vs = common(a.cache.v.scales + pg * a.cache.v.scales_page + row * ND);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int in = (i >> 2) * 8 + (i & 3);
+        const uint32_t at_row = 4 * h * kRow;
+#pragma unroll
+        for (int j = 0; j < Q4::kFours; ++j) w.v[i][j] = load_at<uint16_t>(vc, at_row + 2 * c32, in * kRow + 64 * j);
+        if constexpr (Q4::kTwo) w.v[i][Q4::kFours] = load_at<uint8_t>(vc, at_row + c32, in * kRow + 64 * Q4::kFours);
+        if constexpr (Q4::kOne)
+          w.v[i][Q4::kFours + Q4::kTwo] = load_at<uint8_t>(vc, at_row + (c32 >> 1), in * kRow + kRow - 16);
+      }
+#pragma unroll
+      for (int i = 0; i < ND; ++i) {
+        const uint32_t e0 = load_at<uint32_t>(vs, 4 * h * ND, 4 * i), e1 = load_at<uint32_t>(vs, 4 * h * ND, 8 * ND + 4 * i);
+        w.vs[0][i] = page < 0 ? 0u : e0;  // another page's: nothing that is not finite
+        w.vs[1][i] = page < 0 ? 0u : e1;
+      }
+    }
+  };
+  auto put = [&](int buf, int frag, const uint32_t (&w)[4]) {
+    *reinterpret_cast<u32x4*>(&frags[buf][frag * kFrag + lane * 16]) = u32x4{w[0], w[1], w[2], w[3]};
+  };
+  auto widen = [&](const Q4& w, int step, int buf) {
+#pragma unroll
+    for (int i = 0; i < ND; ++i) {
+      const uint32_t e = w.ks[i / (ND / Q4::kScales)] << 23;
+      const uint32_t f[4] = {widen4<0>(w.k[i], e), widen4<1>(w.k[i], e), widen4<2>(w.k[i], e), widen4<3>(w.k[i], e)};
+      put(buf, wave * ND + i, f);  // key tile wave / 2, step (wave % 2) ND + i of its columns
+    }
+    const int k0 = (int)((uint32_t)keys.base + (uint32_t)step * 64) + wave * 16;
+    const bool edge = k0 < keys.lo || k0 + 16 > keys.hi;
+    uint32_t some_nan = 0;
+#pragma unroll
+    for (int part = 0; part < Q4::kFours + Q4::kTwo + Q4::kOne; ++part) {
+      const bool four = part < Q4::kFours, two = !four && part == Q4::kFours && Q4::kTwo;
+      const int tile0 = four ? part * 4 : Q4::kFours * 4 + (two ? 0 : Q4::kTwo * 2);
+      const int blk = four ? c32 >> 3 : two ? c32 >> 4 : 0;
+      uint32_t e[8], most = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        e[i] = four  ? scale_of<ND, 4>(w.vs[i >> 2], i & 3, tile0, blk)
+               : two ? scale_of<ND, 2>(w.vs[i >> 2], i & 3, tile0, blk)
+                     : scale_of<ND, 1>(w.vs[i >> 2], i & 3, tile0, blk);
+        most = max(most, e[i]);
+      }
+      if (edge) {  // what lies outside may hold anything
+        asm volatile("");
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int j = k0 + (i >> 2) * 8 + 4 * h + (i & 3);
+          e[i] = j >= keys.lo && j < keys.hi ? e[i] : 0;
+        }
+      }
+      if (__any(most >= kNanScale)) {  // such a block counts as 0, and is noted for the rows that see it
+        uint32_t nan_keys = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (e[i] >= kNanScale) {
+            nan_keys |= 1u << i;
+            e[i] = 0;
+          }
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t who = (uint32_t)(__ballot(nan_keys >> (i & 7) & 1) >> (32 * (i >> 3)));
+          uint32_t blocks = who ? 1 : 0;
+          if (four)
+            blocks = (who & 0xff ? 1 : 0) | (who & 0xff00 ? 2 : 0) | (who & 0xff0000 ? 4 : 0) | (who & 0xff000000u ? 8 : 0);
+          else if (two) blocks = (who & 0xffff ? 1 : 0) | (who & 0xffff0000u ? 2 : 0);
+          uint32_t* to = &nan_blocks[buf][wave * 16 + ((i & 7) >> 2) * 8 + 4 * (i >> 3) + (i & 3)];
+          if (lane == 0) *to = (some_nan ? *to : 0) | blocks << tile0;
+        }
+        some_nan = 1;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] >>= 1;  // into the exponent's place
+      auto column = [&](auto byte_c) {
+        constexpr int byte = decltype(byte_c)::value;
+        uint32_t even[4], odd[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x = widen4<byte>(w.v[2 * j][part], e[2 * j]);
+          const uint32_t y = widen4<byte>(w.v[2 * j + 1][part], e[2 * j + 1]);
+          if (four || two) {
+            even[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+            odd[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+          } else {  // a lane's column is one of the byte's two
+            even[j] = __builtin_amdgcn_perm(y, x, c32 & 1 ? 0x07060302u : 0x05040100u);
+          }
+        }
+        const int frag = 4 * ND + wave * ND + tile0 + 2 * byte;
+        put(buf, frag, even);
+        if (four || two) put(buf, frag + 1, odd);
+      };
+      column(std::integral_constant<int, 0>{});
+      if (four) column(std::integral_constant<int, 1>{});
+    }
+    if (lane == 0) nan_any[buf][wave] = some_nan;
+  };
+  auto frag = [&](int buf, int i) {
+    uint32_t w[4];
+    const u32x4 x = *reinterpret_cast<const u32x4*>(&frags[buf][i * kFrag + lane * 16]);
+    w[0] = x[0]; w[1] = x[1]; w[2] = x[2]; w[3] = x[3];
+    return as_frag(w);
+  };
+  auto compute = [&](int step, int buf) {
+    const int k0 = (int)((uint32_t)keys.base + (uint32_t)step * 64);
+    if (k0 >= hi_max) return;  // no row of this wave sees any of them
+    f32x16 z[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int x = 0; x < 16; ++x) z[s][x] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2 * ND; ++i)
+        z[s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(buf, s * 2 * ND + i), q[i], z[s], 0, 0, 0);
+    }
+    if (k0 < lo_max || k0 + 64 > hi_min) {
+      asm volatile("");
+      const int lo = my.lo - k0 - 4 * h, hi = my.hi - k0 - 4 * h;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const int j = 32 * s + 8 * (x >> 2) + (x & 3);
+          z[s][x] = j >= lo && j < hi ? z[s][x] : -INFINITY;
+        }
+    }
+    float top = z[0][0];
+#pragma unroll
+    for (int x = 1; x < 32; ++x) top = fmaxf(top, z[x >> 4][x & 15]);
+    top *= to_log2;
+    if (__any(top > m + kSlack)) {
+      const float now = fmaxf(m, max_of_halves(top));
+      const float shrink = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+      m = now;
+      l *= shrink;
+#pragma unroll
+      for (int i = 0; i < ND; ++i) acc[i] *= shrink;
+    }
+    const float less = m == -INFINITY ? 0.0f : m;
+    bf16x8_t p[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      uint32_t f[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int x = 8 * (s & 1) + 2 * j;
+        const float e0 = __builtin_amdgcn_exp2f(fmaf(z[s >> 1][x], to_log2, -less));
+        const float e1 = __builtin_amdgcn_exp2f(fmaf(z[s >> 1][x + 1], to_log2, -less));
+        l += e0 + e1;
+        f[j] = pack_bf16x2_hw(e0, e1);
+      }
+      p[s] = as_frag(f);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < ND; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(buf, 4 * ND + s * ND + i), p[s], acc[i], 0, 0, 0);
+    const u32x4 any = *reinterpret_cast<const u32x4*>(&nan_any[buf][0]);
+    if (__builtin_amdgcn_readfirstlane(any[0] | any[1] | any[2] | any[3])) {
+#pragma unroll 1
+      for (int j = 0; j < 64; ++j)
+        if (nan_any[buf][j >> 4] && k0 + j >= my.lo && k0 + j < my.hi) poison |= nan_blocks[buf][j];
+    }
+  };
+
+  if (keys.step0 < keys.step1) {
+    Q4 w;
+    int at = 0;
+    look_up(keys.step0);
+    load(w, keys.step0, 0);
+    widen(w, keys.step0, 0);
+    auto fetch = [&](int step) {
+      if (step >= keys.step1) return;
+      if (++at == 16) {
+        at = 0;
+        look_up(step);
+      }
+      load(w, step, at);
+    };
+    fetch(keys.step0 + 1);
+    __syncthreads();
+    int buf = 0;
+    for (int step = keys.step0; step < keys.step1; ++step, buf ^= 1) {
+      if (step + 1 < keys.step1) widen(w, step + 1, buf ^ 1);
+      fetch(step + 2);
+      compute(step, buf);
+      __syncthreads();
+    }
+  }
+
+  l = sum_of_halves(l);
+  if (!has) return;
+  const int64_t token = t.first_token + tok, head = (int64_t)kvh * a.group + gh, row = token * a.q_heads + head;
+  const bool sees_some = my.hi > my.lo;
+  const int64_t all_rows = (int64_t)a.tokens * a.q_heads;
+  const float inv = splits > 1 ? 1.0f : sees_some ? 1.0f / l : 0.0f;
+  float* part_out = a.partial + ((int64_t)split * all_rows + row) * (ND * 32);
+  uint16_t* out = a.out + token * a.out_token + head * a.out_head;
+#pragma unroll
+  for (int part = 0; part < Q4::kFours + Q4::kTwo + Q4::kOne; ++part) {
+    const bool four = part < Q4::kFours, two = !four && part == Q4::kFours && Q4::kTwo;
+    const int tile0 = four ? part * 4 : Q4::kFours * 4 + (two ? 0 : Q4::kTwo * 2), wide = four ? 4 : two ? 2 : 1;
+#pragma unroll
+    for (int rb = 0; rb < 4; ++rb) {
+      // 4 wide columns, from tile0 32 + (8 rb + 4 h) wide on: all of one block
+      const int col = tile0 * 32 + (8 * rb + 4 * h) * wide;
+      const bool nan = poison >> (col >> 5) & 1;
+      float o[16];
+#pragma unroll
+      for (int x = 0; x < 4 * wide; ++x) {
+        const float y = acc[tile0 + x % wide][4 * rb + x / wide] * inv;
+        o[x] = nan ? __uint_as_float(0x7fc00000u) : sees_some ? y : 0.0f;
+      }
+      if (splits > 1) {
+#pragma unroll
+        for (int x = 0; x < 4 * wide; x += 4)
+          *reinterpret_cast<f32x4*>(part_out + col + x) = f32x4{o[x], o[x + 1], o[x + 2], o[x + 3]};
+      } else if (wide == 1) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) store1(out + col + x, o[x]);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4 * wide; x += 8) {
+          const float v8[8] = {o[x], o[x + 1], o[x + 2], o[x + 3], o[x + 4], o[x + 5], o[x + 6], o[x + 7]};
+          store8(out + col + x, v8);
+        }
+      }
+    }
+  }
+  if (h == 0) {
+    if (splits > 1) {
+      float* st = a.partial + (int64_t)splits * all_rows * (ND * 32) + ((int64_t)split * all_rows + row) * 2;
+      st[0] = m;
+      st[1] = sees_some ? l : -1.0f;  // a row that sees no key in any part
+    } else if (a.lse) {
+      a.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    }
+  }
+}
+
 // The parts of a row, added in a fixed order.  A thread takes 4 columns of a
 // row and every `slices`th part, its loads independent of one another; the
 // slices are added through LDS.  stats: each part's maximum and sum.
@@ -556,21 +942,21 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Attn4Args a, int splits, 
 
 constexpr int kMostSplits = 256;
 
-// How a call is cut: 16 or 32 rows to a tile, and the keys in parts until the
-// chip has work enough, of 256 keys at least.
+// How a call is cut: tiles of 16, 32 or 128 rows, by the rows that a sequence
+// has on average, and the keys in parts until the chip has work enough.
 struct Cut {
-  int tiles16, splits;  // tiles of 16 rows to a workgroup
+  int rows, splits;
   int64_t tiles;
 };
 Cut cut_of(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t page_size, int64_t sequences, int64_t width) {
   const int64_t group = q_heads / kv_heads, rows = tokens * group;
   Cut c;
-  c.tiles16 = rows > 16 * sequences ? 2 : 1;
-  const int64_t size = 16 * c.tiles16;
-  c.tiles = rows / size + sequences;
-  const int64_t busy = std::max<int64_t>(1, std::min(c.tiles, std::max(rows / size, std::min(sequences, tokens))) * kv_heads);
+  c.rows = rows > 64 * sequences ? 128 : rows > 16 * sequences ? 32 : 16;
+  c.tiles = rows / c.rows + sequences;
+  const int64_t busy = std::max<int64_t>(1, std::max(rows / c.rows, std::min(sequences, tokens)) * kv_heads);
   const int64_t keys = width * page_size, most = std::max<int64_t>(1, (keys + 127) / 128);
-  const int64_t fill = (768 + busy - 1) / busy, even = busy >= 256 ? (keys + 2047) / 2048 : 1;
+  const int64_t fill = ((c.rows == 128 ? 512 : 768) + busy - 1) / busy;
+  const int64_t even = busy >= 256 && c.rows < 128 ? (keys + 2047) / 2048 : 1;
   c.splits = (int)std::min({most, std::max(fill, even), (int64_t)kMostSplits});
   return c;
 }
@@ -581,8 +967,9 @@ hipError_t go(const Attn4Args& a, const Cut& c, hipStream_t stream) {
   constexpr int64_t kMost = 1 << 23;  // workgroups of a launch: 2^32 threads are refused
   for (int64_t u = 0; u < units; u += kMost) {
     const dim3 grid((unsigned)std::min(kMost, units - u));
-    if (c.tiles16 == 1) hipLaunchKernelGGL((kv4_attention_kernel<ND, 1>), grid, dim3(256), 0, stream, a, c.splits, u);
-    else hipLaunchKernelGGL((kv4_attention_kernel<ND, 2>), grid, dim3(256), 0, stream, a, c.splits, u);
+    if (c.rows == 16) hipLaunchKernelGGL((kv4_attention_kernel<ND, 1>), grid, dim3(256), 0, stream, a, c.splits, u);
+    else if (c.rows == 32) hipLaunchKernelGGL((kv4_attention_kernel<ND, 2>), grid, dim3(256), 0, stream, a, c.splits, u);
+    else hipLaunchKernelGGL((kv4_prompt_kernel<ND>), grid, dim3(256), 0, stream, a, c.splits, u, c.tiles);
   }
   if (c.splits > 1) {
     const int64_t rows = (int64_t)a.tokens * a.q_heads;

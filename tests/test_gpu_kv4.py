@@ -367,6 +367,9 @@ ATTENTION = [  # lengths, new, q heads, heads, d, page, causal, window, scale
     ([20, 40], [33, 12], 4, 2, 128, 16, True, 0, None),            # rows before the beginning
     ([260], [200], 3, 3, 256, 16, True, 0, None),
     ([120, 500], [70, 90], 2, 1, 192, 64, True, 33, None),
+    ([200, 90], [110, 90], 3, 1, 160, 16, True, 0, None),
+    ([180], [100], 2, 2, 224, 32, True, 75, None),
+    ([700, 20], [300, 20], 8, 2, 128, 16, True, 0, 0.5),
     ([64] * 130, [1] * 130, 2, 1, 64, 16, True, 0, None),
     ([1000], [1], 64, 1, 128, 16, True, 0, None),
 ]
