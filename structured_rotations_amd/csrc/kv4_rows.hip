@@ -22,136 +22,226 @@ __device__ __forceinline__ uint32_t scale4(uint32_t top) {
   return (uint32_t)max(e, 127 - 120);
 }
 
-// Where the tokens of a call lie.  Waves walk over tokens; `threads` lanes of
-// a wave's 64 at a time over a token's keys and values, 8 values each.
-struct Place {
-  int64_t page;  // -1: none
-  int in_page;   // -1: before the sequence's beginning or behind the last one
-};
-__device__ __forceinline__ Place place_of(const Cache4& c, const Plan4& p, int64_t row) {
-  const int b = sequence_of(p, row);
-  const int64_t first = p.starts[b], end = p.starts[b + 1];
-  const int64_t pos = (int64_t)p.lengths[b] - (end - row);
-  if (row < first || row >= end) return {-1, -2};
-  if (pos < 0) return {-1, -1};
-  const int64_t page = pos >> c.page_log2;
-  return {page_of(c, p, b, page), (int)(pos - (page << c.page_log2))};
-}
-
-// The u-th 8 values of a token: keys first, then values.
-struct Unit {
-  bool is_k;
-  int head, col;
-  __device__ __forceinline__ Unit(const Cache4& c, int u) {
-    const int per_head = c.d >> 3, side = c.heads * per_head;
-    is_k = u < side;
-    const int in = is_k ? u : u - side;
-    head = in / per_head;
-    col = (in - head * per_head) * 8;
+// Where a wave's tokens lie.  It goes from token to token of one sequence; what
+// it knows of the sequence and of the page serves while they last.
+struct Walker {
+  const Cache4& c;
+  const Plan4& p;
+  int seq = -1;
+  int64_t first = 0, end = 0, len = 0;
+  int64_t page = -1;   // the sequence's
+  int64_t at = -1;     // the cache's; -1: none
+  int in_page = 0;     // place in it; -1: before the sequence's beginning, -2: not of the call
+  __device__ __forceinline__ Walker(const Cache4& c_, const Plan4& p_) : c(c_), p(p_) {}
+  __device__ __forceinline__ void go(int64_t row) {
+    if (row >= end || row < first) {
+      seq = __builtin_amdgcn_readfirstlane(sequence_of(p, row));
+      first = p.starts[seq];
+      end = p.starts[seq + 1];
+      len = p.lengths[seq];
+      page = -1;
+      if (row >= end || row < first) {
+        in_page = -2;
+        first = end = 0;
+        return;
+      }
+    }
+    const int64_t pos = len - (end - row);
+    if (pos < 0) {
+      in_page = -1;
+      at = -1;
+      return;
+    }
+    const int64_t now = pos >> c.page_log2;
+    if (now != page) {
+      page = now;
+      at = page_of(c, p, seq, now);
+    }
+    in_page = (int)(pos - (now << c.page_log2));
   }
 };
-__device__ __forceinline__ int64_t row_in_page(const Cache4& c, int head, int in_page) {
-  return ((int64_t)head << c.page_log2) + in_page;
-}
 
+// A lane's 8 values of every token: the u-th of the token's, keys first.
 template <typename T>
-__global__ __launch_bounds__(256) void kv4_write_kernel(Cache4 c, Plan4 p, Heads k, Heads v, int tokens, int parts) {
-  const int units = c.heads * (c.d >> 2), lane = threadIdx.x & 63;
-  const int per = ((units + 63) / 64 + parts - 1) / parts * 64;
-  const int64_t all = (int64_t)tokens * parts;
-  for (int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); unit < all; unit += (int64_t)gridDim.x * 4) {
-    const int64_t row = unit / parts;
-    const int first = (int)(unit - row * parts) * per, end = min(units, first + per);
-    const Place at = place_of(c, p, row);
-    if (at.page < 0) continue;
-    for (int u0 = first; u0 < end; u0 += 64) {
-      const int u = u0 + lane;
-      if (u >= end) continue;  // quads stay whole: end and u0 are multiples of 4
-      const Unit w(c, u);
-      const Heads& s = w.is_k ? k : v;
-      Raw8<T> x;
-      x.load(static_cast<const T*>(s.p) + row * s.token + w.head * s.head + w.col, 8);
-      float f[8];
+struct Unit {
+  bool has, is_k;
+  uint64_t io, codes, scales;  // addresses of token 0, of the page's first place
+  Unit() = default;
+  __device__ __forceinline__ Unit(const Cache4& c, const Heads& k, const Heads& v, int u) {
+    const int per_head = c.d >> 3, side = c.heads * per_head;
+    has = u < 2 * side;
+    is_k = u < side;
+    const int in = has ? is_k ? u : u - side : 0, head = in / per_head, col = (in - head * per_head) * 8;
+    const Heads& s = is_k ? k : v;
+    const Side4& o = is_k ? c.k : c.v;
+    const int64_t row = (int64_t)head << c.page_log2;
+    io = reinterpret_cast<uint64_t>(s.p) + (uint64_t)(head * s.head + col) * sizeof(T);
+    codes = reinterpret_cast<uint64_t>(o.codes) + (uint64_t)(row * (c.d >> 1) + (col >> 1));
+    scales = reinterpret_cast<uint64_t>(o.scales) + (uint64_t)(row * (c.d >> 5) + (col >> 5));
+  }
+  __device__ __forceinline__ T* row(const Heads& k, const Heads& v, int64_t row) const {
+    return reinterpret_cast<T*>(io + (uint64_t)(row * (is_k ? k.token : v.token)) * sizeof(T));
+  }
+  __device__ __forceinline__ uint32_t* code(const Cache4& c, const Walker& w) const {
+    return reinterpret_cast<uint32_t*>(codes + (uint64_t)(w.at * (is_k ? c.k.codes_page : c.v.codes_page) +
+                                                          (int64_t)w.in_page * (c.d >> 1)));
+  }
+  __device__ __forceinline__ uint8_t* scale(const Cache4& c, const Walker& w) const {
+    return reinterpret_cast<uint8_t*>(scales + (uint64_t)(w.at * (is_k ? c.k.scales_page : c.v.scales_page) +
+                                                          (int64_t)w.in_page * (c.d >> 5)));
+  }
+};
+
+// How the work is cut: a wave takes kRounds times 64 units of each of `run`
+// tokens that follow one another, the next token's loads under way while it
+// turns the present one's.
+struct Cut {
+  int parts, run;
+  int64_t waves;
+};
+
+template <typename T, int kRounds>
+__global__ __launch_bounds__(256) void kv4_write_kernel(Cache4 c, Plan4 p, Heads k, Heads v, int tokens, Cut cut) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  if (wave >= cut.waves) return;
+  const uint32_t group = wave / (uint32_t)cut.parts, part = wave - group * cut.parts;
+  const int64_t row0 = (int64_t)group * cut.run, row1 = min(row0 + cut.run, (int64_t)tokens);
+  Unit<T> unit[kRounds];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = x[i];
-      uint32_t top = amax8(f);
+  for (int r = 0; r < kRounds; ++r) unit[r] = Unit<T>(c, k, v, (part * kRounds + r) * 64 + lane);
+  Walker walk(c, p);
+  Raw8<T> next[kRounds];
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+      if (unit[r].has) next[r].load(unit[r].row(k, v, row), 8);
+  };
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) next[r].fill(0);
+  load(row0);
+  for (int64_t row = row0; row < row1; ++row) {
+    walk.go(row);
+    float f[kRounds][8];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[r][i] = next[r][i];
+    if (row + 1 < row1) load(row + 1);
+    if (walk.in_page < 0 || walk.at < 0) continue;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      uint32_t top = amax8(f[r]);
       top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xb1, 0xf, 0xf, true));
       top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4e, 0xf, 0xf, true));
       const uint32_t e = scale4(top);
       const float scale = __uint_as_float(e << 23);
       uint32_t codes = 0;
-      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[0], f[1], scale, 0);
-      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[2], f[3], scale, 1);
-      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[4], f[5], scale, 2);
-      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[6], f[7], scale, 3);
+      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[r][0], f[r][1], scale, 0);
+      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[r][2], f[r][3], scale, 1);
+      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[r][4], f[r][5], scale, 2);
+      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[r][6], f[r][7], scale, 3);
       if (e == 255) codes = 0;
-      const Side4& o = w.is_k ? c.k : c.v;
-      const int64_t to = row_in_page(c, w.head, at.in_page);
-      *reinterpret_cast<uint32_t*>(o.codes + at.page * o.codes_page + to * (c.d >> 1) + (w.col >> 1)) = codes;
-      if ((lane & 3) == 0) o.scales[at.page * o.scales_page + to * (c.d >> 5) + (w.col >> 5)] = (uint8_t)e;
-    }
-  }
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void kv4_read_kernel(Cache4 c, Plan4 p, Heads k, Heads v, int tokens, int parts) {
-  const int units = c.heads * (c.d >> 2), lane = threadIdx.x & 63;
-  const int per = ((units + 63) / 64 + parts - 1) / parts * 64;
-  const int64_t all = (int64_t)tokens * parts;
-  for (int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); unit < all; unit += (int64_t)gridDim.x * 4) {
-    const int64_t row = unit / parts;
-    const int first = (int)(unit - row * parts) * per, end = min(units, first + per);
-    const Place at = place_of(c, p, row);
-    if (at.in_page == -2) continue;
-    for (int u = first + lane; u < end; u += 64) {
-      const Unit w(c, u);
-      uint32_t codes = 0, e = at.in_page < 0 ? 127 : 255;
-      if (at.page >= 0) {
-        const Side4& o = w.is_k ? c.k : c.v;
-        const int64_t from = row_in_page(c, w.head, at.in_page);
-        codes = *reinterpret_cast<const uint32_t*>(o.codes + at.page * o.codes_page + from * (c.d >> 1) + (w.col >> 1));
-        e = o.scales[at.page * o.scales_page + from * (c.d >> 5) + (w.col >> 5)];
+      if (unit[r].has) {
+        *unit[r].code(c, walk) = codes;
+        if ((lane & 3) == 0) *unit[r].scale(c, walk) = (uint8_t)e;
       }
-      const float scale = __uint_as_float(e << 23);  // the conversion reads the exponent only; 255 gives NaN
-      float f[8];
-      const f32x2 a0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 0);
-      const f32x2 a1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 1);
-      const f32x2 a2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 2);
-      const f32x2 a3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 3);
-      f[0] = a0[0]; f[1] = a0[1]; f[2] = a1[0]; f[3] = a1[1];
-      f[4] = a2[0]; f[5] = a2[1]; f[6] = a3[0]; f[7] = a3[1];
-      const Heads& s = w.is_k ? k : v;
-      store8(static_cast<T*>(s.p) + row * s.token + w.head * s.head + w.col, f);
     }
   }
 }
 
-// Parts of a token, a wave each: one where there are tokens enough, else as
-// many as the chip has room for.
-int parts_of(const Cache4& c, int tokens) {
-  const int rounds = (c.heads * (c.d >> 2) + 63) / 64;
-  return std::min(rounds, std::max(1, 8192 / std::max(1, tokens)));
+template <typename T, int kRounds>
+__global__ __launch_bounds__(256) void kv4_read_kernel(Cache4 c, Plan4 p, Heads k, Heads v, int tokens, Cut cut) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  if (wave >= cut.waves) return;
+  const uint32_t group = wave / (uint32_t)cut.parts, part = wave - group * cut.parts;
+  const int64_t row0 = (int64_t)group * cut.run, row1 = min(row0 + cut.run, (int64_t)tokens);
+  Unit<T> unit[kRounds];
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) unit[r] = Unit<T>(c, k, v, (part * kRounds + r) * 64 + lane);
+  Walker walk(c, p);
+  uint32_t codes[kRounds], e[kRounds];
+  int kind = 0;  // of the token whose codes are held: Walker's in_page
+  auto load = [&](int64_t row) {
+    walk.go(row);
+    kind = walk.in_page;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      codes[r] = 0;
+      e[r] = kind < 0 ? 127 : 255;
+      if (kind >= 0 && walk.at >= 0 && unit[r].has) {
+        codes[r] = *unit[r].code(c, walk);
+        e[r] = *unit[r].scale(c, walk);
+      }
+    }
+  };
+  load(row0);
+  for (int64_t row = row0; row < row1; ++row) {
+    uint32_t w[kRounds], s[kRounds];
+    const int now = kind;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      w[r] = codes[r];
+      s[r] = e[r];
+    }
+    if (row + 1 < row1) load(row + 1);
+    if (now == -2) continue;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const float scale = __uint_as_float(s[r] << 23);  // the conversion reads the exponent only; 255 gives NaN
+      const f32x2 a0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[r], scale, 0);
+      const f32x2 a1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[r], scale, 1);
+      const f32x2 a2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[r], scale, 2);
+      const f32x2 a3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[r], scale, 3);
+      const float f[8] = {a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
+      if (unit[r].has) store8(unit[r].row(k, v, row), f);
+    }
+  }
 }
+
+// A wave for every 64 units of a token where tokens are few; four times as many
+// where they are not, then runs of tokens, until the chip is about twice full.
+template <int kRounds>
+Cut cut_of(const Cache4& c, int tokens) {
+  Cut r;
+  const int rounds = (c.heads * (c.d >> 2) + 63) / 64;
+  r.parts = (rounds + kRounds - 1) / kRounds;
+  const int64_t all = (int64_t)tokens * r.parts;
+  r.run = kRounds == 1 ? 1 : (int)std::min<int64_t>(std::max<int64_t>(1, all / 8192), 64);
+  // launches are of up to 2^25 waves
+  while ((((int64_t)tokens + r.run - 1) / r.run) * r.parts > (1 << 25)) r.run *= 2;
+  r.waves = (((int64_t)tokens + r.run - 1) / r.run) * r.parts;
+  return r;
+}
+bool few(const Cache4& c, int tokens) { return (int64_t)tokens * ((c.heads * (c.d >> 2) + 63) / 64) <= 8192; }
 
 template <typename K>
-hipError_t go(K kernel, const Cache4& c, const Plan4& p, const Heads& k, const Heads& v, int tokens, hipStream_t stream) {
-  const int parts = parts_of(c, tokens);
-  const dim3 grid((unsigned)std::min<int64_t>(((int64_t)tokens * parts + 3) / 4, 1 << 20));
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, c, p, k, v, tokens, parts);
+hipError_t go(K kernel, const Cut& cut, const Cache4& c, const Plan4& p, const Heads& k, const Heads& v, int tokens,
+              hipStream_t stream) {
+  hipLaunchKernelGGL(kernel, dim3((unsigned)((cut.waves + 3) / 4)), dim3(256), 0, stream, c, p, k, v, tokens, cut);
   return hipGetLastError();
+}
+template <typename T>
+hipError_t write_go(const Cache4& c, const Plan4& p, const Heads& k, const Heads& v, int tokens, hipStream_t stream) {
+  return few(c, tokens) ? go(kv4_write_kernel<T, 1>, cut_of<1>(c, tokens), c, p, k, v, tokens, stream)
+                        : go(kv4_write_kernel<T, 4>, cut_of<4>(c, tokens), c, p, k, v, tokens, stream);
+}
+template <typename T>
+hipError_t read_go(const Cache4& c, const Plan4& p, const Heads& k, const Heads& v, int tokens, hipStream_t stream) {
+  return few(c, tokens) ? go(kv4_read_kernel<T, 1>, cut_of<1>(c, tokens), c, p, k, v, tokens, stream)
+                        : go(kv4_read_kernel<T, 4>, cut_of<4>(c, tokens), c, p, k, v, tokens, stream);
 }
 
 }  // namespace
 
 hipError_t launch_kv4_write(const Cache4& c, const Plan4& p, const Heads& k, const Heads& v, int tokens, DT io,
                             hipStream_t stream) {
-  return io == DT::F32 ? go(kv4_write_kernel<float>, c, p, k, v, tokens, stream)
-                       : go(kv4_write_kernel<uint16_t>, c, p, k, v, tokens, stream);
+  return io == DT::F32 ? write_go<float>(c, p, k, v, tokens, stream) : write_go<uint16_t>(c, p, k, v, tokens, stream);
 }
 hipError_t launch_kv4_read(const Cache4& c, const Plan4& p, const Heads& k, const Heads& v, int tokens, DT io,
                            hipStream_t stream) {
-  return io == DT::F32 ? go(kv4_read_kernel<float>, c, p, k, v, tokens, stream)
-                       : go(kv4_read_kernel<uint16_t>, c, p, k, v, tokens, stream);
+  return io == DT::F32 ? read_go<float>(c, p, k, v, tokens, stream) : read_go<uint16_t>(c, p, k, v, tokens, stream);
 }
 
 }  // namespace harp

@@ -16,45 +16,90 @@ namespace harp {
 namespace {
 
 // v of another lane of the same 16: a DPP control.
-template <int kCtrl, int kBanks = 0xf>
-__device__ __forceinline__ float dpp(float v, float old = 0.0f) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)__float_as_uint(old), (int)__float_as_uint(v),
-                                                               kCtrl, 0xf, kBanks, kBanks == 0xf));
-}
-// v of lane ^ kMask.
-template <int kMask>
-__device__ __forceinline__ float lane_xor(float v) {
-  if constexpr (kMask == 1) return dpp<0xb1>(v);        // quad_perm [1, 0, 3, 2]
-  else if constexpr (kMask == 2) return dpp<0x4e>(v);   // quad_perm [2, 3, 0, 1]
-  else if constexpr (kMask == 4) return dpp<0x124, 0xa>(v, dpp<0x12c, 0x5>(v));  // row_ror 4 and 12, by banks of 4
-  else if constexpr (kMask == 8) return dpp<0x128>(v);  // row_ror 8
-  else return __shfl_xor(v, kMask);
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), kCtrl, 0xf, 0xf, true));
 }
 // Sum over the kLanes lanes of a head, in every one of them.
 template <int kLanes>
 __device__ __forceinline__ float head_sum(float v) {
-  v += lane_xor<1>(v);
-  v += lane_xor<2>(v);
+  v += dpp<0xb1>(v);                            // lane ^ 1
+  v += dpp<0x4e>(v);                            // lane ^ 2
   v += dpp<0x141>(v);                           // the other 4 of 8 (mirrored)
   if constexpr (kLanes >= 16) v += dpp<0x140>(v);  // the other 8 of 16 (mirrored)
-  if constexpr (kLanes >= 32) v += lane_xor<16>(v);
-  if constexpr (kLanes >= 64) v += lane_xor<32>(v);
+  if constexpr (kLanes >= 32) v += __shfl_xor(v, 16);
+  if constexpr (kLanes >= 64) v += __shfl_xor(v, 32);
   return v;
 }
 
+// One stage between lanes, but for a sign: with p the partner's value, lanes of
+// bit 0 get v + p and those of bit 1 get v - p, where a - b = p - v is meant.
+// The sign left out is the same in both partners of every later stage, so all
+// of them are made good at the end, by the parity of the lane's bits.
+//
+// Written out: the exchange is an operand of the multiply-add, which the
+// compiler makes two instructions of, with waits between them.  A value may be
+// read that way two instructions after it is written, hence the waits in front;
+// eight values one after the other keep that distance from stage to stage.
+#define HARP_STAGE(ctrl)                                                              \
+  asm("s_nop 1\n\t"                                                                  \
+      "v_fmac_f32_dpp %0, %0, %8 " ctrl "\n\tv_fmac_f32_dpp %1, %1, %8 " ctrl "\n\t" \
+      "v_fmac_f32_dpp %2, %2, %8 " ctrl "\n\tv_fmac_f32_dpp %3, %3, %8 " ctrl "\n\t" \
+      "v_fmac_f32_dpp %4, %4, %8 " ctrl "\n\tv_fmac_f32_dpp %5, %5, %8 " ctrl "\n\t" \
+      "v_fmac_f32_dpp %6, %6, %8 " ctrl "\n\tv_fmac_f32_dpp %7, %7, %8 " ctrl         \
+      : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]), "+v"(v[7]) \
+      : "v"(other))
+// The same onto values of their own, for an exchange that takes two controls.
+#define HARP_STAGE_ONTO(ctrl)                                                           \
+  asm("s_nop 1\n\t"                                                                    \
+      "v_fmac_f32_dpp %0, %8, %16 " ctrl "\n\tv_fmac_f32_dpp %1, %9, %16 " ctrl "\n\t"  \
+      "v_fmac_f32_dpp %2, %10, %16 " ctrl "\n\tv_fmac_f32_dpp %3, %11, %16 " ctrl "\n\t" \
+      "v_fmac_f32_dpp %4, %12, %16 " ctrl "\n\tv_fmac_f32_dpp %5, %13, %16 " ctrl "\n\t" \
+      "v_fmac_f32_dpp %6, %14, %16 " ctrl "\n\tv_fmac_f32_dpp %7, %15, %16 " ctrl          \
+      : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]), "+v"(w[4]), "+v"(w[5]), "+v"(w[6]), "+v"(w[7]) \
+      : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]), "v"(other))
 template <int kMask>
-__device__ __forceinline__ void butterfly(float (&v)[8], int lane, int d) {
-  if (8 * kMask >= d) return;
-  const float own = lane & kMask ? -1.0f : 1.0f;
+__device__ __forceinline__ void butterfly(float (&v)[8], int lane) {
+  const float other = lane & kMask ? -1.0f : 1.0f;
+  if constexpr (kMask == 1) {
+    HARP_STAGE("quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf");
+  } else if constexpr (kMask == 2) {
+    HARP_STAGE("quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf");
+  } else if constexpr (kMask == 4) {  // by banks of 4 lanes: from 4 above, from 4 below
+    float w[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], own, lane_xor<kMask>(v[i]));
+    for (int i = 0; i < 8; ++i) w[i] = v[i];
+    HARP_STAGE_ONTO("row_ror:12 row_mask:0xf bank_mask:0x5");
+    HARP_STAGE_ONTO("row_ror:4 row_mask:0xf bank_mask:0xa");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = w[i];
+  } else if constexpr (kMask == 8) {
+    HARP_STAGE("row_ror:8 row_mask:0xf bank_mask:0xf");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(__shfl_xor(v[i], kMask), other, v[i]);
+  }
 }
-// Sylvester matrix of order d, not normalised: three stages within a lane, the
-// others between lanes.
+#undef HARP_STAGE
+#undef HARP_STAGE_ONTO
+// Sylvester matrix of order d, not normalised: stages between lanes, then three
+// within a lane, of which the last one takes the sign.
 template <int kLanes>
 __device__ __forceinline__ void hadamard(float (&v)[8], int lane, int d) {
+  if constexpr (kLanes == 8) {  // d = 8 to 64
+    if (d > 8) butterfly<1>(v, lane);
+    if (d > 16) butterfly<2>(v, lane);
+    if (d > 32) butterfly<4>(v, lane);
+  } else {  // d = 8 lanes: a power of two, of half that it would have half the lanes
+    butterfly<1>(v, lane);
+    butterfly<2>(v, lane);
+    butterfly<4>(v, lane);
+    butterfly<8>(v, lane);
+    if constexpr (kLanes >= 32) butterfly<16>(v, lane);
+    if constexpr (kLanes >= 64) butterfly<32>(v, lane);
+  }
 #pragma unroll
-  for (int m = 1; m < 8; m *= 2)
+  for (int m = 1; m < 4; m *= 2)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (!(i & m)) {
@@ -62,49 +107,79 @@ __device__ __forceinline__ void hadamard(float (&v)[8], int lane, int d) {
         v[i] = a + b;
         v[i + m] = a - b;
       }
-  butterfly<1>(v, lane, d);
-  butterfly<2>(v, lane, d);
-  butterfly<4>(v, lane, d);
-  if constexpr (kLanes >= 16) butterfly<8>(v, lane, d);
-  if constexpr (kLanes >= 32) butterfly<16>(v, lane, d);
-  if constexpr (kLanes >= 64) butterfly<32>(v, lane, d);
+  const float sign = __popc(lane & (d / 8 - 1)) & 1 ? -1.0f : 1.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = v[i], b = v[i + 4] * sign;
+    v[i] = fmaf(a, sign, b);
+    v[i + 4] = fmaf(a, sign, -b);
+  }
 }
 
 // A lane's share of a token's turn: out = c v + s partner(v), with the partner
 // in lane `from` (pairs j, j + pairs) or in the same lane (interleaved pairs).
-template <bool kInter>
+template <int kLanes, bool kInter>
 struct Turn {
   float c[8], s[8];
   int from;
 
-  // Angles reach 2^31 times a frequency: in turns and 64 bits until the whole
-  // turns are gone.  What fp64 leaves off is 2^-53 of the angle.
+  // Each lane computes every 64th pair's angle, and gets what it needs from the
+  // others.  Angles reach 2^31 times a frequency: in turns and 64 bits until the
+  // whole turns are gone.  What fp64 leaves off is 2^-53 of the angle.
   __device__ __forceinline__ void make(const QkArgs& a, int64_t token, int lane, float back) {
+    constexpr int kRounds = kLanes <= 16 ? 1 : kLanes / 16;  // pairs are at most 4 to a lane of a head
+    const int self = threadIdx.x & 63;
     const double pos = a.pairs == 0 ? 0.0  // no positions either
                        : a.wide     ? (double)static_cast<const int64_t*>(a.positions)[token]
                                     : (double)static_cast<const int32_t*>(a.positions)[token];
+    float sn[kRounds], cs[kRounds];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      sn[r] = 0.0f;
+      cs[r] = 1.0f;
+      if (64 * r + self < a.pairs) {
+        double t = pos * (a.freqs[64 * r + self] * 0.15915494309189533577);
+        t -= rint(t);
+        sincospif(2.0f * (float)t, &sn[r], &cs[r]);
+        sn[r] *= back;
+      }
+    }
     const int e = 8 * lane;
     const bool turned = e < 2 * a.pairs, second = !kInter && e >= a.pairs;
     const int j0 = !turned ? 0 : kInter ? e / 2 : second ? e - a.pairs : e;
 #pragma unroll
     for (int i = 0; i < (kInter ? 4 : 8); ++i) {
-      float sn = 0.0f, cs = 1.0f;
-      if (turned) {
-        double t = pos * (a.freqs[j0 + i] * 0.15915494309189533577);
-        t -= rint(t);
-        sincospif(2.0f * (float)t, &sn, &cs);
+      float x = __shfl(sn[0], (j0 + i) & 63), y = __shfl(cs[0], (j0 + i) & 63);
+#pragma unroll
+      for (int r = 1; r < kRounds; ++r) {
+        const float xr = __shfl(sn[r], (j0 + i) & 63), yr = __shfl(cs[r], (j0 + i) & 63);
+        if (j0 >= 64 * r) {
+          x = xr;
+          y = yr;
+        }
       }
-      sn *= back;
+      if (!turned) {
+        x = 0.0f;
+        y = 1.0f;
+      }
       if constexpr (kInter) {
-        c[2 * i] = c[2 * i + 1] = cs;
-        s[2 * i] = -sn;
-        s[2 * i + 1] = sn;
+        c[2 * i] = c[2 * i + 1] = y;
+        s[2 * i] = -x;
+        s[2 * i + 1] = x;
       } else {
-        c[i] = cs;
-        s[i] = second ? sn : -sn;
+        c[i] = y;
+        s[i] = second ? x : -x;
       }
     }
-    from = (threadIdx.x & 63) + (!turned || kInter ? 0 : (second ? -a.pairs : a.pairs) / 8);
+    from = self + (!turned || kInter ? 0 : (second ? -a.pairs : a.pairs) / 8);
+  }
+  // What the turned values are multiplied by next.
+  __device__ __forceinline__ void times(const float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] *= f[i];
+      s[i] *= f[i];
+    }
   }
   __device__ __forceinline__ void apply(float (&v)[8]) const {
     float o[8];
@@ -115,6 +190,14 @@ struct Turn {
   }
 };
 
+// 1 / sqrt(x) of an x from 2^-100 on: the hardware's estimate (an ulp off) and
+// one step of Newton's method, with what x r^2 is off 1 to twice fp32's width.
+__device__ __forceinline__ float rsqrt_of(float x) {
+  const float r = __builtin_amdgcn_rsqf(x), t = x * r;
+  const float e = fmaf(-t, r, 1.0f) - fmaf(x, r, -t) * r;
+  return fmaf(0.5f * r, e, r);
+}
+
 // 1 / sqrt(mean(x^2) + eps), of any finite head: squares beyond fp32's range
 // are summed again in other units.
 template <int kLanes>
@@ -123,7 +206,7 @@ __device__ __forceinline__ float head_rstd(const float (&v)[8], float d, float e
 #pragma unroll
   for (int i = 0; i < 8; ++i) ss += v[i] * v[i];
   ss = head_sum<kLanes>(ss);
-  float r = 1.0f / sqrtf(ss / d + eps);
+  float r = rsqrt_of(fmaf(ss, 1.0f / d, eps));
   const bool far = !(ss >= least && ss < __uint_as_float(0x7f800000u));
   if (__any(far)) {  // the whole wave, so that every lane has its partners
     const float unit = ss < least ? 0x1p80f : 0x1p-80f;
@@ -148,16 +231,39 @@ struct HeadMap {
     has = 8 * lane < d;
   }
 };
-template <typename T>
-__device__ __forceinline__ T* head_at(const Heads& q, const Heads& k, int64_t token, int h, int col) {
-  const bool is_q = h < q.heads;
-  const Heads& s = is_q ? q : k;
-  return static_cast<T*>(s.p) + token * s.token + (int64_t)(is_q ? h : h - q.heads) * s.head + col;
-}
+// The places of a wave's heads in one pair of arrays, which go from head to head
+// by additions.  (Where a head is none of the one array its address there is not
+// used.)
+template <typename T, int kPar>
+struct Walk {
+  uint64_t q, k, q_step, k_step;
+  __device__ __forceinline__ Walk(const Heads& sq, const Heads& sk, int64_t token, int h, int col) {
+    q = reinterpret_cast<uint64_t>(sq.p) + (uint64_t)(token * sq.token + h * sq.head + col) * sizeof(T);
+    k = reinterpret_cast<uint64_t>(sk.p) + (uint64_t)(token * sk.token + (h - sq.heads) * sk.head + col) * sizeof(T);
+    q_step = (uint64_t)sq.head * (kPar * sizeof(T));
+    k_step = (uint64_t)sk.head * (kPar * sizeof(T));
+  }
+  __device__ __forceinline__ T* at(bool is_q) const { return reinterpret_cast<T*>(is_q ? q : k); }
+  __device__ __forceinline__ void next() {
+    q += q_step;
+    k += k_step;
+  }
+};
 __device__ __forceinline__ void load_signs(const QkArgs& a, int lane, bool has, float (&sg)[8]) {
-  const float unit = 1.0f / sqrtf((float)a.d);
+  const float unit = rsqrt_of((float)a.d);
+  RawCodes w;  // 8 bytes
+  w.w[0] = w.w[1] = 0;
+  if (has) w.load(reinterpret_cast<const uint8_t*>(a.signs) + 8 * lane, 8);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sg[i] = has ? unit * (float)a.signs[8 * lane + i] : 0.0f;
+  for (int i = 0; i < 8; ++i) sg[i] = unit * (float)(int8_t)(w.w[i >> 2] >> (8 * (i & 3)));
+}
+template <typename T>
+__device__ __forceinline__ void load_gamma(const void* gamma, int col, bool has, float (&g)[8]) {
+  Raw8<T> w;
+  w.fill(0x3f800000u);
+  if (gamma && has) w.load(static_cast<const T*>(gamma) + col, 8);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] = w[i];
 }
 __device__ __forceinline__ float least_of(float eps) { return eps < 0x1p-100f ? 0x1p-80f : 0.0f; }
 
@@ -165,26 +271,31 @@ __device__ __forceinline__ float least_of(float eps) { return eps < 0x1p-100f ? 
 template <typename T, int kLanes, bool kInter>
 __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs a, int per, int parts) {
   const HeadMap<kLanes> map(a.d);
-  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t token = unit / parts;
+  // (units of a launch are less than 2^26)
+  const uint32_t unit = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  const int token = (int)(unit / (uint32_t)parts);
   if (token >= a.tokens) return;
-  const int heads = a.q.heads + a.k.heads, first = (int)(unit - token * parts) * per;
+  const int heads = a.q.heads + a.k.heads, first = ((int)unit - token * parts) * per;
   const int end = min(heads, first + per), col = 8 * map.lane;
   Raw8<T> next;
+  Walk<const T, map.kPar> in(a.q, a.k, token, first + map.slot, col);
+  Walk<T, map.kPar> to(a.yq, a.yk, token, first + map.slot, col);
   auto load = [&](int h) {
     next.fill(0);
-    if (map.has && h < end) next.load(head_at<const T>(a.q, a.k, token, h, col), 8);
+    if (map.has && h < end) next.load(in.at(h < a.q.heads), 8);
+    in.next();
   };
   load(first + map.slot);
-  Turn<kInter> turn;
+  Turn<kLanes, kInter> turn;
   turn.make(a, token, map.lane, 1.0f);
-  Raw8<T> gq, gk;
-  gq.fill(0x3f800000u);
-  gk.fill(0x3f800000u);
-  if (a.gamma_q && map.has) gq.load(static_cast<const T*>(a.gamma_q) + col, 8);
-  if (a.gamma_k && map.has) gk.load(static_cast<const T*>(a.gamma_k) + col, 8);
-  float sg[8];
-  if (a.signs) load_signs(a, map.lane, map.has, sg);
+  float gq[8], gk[8];
+  load_gamma<T>(a.gamma_q, col, map.has, gq);
+  load_gamma<T>(a.gamma_k, col, map.has, gk);
+  if (a.signs) {
+    float sg[8];
+    load_signs(a, map.lane, map.has, sg);
+    turn.times(sg);
+  }
   const float d = (float)a.d, least = least_of(a.eps);
   for (int h0 = first; h0 < end; h0 += map.kPar) {
     const int h = h0 + map.slot;
@@ -197,12 +308,9 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs a, int per, in
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = v[i] * r * (is_q ? gq[i] : gk[i]);
     turn.apply(v);
-    if (a.signs) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= sg[i];
-      hadamard<kLanes>(v, map.lane, a.d);
-    }
-    if (map.has && h < end) store8(head_at<T>(a.yq, a.yk, token, h, col), v);
+    if (a.signs) hadamard<kLanes>(v, map.lane, a.d);
+    if (map.has && h < end) store8(to.at(is_q), v);
+    to.next();
   }
 }
 
@@ -210,41 +318,43 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs a, int per, in
 // lanes' shares of the two dgammas in registers; the shares of a workgroup are
 // added in order through LDS, those of the workgroups by the second kernel.
 template <typename T, int kLanes, bool kInter>
-__global__ __launch_bounds__(256) void qk_norm_rope_vjp_kernel(QkArgs a, int per, int parts) {
+__global__ __launch_bounds__(256, 4) void qk_norm_rope_vjp_kernel(QkArgs a, int per, int parts) {
   const HeadMap<kLanes> map(a.d);
   const int heads = a.q.heads + a.k.heads, col = 8 * map.lane;
-  const int64_t units = a.tokens * parts, step = (int64_t)gridDim.x * 4;
-  Raw8<T> gq, gk;
-  gq.fill(0x3f800000u);
-  gk.fill(0x3f800000u);
-  if (a.gamma_q && map.has) gq.load(static_cast<const T*>(a.gamma_q) + col, 8);
-  if (a.gamma_k && map.has) gk.load(static_cast<const T*>(a.gamma_k) + col, 8);
-  float sg[8], sum_q[8], sum_k[8];
+  // tokens up to 2^30 in one part, or up to 4096 in several
+  const uint32_t units = (uint32_t)(a.tokens * parts), step = gridDim.x * 4;
+  float gq[8], gk[8], sg[8], sum_q[8], sum_k[8];
+  load_gamma<T>(a.gamma_q, col, map.has, gq);
+  load_gamma<T>(a.gamma_k, col, map.has, gk);
   if (a.signs) load_signs(a, map.lane, map.has, sg);
 #pragma unroll
   for (int i = 0; i < 8; ++i) sum_q[i] = sum_k[i] = 0.0f;
   const float d = (float)a.d, least = least_of(a.eps);
-  for (int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); unit < units; unit += step) {
-    const int64_t token = unit / parts;
-    const int first = (int)(unit - token * parts) * per, end = min(heads, first + per);
+  for (uint32_t unit = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6)); unit < units; unit += step) {
+    const int token = (int)(unit / (uint32_t)parts);
+    const int first = ((int)unit - token * parts) * per, end = min(heads, first + per);
     Raw8<T> xn, gn;
+    Walk<const T, map.kPar> x_at(a.q, a.k, token, first + map.slot, col), g_at(a.yq, a.yk, token, first + map.slot, col);
+    Walk<T, map.kPar> to(a.dq, a.dk, token, first + map.slot, col);
     auto load = [&](int h) {
       xn.fill(0);
       gn.fill(0);
       if (map.has && h < end) {
-        xn.load(head_at<const T>(a.q, a.k, token, h, col), 8);
-        gn.load(head_at<const T>(a.yq, a.yk, token, h, col), 8);
+        xn.load(x_at.at(h < a.q.heads), 8);
+        gn.load(g_at.at(h < a.q.heads), 8);
       }
+      x_at.next();
+      g_at.next();
     };
     load(first + map.slot);
-    Turn<kInter> turn;
+    Turn<kLanes, kInter> turn;
     turn.make(a, token, map.lane, -1.0f);
     for (int h0 = first; h0 < end; h0 += map.kPar) {
       const int h = h0 + map.slot;
       float x[8], g[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[i] = xn[i];
+        x[i] = xn[i];  // zeros where there is no head: nothing is added for it
         g[i] = gn[i];
       }
       load(h + map.kPar);
@@ -255,21 +365,32 @@ __global__ __launch_bounds__(256) void qk_norm_rope_vjp_kernel(QkArgs a, int per
         for (int i = 0; i < 8; ++i) g[i] *= sg[i];
       }
       turn.apply(g);
-      const bool is_q = h < a.q.heads, counts = h < end;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = h < end ? x[i] * r : 0.0f;
+      const bool is_q = h < a.q.heads;
+      if (a.partial) {
+        if (h0 + map.kPar <= a.q.heads) {  // all of the wave's heads are queries'
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum_q[i] = fmaf(g[i], x[i], sum_q[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            sum_q[i] = fmaf(g[i], is_q ? x[i] : 0.0f, sum_q[i]);
+            sum_k[i] = fmaf(g[i], is_q ? 0.0f : x[i], sum_k[i]);
+          }
+        }
+      }
       float dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[i] *= r;
-        const float t = counts ? g[i] * x[i] : 0.0f;
-        sum_q[i] += is_q ? t : 0.0f;
-        sum_k[i] += is_q ? 0.0f : t;
         g[i] *= is_q ? gq[i] : gk[i];
-        dot += g[i] * x[i];
+        dot = fmaf(g[i], x[i], dot);
       }
-      const float mean = head_sum<kLanes>(dot) / d;
+      const float mean = head_sum<kLanes>(dot) * (1.0f / d);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = r * (g[i] - x[i] * mean);
-      if (map.has && counts) store8(head_at<T>(a.dq, a.dk, token, h, col), g);
+      for (int i = 0; i < 8; ++i) g[i] = r * fmaf(x[i], -mean, g[i]);
+      if (map.has && h < end) store8(to.at(is_q), g);
+      to.next();
     }
   }
   if (a.partial == nullptr) return;
@@ -290,23 +411,30 @@ __global__ __launch_bounds__(256) void qk_norm_rope_vjp_kernel(QkArgs a, int per
 }
 
 // dgamma_q and dgamma_k = the workgroups' partial sums added in a fixed order:
-// 16 columns by 64 slices of them per workgroup.  parts == 0 writes zeros.
+// 16 columns by 64 slices of them per workgroup, then a wave for each column.
+// parts == 0 writes zeros.  (1024 parts of 256 columns: 7 us with four loads in
+// flight and the slices added by one thread.)
 __global__ __launch_bounds__(1024) void qk_dgamma_kernel(const float* __restrict__ partial, int parts, int d,
                                                          float* __restrict__ dgamma_q, float* __restrict__ dgamma_k) {
   __shared__ float sum[64][17];
   const int c = threadIdx.x & 15, slice = threadIdx.x >> 4;
-  const int col = (int)blockIdx.x * 16 + c;
   float s[4] = {0, 0, 0, 0};
-  if (col < 2 * d)
-    for (int p = slice; p < parts; p += 256)
+  {
+    const int col = (int)blockIdx.x * 16 + c;
+    if (col < 2 * d)
+      for (int p = slice; p < parts; p += 1024) {
+        float x[16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (p + 64 * i < parts) s[i] += partial[(int64_t)(p + 64 * i) * 2 * d + col];
+        for (int i = 0; i < 16; ++i) x[i] = p + 64 * i < parts ? partial[(int64_t)(p + 64 * i) * 2 * d + col] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i & 3] += x[i];
+      }
+  }
   sum[slice][c] = (s[0] + s[1]) + (s[2] + s[3]);
   __syncthreads();
-  if (slice == 0 && col < 2 * d) {
-    float t = 0.0f;
-    for (int i = 0; i < 64; ++i) t += sum[i][c];
+  const int col = (int)blockIdx.x * 16 + (threadIdx.x >> 6);
+  const float t = wave_sum(sum[threadIdx.x & 63][threadIdx.x >> 6]);
+  if ((threadIdx.x & 63) == 0 && col < 2 * d) {
     float* out = col < d ? dgamma_q : dgamma_k;
     if (out) out[col < d ? col : col - d] = t;
   }

@@ -23,7 +23,7 @@ import torch
 from . import _lib
 from ._lib import lib
 from ._streams import launch, new
-from .q8 import _IO, _IO_NAME, _named, _on_gpu, _p, _vec, _work
+from .q8 import _IO, _IO_NAME, _named, _on_gpu as _on_one_gpu, _p, _vec, _work
 
 BLOCK = 32
 SCALES = torch.float8_e8m0fnu
@@ -64,9 +64,8 @@ def _heads(t, name, dtypes, tokens=None, heads=None, d=None):
     if len(shape) != 3:
         raise ValueError(f"{name} must be tokens x heads x d, got {tuple(shape)}")
     n, h, c = shape
-    if (tokens is not None and n != tokens) or (heads is not None and h != heads) or (d is not None and c != d):
-        raise ValueError(f"{name} must be {'tokens' if tokens is None else tokens} x "
-                         f"{'heads' if heads is None else heads} x {'d' if d is None else d}, got {n} x {h} x {c}")
+    if tokens is not None and (n != tokens or c != d or (heads is not None and h != heads)):
+        raise ValueError(f"{name} must be {tokens} x {'heads' if heads is None else heads} x {d}, got {n} x {h} x {c}")
     if h < 1 or c < 1:
         raise ValueError(f"{name} has no heads")
     st, sh, sd = t.stride()
@@ -85,7 +84,28 @@ def _out_heads(t, name, dtype, shape, like, stream):
 
 
 def _cache(cache, kv_heads=None, d=None):
-    """What the library takes of a cache: its pointers and distances, its sizes."""
+    """What the library takes of a cache (its pointers and distances), and its
+    sizes.  The usual one, whole and contiguous, by few comparisons (a decoding
+    step is a few calls of 10 us each); _cache_slowly has the others and the words."""
+    try:
+        kc, ks, vc, vs = cache
+        shape = kc.shape
+        pages, h, ps, c = shape
+        scales = (pages, h, ps, c >> 4)
+        if (c & 15 == 0 and pages > 0 and h > 0 and ps > 0 and c > 0 and kc.dtype is torch.uint8 and
+                vc.dtype is torch.uint8 and ks.dtype is SCALES and vs.dtype is SCALES and vc.shape == shape and
+                ks.shape == scales and vs.shape == scales and kc.is_contiguous() and ks.is_contiguous() and
+                vc.is_contiguous() and vs.is_contiguous() and (d is None or 2 * c == d) and
+                (kv_heads is None or h == kv_heads)):
+            n = h * ps * c
+            e = n >> 4
+            return (kc.data_ptr(), n, ks.data_ptr(), e, vc.data_ptr(), n, vs.data_ptr(), e), (pages, h, ps, 2 * c)
+    except (AttributeError, TypeError, ValueError):
+        pass
+    return _cache_slowly(cache, kv_heads, d)
+
+
+def _cache_slowly(cache, kv_heads, d):
     kc, ks, vc, vs = cache
     args = []
     shape = None
@@ -107,19 +127,42 @@ def _cache(cache, kv_heads=None, d=None):
                 raise ValueError("the cache is empty")
         elif (pages, h, ps, c * per) != shape:
             raise ValueError(f"{name} must be {shape[0]} x {shape[1]} x {shape[2]} x {shape[3] // per}, got {tuple(t.shape)}")
-        page = h * ps * c
         if t.is_contiguous():
-            pass
+            page = h * ps * c
         elif t[0].is_contiguous():
-            page = t.stride(0) if pages > 1 else page
+            page = t.stride(0)
         else:
             raise ValueError(f"{name} must be contiguous within a page")
         args += [t.data_ptr(), page]
     return args, shape
 
 
+def _on_gpu(*tensors):
+    """As that of q8.py, which has the words."""
+    dev = tensors[0].get_device()
+    if dev >= 0:
+        for t in tensors:
+            if t is not None and t.get_device() != dev:
+                break
+        else:
+            return dev
+    return _on_one_gpu(*tensors)
+
+
 def _plan(starts, lengths, table):
-    """What the library takes of a plan."""
+    """What the library takes of a plan; as _cache."""
+    try:
+        n, width = table.shape
+        if (starts.dtype is torch.int32 and lengths.dtype is torch.int32 and table.dtype is torch.int32 and width > 0 and
+                starts.shape == (n + 1,) and lengths.shape == (n,) and starts.is_contiguous() and
+                lengths.is_contiguous() and table.is_contiguous()):
+            return starts.data_ptr(), lengths.data_ptr(), table.data_ptr(), width, n, width
+    except (AttributeError, TypeError, ValueError):
+        pass
+    return _plan_slowly(starts, lengths, table)
+
+
+def _plan_slowly(starts, lengths, table):
     for t, name, dims in ((starts, "starts", 1), (lengths, "lengths", 1), (table, "table", 2)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a tensor")
@@ -137,7 +180,7 @@ def _plan(starts, lengths, table):
     if not starts.is_contiguous() or not lengths.is_contiguous() or (n > 0 and width > 1 and table.stride(1) != 1):
         raise ValueError("starts, lengths and the rows of table must be contiguous")
     ld = table.stride(0) if n > 1 else width
-    return [starts.data_ptr(), lengths.data_ptr(), table.data_ptr(), ld, n, width]
+    return starts.data_ptr(), lengths.data_ptr(), table.data_ptr(), ld, n, width
 
 
 # ---------------------------------------------------- norm, position, rotation
@@ -318,7 +361,7 @@ def harp_kv4_attention(q, cache: Cache4, starts, lengths, table, scale: Optional
     if lse is True:
         lse = new((tokens, hq), torch.float32, q, stream)
     elif lse is not None:
-        if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32:
+        if not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32:
             raise TypeError("lse must be True or a torch.float32 tensor")
         if lse.shape != (tokens, hq) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous, {tokens} x {hq}, got {tuple(lse.shape)}")
