@@ -9,10 +9,18 @@
 
 #include "common.h"
 #include "kernels.h"
+#include "q8.h"
 
 namespace harp {
 
 constexpr int kBlk4 = 32;  // values per scale
+
+// From so many bytes on an array of heads is streamed, past the caches: the 8
+// L2s hold 4 MiB each, so little of it would be left there for its next reader,
+// and it would push out what is (norm_rope of 16384 x 32+8 x 128: 72 us, streamed
+// 64; reading 41 million values of a cache: 61 us, streamed 38).  Less is left
+// to the caches, from which its reader gets it.
+constexpr int64_t kStreamBytes = 32LL << 20;
 
 // An array of tokens x heads x d values: distances in elements.
 struct Heads {
@@ -76,6 +84,49 @@ int64_t kv4_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_head
 hipError_t launch_kv4_attention(const Attn4Args& a, hipStream_t stream);
 
 // ------------------------------------------------------------ device side
+// Eight values that are not read again before the caches have seen as much
+// again as they hold: loads and stores that do not take their place there.
+typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_at4 __attribute__((ext_vector_type(4), aligned(4)));
+template <bool kStream>
+__device__ __forceinline__ void load8(Raw8<uint16_t>& w, const uint16_t* p) {
+  if constexpr (!kStream) return w.load(p, 8);
+  const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4_at2*>(p));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w.w[i] = x[i];
+}
+template <bool kStream>
+__device__ __forceinline__ void load8(Raw8<float>& w, const float* p) {
+  if constexpr (!kStream) return w.load(p, 8);
+  const u32x4_at4* q = reinterpret_cast<const u32x4_at4*>(p);
+  const u32x4 x = __builtin_nontemporal_load(q), y = __builtin_nontemporal_load(q + 1);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w.w[i] = x[i];
+    w.w[i + 4] = y[i];
+  }
+}
+template <bool kStream>
+__device__ __forceinline__ void put8(uint16_t* p, const float (&v)[8]) {
+  if constexpr (!kStream) return store8(p, v);
+  u32x4 x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = pack_bf16x2_hw(v[2 * i], v[2 * i + 1]);
+  __builtin_nontemporal_store(x, reinterpret_cast<u32x4_at2*>(p));
+}
+template <bool kStream>
+__device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
+  if constexpr (!kStream) return store8(p, v);
+  u32x4 x, y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = __float_as_uint(v[i]);
+    y[i] = __float_as_uint(v[i + 4]);
+  }
+  __builtin_nontemporal_store(x, reinterpret_cast<u32x4_at4*>(p));
+  __builtin_nontemporal_store(y, reinterpret_cast<u32x4_at4*>(p) + 1);
+}
+
 // The last b of 0 .. n - 1 with f(b) <= value, or 0: f does not decrease, and
 // value is the same in every lane of the wave, which looks at 64 places at a time.
 // Whatever f gives, the result is in range.

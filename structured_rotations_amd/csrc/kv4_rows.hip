@@ -100,7 +100,7 @@ struct Cut {
   int64_t waves;
 };
 
-template <typename T, int kRounds>
+template <typename T, int kRounds, bool kStream>
 __global__ __launch_bounds__(256) void kv4_write_kernel(Cache4 c, Plan4 p, Heads k, Heads v, int tokens, Cut cut) {
   const int lane = threadIdx.x & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(256) void kv4_write_kernel(Cache4 c, Plan4 p, Heads
   auto load = [&](int64_t row) {
 #pragma unroll
     for (int r = 0; r < kRounds; ++r)
-      if (unit[r].has) next[r].load(unit[r].row(k, v, row), 8);
+      if (unit[r].has) load8<kStream>(next[r], unit[r].row(k, v, row));
   };
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) next[r].fill(0);
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(256) void kv4_write_kernel(Cache4 c, Plan4 p, Heads
   }
 }
 
-template <typename T, int kRounds>
+template <typename T, int kRounds, bool kStream>
 __global__ __launch_bounds__(256) void kv4_read_kernel(Cache4 c, Plan4 p, Heads k, Heads v, int tokens, Cut cut) {
   const int lane = threadIdx.x & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(Cache4 c, Plan4 p, Heads 
       const f32x2 a2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[r], scale, 2);
       const f32x2 a3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[r], scale, 3);
       const float f[8] = {a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
-      if (unit[r].has) store8(unit[r].row(k, v, row), f);
+      if (unit[r].has) put8<kStream>(unit[r].row(k, v, row), f);
     }
   }
 }
@@ -224,13 +224,17 @@ hipError_t go(K kernel, const Cut& cut, const Cache4& c, const Plan4& p, const H
 }
 template <typename T>
 hipError_t write_go(const Cache4& c, const Plan4& p, const Heads& k, const Heads& v, int tokens, hipStream_t stream) {
-  return few(c, tokens) ? go(kv4_write_kernel<T, 1>, cut_of<1>(c, tokens), c, p, k, v, tokens, stream)
-                        : go(kv4_write_kernel<T, 4>, cut_of<4>(c, tokens), c, p, k, v, tokens, stream);
+  if (few(c, tokens)) return go(kv4_write_kernel<T, 1, false>, cut_of<1>(c, tokens), c, p, k, v, tokens, stream);
+  const bool streamed = 2LL * tokens * c.heads * c.d * (int)sizeof(T) >= kStreamBytes;
+  return go(streamed ? kv4_write_kernel<T, 4, true> : kv4_write_kernel<T, 4, false>, cut_of<4>(c, tokens), c, p, k, v, tokens,
+            stream);
 }
 template <typename T>
 hipError_t read_go(const Cache4& c, const Plan4& p, const Heads& k, const Heads& v, int tokens, hipStream_t stream) {
-  return few(c, tokens) ? go(kv4_read_kernel<T, 1>, cut_of<1>(c, tokens), c, p, k, v, tokens, stream)
-                        : go(kv4_read_kernel<T, 4>, cut_of<4>(c, tokens), c, p, k, v, tokens, stream);
+  if (few(c, tokens)) return go(kv4_read_kernel<T, 1, false>, cut_of<1>(c, tokens), c, p, k, v, tokens, stream);
+  const bool streamed = 2LL * tokens * c.heads * c.d * (int)sizeof(T) >= kStreamBytes;
+  return go(streamed ? kv4_read_kernel<T, 4, true> : kv4_read_kernel<T, 4, false>, cut_of<4>(c, tokens), c, p, k, v, tokens,
+            stream);
 }
 
 }  // namespace

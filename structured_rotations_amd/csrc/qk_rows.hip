@@ -268,7 +268,7 @@ __device__ __forceinline__ void load_gamma(const void* gamma, int col, bool has,
 __device__ __forceinline__ float least_of(float eps) { return eps < 0x1p-100f ? 0x1p-80f : 0.0f; }
 
 // A wave takes `per` heads of a token.
-template <typename T, int kLanes, bool kInter>
+template <typename T, int kLanes, bool kInter, bool kStream>
 __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs a, int per, int parts) {
   const HeadMap<kLanes> map(a.d);
   // (units of a launch are less than 2^26)
@@ -282,7 +282,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs a, int per, in
   Walk<T, map.kPar> to(a.yq, a.yk, token, first + map.slot, col);
   auto load = [&](int h) {
     next.fill(0);
-    if (map.has && h < end) next.load(in.at(h < a.q.heads), 8);
+    if (map.has && h < end) load8<kStream>(next, in.at(h < a.q.heads));
     in.next();
   };
   load(first + map.slot);
@@ -309,7 +309,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs a, int per, in
     for (int i = 0; i < 8; ++i) v[i] = v[i] * r * (is_q ? gq[i] : gk[i]);
     turn.apply(v);
     if (a.signs) hadamard<kLanes>(v, map.lane, a.d);
-    if (map.has && h < end) store8(to.at(is_q), v);
+    if (map.has && h < end) put8<kStream>(to.at(is_q), v);
     to.next();
   }
 }
@@ -317,7 +317,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs a, int per, in
 // The reverse mode: workgroups walk over the parts of tokens, keeping their
 // lanes' shares of the two dgammas in registers; the shares of a workgroup are
 // added in order through LDS, those of the workgroups by the second kernel.
-template <typename T, int kLanes, bool kInter>
+template <typename T, int kLanes, bool kInter, bool kStream>
 __global__ __launch_bounds__(256, 4) void qk_norm_rope_vjp_kernel(QkArgs a, int per, int parts) {
   const HeadMap<kLanes> map(a.d);
   const int heads = a.q.heads + a.k.heads, col = 8 * map.lane;
@@ -340,8 +340,8 @@ __global__ __launch_bounds__(256, 4) void qk_norm_rope_vjp_kernel(QkArgs a, int 
       xn.fill(0);
       gn.fill(0);
       if (map.has && h < end) {
-        xn.load(x_at.at(h < a.q.heads), 8);
-        gn.load(g_at.at(h < a.q.heads), 8);
+        load8<kStream>(xn, x_at.at(h < a.q.heads));
+        load8<kStream>(gn, g_at.at(h < a.q.heads));
       }
       x_at.next();
       g_at.next();
@@ -389,7 +389,7 @@ __global__ __launch_bounds__(256, 4) void qk_norm_rope_vjp_kernel(QkArgs a, int 
       const float mean = head_sum<kLanes>(dot) * (1.0f / d);
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] = r * fmaf(x[i], -mean, g[i]);
-      if (map.has && h < end) store8(to.at(is_q), g);
+      if (map.has && h < end) put8<kStream>(to.at(is_q), g);
       to.next();
     }
   }
@@ -458,6 +458,11 @@ int64_t vjp_groups(int64_t tokens, int64_t heads, int64_t d) {
   return std::min<int64_t>((tokens * s.parts + 3) / 4, 1024);
 }
 
+template <typename T>
+bool streamed(const QkArgs& a) {
+  return a.tokens * (a.q.heads + a.k.heads) * a.d * (int)sizeof(T) >= kStreamBytes;
+}
+
 template <typename T, int kLanes>
 void go(const QkArgs& a, hipStream_t stream) {
   const Split s = split_of(a.tokens, a.q.heads + a.k.heads, kLanes);
@@ -471,10 +476,11 @@ void go(const QkArgs& a, hipStream_t stream) {
       if (h->p) h->p = static_cast<char*>(h->p) + t * h->token * eb;
     if (a.positions) b.positions = static_cast<const char*>(a.positions) + t * (a.wide ? 8 : 4);
     const dim3 grid((unsigned)((b.tokens * s.parts + 3) / 4));
-    if (a.interleaved)
-      hipLaunchKernelGGL((qk_norm_rope_kernel<T, kLanes, true>), grid, dim3(256), 0, stream, b, s.per, s.parts);
-    else
-      hipLaunchKernelGGL((qk_norm_rope_kernel<T, kLanes, false>), grid, dim3(256), 0, stream, b, s.per, s.parts);
+    const auto kernel = a.interleaved ? streamed<T>(a) ? qk_norm_rope_kernel<T, kLanes, true, true>
+                                                       : qk_norm_rope_kernel<T, kLanes, true, false>
+                        : streamed<T>(a) ? qk_norm_rope_kernel<T, kLanes, false, true>
+                                         : qk_norm_rope_kernel<T, kLanes, false, false>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, b, s.per, s.parts);
   }
 }
 template <typename T, int kLanes>
@@ -483,10 +489,11 @@ void vjp_go(const QkArgs& a, hipStream_t stream) {
   const int64_t groups = vjp_groups(a.tokens, a.q.heads + a.k.heads, a.d);
   if (groups > 0) {
     const dim3 grid((unsigned)groups);
-    if (a.interleaved)
-      hipLaunchKernelGGL((qk_norm_rope_vjp_kernel<T, kLanes, true>), grid, dim3(256), 0, stream, a, s.per, s.parts);
-    else
-      hipLaunchKernelGGL((qk_norm_rope_vjp_kernel<T, kLanes, false>), grid, dim3(256), 0, stream, a, s.per, s.parts);
+    const auto kernel = a.interleaved ? streamed<T>(a) ? qk_norm_rope_vjp_kernel<T, kLanes, true, true>
+                                                       : qk_norm_rope_vjp_kernel<T, kLanes, true, false>
+                        : streamed<T>(a) ? qk_norm_rope_vjp_kernel<T, kLanes, false, true>
+                                         : qk_norm_rope_vjp_kernel<T, kLanes, false, false>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, s.per, s.parts);
   }
   if (a.dgamma_q || a.dgamma_k)
     hipLaunchKernelGGL(qk_dgamma_kernel, dim3((2 * a.d + 15) / 16), dim3(1024), 0, stream, a.partial, (int)groups, a.d,
