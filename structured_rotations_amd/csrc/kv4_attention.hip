@@ -154,23 +154,46 @@ constexpr uint32_t kNanScale = 0xff000000u;  // of such words, and above
 constexpr float kSlack = 8.0f;
 
 // ------------------------------------------------------------- few rows
-// A wave takes 32 keys at a time, every fourth of its workgroup's, with its
-// loads straight into the layouts of the matrix instructions, one step ahead.
+// A wave takes 32 keys at a time, every fourth 32 of its workgroup's part.  Its
+// loads go straight into a ring of its own in LDS, kDepth - 1 steps ahead: what
+// keeps HBM busy is bytes in flight, and registers are too few for them (one
+// step ahead in registers, three waves a SIMD: 5.2 TB/s at 64 x 16384 tokens of
+// 8 x 128).  No barrier is needed: a wave reads what it loaded itself.
+//
+// A step in LDS, of two halves of 16 keys each (their pages may differ):
+//   K   ND % 4 == 0: as the lanes take it, 16 bytes each, one after the other;
+//       else the rows as they are
+//   V   by parts of the columns.  Lane c of 16 has the columns 8 c .. of a part
+//       of 128 (a word of a row), 4 c .. of one of 64 (a half), 2 c .. of one of
+//       32 (a byte).  Of four keys 4 g + i, i outermost, so that a wave's words
+//       are consecutive.
+//   scales of K, of V: rows as they are
 template <int ND>
 struct Step4 {
-  static constexpr int kUnit = ND % 4 == 0 ? 4 : ND % 2 == 0 ? 2 : 1;  // words of K per load
-  static constexpr int kUnits = ND / kUnit;
-  static constexpr int kWords = ND / 4, kHalf = (ND >> 1) & 1, kByte = ND & 1;  // how V's columns go to 16 lanes
-  uint32_t k[2][ND];
-  uint32_t ks[2][kUnits];
-  uint32_t v[8][kWords + kHalf + kByte];
-  uint32_t vs[2][ND];
+  static constexpr int kUnit = ND % 4 == 0 ? 4 : ND % 2 == 0 ? 2 : 1;  // words of K that a lane takes at once
+  static constexpr int kWords = ND / 4, kHalf = (ND >> 1) & 1, kByte = ND & 1;
+  static constexpr int kSide = 256 * ND;                     // 16 keys' codes
+  static constexpr int kV = 2 * kSide, kScales = 4 * kSide;  // where they begin
+  static constexpr int kBytes = 4 * kSide + 64 * ND;
+  static constexpr int kScaleLoads = (ND + 3) / 4;
+  static constexpr int kLoads = 2 * ((ND + 3) / 4) + 2 * (kWords + kHalf + kByte) + kScaleLoads;
+  static constexpr int kDepth = ND <= 4 ? 3 : 2;
 };
 
-// Workgroups a compute unit is to have room for, which bounds the registers:
-// loads in flight are what these kernels live by (64 sequences of up to 8192, d
-// = 128: one wave per SIMD and what the compiler takes, 112 us; three, 90 us).
-constexpr int room_for(int nd, int nq) { return nq == 1 && nd <= 4 ? 3 : nd * nq <= 8 ? 2 : 1; }
+// Waits until at most kLeft of the wave's loads are under way.
+template <int kLeft>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kLeft) : "memory");
+}
+__device__ __forceinline__ void load_lds4(uint64_t from, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(from)
+               : "memory");
+}
+
+// Workgroups a compute unit is to have room for, which bounds the registers.
+constexpr int room_for(int nd, int nq) { return nd <= 4 && (nq == 1 || nd <= 2) ? 3 : nd * nq <= 10 ? 2 : 1; }
 
 template <int ND, int NQ>
 __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(Attn4Args a, int splits, int64_t unit0) {
@@ -233,57 +256,66 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
   }
   const float to_log2 = a.scale * kLog2e;
 
+  // the rings of the four waves; at the end what they have to add
+  constexpr int kPad = kD + 4, kRing = Step::kBytes * Step::kDepth, kShare = 16 * kPad * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t memory[4 * (kRing > kShare ? kRing : kShare)];
+  __shared__ float stat[4][16][2];
+  const uint8_t* ring = memory + wave * kRing;
+  const uint32_t ring_at = lds_address(ring);
+
   // Pages of this wave's next 32 steps, two to a step, in the lanes.
   int pages = -1;
   auto look_up = [&](int step) {
     const int64_t key = (int64_t)base + ((int64_t)step + (lane >> 1) * 4) * 32 + (lane & 1) * 16;
     pages = key < hi_all ? page_of(a.cache, a.plan, t.seq, key >> ps_log2) : -1;
   };
-  // Lane's places in 16 keys' rows: unsigned 32-bit, so that loads take a base
-  // common to the lanes and an offset.
-  const uint32_t k_off = c16 * kRow + g * Step::kUnit * 4, ks_off = c16 * ND + g * Step::kUnit / 4;
-  const uint32_t v_off = 4 * g * kRow, vs_off = 4 * g * ND;
-  auto load = [&](Step& w, int step, int at) {
+  // the lane's scales: of K or V, of which half, which word of the 4 ND
+  uint64_t scales_at[Step::kScaleLoads];
+#pragma unroll
+  for (int n = 0; n < Step::kScaleLoads; ++n) {
+    const int w = 64 * n + lane;
+    scales_at[n] = reinterpret_cast<uint64_t>(w < 8 * ND ? a.cache.k.scales : a.cache.v.scales) +
+                   (uint64_t)((((int64_t)kvh << ps_log2) * ND) + w % (4 * ND) * 4);
+  }
+  uint32_t lost = 0;  // slot by slot, two bits: keys without a page
+  auto load = [&](int step, int at, int slot) {
+    const uint32_t to = ring_at + slot * Step::kBytes;
+    int64_t k_scales[2], v_scales[2];
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");  // the slot's last step has been read
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int page = __builtin_amdgcn_readlane(pages, 2 * at + s);
       const uint32_t key = (uint32_t)base + (uint32_t)step * 32 + s * 16;
       const uint32_t in_page = key & ((1u << ps_log2) - 1);
       const int64_t row = ((int64_t)kvh << ps_log2) + in_page, pg = page < 0 ? 0 : page;
-      const auto kc = common(a.cache.k.codes + pg * a.cache.k.codes_page + row * kRow);
-      const auto ks = common(a.cache.k.scales + pg * a.cache.k.scales_page + row * ND);
-      const auto vc = common(a.cache.v.codes + pg * a.cache.v.codes_page + row * kRow);
-      const auto vs = common(a.cache.v.scales + pg * a.cache.v.scales_page + row * ND);
+      const uint32_t bit = 1u << (2 * slot + s);
+      lost = page < 0 ? lost | bit : lost & ~bit;
+      const TileSrc k = tile_src(a.cache.k.codes + pg * a.cache.k.codes_page + row * kRow, 16 * kRow);
+      const TileSrc v = tile_src(a.cache.v.codes + pg * a.cache.v.codes_page + row * kRow, 16 * kRow);
+      k_scales[s] = pg * a.cache.k.scales_page + (int64_t)in_page * ND;
+      v_scales[s] = pg * a.cache.v.scales_page + (int64_t)in_page * ND;
 #pragma unroll
-      for (int u = 0; u < Step::kUnits; ++u) {
-        if constexpr (Step::kUnit == 4) {
-          const u32x4 x = load_at<u32x4>(kc, k_off, u * 64);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w.k[s][u * 4 + i] = x[i];
-        } else if constexpr (Step::kUnit == 2) {
-          const u32x2 x = load_at<u32x2>(kc, k_off, u * 32);
-          w.k[s][u * 2] = x[0];
-          w.k[s][u * 2 + 1] = x[1];
-        } else {
-          w.k[s][u] = load_at<uint32_t>(kc, k_off, u * 16);
-        }
-        const uint32_t e = load_at<uint8_t>(ks, ks_off, u * Step::kUnit);
-        w.ks[s][u] = page < 0 ? 255u : e;  // no page: NaN
+      for (int u = 0; u < (ND + 3) / 4; ++u) {
+        const uint32_t off = ND % 4 == 0 ? c16 * kRow + g * 16 + u * 64 : lane * 16 + u * 1024;
+        if (ND % 4 == 0 || lane < 16 * ND - 64 * u) load_lds16(k, to + s * Step::kSide + u * 1024, off, 0);
       }
+      const uint32_t v_to = to + Step::kV + s * Step::kSide;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int u = 0; u < Step::kWords; ++u)
+        load_lds16(v, v_to + u * 1024, (4 * ((lane >> 2) & 3) + (lane >> 4)) * kRow + (lane & 3) * 16 + u * 64, 0);
+      if constexpr (Step::kHalf)
+        if (lane < 32)
+          load_lds16(v, v_to + Step::kWords * 1024, (4 * ((lane >> 1) & 3) + (lane >> 3)) * kRow + (lane & 1) * 16 + Step::kWords * 64, 0);
+      if constexpr (Step::kByte)
+        if (lane < 16)
+          load_lds16(v, v_to + Step::kWords * 1024 + Step::kHalf * 512, (4 * (lane & 3) + (lane >> 2)) * kRow + kRow - 16, 0);
+    }
 #pragma unroll
-        for (int j = 0; j < Step::kWords; ++j) w.v[4 * s + i][j] = load_at<uint32_t>(vc, v_off + 4 * c16, i * kRow + 64 * j);
-        if constexpr (Step::kHalf)
-          w.v[4 * s + i][Step::kWords] = load_at<uint16_t>(vc, v_off + 2 * c16, i * kRow + 64 * Step::kWords);
-        if constexpr (Step::kByte)
-          w.v[4 * s + i][Step::kWords + Step::kHalf] = load_at<uint8_t>(vc, v_off + c16, i * kRow + kRow - 16);
-      }
-#pragma unroll
-      for (int i = 0; i < ND; ++i) {
-        const uint32_t e = load_at<uint32_t>(vs, vs_off, 4 * i);
-        w.vs[s][i] = page < 0 ? 0u : e;  // another page's: nothing that is not finite
-      }
+    for (int n = 0; n < Step::kScaleLoads; ++n) {
+      const int w = 64 * n + lane;
+      const bool second = w / (4 * ND) & 1;
+      const int64_t off = w < 8 * ND ? second ? k_scales[1] : k_scales[0] : second ? v_scales[1] : v_scales[0];
+      if (w < 16 * ND) load_lds4(scales_at[n] + (uint64_t)off, to + Step::kScales + 256 * n);
     }
   };
 
@@ -291,22 +323,44 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
 #pragma unroll
   for (int n = 0; n < NQ; ++n) poison[n] = 0;
 
-  auto compute = [&](const Step& w, int step) {
+  auto compute = [&](int step, int slot) {
     const int k0 = (int)((uint32_t)base + (uint32_t)step * 32);
+    const uint8_t* in = ring + slot * Step::kBytes;
+    const uint32_t missing = lost >> (2 * slot) & 3;
     // scores: rows of keys, columns of queries
     f32x4 z[NQ][2];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) z[n][0] = z[n][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < ND; ++i)
+    for (int u = 0; u < ND / Step::kUnit; ++u) {
+      uint32_t kw[2][Step::kUnit], e[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const uint32_t e = w.ks[s][i / Step::kUnit] << 23;
-        const uint32_t f[4] = {widen4<0>(w.k[s][i], e), widen4<1>(w.k[s][i], e), widen4<2>(w.k[s][i], e),
-                               widen4<3>(w.k[s][i], e)};
+        const uint8_t* k = in + s * Step::kSide;
+        if constexpr (Step::kUnit == 4) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(k + u * 1024 + lane * 16);
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) z[n][s] = mfma16(as_frag(f), q[n][i], z[n][s]);
+          for (int i = 0; i < 4; ++i) kw[s][i] = x[i];
+        } else if constexpr (Step::kUnit == 2) {
+          const u32x2 x = *reinterpret_cast<const u32x2*>(k + c16 * kRow + (u * 4 + g) * 8);
+          kw[s][0] = x[0];
+          kw[s][1] = x[1];
+        } else {
+          kw[s][0] = *reinterpret_cast<const uint32_t*>(k + c16 * kRow + (u * 4 + g) * 4);
+        }
+        e[s] = (uint32_t)in[Step::kScales + (16 * s + c16) * ND + (u * 4 + g) * Step::kUnit / 4] << 23;
+        if (missing >> s & 1) e[s] = 255u << 23;  // no page: NaN
       }
+#pragma unroll
+      for (int i = 0; i < Step::kUnit; ++i)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const uint32_t f[4] = {widen4<0>(kw[s][i], e[s]), widen4<1>(kw[s][i], e[s]), widen4<2>(kw[s][i], e[s]),
+                                 widen4<3>(kw[s][i], e[s])};
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) z[n][s] = mfma16(as_frag(f), q[n][u * Step::kUnit + i], z[n][s]);
+        }
+    }
     if (k0 < lo_max || k0 + 32 > hi_min) {  // some row does not see all of these keys
       asm volatile("");                     // a branch, no 16 comparisons at every step
 #pragma unroll
@@ -349,6 +403,14 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
     }
     // V's columns by parts: 8 columns to a lane (words), 4 (halves), 2 (bytes)
     const bool edge = k0 < lo_all || k0 + 32 > hi_all;
+    uint32_t vs[2][ND];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < ND; ++i) {
+        vs[s][i] = reinterpret_cast<const uint32_t*>(in + Step::kScales + (32 + 16 * s + 4 * g) * ND)[i];
+        if (missing >> s & 1) vs[s][i] = 0;  // another page's: nothing that is not finite
+      }
 #pragma unroll
     for (int part = 0; part < Step::kWords + Step::kHalf + Step::kByte; ++part) {
       const bool word = part < Step::kWords, half = !word && part == Step::kWords && Step::kHalf;
@@ -360,9 +422,9 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
       uint32_t e[8], most = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        e[i] = word   ? scale_of<ND, 4>(w.vs[i >> 2], i & 3, blk0, blk)
-               : half ? scale_of<ND, 2>(w.vs[i >> 2], i & 3, blk0, blk)
-                      : scale_of<ND, 1>(w.vs[i >> 2], i & 3, blk0, blk);
+        e[i] = word   ? scale_of<ND, 4>(vs[i >> 2], i & 3, blk0, blk)
+               : half ? scale_of<ND, 2>(vs[i >> 2], i & 3, blk0, blk)
+                      : scale_of<ND, 1>(vs[i >> 2], i & 3, blk0, blk);
         most = max(most, e[i]);
       }
       if (edge) {  // what lies outside may hold anything
@@ -399,13 +461,21 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) e[i] >>= 1;  // into the exponent's place
+      uint32_t vw[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint8_t* v = in + Step::kV + (i >> 2) * Step::kSide;
+        if (word) vw[i] = *reinterpret_cast<const uint32_t*>(v + part * 1024 + (i & 3) * 256 + lane * 4);
+        else if (half) vw[i] = *reinterpret_cast<const uint16_t*>(v + Step::kWords * 1024 + (i & 3) * 128 + lane * 2);
+        else vw[i] = v[Step::kWords * 1024 + Step::kHalf * 512 + (i & 3) * 64 + lane];
+      }
       auto column = [&](auto byte_c) {
         constexpr int byte = decltype(byte_c)::value;
         uint32_t even[4], odd[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t x = widen4<byte>(w.v[2 * j][part], e[2 * j]);
-          const uint32_t y = widen4<byte>(w.v[2 * j + 1][part], e[2 * j + 1]);
+          const uint32_t x = widen4<byte>(vw[2 * j], e[2 * j]);
+          const uint32_t y = widen4<byte>(vw[2 * j + 1], e[2 * j + 1]);
           even[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
           odd[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
         }
@@ -424,41 +494,30 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
     }
   };
 
-  if (step0 + wave < step1) {
-    Step w0, w1;
-    int step = step0 + wave, at = 0;
-    look_up(step);
-    load(w0, step, at);
-    while (true) {
-      int next = step + 4;
-      if (next < step1) {
-        if (++at == 32) {
-          at = 0;
-          look_up(next);
-        }
-        load(w1, next, at);
-      }
-      compute(w0, step);
-      step = next;
-      if (step >= step1) break;
-      next = step + 4;
-      if (next < step1) {
-        if (++at == 32) {
-          at = 0;
-          look_up(next);
-        }
-        load(w0, next, at);
-      }
-      compute(w1, step);
-      step = next;
-      if (step >= step1) break;
+  const int mine = step1 > step0 + wave ? (step1 - step0 - wave + 3) / 4 : 0;  // steps of this wave
+  if (mine > 0) {
+    int at = -1, ahead = 0;  // steps whose loads have been issued
+    auto fetch = [&]() {
+      if (ahead >= mine) return;
+      const int step = step0 + wave + 4 * ahead;
+      if ((at = (at + 1) & 31) == 0) look_up(step);
+      load(step, at, ahead % Step::kDepth);
+      ++ahead;
+    };
+#pragma unroll
+    for (int i = 0; i < Step::kDepth - 1; ++i) fetch();
+    for (int i = 0; i < mine; ++i) {
+      fetch();
+      const int left = ahead - i - 1;
+      if (Step::kDepth > 2 && left >= 2) wait_loads<2 * Step::kLoads>();
+      else if (left >= 1) wait_loads<Step::kLoads>();
+      else wait_loads<0>();
+      compute(step0 + wave + 4 * i, i % Step::kDepth);
     }
   }
 
   // The waves' parts, one tile of 16 rows after the other, in order.
-  constexpr int kPad = kD + 4;
-  __shared__ float share[4][16][kPad];
-  __shared__ float stat[4][16][2];
+  float(*share)[16][kPad] = reinterpret_cast<float(*)[16][kPad]>(memory);
   const int64_t all_rows = (int64_t)a.tokens * a.q_heads;
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
