@@ -1,22 +1,24 @@
 // Attention over a cache in 4 bits.
 //
 // For one key head, the rows of a sequence are its call's tokens times the
-// query heads that share the key head.  With S = K Q^T (keys by rows) and
-// O^T = V^T P^T, the matrix instructions' layouts fit one another: what a lane
-// holds of S, for one row of Q and its keys, is what it has to give of P, and
-// both products have a lane's row of Q in common, so the softmax needs no
-// exchange but the maximum.  The order of keys within a step is free; it is
-// the one in which S comes out.
+// query heads that share the key head.  With S = K Q^T (keys by rows), the matrix
+// instructions' layouts fit one another: what a lane holds of S, for one row of Q
+// and some keys, is what it has to give of P to the product with V, so the
+// softmax needs no exchange but the maximum.  The order of keys within a step is
+// free; it is the one in which S comes out.
 //
 // K's and V's codes become bf16 exactly (E2M1 times a power of two) by one
 // conversion instruction for two values, scale included.  A lane's piece of K
-// is as it is in memory; V has to be transposed: a lane takes the same columns
-// of 8 keys and pairs them by byte permutations.
+// is as it is in memory; two neighbours of V belong to one key and two columns,
+// where a product wants two keys of one column.  The kernel for few rows lets
+// the instruction pick them (mfma_pairs), the one for many pairs them by byte
+// permutations when it puts them into LDS.
 //
 // Scores, maxima, sums and accumulators are fp32.  The weights are rounded to
 // bf16 for the product with V: each is off by at most 2^-9 of itself, the result
 // by about as much as its own rounding to bf16 adds.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "kv4.h"
@@ -26,6 +28,7 @@ namespace harp {
 namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ bf16x8_t as_frag(const uint32_t (&w)[4]) {
@@ -35,6 +38,15 @@ __device__ __forceinline__ bf16x8_t as_frag(const uint32_t (&w)[4]) {
 }
 __device__ __forceinline__ f32x4 mfma16(const bf16x8_t& a, const bf16x8_t& b, const f32x4& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+// Adds the product of P and of one column of every pair in V.  An instruction for
+// matrices of which two of four values are zero takes only the two, and the
+// places (a bit pair each) that they have: of V's values (key 0, column 0), (key
+// 0, column 1), (key 1, column 0), (key 1, column 1) the places 0 and 2 or 1 and
+// 3 are one column's keys, at the price of a product without the other.
+template <int kOdd>
+__device__ __forceinline__ f32x4 mfma_pairs(const bf16x8_t& p, const bf16x16_t& v, const f32x4& c) {
+  return __builtin_amdgcn_smfmac_f32_16x16x64_bf16(p, v, c, kOdd ? 0xdddd : 0x8888, 0, 0);
 }
 // Byte kByte's two codes, times 2^(e - 127), e in the exponent's place.
 template <int kByte>
@@ -88,7 +100,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // they see: row r (0 ..) of the sequence's is token r / group, head r % group.
 struct TileRows {
   int seq, first_token, tokens, len;  // the call's array; the sequence's length
-  int64_t row0, rows;                 // the tile's first row; the sequence's
+  int row0, rows;                     // the tile's first row; the sequence's (tokens x heads: 2^30 at most)
   __device__ __forceinline__ int pos(int64_t token) const { return (int)((int64_t)len - tokens + token); }
 };
 // Tiles of kRows rows: sequence b's begin at starts[b] group / kRows + b, which
@@ -101,9 +113,11 @@ __device__ __forceinline__ bool tile_rows(const Attn4Args& a, int64_t tile, int 
   t->first_token = s0;
   t->tokens = s1 - s0;
   t->len = max(a.plan.lengths[b], 0);
-  t->rows = (int64_t)t->tokens * a.group;
-  t->row0 = (tile - first(b)) * tile_size;
-  return t->row0 >= 0 && t->row0 < t->rows;
+  t->rows = t->tokens * a.group;
+  const int64_t row0 = (tile - first(b)) * tile_size;
+  if (row0 < 0 || row0 >= t->rows) return false;
+  t->row0 = (int)row0;
+  return true;
 }
 // The keys lo .. hi - 1 that the token at position pos sees.  Beyond what the
 // table has room for (`cap` keys), one place stands for all the others: it has
@@ -125,8 +139,8 @@ struct KeyRange {
 template <int kStep>
 __device__ __forceinline__ KeyRange key_range(const Attn4Args& a, const TileRows& t, int tile_size, int64_t cap, int split,
                                               int splits, int unit) {
-  const int64_t row1 = min(t.row0 + tile_size, t.rows);
-  const int tok0 = (int)(t.row0 / a.group), tok1 = (int)((row1 - 1) / a.group);
+  const uint32_t group = a.group, last = min(t.row0 + tile_size, t.rows) - 1;
+  const int tok0 = (int)((uint32_t)t.row0 / group), tok1 = (int)(last / group);
   const Sees s0 = sees(a, t.len, t.pos(tok0), cap), s1 = sees(a, t.len, t.pos(tok1), cap);
   KeyRange r;
   r.hi = max(s0.hi, s1.hi);
@@ -147,6 +161,13 @@ __device__ __forceinline__ uint32_t scale_of(const uint32_t (&vs)[ND], int key, 
   const uint32_t lo = vs[in], hi = at % 4 + kSpan > 4 ? vs[in + 1 < ND ? in + 1 : in] : lo;
   return __builtin_amdgcn_perm(hi, lo, (uint32_t)(at % 4 + blk) << 24 | 0x0c0c0cu);
 }
+// The same, in an exponent's place, with other bits around it, which a conversion does not look at.
+template <int ND, int kSpan>
+__device__ __forceinline__ uint32_t exponent_of(const uint32_t (&vs)[ND], int key, int blk0, int blk) {
+  const int at = ND * key + blk0, in = at / 4;
+  if (at % 4 + kSpan > 4) return scale_of<ND, kSpan>(vs, key, blk0, blk) >> 1;
+  return __builtin_amdgcn_alignbit(vs[in], vs[in], 8 * (at % 4 + blk) + 9);
+}
 constexpr uint32_t kNanScale = 0xff000000u;  // of such words, and above
 
 // Weights go by a reference that a score may pass by this much (in powers of
@@ -154,62 +175,243 @@ constexpr uint32_t kNanScale = 0xff000000u;  // of such words, and above
 constexpr float kSlack = 8.0f;
 
 // ------------------------------------------------------------- few rows
-// A wave takes 32 keys at a time, every fourth 32 of its workgroup's part.  Its
-// loads go straight into a ring of its own in LDS, kDepth - 1 steps ahead: what
-// keeps HBM busy is bytes in flight, and registers are too few for them (one
-// step ahead in registers, three waves a SIMD: 5.2 TB/s at 64 x 16384 tokens of
-// 8 x 128).  No barrier is needed: a wave reads what it loaded itself.
+// The four waves of a workgroup take 32 keys at a time in turn.  A wave's loads go
+// straight into a ring of its own in LDS, kDepth - 1 steps ahead: what keeps HBM
+// busy is bytes in flight, and registers are too few for them.  No barrier is
+// needed: a wave reads what it loaded itself.  (64 x 1 over 16384, 32/8 x 128:
+// 216 us, 5.3 TB/s; a copy of this kernel without its arithmetic reads 5.2 to 5.5
+// TB/s, so what is left there is the order of the reads.)
 //
 // A step in LDS, of two halves of 16 keys each (their pages may differ):
 //   K   ND % 4 == 0: as the lanes take it, 16 bytes each, one after the other;
 //       else the rows as they are
 //   V   by parts of the columns.  Lane c of 16 has the columns 8 c .. of a part
 //       of 128 (a word of a row), 4 c .. of one of 64 (a half), 2 c .. of one of
-//       32 (a byte).  Of four keys 4 g + i, i outermost, so that a wave's words
-//       are consecutive.
+//       32 (a byte).  Of four keys 4 j + i, i outermost, so that a wave's words
+//       are in different banks; the second half is kSkew further for the same.
 //   scales of K, of V: rows as they are
 template <int ND>
 struct Step4 {
   static constexpr int kUnit = ND % 4 == 0 ? 4 : ND % 2 == 0 ? 2 : 1;  // words of K that a lane takes at once
   static constexpr int kWords = ND / 4, kHalf = (ND >> 1) & 1, kByte = ND & 1;
   static constexpr int kSide = 256 * ND;                     // 16 keys' codes
-  static constexpr int kV = 2 * kSide, kScales = 4 * kSide;  // where they begin
-  static constexpr int kBytes = 4 * kSide + 64 * ND;
-  static constexpr int kScaleLoads = (ND + 3) / 4;
-  static constexpr int kLoads = 2 * ((ND + 3) / 4) + 2 * (kWords + kHalf + kByte) + kScaleLoads;
+  static constexpr int kV = 2 * kSide, kSkew = 64;  // where V begins; what the second half is off, for the banks' sake
+  static constexpr int kScales = 4 * kSide + kSkew;
+  static constexpr int kBytes = kScales + 64 * ND;
+  static constexpr int kLoads = 2 * ((ND + 3) / 4) + 2 * (kWords + kHalf + kByte) + 2;
   static constexpr int kDepth = ND <= 4 ? 3 : 2;
 };
+
+// How the keys are shared out.  An item is a tile of rows of one sequence with one
+// key head; it takes steps of 32 keys, as many for every tile of a sequence.  All
+// steps of all items, one after the other, are cut into equal parts, one for
+// each workgroup that has room on the chip: whatever the lengths are, which only
+// the device knows, the parts are done at about the same time.  A workgroup
+// finishes items that are its own as a whole; of others it leaves parts: in its
+// first slot that of the item that began before it, in its second slot that of
+// the one that it begins and does not end.  (64 x 1 over 50 .. 8192 keys, 32/8 x
+// 128: 70 us; cut as for sequences of the table's width, one workgroup for an
+// item or a fixed fraction of one: 82.  64 x 4 over 4096: 76, not 100.)
+//
+// Where there are many items for each workgroup (see cut_of) each has one of its
+// own instead, and the chip's scheduler evens them out: the way from one item to
+// the next costs a workgroup about as much as 12 steps, mostly waiting, which
+// another workgroup's start does not (1024 x 1 over 1024: 235 us, not 257).
+constexpr int kLeastSteps = 8;  // of a part
+constexpr int kItemSteps = 12;  // what an item weighs besides its steps, half of it on either side of them
+struct Work {
+  int first_token, tokens, len;
+  int each, tiles;  // steps of an item (and kItemSteps), tiles of the sequence
+};
+__device__ __forceinline__ Work work_of(const Attn4Args& a, int b, int tile_size, int64_t cap) {
+  Work w{};
+  if (b >= a.plan.sequences) return w;
+  const int s0 = min(max(a.plan.starts[b], 0), a.tokens), s1 = min(max(a.plan.starts[b + 1], s0), a.tokens);
+  w.first_token = s0;
+  w.tokens = s1 - s0;
+  w.len = max(a.plan.lengths[b], 0);
+  const int64_t hi = min((int64_t)w.len, cap + 1);
+  // with a window, a tile's first token sees back from its place, and steps begin at multiples of 32
+  const int64_t span = a.window && a.causal ? min(hi, (int64_t)a.window + tile_size + 32) : hi;
+  w.each = (int)((span + 31) >> 5) + kItemSteps;
+  w.tiles = (w.tokens * a.group + tile_size - 1) / tile_size;
+  return w;
+}
+__device__ __forceinline__ Work uniform(Work w) {
+  const auto u = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+  return {u(w.first_token), u(w.tokens), u(w.len), u(w.each), u(w.tiles)};
+}
+// x / y of numbers from 0 on: exact below 2^52, where a fraction's distance from
+// the next integer is more than the rounding of the quotient.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) { return (int64_t)((double)x / (double)y); }
+__device__ __forceinline__ int64_t scan_of(int64_t v) {  // inclusive, over the wave
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const int64_t below = __shfl_up((long long)v, o);
+    if ((int)(threadIdx.x & 63) >= o) v += below;
+  }
+  return v;
+}
+__device__ __forceinline__ int64_t last_lane(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)v, 63) |
+                   (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), 63) << 32);
+}
 
 // Waits until at most kLeft of the wave's loads are under way.
 template <int kLeft>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kLeft) : "memory");
 }
-__device__ __forceinline__ void load_lds4(uint64_t from, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+// Loads straight into LDS, `lds` and on, lane by lane: 16 bytes from an address
+// that all lanes have in common and the lane's offset, or 4 from the lane's own
+// address.  kAt is added on both sides.
+template <int kAt>
+__device__ __forceinline__ void load_lds16_at(Global<uint8_t> base, uint32_t lane_offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3"
                :
-               : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(from)
+               : "s"(lds), "v"(lane_offset), "s"(base), "n"(kAt)
                : "memory");
 }
+__device__ __forceinline__ void load_lds4_at(Global<uint8_t> base, uint32_t lane_offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" : : "s"(lds), "v"(lane_offset), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_lds4(uint64_t from, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(from) : "memory");
+}
 
-// Workgroups a compute unit is to have room for, which bounds the registers.
-constexpr int room_for(int nd, int nq) { return nd <= 4 && (nq == 1 || nd <= 2) ? 3 : nd * nq <= 10 ? 2 : 1; }
+// The workspace: two slots of a tile's rows for each workgroup (values, then each
+// row's maximum and sum), then for each row of the call the first workgroup that
+// has a part of it, and how many have (<< 8) with its place in the tile, or 0
+// where there is nothing to add.
+struct Slots {
+  float* values;
+  f32x2* stats;
+  int2* of_row;
+};
+__device__ __forceinline__ Slots slots_of(float* workspace, int groups, int tile_size, int d) {
+  Slots s;
+  const int64_t rows = 2LL * groups * tile_size;
+  s.values = workspace;
+  s.stats = reinterpret_cast<f32x2*>(workspace + rows * d);
+  s.of_row = reinterpret_cast<int2*>(s.stats + rows);
+  return s;
+}
+
+// Workgroups a compute unit is to have room for, which bounds the registers: as
+// many as these and LDS allow without spilling (64 x 1 over 4096, d = 192: 2 58 us,
+// 3, of 168 registers, 63; d = 96: 3 and 4, of 128, 64).
+constexpr int room_for(int nd, int nq) {
+  return nq == 1 ? (nd <= 2 ? 4 : nd <= 4 ? 3 : 2) : nd == 1 ? 4 : nd == 2 ? 3 : nd <= 5 ? 2 : 1;
+}
 
 template <int ND, int NQ>
-__global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(Attn4Args a, int splits, int64_t unit0) {
+__global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(Attn4Args a, int parts, int64_t item0) {
   using Step = Step4<ND>;
   constexpr int kRow = ND * 16, kTileRows = 16 * NQ, kAcc = 2 * ND, kD = ND * 32;
-  const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
+  const int own_lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // one workgroup: a part of the keys of a key head of a tile of rows
-  const int64_t unit = unit0 + blockIdx.x, rest = unit / splits, tile = rest / a.cache.heads;
-  const int split = (int)(unit - rest * splits), kvh = (int)(rest - tile * a.cache.heads);
-  TileRows t;
-  if (!tile_rows(a, tile, kTileRows, &t)) return;
   const int ps_log2 = a.cache.page_log2;
   const int64_t cap = (int64_t)a.plan.width << ps_log2;
-  const KeyRange keys = key_range<32>(a, t, kTileRows, cap, split, splits, 4);
-  const int hi_all = keys.hi, lo_all = keys.lo, base = keys.base, step0 = keys.step0, step1 = keys.step1;
+
+  // the rings of the four waves; at an item's end what they have to add
+  constexpr int kPad = kD + 4, kRing = Step::kBytes * Step::kDepth, kShare = 16 * kPad * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t memory[4 * (kRing > kShare ? kRing : kShare)];
+  __shared__ float stat[4][16][2];
+  const uint8_t* ring = memory + wave * kRing;
+  const uint32_t ring_at = lds_address(ring);
+
+  // the part: steps `at` .. `end` - 1 of all
+  const int sequences = a.plan.sequences, heads = a.cache.heads;
+  const bool whole = parts == 0;  // one item, all of it
+  Work of;
+  int seq, tile, kvh, first = 0;  // the item, and its step where the part begins
+  int64_t at = 0, end = 1, chunk = 1;
+  if (whole) {
+    const int64_t unit = item0 + blockIdx.x, of_tile = quotient(unit, heads);
+    TileRows t;
+    if (!tile_rows(a, of_tile, kTileRows, &t)) return;
+    of = {t.first_token, t.tokens, t.len, 1, INT_MAX};
+    seq = t.seq;
+    tile = t.row0 / kTileRows;
+    kvh = (int)(unit - of_tile * heads);
+  } else {
+    const auto weight = [&](const Work& w) { return (int64_t)w.tiles * heads * w.each; };
+    const int per = (sequences + 63) / 64;  // sequences to a lane
+    Work work = work_of(a, own_lane * per, kTileRows, cap);
+    int64_t own = weight(work);
+#pragma unroll 4
+    for (int i = 1; i < per; ++i) own += weight(work_of(a, own_lane * per + i, kTileRows, cap));
+    int64_t up_to = scan_of(own);
+    const int64_t total = last_lane(up_to);
+    chunk = max(quotient(total + parts - 1, parts), (int64_t)kLeastSteps);
+    at = chunk * blockIdx.x;
+    end = min(total, at + chunk);
+    if (at >= end) return;
+    int64_t before = 0;  // steps of the sequences before seq
+    const auto of_who = [&](int who, int x) { return __builtin_amdgcn_readlane(x, who); };
+    const auto find = [&]() {  // the lane whose steps `at` is one of
+      const int who = __ffsll((unsigned long long)__ballot(before + up_to > at)) - 1;
+      const int64_t less = up_to - own;
+      before +=
+          (int64_t)((uint64_t)(uint32_t)of_who(who, (int)less) | (uint64_t)(uint32_t)of_who(who, (int)(less >> 32)) << 32);
+      return who;
+    };
+    int who = find();
+    seq = who * per;
+    if (per > 1) {
+      for (int left = min(per, sequences - seq);; seq += 64, left -= 64) {
+        work = work_of(a, own_lane < left ? seq + own_lane : sequences, kTileRows, cap);
+        own = weight(work);
+        up_to = scan_of(own);
+        const int64_t all = last_lane(up_to);
+        if (at < before + all || left <= 64) break;
+        before += all;
+      }
+      who = find();
+      seq += who;
+    }
+    of = {of_who(who, work.first_token), of_who(who, work.tokens), of_who(who, work.len), of_who(who, work.each),
+          of_who(who, work.tiles)};
+    const int item = (int)quotient(at - before, of.each);
+    tile = item / heads;
+    kvh = item - tile * heads;
+    first = (int)(at - before - (int64_t)item * of.each);
+  }
+  const int64_t begin = at;
+  while (at < end) {
+  // (offsets made of it are not kept from one item to the next, which costs registers)
+  int lane = own_lane;
+  asm volatile("" : "+v"(lane));
+  const int c16 = lane & 15, g = lane >> 4;
+  const int count = (int)min((int64_t)(of.each - first), end - at);
+  const int64_t item_at = at - first;
+  const bool begins = item_at >= begin, shared = !begins || item_at + of.each > end;
+  const int kvh_now = kvh;
+  TileRows t;
+  t.seq = seq;
+  t.first_token = of.first_token;
+  t.tokens = of.tokens;
+  t.len = of.len;
+  t.rows = of.tokens * a.group;
+  t.row0 = tile * kTileRows;
+  const int each = of.each;
+  const KeyRange keys = key_range<32>(a, t, kTileRows, cap, 0, 1, 1);
+  const int hi_all = keys.hi, lo_all = keys.lo, base = keys.base;
+  const int step0 = min(keys.step1, max(first - kItemSteps / 2, 0));  // 0 of a whole item
+  const int step1 = whole ? keys.step1 : min(keys.step1, max(first + count - kItemSteps / 2, 0));
+  // on to the next item
+  at += count;
+  first = 0;
+  if (++kvh == heads) {
+    kvh = 0;
+    if (++tile == of.tiles) {
+      tile = 0;
+      do {
+        ++seq;
+        of = uniform(work_of(a, seq, kTileRows, cap));
+      } while (of.tiles == 0 && seq < sequences);
+    }
+  }
 
   // this lane's row of each tile of 16: its queries, its keys
   Sees row_sees[NQ];
@@ -217,15 +419,15 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
   int hi_min = hi_all, lo_max = lo_all;
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    const int64_t r = t.row0 + n * 16 + c16;
+    const int r = t.row0 + n * 16 + c16;
     const bool has = r < t.rows;
-    const int tok = has ? (int)(r / a.group) : 0, gh = has ? (int)(r - (int64_t)tok * a.group) : 0;
+    const int tok = has ? (int)((uint32_t)r / (uint32_t)a.group) : 0, gh = has ? r - tok * a.group : 0;
     row_sees[n] = has ? sees(a, t.len, t.pos(tok), cap) : Sees{0, 0};
     if (has) {
       hi_min = min(hi_min, row_sees[n].hi);
       lo_max = max(lo_max, row_sees[n].lo);
     }
-    const uint16_t* p = a.q + (int64_t)(t.first_token + tok) * a.q_token + (int64_t)(kvh * a.group + gh) * a.q_head;
+    const uint16_t* p = a.q + (int64_t)(t.first_token + tok) * a.q_token + (int64_t)(kvh_now * a.group + gh) * a.q_head;
 #pragma unroll
     for (int s = 0; s < ND; ++s) {
       const int u = s / Step::kUnit, in = s % Step::kUnit;
@@ -256,67 +458,78 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
   }
   const float to_log2 = a.scale * kLog2e;
 
-  // the rings of the four waves; at the end what they have to add
-  constexpr int kPad = kD + 4, kRing = Step::kBytes * Step::kDepth, kShare = 16 * kPad * 4;
-  __shared__ __attribute__((aligned(16))) uint8_t memory[4 * (kRing > kShare ? kRing : kShare)];
-  __shared__ float stat[4][16][2];
-  const uint8_t* ring = memory + wave * kRing;
-  const uint32_t ring_at = lds_address(ring);
-
-  // Pages of this wave's next 32 steps, two to a step, in the lanes.
+  // Pages of the next 32 steps, two to a step, in the lanes.
   int pages = -1;
   auto look_up = [&](int step) {
     const int64_t key = (int64_t)base + ((int64_t)step + (lane >> 1) * 4) * 32 + (lane & 1) * 16;
     pages = key < hi_all ? page_of(a.cache, a.plan, t.seq, key >> ps_log2) : -1;
   };
-  // the lane's scales: of K or V, of which half, which word of the 4 ND
-  uint64_t scales_at[Step::kScaleLoads];
-#pragma unroll
-  for (int n = 0; n < Step::kScaleLoads; ++n) {
-    const int w = 64 * n + lane;
-    scales_at[n] = reinterpret_cast<uint64_t>(w < 8 * ND ? a.cache.k.scales : a.cache.v.scales) +
-                   (uint64_t)((((int64_t)kvh << ps_log2) * ND) + w % (4 * ND) * 4);
-  }
+  // the key head's places in a page
+  const uint8_t* const k_at = a.cache.k.codes + ((int64_t)kvh_now << ps_log2) * kRow;
+  const uint8_t* const v_at = a.cache.v.codes + ((int64_t)kvh_now << ps_log2) * kRow;
+  const int64_t scales_at = ((int64_t)kvh_now << ps_log2) * ND;
   uint32_t lost = 0;  // slot by slot, two bits: keys without a page
-  auto load = [&](int step, int at, int slot) {
-    const uint32_t to = ring_at + slot * Step::kBytes;
-    int64_t k_scales[2], v_scales[2];
-    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");  // the slot's last step has been read
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int page = __builtin_amdgcn_readlane(pages, 2 * at + s);
-      const uint32_t key = (uint32_t)base + (uint32_t)step * 32 + s * 16;
-      const uint32_t in_page = key & ((1u << ps_log2) - 1);
-      const int64_t row = ((int64_t)kvh << ps_log2) + in_page, pg = page < 0 ? 0 : page;
-      const uint32_t bit = 1u << (2 * slot + s);
-      lost = page < 0 ? lost | bit : lost & ~bit;
-      const TileSrc k = tile_src(a.cache.k.codes + pg * a.cache.k.codes_page + row * kRow, 16 * kRow);
-      const TileSrc v = tile_src(a.cache.v.codes + pg * a.cache.v.codes_page + row * kRow, 16 * kRow);
-      k_scales[s] = pg * a.cache.k.scales_page + (int64_t)in_page * ND;
-      v_scales[s] = pg * a.cache.v.scales_page + (int64_t)in_page * ND;
+  // 16 keys' codes, kHalves halves of them that follow one another
+  auto load_codes = [&](auto halves_c, Global<uint8_t> k, Global<uint8_t> v, uint32_t to, uint32_t skew) {
+    constexpr int kHalves = decltype(halves_c)::value;
+    auto half = [&](auto s_c) {
+      constexpr int kAt = decltype(s_c)::value * Step::kSide;  // 16 rows in memory, and their place in LDS
+      const uint32_t v_to = to + Step::kV + skew + decltype(s_c)::value * Step::kSkew;
 #pragma unroll
       for (int u = 0; u < (ND + 3) / 4; ++u) {
         const uint32_t off = ND % 4 == 0 ? c16 * kRow + g * 16 + u * 64 : lane * 16 + u * 1024;
-        if (ND % 4 == 0 || lane < 16 * ND - 64 * u) load_lds16(k, to + s * Step::kSide + u * 1024, off, 0);
+        if (ND % 4 == 0 || lane < 16 * ND - 64 * u) load_lds16_at<kAt>(k, off, to + u * 1024);
       }
-      const uint32_t v_to = to + Step::kV + s * Step::kSide;
 #pragma unroll
       for (int u = 0; u < Step::kWords; ++u)
-        load_lds16(v, v_to + u * 1024, (4 * ((lane >> 2) & 3) + (lane >> 4)) * kRow + (lane & 3) * 16 + u * 64, 0);
+        load_lds16_at<kAt>(v, (4 * ((lane >> 2) & 3) + (lane >> 4)) * kRow + (lane & 3) * 16 + u * 64,
+                           v_to + u * 1024);
       if constexpr (Step::kHalf)
         if (lane < 32)
-          load_lds16(v, v_to + Step::kWords * 1024, (4 * ((lane >> 1) & 3) + (lane >> 3)) * kRow + (lane & 1) * 16 + Step::kWords * 64, 0);
+          load_lds16_at<kAt>(v, (4 * ((lane >> 1) & 3) + (lane >> 3)) * kRow + (lane & 1) * 16 + Step::kWords * 64,
+                             v_to + Step::kWords * 1024);
       if constexpr (Step::kByte)
         if (lane < 16)
-          load_lds16(v, v_to + Step::kWords * 1024 + Step::kHalf * 512, (4 * (lane & 3) + (lane >> 2)) * kRow + kRow - 16, 0);
+          load_lds16_at<kAt>(v, (4 * (lane & 3) + (lane >> 2)) * kRow + kRow - 16,
+                             v_to + Step::kWords * 1024 + Step::kHalf * 512);
+    };
+    half(std::integral_constant<int, 0>{});
+    if constexpr (kHalves == 2) half(std::integral_constant<int, 1>{});
+  };
+  auto load = [&](int step, int page_at, int slot) {
+    const uint32_t to = ring_at + slot * Step::kBytes;
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");  // the slot's last step has been read
+    const uint32_t key = (uint32_t)base + (uint32_t)step * 32, in_page = key & ((1u << ps_log2) - 1);
+    const int page = __builtin_amdgcn_readlane(pages, 2 * page_at);
+    const int64_t pg = max(page, 0), in_scales = scales_at + (int64_t)in_page * ND;
+    const auto k = common(k_at + pg * a.cache.k.codes_page + (int64_t)in_page * kRow);
+    const auto v = common(v_at + pg * a.cache.v.codes_page + (int64_t)in_page * kRow);
+    const auto ks = common(a.cache.k.scales + pg * a.cache.k.scales_page + in_scales);
+    const auto vs = common(a.cache.v.scales + pg * a.cache.v.scales_page + in_scales);
+    const uint32_t scales_to = to + Step::kScales;
+    uint32_t missing = page < 0 ? 3 : 0;
+    if (ps_log2 > 4) {  // all 32 keys in one page (of which 16 may not be the sequence's)
+      load_codes(std::integral_constant<int, 2>{}, k, v, to, 0);
+      if (ND == 8 || lane < 8 * ND) {
+        load_lds4_at(ks, lane * 4, scales_to);
+        load_lds4_at(vs, lane * 4, scales_to + 32 * ND);
+      }
+    } else {
+      const int page2 = __builtin_amdgcn_readlane(pages, 2 * page_at + 1);
+      const int64_t pg2 = max(page2, 0);
+      missing = (page < 0 ? 1 : 0) | (page2 < 0 ? 2 : 0);
+      load_codes(std::integral_constant<int, 1>{}, k, v, to, 0);
+      load_codes(std::integral_constant<int, 1>{}, common(k_at + pg2 * a.cache.k.codes_page),
+                 common(v_at + pg2 * a.cache.v.codes_page), to + Step::kSide, Step::kSkew);
+      if (ND == 8 || lane < 8 * ND) {
+        const auto own = [&](Global<uint8_t> one, Global<uint8_t> two) {
+          return reinterpret_cast<uint64_t>(lane < 4 * ND ? one : two - 16 * ND) + lane * 4;
+        };
+        load_lds4(own(ks, common(a.cache.k.scales + pg2 * a.cache.k.scales_page + scales_at)), scales_to);
+        load_lds4(own(vs, common(a.cache.v.scales + pg2 * a.cache.v.scales_page + scales_at)), scales_to + 32 * ND);
+      }
     }
-#pragma unroll
-    for (int n = 0; n < Step::kScaleLoads; ++n) {
-      const int w = 64 * n + lane;
-      const bool second = w / (4 * ND) & 1;
-      const int64_t off = w < 8 * ND ? second ? k_scales[1] : k_scales[0] : second ? v_scales[1] : v_scales[0];
-      if (w < 16 * ND) load_lds4(scales_at[n] + (uint64_t)off, to + Step::kScales + 256 * n);
-    }
+    lost = (lost & ~(3u << (2 * slot))) | missing << (2 * slot);
   };
 
   uint32_t poison[NQ];  // blocks of the row's result that are NaN
@@ -349,7 +562,11 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
           kw[s][0] = *reinterpret_cast<const uint32_t*>(k + c16 * kRow + (u * 4 + g) * 4);
         }
         e[s] = (uint32_t)in[Step::kScales + (16 * s + c16) * ND + (u * 4 + g) * Step::kUnit / 4] << 23;
-        if (missing >> s & 1) e[s] = 255u << 23;  // no page: NaN
+      }
+      if (missing) {
+        asm volatile("");  // (a branch)
+        if (missing & 1) e[0] = 255u << 23;  // no page: NaN
+        if (missing & 2) e[1] = 255u << 23;
       }
 #pragma unroll
       for (int i = 0; i < Step::kUnit; ++i)
@@ -387,8 +604,11 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
         const float shrink = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[n] - now);
         m[n] = now;
         l[n] *= shrink;
+        f32x4 of_row;  // the accumulators' rows are the queries
 #pragma unroll
-        for (int i = 0; i < kAcc; ++i) acc[n][i] *= shrink;
+        for (int r = 0; r < 4; ++r) of_row[r] = __shfl(shrink, 4 * g + r);
+#pragma unroll
+        for (int i = 0; i < kAcc; ++i) acc[n][i] *= of_row;
       }
       const float less = m[n] == -INFINITY ? 0.0f : m[n];
       float e[8];
@@ -401,16 +621,31 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
                              pack_bf16x2_hw(e[6], e[7])};
       p[n] = as_frag(f);
     }
-    // V's columns by parts: 8 columns to a lane (words), 4 (halves), 2 (bytes)
+    // V's columns by parts: 8 columns to a lane (words), 4 (halves), 2 (bytes).  A product's lane of P has keys 4 g ..
+    // of both halves; to them belong, in the lanes of V, of half g % 2 the keys 4 (g / 2) .. and 8 + 4 (g / 2) ..
+    const int side = g & 1, key0 = 4 * (g >> 1);  // key i of the lane's 8: half `side`, key0 + 8 (i / 4) + i % 4
     const bool edge = k0 < lo_all || k0 + 32 > hi_all;
+    const uint32_t* scales = reinterpret_cast<const uint32_t*>(in + Step::kScales + 32 * ND);
+    bool some_nan = false;  // a byte of the step's scales is 255
+    if (ND == 8 || lane < 8 * ND) {
+      const uint32_t w = scales[lane];
+      some_nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & w & 0x80808080u;
+    }
+    some_nan = __any(some_nan);
     uint32_t vs[2][ND];
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < ND; ++i) {
-        vs[s][i] = reinterpret_cast<const uint32_t*>(in + Step::kScales + (32 + 16 * s + 4 * g) * ND)[i];
-        if (missing >> s & 1) vs[s][i] = 0;  // another page's: nothing that is not finite
-      }
+      for (int i = 0; i < ND; ++i) vs[h][i] = scales[(16 * side + key0 + 8 * h) / 4 * ND + i];
+    if (missing) {  // another page's: nothing that is not finite
+      asm volatile("");
+      const bool mine = missing >> side & 1;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < ND; ++i) vs[h][i] = mine ? 0 : vs[h][i];
+    }
+    const uint8_t* v_in = in + Step::kV + side * (Step::kSide + Step::kSkew);
 #pragma unroll
     for (int part = 0; part < Step::kWords + Step::kHalf + Step::kByte; ++part) {
       const bool word = part < Step::kWords, half = !word && part == Step::kWords && Step::kHalf;
@@ -418,30 +653,27 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
       const int tile0 = word ? part * 8 : Step::kWords * 8 + (half ? 0 : Step::kHalf * 4);
       const int blk0 = word ? part * 4 : half ? Step::kWords * 4 : ND - 1;
       const int blk = word ? c16 >> 2 : half ? c16 >> 3 : 0;
-      // the scale of the lane's block, one byte of the four keys' scales, as a number's highest byte
-      uint32_t e[8], most = 0;
+      uint32_t e[8];  // of the lane's block
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        e[i] = word   ? scale_of<ND, 4>(vs[i >> 2], i & 3, blk0, blk)
-               : half ? scale_of<ND, 2>(vs[i >> 2], i & 3, blk0, blk)
-                      : scale_of<ND, 1>(vs[i >> 2], i & 3, blk0, blk);
-        most = max(most, e[i]);
-      }
+      for (int i = 0; i < 8; ++i)
+        e[i] = word   ? exponent_of<ND, 4>(vs[i >> 2], i & 3, blk0, blk)
+               : half ? exponent_of<ND, 2>(vs[i >> 2], i & 3, blk0, blk)
+                      : exponent_of<ND, 1>(vs[i >> 2], i & 3, blk0, blk);
       if (edge) {  // what lies outside may hold anything
         asm volatile("");
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int j = k0 + 16 * (i >> 2) + 4 * g + (i & 3);
+          const int j = k0 + 16 * side + key0 + 8 * (i >> 2) + (i & 3);
           e[i] = j >= lo_all && j < hi_all ? e[i] : 0;
         }
       }
-      if (__any(most >= kNanScale)) {
+      if (some_nan) {
         // NaN times a weight of 0 would reach rows that do not see the key: such a block counts as 0, and is noted for
         // the rows that do see it
         uint32_t nan_keys = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (e[i] >= kNanScale) {
+          if ((e[i] >> 23 & 255) == 255) {
             nan_keys |= 1u << i;
             e[i] = 0;
           }
@@ -449,7 +681,7 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
         for (int i = 0; i < 32; ++i) {
           const uint32_t who = (uint32_t)(__ballot(nan_keys >> (i & 7) & 1) >> (16 * (i >> 3))) & 0xffff;
           if (who == 0) continue;
-          const int j = k0 + 16 * ((i & 7) >> 2) + 4 * (i >> 3) + (i & 3);
+          const int j = k0 + 16 * (i >> 3 & 1) + 8 * ((i & 7) >> 2) + 4 * (i >> 4) + (i & 3);
           uint32_t blocks = who ? 1 : 0;
           if (word)
             blocks = (who & 0xf ? 1 : 0) | (who & 0xf0 ? 2 : 0) | (who & 0xf00 ? 4 : 0) | (who & 0xf000 ? 8 : 0);
@@ -459,46 +691,43 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
             if (j >= row_sees[n].lo && j < row_sees[n].hi) poison[n] |= blocks << blk0;
         }
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] >>= 1;  // into the exponent's place
       uint32_t vw[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint8_t* v = in + Step::kV + (i >> 2) * Step::kSide;
-        if (word) vw[i] = *reinterpret_cast<const uint32_t*>(v + part * 1024 + (i & 3) * 256 + lane * 4);
-        else if (half) vw[i] = *reinterpret_cast<const uint16_t*>(v + Step::kWords * 1024 + (i & 3) * 128 + lane * 2);
-        else vw[i] = v[Step::kWords * 1024 + Step::kHalf * 512 + (i & 3) * 64 + lane];
+        // four keys' pieces of a part follow one another, key % 4 outermost
+        const uint8_t* v = v_in + Step::kWords * 1024 * !word + Step::kHalf * 512 * (!word && !half);
+        const int at = (i & 3) * 64 + (key0 / 4 + 2 * (i >> 2)) * 16 + c16;
+        if (word) vw[i] = reinterpret_cast<const uint32_t*>(v + part * 1024)[at];
+        else if (half) vw[i] = reinterpret_cast<const uint16_t*>(v)[at];
+        else vw[i] = v[at];
       }
-      auto column = [&](auto byte_c) {
+      auto columns = [&](auto byte_c) {
         constexpr int byte = decltype(byte_c)::value;
-        uint32_t even[4], odd[4];
+        uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t x = widen4<byte>(vw[2 * j], e[2 * j]);
-          const uint32_t y = widen4<byte>(vw[2 * j + 1], e[2 * j + 1]);
-          even[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
-          odd[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
-        }
+        for (int i = 0; i < 8; ++i) w[i] = widen4<byte>(vw[i], e[i]);
+        bf16x16_t pairs;
+        __builtin_memcpy(&pairs, w, 32);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-          acc[n][tile0 + 2 * byte] = mfma16(as_frag(even), p[n], acc[n][tile0 + 2 * byte]);
-          acc[n][tile0 + 2 * byte + 1] = mfma16(as_frag(odd), p[n], acc[n][tile0 + 2 * byte + 1]);
+          acc[n][tile0 + 2 * byte] = mfma_pairs<0>(p[n], pairs, acc[n][tile0 + 2 * byte]);
+          acc[n][tile0 + 2 * byte + 1] = mfma_pairs<1>(p[n], pairs, acc[n][tile0 + 2 * byte + 1]);
         }
       };
-      column(std::integral_constant<int, 0>{});
-      if (bytes > 1) column(std::integral_constant<int, 1>{});
+      columns(std::integral_constant<int, 0>{});
+      if (bytes > 1) columns(std::integral_constant<int, 1>{});
       if (bytes > 2) {
-        column(std::integral_constant<int, 2>{});
-        column(std::integral_constant<int, 3>{});
+        columns(std::integral_constant<int, 2>{});
+        columns(std::integral_constant<int, 3>{});
       }
     }
   };
 
-  const int mine = step1 > step0 + wave ? (step1 - step0 - wave + 3) / 4 : 0;  // steps of this wave
-  if (mine > 0) {
+  const int turns = step1 > step0 + wave ? (step1 - step0 - wave + 3) / 4 : 0;  // steps of this wave
+  if (turns > 0) {
     int at = -1, ahead = 0;  // steps whose loads have been issued
     auto fetch = [&]() {
-      if (ahead >= mine) return;
+      if (ahead >= turns) return;
       const int step = step0 + wave + 4 * ahead;
       if ((at = (at + 1) & 31) == 0) look_up(step);
       load(step, at, ahead % Step::kDepth);
@@ -506,7 +735,7 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
     };
 #pragma unroll
     for (int i = 0; i < Step::kDepth - 1; ++i) fetch();
-    for (int i = 0; i < mine; ++i) {
+    for (int i = 0; i < turns; ++i) {
       fetch();
       const int left = ahead - i - 1;
       if (Step::kDepth > 2 && left >= 2) wait_loads<2 * Step::kLoads>();
@@ -517,8 +746,11 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
   }
 
   // The waves' parts, one tile of 16 rows after the other, in order.
+  int thread = threadIdx.x;
+  asm volatile("" : "+v"(thread));
   float(*share)[16][kPad] = reinterpret_cast<float(*)[16][kPad]>(memory);
-  const int64_t all_rows = (int64_t)a.tokens * a.q_heads;
+  const Slots slots = slots_of(a.partial, parts, kTileRows, kD);
+  const int64_t slot = 2 * (int64_t)blockIdx.x + begins;
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     l[n] = sum_of_groups(l[n]);
@@ -527,23 +759,25 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
       stat[wave][c16][0] = m[n];
       stat[wave][c16][1] = l[n];
     }
+    uint32_t nan_blocks[4];  // of the accumulators' rows
+#pragma unroll
+    for (int r = 0; r < 4; ++r) nan_blocks[r] = __shfl(poison[n], 4 * g + r);
 #pragma unroll
     for (int i = 0; i < kAcc; ++i) {
       const bool word = i < Step::kWords * 8, half = !word && i < Step::kWords * 8 + Step::kHalf * 4;
       const int wide = word ? 8 : half ? 4 : 2;
       const int first = word ? i / 8 * 128 : Step::kWords * 128 + (half ? 0 : Step::kHalf * 64);
       const int in = word ? i % 8 : half ? i - Step::kWords * 8 : i - Step::kWords * 8 - Step::kHalf * 4;
-      const int blk = first / 32 + (word ? g : half ? g >> 1 : 0);  // of the lane's four values
-      const bool nan = poison[n] >> blk & 1;
+      const int blk = first / 32 + (word ? c16 >> 2 : half ? c16 >> 3 : 0);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        share[wave][c16][first + (4 * g + r) * wide + in] = nan ? __uint_as_float(0x7fc00000u) : acc[n][i][r];
+        share[wave][4 * g + r][first + c16 * wide + in] = nan_blocks[r] >> blk & 1 ? __uint_as_float(0x7fc00000u) : acc[n][i][r];
     }
     __syncthreads();
     // a row's 8 columns per thread
-    for (int u = threadIdx.x; u < 16 * kD / 8; u += 256) {
+    for (int u = thread; u < 16 * kD / 8; u += 256) {
       const int rr = u / (kD / 8), col = (u - rr * (kD / 8)) * 8;
-      const int64_t r = t.row0 + n * 16 + rr;
+      const int r = t.row0 + n * 16 + rr;
       if (r >= t.rows) continue;
       float top = stat[0][rr][0];
 #pragma unroll
@@ -559,29 +793,32 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] += f * share[w][rr][col + i];
       }
-      const int tok = (int)(r / a.group), gh = (int)(r - (int64_t)tok * a.group);
-      const int64_t token = t.first_token + tok, head = (int64_t)kvh * a.group + gh;
+      const int tok = (int)((uint32_t)r / (uint32_t)a.group), gh = r - tok * a.group;
+      const int64_t token = t.first_token + tok, head = (int64_t)kvh_now * a.group + gh;
       const int64_t row = token * a.q_heads + head;
-      if (splits > 1) {
-        float* p = a.partial + ((int64_t)split * all_rows + row) * kD + col;
+      const Sees s = sees(a, t.len, t.pos(tok), cap);
+      const bool sees_some = s.hi > s.lo;
+      if (begins && !whole && col == 0) {  // the first workgroup, and how many share the item
+        const int owners = shared ? (int)quotient(item_at - begin + each - 1, chunk) + 1 : 0;
+        slots.of_row[row] = {(int)blockIdx.x, owners << 8 | (n * 16 + rr)};
+      }
+      if (shared) {
+        const int64_t place = slot * kTileRows + n * 16 + rr;
+        float* p = slots.values + place * kD + col;
 #pragma unroll
         for (int i = 0; i < 8; i += 4) *reinterpret_cast<f32x4*>(p + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
-        if (col == 0) {
-          const Sees s = sees(a, t.len, t.pos(tok), cap);
-          float* st = a.partial + (int64_t)splits * all_rows * kD + ((int64_t)split * all_rows + row) * 2;
-          st[0] = top;
-          st[1] = s.hi > s.lo ? sum : -1.0f;  // a row that sees no key in any part
-        }
+        if (col == 0) slots.stats[place] = {top, sees_some ? sum : -1.0f};  // below 0: the row sees no key at all
       } else {
-        const Sees s = sees(a, t.len, t.pos(tok), cap);
         // no key: 0; keys of weight 0 only (all scores -infinity): 0 / 0
-        const float inv = s.hi > s.lo ? 1.0f / sum : 0.0f;
+        const float inv = sees_some ? 1.0f / sum : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = s.hi > s.lo ? o[i] * inv : 0.0f;
+        for (int i = 0; i < 8; ++i) o[i] = sees_some ? o[i] * inv : 0.0f;
         store8(a.out + token * a.out_token + head * a.out_head + col, o);
         if (a.lse && col == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
       }
     }
+  }
+  __syncthreads();  // the parts have been read: their place is the rings' again
   }
 }
 
@@ -619,9 +856,9 @@ __global__ __launch_bounds__(256, ND <= 4 ? 2 : 1) void kv4_prompt_kernel(Attn4A
   const KeyRange keys = key_range<64>(a, t, kRows, cap, split, splits, 1);
 
   // this lane's row: its queries, its keys
-  const int64_t r = t.row0 + wave * 32 + c32;
+  const int r = t.row0 + wave * 32 + c32;
   const bool has = r < t.rows;
-  const int tok = has ? (int)(r / a.group) : 0, gh = has ? (int)(r - (int64_t)tok * a.group) : 0;
+  const int tok = has ? (int)((uint32_t)r / (uint32_t)a.group) : 0, gh = has ? r - tok * a.group : 0;
   const Sees my = has ? sees(a, t.len, t.pos(tok), cap) : Sees{0, 0};
   int hi_min = has ? my.hi : keys.hi, lo_max = has ? my.lo : keys.lo, hi_max = my.hi;
 #pragma unroll
@@ -948,37 +1185,49 @@ struct Part {
     top = now;
   }
 };
-__global__ __launch_bounds__(256) void kv4_join_kernel(Attn4Args a, int splits, int slices) {
+// groups > 0: the slots of so many workgroups, tiles of tile_size rows; else
+// `splits` parts of every row, [part][row].
+__global__ __launch_bounds__(256) void kv4_join_kernel(Attn4Args a, int groups, int tile_size, int splits, int slices) {
   __shared__ Part share[256];
   const int64_t all_rows = (int64_t)a.tokens * a.q_heads;
   const int d = a.cache.d, lanes = d / 4, items = 256 / slices;
   const int slice = threadIdx.x / items, mine = threadIdx.x - slice * items;
-  const float* stats = a.partial + (int64_t)splits * all_rows * d;
+  const Slots slots = slots_of(a.partial, groups, tile_size, d);
+  const f32x2* stats = groups ? slots.stats : reinterpret_cast<const f32x2*>(a.partial + (int64_t)splits * all_rows * d);
   // rows behind the last sequence have no parts
   const int64_t rows = (int64_t)min(max(a.plan.starts[a.plan.sequences], 0), a.tokens) * a.q_heads;
-  for (int64_t first = (int64_t)blockIdx.x * items; first < rows * lanes; first += (int64_t)gridDim.x * items) {
+  for (int64_t first = (int64_t)blockIdx.x * items; first < all_rows * lanes; first += (int64_t)gridDim.x * items) {
     const int64_t item = first + mine, row = item / lanes;
     const int col = 4 * (int)(item - row * lanes);
     Part p = {-INFINITY, 0.0f, {0, 0, 0, 0}};
     bool none = false;
-    if (row < rows) {
-      const float* from = a.partial + row * d + col;
-      for (int i0 = slice; i0 < splits; i0 += 8 * slices) {
-        f32x2 st[8];
-        f32x4 x[8];
+    int parts = row < rows ? splits : 0;
+    int64_t at = row, step = all_rows, second = 0;  // of part i: at + i step, less `second` from the second on
+    const int2 of = groups ? slots.of_row[min(row, all_rows - 1)] : int2{0, 0};
+    if (groups && row < rows) {
+      // (rows of a plan that makes no sense may have no record)
+      const int owner = min(max(of.x, 0), groups - 1), local = min(of.y & 255, tile_size - 1);
+      parts = min(of.y >> 8, groups - owner);
+      at = (2LL * owner + 1) * tile_size + local;
+      step = 2LL * tile_size;
+      second = tile_size;
+    }
+    for (int i0 = slice; i0 < parts; i0 += 8 * slices) {
+      f32x2 st[8];
+      f32x4 x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int64_t at = (int64_t)min(i0 + i * slices, splits - 1) * all_rows;
-          st[i] = *reinterpret_cast<const f32x2*>(stats + (at + row) * 2);
-          x[i] = *reinterpret_cast<const f32x4*>(from + at * d);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i0 + i * slices < splits) {
-            none |= st[i][1] < 0.0f;
-            p.add(st[i][0], st[i][1], x[i]);
-          }
+      for (int i = 0; i < 8; ++i) {
+        const int n = min(i0 + i * slices, parts - 1);
+        const int64_t from = at + n * step - (n > 0 ? second : 0);
+        st[i] = stats[from];
+        x[i] = *reinterpret_cast<const f32x4*>(a.partial + from * d + col);
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i0 + i * slices < parts) {
+          none |= st[i][1] < 0.0f;
+          p.add(st[i][0], st[i][1], x[i]);
+        }
     }
     if (slices > 1) {
       __syncthreads();  // the last items' are done with
@@ -987,7 +1236,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Attn4Args a, int splits, 
       if (slice == 0)
         for (int i = 1; i < slices; ++i) p.add(share[i * items + mine].top, share[i * items + mine].sum, share[i * items + mine].o);
     }
-    if (slice == 0 && row < rows) {
+    if (slice == 0 && parts > 0) {
       const int token = (int)(row / a.q_heads), head = (int)(row - (int64_t)token * a.q_heads);
       const float inv = none ? 0.0f : 1.0f / p.sum;
       if (none) p.o = f32x4{0, 0, 0, 0};
@@ -999,45 +1248,63 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Attn4Args a, int splits, 
   }
 }
 
-constexpr int kMostSplits = 256;
+constexpr int kMostSplits = 256, kUnits = 256;  // parts, compute units
 
 // How a call is cut: tiles of 16, 32 or 128 rows, by the rows that a sequence
-// has on average, and the keys in parts until the chip has work enough.
+// has on average.  Few rows: equal parts (`groups`) for as many workgroups as
+// have room, or an item to each workgroup (0) from 4 items for each such place
+// on (256 x 1 over 1024 has 2.7: 77 us in parts, 71 in items; over 20 .. 2048: 83
+// and 83, and the worse the longer one sequence is next to the others).  Many:
+// the keys in `splits` parts until the chip has work enough.
 struct Cut {
-  int rows, splits;
+  int rows, groups, splits;
   int64_t tiles;
 };
-Cut cut_of(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t page_size, int64_t sequences, int64_t width) {
-  const int64_t group = q_heads / kv_heads, rows = tokens * group;
-  Cut c;
+Cut cut_of(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t page_size, int64_t sequences,
+           int64_t width) {
+  const int64_t group = q_heads / kv_heads, rows = tokens * group, keys = width * page_size;
+  Cut c{};
   c.rows = rows > 64 * sequences ? 128 : rows > 16 * sequences ? 32 : 16;
   c.tiles = rows / c.rows + sequences;
-  const int64_t busy = std::max<int64_t>(1, std::max(rows / c.rows, std::min(sequences, tokens)) * kv_heads);
-  const int64_t keys = width * page_size, most = std::max<int64_t>(1, (keys + 127) / 128);
-  const int64_t fill = ((c.rows == 128 ? 512 : 768) + busy - 1) / busy;
-  const int64_t even = busy >= 256 && c.rows < 128 ? (keys + 2047) / 2048 : 1;
-  c.splits = (int)std::min({most, std::max(fill, even), (int64_t)kMostSplits});
+  c.splits = 1;
+  // items that there are, whatever the sequences' shares of the tokens
+  const int64_t items = std::max<int64_t>(1, std::max(rows / c.rows, std::min(sequences, tokens)) * kv_heads);
+  if (c.rows < 128) {
+    const int64_t room = kUnits * room_for((int)d / 32, c.rows / 16);
+    // steps, if every sequence fills the table
+    const int64_t most = c.tiles * kv_heads * ((keys + 31) / 32 + 2 + kItemSteps);
+    if (items < 4 * room) c.groups = (int)std::min(room, (most + kLeastSteps - 1) / kLeastSteps);
+  } else {
+    const int64_t most = std::max<int64_t>(1, (keys + 127) / 128);
+    c.splits = (int)std::min({most, (512 + items - 1) / items, (int64_t)kMostSplits});
+  }
   return c;
+}
+int64_t workspace_of(const Cut& c, int64_t rows, int64_t d) {
+  if (c.groups) return (2LL * c.groups * c.rows * (d + 2) + 2 * rows) * 4;
+  return c.splits == 1 ? 0 : rows * c.splits * (d + 2) * 4;
 }
 
 template <int ND>
 hipError_t go(const Attn4Args& a, const Cut& c, hipStream_t stream) {
-  const int64_t units = c.tiles * a.cache.heads * c.splits;
   constexpr int64_t kMost = 1 << 23;  // workgroups of a launch: 2^32 threads are refused
+  const int64_t rows = (int64_t)a.tokens * a.q_heads;
+  const int64_t units = c.groups ? c.groups : c.tiles * a.cache.heads * c.splits;
   for (int64_t u = 0; u < units; u += kMost) {
     const dim3 grid((unsigned)std::min(kMost, units - u));
-    if (c.rows == 16) hipLaunchKernelGGL((kv4_attention_kernel<ND, 1>), grid, dim3(256), 0, stream, a, c.splits, u);
-    else if (c.rows == 32) hipLaunchKernelGGL((kv4_attention_kernel<ND, 2>), grid, dim3(256), 0, stream, a, c.splits, u);
+    if (c.rows == 16) hipLaunchKernelGGL((kv4_attention_kernel<ND, 1>), grid, dim3(256), 0, stream, a, c.groups, u);
+    else if (c.rows == 32) hipLaunchKernelGGL((kv4_attention_kernel<ND, 2>), grid, dim3(256), 0, stream, a, c.groups, u);
     else hipLaunchKernelGGL((kv4_prompt_kernel<ND>), grid, dim3(256), 0, stream, a, c.splits, u, c.tiles);
   }
-  if (c.splits > 1) {
-    const int64_t rows = (int64_t)a.tokens * a.q_heads;
-    int slices = 1;
-    while (slices < 32 && slices * 8 < c.splits) slices *= 2;
-    const int64_t items = rows * (ND * 8), per = 256 / slices;
-    hipLaunchKernelGGL(kv4_join_kernel, dim3((unsigned)std::min((items + per - 1) / per, kMost)), dim3(256), 0, stream,
-                       a, c.splits, slices);
-  }
+  if (!c.groups && c.splits == 1) return hipGetLastError();
+  // parts that a row has, if all are alike
+  const int64_t parts =
+      c.groups ? c.groups / std::max<int64_t>(1, (int64_t)std::min(a.tokens, a.plan.sequences) * a.cache.heads) : c.splits;
+  int slices = 1;
+  while (slices < 32 && slices * 8 < parts) slices *= 2;
+  const int64_t items = rows * (ND * 8), per = 256 / slices;
+  hipLaunchKernelGGL(kv4_join_kernel, dim3((unsigned)std::min((items + per - 1) / per, kMost)), dim3(256), 0, stream, a,
+                     c.groups, c.rows, c.splits, slices);
   return hipGetLastError();
 }
 
@@ -1046,12 +1313,12 @@ hipError_t go(const Attn4Args& a, const Cut& c, hipStream_t stream) {
 int64_t kv4_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t page_size,
                                 int64_t sequences, int64_t width) {
   if (tokens == 0 || sequences == 0) return 0;
-  const Cut c = cut_of(tokens, q_heads, kv_heads, page_size, sequences, width);
-  return c.splits == 1 ? 0 : tokens * q_heads * c.splits * (d + 2) * 4;
+  return workspace_of(cut_of(tokens, q_heads, kv_heads, d, page_size, sequences, width), tokens * q_heads, d);
 }
 
 hipError_t launch_kv4_attention(const Attn4Args& a, hipStream_t stream) {
-  const Cut c = cut_of(a.tokens, a.q_heads, a.cache.heads, 1LL << a.cache.page_log2, a.plan.sequences, a.plan.width);
+  const Cut c = cut_of(a.tokens, a.q_heads, a.cache.heads, a.cache.d, 1LL << a.cache.page_log2, a.plan.sequences,
+                       a.plan.width);
   switch (a.cache.d / 32) {
     case 1: return go<1>(a, c, stream);
     case 2: return go<2>(a, c, stream);

@@ -372,6 +372,13 @@ ATTENTION = [  # lengths, new, q heads, heads, d, page, causal, window, scale
     ([700, 20], [300, 20], 8, 2, 128, 16, True, 0, 0.5),
     ([64] * 130, [1] * 130, 2, 1, 64, 16, True, 0, None),
     ([1000], [1], 64, 1, 128, 16, True, 0, None),
+    # many sequences, some without a token, of very different lengths
+    ([(37 * i) % 190 for i in range(200)], [(1, 0, 2, 1)[i % 4] for i in range(200)], 2, 1, 64, 16, True, 0, None),
+    ([2500, 0, 1900, 64, 3100], [1, 0, 1, 1, 2], 8, 8, 96, 16, True, 0, None),
+    ([1500 if i == 70 else 5 for i in range(90)], [1] * 90, 4, 2, 128, 32, True, 0, None),
+    # more tiles and heads than a chip has room for
+    ([1 + (23 * i) % 37 for i in range(69)], [i % 3 for i in range(69)], 32, 32, 256, 16, True, 0, None),
+    ([15 + (17 * i) % 30 for i in range(33)], [20] * 33, 32, 32, 192, 32, True, 19, None),
 ]
 
 
