@@ -828,6 +828,22 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
 // next 64 keys, straight from memory into the fragments of the 32 x 32 x 16
 // instruction, and writes them to LDS as they are read, 16 bytes a lane one
 // after the other, while the products of the present 64 keys run.
+// Of kAll products and the reads of LDS that they need, in this order: kAhead reads,
+// then one after every product.  (Left alone, the reads come one or two ahead, and
+// each product waits: 4 x 2048 over 8192, 32/8 x 128: 663, not 655 us; 2 x 1024
+// over 4096 with d = 256: 251, not 233, 6 ahead 243.)
+template <int kAll, int kAhead>
+__device__ __forceinline__ void read_ahead() {
+  constexpr int ahead = kAhead < kAll ? kAhead : kAll;
+  __builtin_amdgcn_sched_group_barrier(0x100, ahead, 0);
+#pragma unroll
+  for (int i = 0; i < kAll - ahead; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, ahead, 0);
+}
+
 template <int ND>
 struct Quarter4 {
   static constexpr int kScales = ND % 4 == 0 ? ND / 4 : ND <= 2 ? 1 : ND;  // of a lane's ND words of K
@@ -1040,10 +1056,13 @@ __global__ __launch_bounds__(256, ND <= 4 ? 2 : 1) void kv4_prompt_kernel(Attn4A
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
       for (int x = 0; x < 16; ++x) z[s][x] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 2 * ND; ++i)
-        z[s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(buf, s * 2 * ND + i), q[i], z[s], 0, 0, 0);
     }
+#pragma unroll
+    for (int i = 0; i < 2 * ND; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        z[s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(buf, s * 2 * ND + i), q[i], z[s], 0, 0, 0);
+    read_ahead<4 * ND, 4>();
     if (k0 < lo_max || k0 + 64 > hi_min) {
       asm volatile("");
       const int lo = my.lo - k0 - 4 * h, hi = my.hi - k0 - 4 * h;
@@ -1087,6 +1106,7 @@ __global__ __launch_bounds__(256, ND <= 4 ? 2 : 1) void kv4_prompt_kernel(Attn4A
 #pragma unroll
       for (int i = 0; i < ND; ++i)
         acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(buf, 4 * ND + s * ND + i), p[s], acc[i], 0, 0, 0);
+    read_ahead<4 * ND, 4>();
     const u32x4 any = *reinterpret_cast<const u32x4*>(&nan_any[buf][0]);
     if (__builtin_amdgcn_readfirstlane(any[0] | any[1] | any[2] | any[3])) {
 #pragma unroll 1
