@@ -340,9 +340,13 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
     Work work = work_of(a, own_lane * per, kTileRows, cap);
     int64_t own = weight(work);
 #pragma unroll 4
-    for (int i = 1; i < per; ++i) own += weight(work_of(a, own_lane * per + i, kTileRows, cap));
+    for (int i = 1; i < per; ++i)  // (64 of these do not pass 63 bits)
+      own = min(own + weight(work_of(a, own_lane * per + i, kTileRows, cap)), (int64_t)1 << 56);
     int64_t up_to = scan_of(own);
-    const int64_t total = last_lane(up_to);
+    // A plan whose rows overlap may ask for more than any other can: no more than that is done.
+    const int64_t each = ((min(cap, (int64_t)INT_MAX) + 32) >> 5) + kItemSteps;
+    const int64_t most = ((int64_t)a.tokens * a.group / kTileRows + sequences) * heads * each;
+    const int64_t total = min(last_lane(up_to), most);
     chunk = max(quotient(total + parts - 1, parts), (int64_t)kLeastSteps);
     at = chunk * blockIdx.x;
     end = min(total, at + chunk);
@@ -375,7 +379,7 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
     const int item = (int)quotient(at - before, of.each);
     tile = item / heads;
     kvh = item - tile * heads;
-    first = (int)(at - before - (int64_t)item * of.each);
+    first = (int)min(max(at - before - (int64_t)item * of.each, (int64_t)0), (int64_t)of.each - 1);
   }
   const int64_t begin = at;
   while (at < end) {
@@ -410,6 +414,7 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
         ++seq;
         of = uniform(work_of(a, seq, kTileRows, cap));
       } while (of.tiles == 0 && seq < sequences);
+      if (seq >= sequences) end = at;
     }
   }
 
@@ -578,7 +583,7 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
           for (int n = 0; n < NQ; ++n) z[n][s] = mfma16(as_frag(f), q[n][u * Step::kUnit + i], z[n][s]);
         }
     }
-    if (k0 < lo_max || k0 + 32 > hi_min) {  // some row does not see all of these keys
+    if (k0 < lo_max || (uint32_t)k0 + 32 > (uint32_t)hi_min) {  // some row does not see all of these keys
       asm volatile("");                     // a branch, no 16 comparisons at every step
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
@@ -624,7 +629,7 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
     // V's columns by parts: 8 columns to a lane (words), 4 (halves), 2 (bytes).  A product's lane of P has keys 4 g ..
     // of both halves; to them belong, in the lanes of V, of half g % 2 the keys 4 (g / 2) .. and 8 + 4 (g / 2) ..
     const int side = g & 1, key0 = 4 * (g >> 1);  // key i of the lane's 8: half `side`, key0 + 8 (i / 4) + i % 4
-    const bool edge = k0 < lo_all || k0 + 32 > hi_all;
+    const bool edge = k0 < lo_all || (uint32_t)k0 + 32 > (uint32_t)hi_all;
     const uint32_t* scales = reinterpret_cast<const uint32_t*>(in + Step::kScales + 32 * ND);
     bool some_nan = false;  // a byte of the step's scales is 255
     if (ND == 8 || lane < 8 * ND) {
@@ -980,7 +985,7 @@ __global__ __launch_bounds__(256, ND <= 4 ? 2 : 1) void kv4_prompt_kernel(Attn4A
       put(buf, wave * ND + i, f);  // key tile wave / 2, step (wave % 2) ND + i of its columns
     }
     const int k0 = (int)((uint32_t)keys.base + (uint32_t)step * 64) + wave * 16;
-    const bool edge = k0 < keys.lo || k0 + 16 > keys.hi;
+    const bool edge = k0 < keys.lo || (uint32_t)k0 + 16 > (uint32_t)keys.hi;
     uint32_t some_nan = 0;
 #pragma unroll
     for (int part = 0; part < Q4::kFours + Q4::kTwo + Q4::kOne; ++part) {
@@ -1069,7 +1074,7 @@ __global__ __launch_bounds__(256, ND <= 4 ? 2 : 1) void kv4_prompt_kernel(Attn4A
       for (int s = 0; s < 2; ++s)
         z[s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(buf, s * 2 * ND + i), q[i], z[s], 0, 0, 0);
     read_ahead<4 * ND, 4>();
-    if (k0 < lo_max || k0 + 64 > hi_min) {
+    if (k0 < lo_max || (uint32_t)k0 + 64 > (uint32_t)hi_min) {
       asm volatile("");
       const int lo = my.lo - k0 - 4 * h, hi = my.hi - k0 - 4 * h;
 #pragma unroll

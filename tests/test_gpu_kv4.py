@@ -459,6 +459,18 @@ def test_plans_that_make_no_sense_stay_within_bounds():
         assert out.shape == q.shape and k.shape == x.shape
 
 
+def test_a_plan_that_gives_rows_to_many_sequences_ends():
+    say("rows of many sequences")
+    p = Plan([90] * 300, [1] * 300, 2, 64, 16).fill()
+    cache, plan = p.cache_on_gpu(), p.on_gpu()
+    starts = torch.tensor([0, 300] * 150 + [250], dtype=torch.int32, device="cuda")
+    buf = torch.full((302, 4, 64), 7.0, dtype=BF, device="cuda")
+    q = torch.randn(300, 4, 64, device="cuda").to(BF)
+    kv4.harp_kv4_attention(q, cache, starts, *plan[1:], out=buf[1:301])
+    torch.cuda.synchronize()
+    assert (buf[0] == 7).all() and (buf[301] == 7).all() and (buf[251:] == 7).all()
+
+
 def test_no_sequences_and_no_tokens():
     c = kv4.harp_kv4_cache(3, 2, 16, 64)
     none = (torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda"),
