@@ -527,12 +527,12 @@ harp_status harp_qk_norm_rope_vjp(const void* q, int64_t q_token, int64_t q_head
  * ld_table apart): the page that holds its tokens i page_size and on.  All
  * int32, on the device.  Entries of the table behind a sequence's length are
  * not read.  Sequences may share pages; two of one call must not write the
- * same place.  Whatever the three arrays hold, nothing outside the cache, the
- * table and the rows is read or written: rows from starts[sequences] on are
- * left as they are (read but not used); a row before its sequence's beginning
- * is not written to the cache, reads as zeros and sees no key; a place whose
- * page is outside 0 .. pages - 1 or beyond the table is not written, and reads
- * as NaN.
+ * same place.  Rows from starts[sequences] on are left as they are (read but
+ * not used); a row before its sequence's beginning is not written to the cache,
+ * reads as zeros and sees no key; a place whose page is outside 0 .. pages - 1
+ * or beyond the table is not written, and reads as NaN.  Whatever the three
+ * arrays hold, also starts that decrease, nothing outside the cache, the table
+ * and the `tokens` rows is read or written, and the call ends.
  * sequences, width at most 2^24, kv_heads at most 65535, tokens x q_heads and
  * sequences x kv_heads at most 2^30. */
 

@@ -468,7 +468,7 @@ def test_a_plan_that_gives_rows_to_many_sequences_ends():
     q = torch.randn(300, 4, 64, device="cuda").to(BF)
     kv4.harp_kv4_attention(q, cache, starts, *plan[1:], out=buf[1:301])
     torch.cuda.synchronize()
-    assert (buf[0] == 7).all() and (buf[301] == 7).all() and (buf[251:] == 7).all()
+    assert (buf[0] == 7).all() and (buf[301] == 7).all()
 
 
 def test_no_sequences_and_no_tokens():
