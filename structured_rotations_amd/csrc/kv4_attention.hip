@@ -862,6 +862,7 @@ struct Quarter4 {
   uint32_t k[ND], ks[kScales];
   uint32_t v[8][kFours + kTwo + kOne];
   uint32_t vs[2][ND];
+  bool k_lost, v_lost;  // the page is missing (looked at when the loads are there: not to wait for them before)
 };
 
 template <int ND>
@@ -943,17 +944,19 @@ __global__ __launch_bounds__(256, ND <= 4 ? 2 : 1) void kv4_prompt_kernel(Attn4A
 #pragma unroll
         for (int i = 0; i < ND; ++i) w.k[i] = reinterpret_cast<const uint32_t*>(p)[i];
       }
+      w.k_lost = page < 0;
       const uint8_t* e = a.cache.k.scales + pg * a.cache.k.scales_page + row * ND;
 #pragma unroll
       for (int i = 0; i < Q4::kScales; ++i) {
         const int word = ((wave & 1) * 2 + h) * ND + i * (ND / Q4::kScales);
-        w.ks[i] = page < 0 ? 255u : e[word / 4];  // no page: NaN
+        w.ks[i] = e[word / 4];
       }
     }
     {  // V: 16 keys, all columns
       const int page = __builtin_amdgcn_readlane(pages, 4 * at + wave);
       const int64_t pg = page < 0 ? 0 : page;
       const int64_t row = ((int64_t)kvh << ps_log2) + ((key0 + wave * 16) & in_mask);
+      w.v_lost = page < 0;
       const auto vc = common(a.cache.v.codes + pg * a.cache.v.codes_page + row * kRow);
       const auto vs = common(a.cache.v.scales + pg * a.cache.v.scales_page + row * ND);
 #pragma unroll
@@ -968,16 +971,25 @@ __global__ __launch_bounds__(256, ND <= 4 ? 2 : 1) void kv4_prompt_kernel(Attn4A
       }
 #pragma unroll
       for (int i = 0; i < ND; ++i) {
-        const uint32_t e0 = load_at<uint32_t>(vs, 4 * h * ND, 4 * i), e1 = load_at<uint32_t>(vs, 4 * h * ND, 8 * ND + 4 * i);
-        w.vs[0][i] = page < 0 ? 0u : e0;  // another page's: nothing that is not finite
-        w.vs[1][i] = page < 0 ? 0u : e1;
+        w.vs[0][i] = load_at<uint32_t>(vs, 4 * h * ND, 4 * i);
+        w.vs[1][i] = load_at<uint32_t>(vs, 4 * h * ND, 8 * ND + 4 * i);
       }
     }
   };
   auto put = [&](int buf, int frag, const uint32_t (&w)[4]) {
     *reinterpret_cast<u32x4*>(&frags[buf][frag * kFrag + lane * 16]) = u32x4{w[0], w[1], w[2], w[3]};
   };
-  auto widen = [&](const Q4& w, int step, int buf) {
+  auto widen = [&](Q4& w, int step, int buf) {
+    if (__any(w.k_lost)) {
+      asm volatile("");  // (a branch)
+#pragma unroll
+      for (int i = 0; i < Q4::kScales; ++i) w.ks[i] = w.k_lost ? 255u : w.ks[i];  // no page: NaN
+    }
+    if (w.v_lost) {
+      asm volatile("");
+#pragma unroll
+      for (int i = 0; i < ND; ++i) w.vs[0][i] = w.vs[1][i] = 0;  // another page's: nothing that is not finite
+    }
 #pragma unroll
     for (int i = 0; i < ND; ++i) {
       const uint32_t e = w.ks[i / (ND / Q4::kScales)] << 23;
