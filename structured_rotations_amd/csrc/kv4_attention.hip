@@ -833,9 +833,10 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
 // next 64 keys, straight from memory into the fragments of the 32 x 32 x 16
 // instruction, and writes them to LDS as they are read, 16 bytes a lane one
 // after the other, while the products of the present 64 keys run.
-// 4 x 2048 over 8192, 32/8 x 128: 655 to 672 us, 910 to 930 TFLOP/s.  The matrix
+// 4 x 2048 over 8192, 32/8 x 128: 646 to 655 us, 930 to 945 TFLOP/s.  The matrix
 // units are busy 39% of the time, the vector units 52 to 61% (a third of it the
-// exponentials), LDS half; two waves a SIMD overlap too little of one another.
+// exponentials), LDS half; two waves a SIMD, one with products and one with
+// vector work, take 1.5 times as long as the longer of them alone.
 // 256 rows a workgroup, four of its eight waves widening K and four V, halve the
 // widening and are no faster (717 us next to 690 in one session), nor is a higher
 // priority while products run (714).

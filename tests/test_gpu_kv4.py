@@ -471,6 +471,22 @@ def test_a_plan_that_gives_rows_to_many_sequences_ends():
     assert (buf[0] == 7).all() and (buf[301] == 7).all()
 
 
+@pytest.mark.parametrize("lengths,new,heads,d", [([300, 40, 5], [1, 1, 1], 2, 128), ([300, 40, 5], [6, 6, 6], 2, 96),
+                                                 ([400], [100], 1, 64)])
+def test_a_workspace_is_used_up_to_its_size(lengths, new, heads, d):
+    p = Plan(lengths, new, heads, d, 16).fill()
+    q = gpu(p.rng.standard_normal((p.rows, 4, d)).astype(np.float32), BF)
+    cache, plan = p.cache_on_gpu(), p.on_gpu()
+    need = kv4.harp_kv4_attention_workspace(p.rows, 4, heads, d, 16, len(lengths), plan[2].shape[1])
+    assert need > 0
+    buf = torch.full((need + 512,), 0x5a, dtype=torch.uint8, device="cuda")
+    out, lse = kv4.harp_kv4_attention(q, cache, *plan, lse=True, workspace=buf[256:256 + need])
+    assert (buf[:256] == 0x5a).all() and (buf[256 + need:] == 0x5a).all()
+    check_attention(p, q, out, lse, 1 / math.sqrt(d), True, 0)
+    with pytest.raises(Exception, match="workspace"):
+        kv4.harp_kv4_attention(q, cache, *plan, workspace=buf[256:256 + need - 1])
+
+
 def test_no_sequences_and_no_tokens():
     c = kv4.harp_kv4_cache(3, 2, 16, 64)
     none = (torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda"),
