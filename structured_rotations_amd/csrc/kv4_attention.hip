@@ -15,7 +15,7 @@
 // permutations when it puts them into LDS.
 //
 // Scores, maxima, sums and accumulators are fp32.  The weights are rounded to
-// bf16 for the product with V: each is off by at most 2^-9 of itself, the result
+// bf16 for the product with V: each is off by at most 2^-8 of itself, the result
 // by about as much as its own rounding to bf16 adds.
 #include <algorithm>
 #include <climits>
