@@ -561,9 +561,12 @@ harp_status harp_kv4_read(const uint8_t* k_codes, int64_t kc_page, const uint8_t
  *   lse = ln sum exp(z_j)   (fp32, tokens x q_heads, contiguous; NULL: none).
  * A row that sees no key: out = 0, lse = -infinity.  A key that a row does not
  * see has no effect on it, whatever the cache holds there, with one exception:
- * scales of 253 and 254 whose values exceed BF16's range (harp_kv4_write makes
- * none) within a sequence's length.  scale > 0, finite.  Sums in fp32; the
- * weights exp(z_j - max) are rounded to BF16 for the product with the values.
+ * values beyond BF16's range (of scales 253 and 254; harp_kv4_write makes none)
+ * within a sequence's length leave its rows infinite or NaN in their columns.
+ * scale > 0, finite.  Weights and sums in fp32.  For the product with the values
+ * a weight is the sum of two BF16 numbers, off by at most 2^-16 of itself; where
+ * a sequence has more than 16 rows to a key head on average it is one, off by at
+ * most 2^-8, and the sum that divides the product is that of the rounded weights.
  * The result of a call does not depend on the order in which its parts are
  * computed.  out: BF16, must not overlap any input.
  * workspace: harp_kv4_attention_workspace() bytes (may be 0; -1: sizes out of

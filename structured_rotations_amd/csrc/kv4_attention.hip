@@ -14,9 +14,21 @@
 // the instruction pick them (mfma_pairs), the one for many pairs them by byte
 // permutations when it puts them into LDS.
 //
-// Scores, maxima, sums and accumulators are fp32.  The weights are rounded to
-// bf16 for the product with V: each is off by at most 2^-8 of itself, the result
-// by about as much as its own rounding to bf16 adds.
+// Scores, weights, maxima, sums and accumulators are fp32.  The product with V
+// takes the weights as bf16.  Rounding them once is off by up to 2^-8 of each, of
+// the heaviest too, since a row's weights go by a reference that its largest score
+// may pass.
+// - Tiles of 16 rows: what the rounding left off goes into a second product, which
+//   leaves 2^-16 of a weight, and the result off by its own rounding only (1.6e-3 in
+//   relative l2 against 64 bits; with one product 1.8e-3).  Bytes bound this kernel:
+//   64 x 1 over 50 .. 8192 keys, 32/8 x 128, 71.5 us, with one product 69.8.
+// - Tiles of 32 and 128 rows: products and vector work count, and a second product
+//   costs more (64 x 8 over 4096, 64/8 x 128: 150 us, one 134; 4 x 2048 over 8192, 32/8 x
+//   128: 832, one 640).  There is one, and what divides it is the sum of the weights as
+//   they were rounded (138 and 656 us): rounding then moves a result by up to 2^-8 of the
+//   values' distances from it, not of the values, and a row with one heavy key not at
+//   all.  (4 x 2048 over 2048 .. 8192: off by 1.7e-3, by the result's rounding alone 1.5e-3.)
+//   lse takes the sum of the weights as they were.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -55,6 +67,21 @@ __device__ __forceinline__ uint32_t widen4(uint32_t codes, uint32_t e) {
   uint32_t w;
   __builtin_memcpy(&w, &v, 4);
   return w;
+}
+// One factor for each of two weights rounded to bf16 (w), and an fp32 number added
+// to the products.  (Exact where the result has no more than 24 bits.)
+template <uint32_t kFactors>
+__device__ __forceinline__ float dot_weights(uint32_t w, float c) {
+  uint32_t factors = kFactors;
+  asm("" : "+s"(factors));  // in a register: -1 in the lower half would become the instruction's own -1.0, which is in the upper
+  bf16x2_t x, y;
+  __builtin_memcpy(&x, &w, 4);
+  __builtin_memcpy(&y, &factors, 4);
+  return __builtin_amdgcn_fdot2_f32_bf16(x, y, c, false);
+}
+// What their rounding left off two weights, as bf16.
+__device__ __forceinline__ uint32_t left_off(uint32_t w, float a, float b) {
+  return pack_bf16x2_hw(dot_weights<0x0000bf80u>(w, a), dot_weights<0xbf800000u>(w, b));  // -1, 0; 0, -1
 }
 // Largest over the lanes that are 16 and 32 apart, in every one of them.
 __device__ __forceinline__ float max_of_groups(float v) {
@@ -308,6 +335,7 @@ template <int ND, int NQ>
 __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(Attn4Args a, int parts, int64_t item0) {
   using Step = Step4<ND>;
   constexpr int kRow = ND * 16, kTileRows = 16 * NQ, kAcc = 2 * ND, kD = ND * 32;
+  constexpr bool kExact = NQ == 1;  // weights as two bf16 numbers
   const int own_lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ps_log2 = a.cache.page_log2;
@@ -453,11 +481,11 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
   lo_max = __builtin_amdgcn_readfirstlane(lo_max);
 
   f32x4 acc[NQ][kAcc];
-  float m[NQ], l[NQ];
+  float m[NQ], l[NQ], rounded[NQ];  // sums of the weights, as they are and as a single bf16 number
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     m[n] = -INFINITY;
-    l[n] = 0.0f;
+    l[n] = rounded[n] = 0.0f;
 #pragma unroll
     for (int i = 0; i < kAcc; ++i) acc[n][i] = f32x4{0, 0, 0, 0};
   }
@@ -597,7 +625,7 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
           }
       }
     }
-    bf16x8_t p[NQ];
+    bf16x8_t p[NQ], rest[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       float top = z[n][0][0];
@@ -609,6 +637,7 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
         const float shrink = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[n] - now);
         m[n] = now;
         l[n] *= shrink;
+        rounded[n] *= shrink;
         f32x4 of_row;  // the accumulators' rows are the queries
 #pragma unroll
         for (int r = 0; r < 4; ++r) of_row[r] = __shfl(shrink, 4 * g + r);
@@ -622,9 +651,15 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
         e[i] = __builtin_amdgcn_exp2f(fmaf(z[n][i >> 2][i & 3], to_log2, -less));
         l[n] += e[i];
       }
-      const uint32_t f[4] = {pack_bf16x2_hw(e[0], e[1]), pack_bf16x2_hw(e[2], e[3]), pack_bf16x2_hw(e[4], e[5]),
-                             pack_bf16x2_hw(e[6], e[7])};
+      uint32_t f[4], left[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[i] = pack_bf16x2_hw(e[2 * i], e[2 * i + 1]);
+        if constexpr (kExact) left[i] = left_off(f[i], e[2 * i], e[2 * i + 1]);
+        else rounded[n] = dot_weights<0x3f803f80u>(f[i], rounded[n]);  // 1, 1
+      }
       p[n] = as_frag(f);
+      if constexpr (kExact) rest[n] = as_frag(left);
     }
     // V's columns by parts: 8 columns to a lane (words), 4 (halves), 2 (bytes).  A product's lane of P has keys 4 g ..
     // of both halves; to them belong, in the lanes of V, of half g % 2 the keys 4 (g / 2) .. and 8 + 4 (g / 2) ..
@@ -715,8 +750,13 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
         __builtin_memcpy(&pairs, w, 32);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-          acc[n][tile0 + 2 * byte] = mfma_pairs<0>(p[n], pairs, acc[n][tile0 + 2 * byte]);
-          acc[n][tile0 + 2 * byte + 1] = mfma_pairs<1>(p[n], pairs, acc[n][tile0 + 2 * byte + 1]);
+          f32x4 &even = acc[n][tile0 + 2 * byte], &odd = acc[n][tile0 + 2 * byte + 1];
+          even = mfma_pairs<0>(p[n], pairs, even);
+          odd = mfma_pairs<1>(p[n], pairs, odd);
+          if constexpr (kExact) {
+            even = mfma_pairs<0>(rest[n], pairs, even);
+            odd = mfma_pairs<1>(rest[n], pairs, odd);
+          }
         }
       };
       columns(std::integral_constant<int, 0>{});
@@ -759,6 +799,15 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     l[n] = sum_of_groups(l[n]);
+    if constexpr (!kExact) {  // the results by the rounded weights; with others' by the weights as they are
+      rounded[n] = sum_of_groups(rounded[n]);
+      const float ratio = l[n] == 0.0f ? 1.0f : l[n] / rounded[n];
+      f32x4 of_row;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) of_row[r] = __shfl(ratio, 4 * g + r);
+#pragma unroll
+      for (int i = 0; i < kAcc; ++i) acc[n][i] *= of_row;
+    }
     __syncthreads();
     if (g == 0) {
       stat[wave][c16][0] = m[n];
@@ -916,7 +965,7 @@ __global__ __launch_bounds__(256, ND <= 4 ? 2 : 1) void kv4_prompt_kernel(Attn4A
   for (int i = 0; i < ND; ++i)
 #pragma unroll
     for (int x = 0; x < 16; ++x) acc[i][x] = 0.0f;
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, l = 0.0f, rounded = 0.0f;  // sums of the weights, as they are and as V's product takes them
   uint32_t poison = 0;
   const float to_log2 = a.scale * kLog2e;
 
@@ -1107,6 +1156,7 @@ __global__ __launch_bounds__(256, ND <= 4 ? 2 : 1) void kv4_prompt_kernel(Attn4A
       const float shrink = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - now);
       m = now;
       l *= shrink;
+      rounded *= shrink;
 #pragma unroll
       for (int i = 0; i < ND; ++i) acc[i] *= shrink;
     }
@@ -1122,6 +1172,7 @@ __global__ __launch_bounds__(256, ND <= 4 ? 2 : 1) void kv4_prompt_kernel(Attn4A
         const float e1 = __builtin_amdgcn_exp2f(fmaf(z[s >> 1][x + 1], to_log2, -less));
         l += e0 + e1;
         f[j] = pack_bf16x2_hw(e0, e1);
+        rounded = dot_weights<0x3f803f80u>(f[j], rounded);  // 1, 1
       }
       p[s] = as_frag(f);
     }
@@ -1165,11 +1216,13 @@ __global__ __launch_bounds__(256, ND <= 4 ? 2 : 1) void kv4_prompt_kernel(Attn4A
   }
 
   l = sum_of_halves(l);
+  rounded = sum_of_halves(rounded);
   if (!has) return;
   const int64_t token = t.first_token + tok, head = (int64_t)kvh * a.group + gh, row = token * a.q_heads + head;
   const bool sees_some = my.hi > my.lo;
   const int64_t all_rows = (int64_t)a.tokens * a.q_heads;
-  const float inv = splits > 1 ? 1.0f : sees_some ? 1.0f / l : 0.0f;
+  // a part's result goes by its own rounded weights, and with others by the weights as they are
+  const float inv = splits > 1 ? l == 0.0f ? 1.0f : l / rounded : sees_some ? 1.0f / rounded : 0.0f;
   float* part_out = a.partial + ((int64_t)split * all_rows + row) * (ND * 32);
   uint16_t* out = a.out + token * a.out_token + head * a.out_head;
 #pragma unroll

@@ -1,0 +1,85 @@
+"""What attention over a 4-bit cache and its heads compute, where a little less
+would not be seen in ordinary values: weights of one dominant key.
+
+Tolerances.  u = 2^-24 and h = 2^-8 are the largest relative errors of one
+rounding to fp32 and to bf16; half a step of bf16 at x is 2^(floor(log2 |x|) - 8).
+Each test says how its own follows from them.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4_oracle as K
+from structured_rotations_amd import kv4
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+U, H = 2.0 ** -24, 2.0 ** -8
+
+
+def cpu(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def gpu(a, dtype=None):
+    return torch.from_numpy(np.ascontiguousarray(a)).to("cuda", dtype)
+
+
+def say(*a):
+    print("\n[case]", *a, flush=True)
+
+
+def half_step(x):
+    return 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -120))) - 8)
+
+
+# ------------------------------------------------------------------- weights
+@pytest.mark.parametrize("tokens,heads", [(1, 16), (1, 48), (4, 64)], ids=["tiles of 16", "tiles of 32", "tiles of 128"])
+def test_a_key_that_outweighs_the_others_and_comes_late(tokens, heads):
+    """Two keys of score 0, then one a few units above: the reference that its
+    weight goes by is theirs, and the result is its value to within the result's
+    rounding.
+
+    Scores here are exact: at most two products of few bits each.  A result is
+    off by half its step; by 2^-19 of `size`, the weighted mean of |v|, for the
+    exponentials, sums and divisions; in tiles of 16 rows by 2^-16 of `size`, the
+    weights having 16 bits; in larger ones by h (1 + 2^-7) of `spread`, the
+    weighted mean of |v - result|, the weights having 8 and their sum being that
+    of the rounded ones."""
+    say("late peak", tokens, heads)
+    n, d = 1024, 64
+    kc, vc = np.zeros((n, d // 2), np.uint8), np.zeros((n, d // 2), np.uint8)
+    kc[:, 0] = 0x0f << 4                                     # all keys: 0, -6 in columns 0 and 1
+    kc[[69, 133], 0], kc[199, 0] = 0x00, 0x02                # two early ones: 0, 0; the late one: 1, 0
+    rng = np.random.default_rng(0)
+    vc[:] = rng.integers(0, 256, (n, d // 2))
+    vc[[69, 133]] = rng.integers(0, 2, (2, d // 2)) * 0x99   # 0 or -0.5
+    vc[199] = rng.choice([0x33, 0x35, 0x57, 0x62], d // 2)   # 1.5, 3, 4, 6, 1
+    pages = rng.permutation(n // 64)
+    cache = []
+    for c in (kc, vc):
+        codes, scales = np.zeros((n // 64, 1, 64, d // 2), np.uint8), np.full((n // 64, 1, 64, d // 32), 127, np.uint8)
+        codes[pages, 0] = c.reshape(-1, 64, d // 2)
+        cache += [codes, scales]
+    q = np.zeros((tokens, heads, d), np.float32)
+    q[..., 0] = rng.uniform(0.5, 5.4, (tokens, heads))       # up to 7.8 powers of two above
+    q[..., 1] = 6.0
+    q = gpu(q, BF)
+    plan = [np.array([0, tokens]), np.array([n]), pages[None]]
+    out, lse = kv4.harp_kv4_attention(q, kv4.Cache4(*(gpu(c) if i % 2 == 0 else gpu(c).view(kv4.SCALES) for i, c in enumerate(cache))),
+                                      *(gpu(x.astype(np.int32)) for x in plan), scale=1.0, lse=True)
+    k, v = (K.sequence(cache[i], cache[i + 1], pages, n)[0] for i in (0, 2))
+    z = cpu(q) @ k.T                                         # every key is in front of every row
+    w = np.exp(z - z.max(-1, keepdims=True))
+    w /= w.sum(-1, keepdims=True)
+    want = w @ v
+    size = w @ np.abs(v)
+    if tokens * heads <= 16:
+        tol = 2.0 ** -16 * size
+    else:
+        tol = np.stack([np.stack([w[i, j] @ np.abs(v - want[i, j]) for j in range(heads)]) for i in range(tokens)]) * (H * (1 + 2.0 ** -7))
+    err = np.abs(cpu(out) - want)
+    assert (err <= half_step(np.abs(want) + tol) + tol + 2.0 ** -19 * size).all(), (err / size).max()
+    wl = np.log(np.exp(z).sum(-1))
+    assert (np.abs(cpu(lse) - wl) <= 2.0 ** -20 + 2.0 ** -22 * np.abs(wl)).all()
