@@ -377,9 +377,10 @@ __global__ __launch_bounds__(256, 4) void qk_norm_rope_vjp_kernel(QkArgs a, int 
           for (int i = 0; i < 8; ++i) sum_q[i] = fmaf(g[i], x[i], sum_q[i]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            sum_q[i] = fmaf(g[i], is_q ? x[i] : 0.0f, sum_q[i]);
-            sum_k[i] = fmaf(g[i], is_q ? 0.0f : x[i], sum_k[i]);
+          for (int i = 0; i < 8; ++i) {  // (no product with 0: a gradient may be infinite or NaN)
+            const float sum = fmaf(g[i], x[i], is_q ? sum_q[i] : sum_k[i]);
+            sum_q[i] = is_q ? sum : sum_q[i];
+            sum_k[i] = is_q ? sum_k[i] : sum;
           }
         }
       }

@@ -1,5 +1,6 @@
 """What attention over a 4-bit cache and its heads compute, where a little less
-would not be seen in ordinary values: weights of one dominant key.
+would not be seen in ordinary values: weights of one dominant key, and gradients
+next to others that are not numbers.
 
 Tolerances.  u = 2^-24 and h = 2^-8 are the largest relative errors of one
 rounding to fp32 and to bf16; half a step of bf16 at x is 2^(floor(log2 |x|) - 8).
@@ -83,3 +84,23 @@ def test_a_key_that_outweighs_the_others_and_comes_late(tokens, heads):
     assert (err <= half_step(np.abs(want) + tol) + tol + 2.0 ** -19 * size).all(), (err / size).max()
     wl = np.log(np.exp(z).sum(-1))
     assert (np.abs(cpu(lse) - wl) <= 2.0 ** -20 + 2.0 ** -22 * np.abs(wl)).all()
+
+
+# ----------------------------------------------------- gradients side by side
+@pytest.mark.parametrize("hq,hk,d", [(3, 2, 128), (1, 1, 64), (5, 3, 80), (2, 1, 256)])
+def test_gradients_that_are_not_numbers_stay_with_their_own_gamma(hq, hk, d):
+    """Queries and keys share a wave, not a sum."""
+    say("NaN gradients", hq, hk, d)
+    rng = np.random.default_rng(d)
+    n = 9
+    q, k, dq, dk = (gpu(rng.standard_normal((n, h, d)).astype(np.float32)) for h in (hq, hk, hq, hk))
+    pos, f = torch.arange(n, device="cuda"), gpu(10000.0 ** (-np.arange(8) / 8.0))
+    g = torch.ones(d, device="cuda")
+    good = kv4.harp_qk_norm_rope_vjp(q, k, pos, f, dq, dk, g, g)
+    bad_q, bad_k = dq.clone(), dk.clone()
+    bad_q[4, 0, 20], bad_k[2, hk - 1, 20], bad_k[3, 0, 30] = float("inf"), float("nan"), float("-inf")
+    r = kv4.harp_qk_norm_rope_vjp(q, k, pos, f, dq, bad_k, g, g)
+    assert torch.equal(r.dgamma_q, good.dgamma_q) and torch.equal(r.dq, good.dq)
+    assert torch.isnan(r.dgamma_k[20]) and not torch.isfinite(r.dgamma_k[30])
+    r = kv4.harp_qk_norm_rope_vjp(q, k, pos, f, bad_q, dk, g, g)
+    assert torch.equal(r.dgamma_k, good.dgamma_k) and torch.equal(r.dk, good.dk) and not torch.isfinite(r.dgamma_q[20])
