@@ -198,23 +198,32 @@ __device__ __forceinline__ float rsqrt_of(float x) {
   return fmaf(0.5f * r, e, r);
 }
 
-// 1 / sqrt(mean(x^2) + eps), of any finite head: squares beyond fp32's range
-// are summed again in other units.
+// 1 / sqrt(mean(x^2) + eps).  A head whose squares leave fp32's range is brought
+// into it first, by a power of two that `unit` tells (1 for all others): v and the
+// result are then of the head in those units, of which v times the result does not
+// depend.  The smallest heads' 1 / rms is more than fp32 holds.
+// (0x1p100: squares from 2^-298 on become 2^-98, and their sum, below 2^-80, 2^120;
+// eps is below 2^-100 where they are taken for small.)
 template <int kLanes>
-__device__ __forceinline__ float head_rstd(const float (&v)[8], float d, float eps, float least) {
+__device__ __forceinline__ float head_rstd(float (&v)[8], float d, float eps, float least, float* unit) {
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ss += v[i] * v[i];
   ss = head_sum<kLanes>(ss);
-  float r = rsqrt_of(fmaf(ss, 1.0f / d, eps));
-  const bool far = !(ss >= least && ss < __uint_as_float(0x7f800000u));
+  const float mean = fmaf(ss, 1.0f / d, eps);
+  float r = rsqrt_of(mean);
+  const bool far = !(ss >= least && mean < __uint_as_float(0x7f800000u));
+  *unit = 1.0f;
   if (__any(far)) {  // the whole wave, so that every lane has its partners
-    const float unit = ss < least ? 0x1p80f : 0x1p-80f;
+    if (far) *unit = ss < least ? 0x1p100f : 0x1p-80f;
     float t = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += (v[i] * unit) * (v[i] * unit);
+    for (int i = 0; i < 8; ++i) {
+      v[i] *= *unit;
+      t += v[i] * v[i];
+    }
     t = head_sum<kLanes>(t);
-    if (far) r = unit / sqrtf(t / d + eps * unit * unit);
+    if (far) r = 1.0f / sqrtf(t / d + eps * *unit * *unit);
   }
   return r;
 }
@@ -305,7 +314,8 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs a, int per, in
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = next[i];
     load(h + map.kPar);
-    const float r = head_rstd<kLanes>(v, d, a.eps, least);
+    float in_units;  // v times r does not depend on it
+    const float r = head_rstd<kLanes>(v, d, a.eps, least, &in_units);
     const bool is_q = h < a.q.heads;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = v[i] * r * (is_q ? gq[i] : gk[i]);
@@ -361,7 +371,8 @@ __global__ __launch_bounds__(256, 4) void qk_norm_rope_vjp_kernel(QkArgs a, int 
         g[i] = gn[i];
       }
       load(h + map.kPar);
-      const float r = head_rstd<kLanes>(x, d, a.eps, least);
+      float in_units;
+      const float r = head_rstd<kLanes>(x, d, a.eps, least, &in_units);
       if (a.signs) {
         hadamard<kLanes>(g, map.lane, a.d);
 #pragma unroll
@@ -393,6 +404,10 @@ __global__ __launch_bounds__(256, 4) void qk_norm_rope_vjp_kernel(QkArgs a, int 
       const float mean = head_sum<kLanes>(dot) * (1.0f / d);
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] = r * fmaf(x[i], -mean, g[i]);
+      if (__any(in_units != 1.0f)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] *= in_units;
+      }
       if (map.has && h < end) put8<kStream>(to.at(is_q), g);
       to.next();
     }

@@ -1,11 +1,13 @@
 """What attention over a 4-bit cache and its heads compute, where a little less
-would not be seen in ordinary values: weights of one dominant key, and gradients
-next to others that are not numbers.
+would not be seen in ordinary values: weights of one dominant key, heads at the
+ends of fp32's range, and gradients next to others that are not numbers.
 
 Tolerances.  u = 2^-24 and h = 2^-8 are the largest relative errors of one
 rounding to fp32 and to bf16; half a step of bf16 at x is 2^(floor(log2 |x|) - 8).
 Each test says how its own follows from them.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -84,6 +86,40 @@ def test_a_key_that_outweighs_the_others_and_comes_late(tokens, heads):
     assert (err <= half_step(np.abs(want) + tol) + tol + 2.0 ** -19 * size).all(), (err / size).max()
     wl = np.log(np.exp(z).sum(-1))
     assert (np.abs(cpu(lse) - wl) <= 2.0 ** -20 + 2.0 ** -22 * np.abs(wl)).all()
+
+
+# --------------------------------------------------------- the ends of a range
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256, 512, 80])
+def test_heads_of_the_smallest_and_largest_values(d, io):
+    """Norms do not depend on a head's size, without eps: 2^-19 of the norm as
+    for any head, a bf16 result h more.  Gradients in the head's own size:
+    2^-18 of r |g|, and of a bf16 result h of itself."""
+    say("ends of the range", d, io)
+    rng = np.random.default_rng(d)
+    sizes = np.array([-148, -140, -133, -128, -126, -120, -100, -60, -39, 0, 40, 63, 64, 100, 120, 124], np.float64)
+    x = np.clip(rng.standard_normal((len(sizes), 3, d)), -4, 4) * 2.0 ** sizes[:, None, None]
+    x = gpu(x.astype(np.float32), {"f32": torch.float32, "bf16": BF}[io])
+    x[:2, :, 0] = 2.0 ** -133                                # no head of zeros only: bf16 holds nothing smaller
+    x[-1, 0, :] = 3.0e38
+    signs = gpu(rng.choice([-1, 1], d).astype(np.int8)) if d != 80 else None
+    s = None if signs is None else cpu(signs)
+    y, _ = kv4.harp_qk_norm_rope(x, None, None, None, eps=0.0, signs=signs)
+    # in units of the head's largest value, so that the oracle's squares stay finite
+    top = np.abs(cpu(x)).max(-1, keepdims=True)
+    zero, none = np.zeros(len(sizes)), np.zeros(0)
+    want = K.norm_rope(cpu(x) / top, zero, none, None, 0.0, False, s)
+    err = np.linalg.norm(cpu(y) - want, axis=-1) / math.sqrt(d)
+    assert err.max() <= 2.0 ** -19 + (H if io == "bf16" else 0), err.max(-1)
+    dy = rng.standard_normal(x.shape) * np.clip(top, 2.0 ** -60, 2.0 ** 60)
+    dy = gpu(dy.astype(np.float32), x.dtype)
+    r = kv4.harp_qk_norm_rope_vjp(x, None, None, None, dy, None, eps=0.0, signs=signs, want_dgamma=True)
+    dx, dgamma, size, gsize = K.norm_rope_vjp(cpu(x) / top, zero, none, None, 0.0, False, s, cpu(dy))
+    keep = (size / top[..., 0] < 2.0 ** 126) & (size / top[..., 0] > 2.0 ** -100)        # what fp32 and bf16 hold
+    assert keep.sum() > keep.size / 2
+    err = np.linalg.norm(cpu(r.dq) * top - dx, axis=-1)
+    assert (err <= 2.0 ** -18 * size + (H * np.linalg.norm(dx, axis=-1) if io == "bf16" else 0))[keep].all()
+    assert (np.abs(cpu(r.dgamma_q) - dgamma) <= 2.0 ** -17 * gsize).all()
 
 
 # ----------------------------------------------------- gradients side by side
