@@ -116,6 +116,19 @@ __device__ __forceinline__ void hadamard(float (&v)[8], int lane, int d) {
   }
 }
 
+// The angle pos times freq (radians) in turns, less whole ones.  It reaches 2^31
+// times a frequency of 8, and 2^-53 of that is not little: 1 / 2 pi is the sum of
+// two fp64 numbers, and what each product leaves off is kept until the whole turns
+// are gone, which leaves an error of 2^-53 turns.  (Products are not to be joined
+// with what follows them, or what they leave off would count twice.)
+__device__ __forceinline__ double fraction_of_turn(double pos, double freq) {
+#pragma clang fp contract(off)
+  constexpr double kTurn = 0x1.45f306dc9c883p-3, kTurnRest = -0x1.6b01ec5417056p-57;
+  const double per = freq * kTurn, per_rest = fma(freq, kTurn, -per) + freq * kTurnRest;
+  const double turns = pos * per, rest = fma(pos, per, -turns) + pos * per_rest;
+  return (turns - rint(turns)) + rest;
+}
+
 // A lane's share of a token's turn: out = c v + s partner(v), with the partner
 // in lane `from` (pairs j, j + pairs) or in the same lane (interleaved pairs).
 template <int kLanes, bool kInter>
@@ -124,8 +137,8 @@ struct Turn {
   int from;
 
   // Each lane computes every 64th pair's angle, and gets what it needs from the
-  // others.  Angles reach 2^31 times a frequency: in turns and 64 bits until the
-  // whole turns are gone.  What fp64 leaves off is 2^-53 of the angle.
+  // others.  What the rounding of a fraction of a turn to fp32 leaves off turns sine
+  // and cosine once more.
   __device__ __forceinline__ void make(const QkArgs& a, int64_t token, int lane, float back) {
     constexpr int kRounds = kLanes <= 16 ? 1 : kLanes / 16;  // pairs are at most 4 to a lane of a head
     const int self = threadIdx.x & 63;
@@ -138,10 +151,12 @@ struct Turn {
       sn[r] = 0.0f;
       cs[r] = 1.0f;
       if (64 * r + self < a.pairs) {
-        double t = pos * (a.freqs[64 * r + self] * 0.15915494309189533577);
-        t -= rint(t);
-        sincospif(2.0f * (float)t, &sn[r], &cs[r]);
-        sn[r] *= back;
+        const double t = fraction_of_turn(pos, a.freqs[64 * r + self]);
+        const float near = (float)t, off = 6.28318530717958648f * (float)(t - (double)near);
+        float x, y;
+        sincospif(2.0f * near, &x, &y);
+        sn[r] = fmaf(y, off, x) * back;
+        cs[r] = fmaf(-x, off, y);
       }
     }
     const int e = 8 * lane;

@@ -1,12 +1,14 @@
 """What attention over a 4-bit cache and its heads compute, where a little less
-would not be seen in ordinary values: weights of one dominant key, heads at the
-ends of fp32's range, and gradients next to others that are not numbers.
+would not be seen in ordinary values: weights of one dominant key, angles of far
+positions, heads at the ends of fp32's range, and gradients next to others that
+are not numbers.
 
 Tolerances.  u = 2^-24 and h = 2^-8 are the largest relative errors of one
 rounding to fp32 and to bf16; half a step of bf16 at x is 2^(floor(log2 |x|) - 8).
 Each test says how its own follows from them.
 """
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -86,6 +88,54 @@ def test_a_key_that_outweighs_the_others_and_comes_late(tokens, heads):
     assert (err <= half_step(np.abs(want) + tol) + tol + 2.0 ** -19 * size).all(), (err / size).max()
     wl = np.log(np.exp(z).sum(-1))
     assert (np.abs(cpu(lse) - wl) <= 2.0 ** -20 + 2.0 ** -22 * np.abs(wl)).all()
+
+
+# -------------------------------------------------------------------- angles
+def _turns_of_a_radian(bits=400):
+    """1 / (2 pi) as a fraction, pi by Machin's formula."""
+    one = 1 << bits
+
+    def arctan(x):
+        total, term, n = 0, one // x, 1
+        while term:
+            total += term // n if n % 4 == 1 else -(term // n)
+            term //= x * x
+            n += 2
+        return total
+    return Fraction(one, 8 * (4 * arctan(5) - arctan(239)))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("wide", [False, True])
+def test_angles_of_far_positions(wide, interleaved):
+    """Positions next to the ends of their range and frequencies up to 8, against
+    angles reduced exactly.  A pair that is alone in its head: its square and root
+    6 u, products 3 u, cosine and sine 4 u off each and rounded once more, over the
+    pair 7 u: 2^-20 of the norm.  Whole heads 2^-19."""
+    say("far angles", wide, interleaved)
+    rng = np.random.default_rng(int(wide) + 2 * int(interleaved))
+    d, n = 48, 64
+    # three whose products with the rounded 1 / (2 pi) are far off, and others of all sizes
+    freqs = np.concatenate([[float.fromhex(x) for x in ("0x1.c349b066fca73p+2", "0x1.f2a18f4e1c580p+2", "0x1.c75b84f6199a9p+2")],
+                            rng.uniform(4, 8, 9), rng.uniform(1, 2, 6), 10.0 ** rng.uniform(-5, 0, 6)])
+    far = 2 ** 31 if wide else 2 ** 31 - 1
+    pos = np.concatenate([[far, -2 ** 31, far - 1, 0, 1], rng.integers(2 ** 31 - 5000, 2 ** 31, n - 25), -rng.integers(2 ** 30, 2 ** 31, 20)])
+    x = rng.standard_normal((n, 2, d)).astype(np.float32)
+    x[:, 1] = 0                                              # one pair alone in the second head
+    x[np.arange(n), 1, np.arange(n) % 24 * (2 if interleaved else 1)] = 1.0
+    y, _ = kv4.harp_qk_norm_rope(gpu(x), None, gpu(pos.astype(np.int64 if wide else np.int32)), gpu(freqs), eps=0.0,
+                                 interleaved=interleaved)
+    turn = _turns_of_a_radian()
+    parts = [[Fraction(int(p)) * Fraction(float(f)) * turn for f in freqs] for p in pos]
+    angle = np.array([[2 * math.pi * float(t - round(t)) for t in row] for row in parts])[:, None]
+    a, b = (slice(0, None, 2), slice(1, None, 2)) if interleaved else (slice(0, 24), slice(24, 48))
+    u = x.astype(np.float64)
+    u /= np.sqrt((u * u).mean(-1, keepdims=True))
+    want = np.zeros_like(u)
+    want[..., a] = u[..., a] * np.cos(angle) - u[..., b] * np.sin(angle)
+    want[..., b] = u[..., a] * np.sin(angle) + u[..., b] * np.cos(angle)
+    err = np.linalg.norm(cpu(y) - want, axis=-1) / math.sqrt(d)
+    assert err[:, 0].max() <= 2.0 ** -19 and err[:, 1].max() <= 2.0 ** -20, err.max(0)
 
 
 # --------------------------------------------------------- the ends of a range
