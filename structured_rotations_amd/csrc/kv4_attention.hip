@@ -291,19 +291,19 @@ __device__ __forceinline__ void wait_loads() {
 }
 // Loads straight into LDS, `lds` and on, lane by lane: 16 bytes from an address
 // that all lanes have in common and the lane's offset, or 4 from the lane's own
-// address.  kAt is added on both sides.
+// address.  kAt is added on both sides.  (The waits: see load_lds16 in q8.h.)
 template <int kAt>
 __device__ __forceinline__ void load_lds16_at(Global<uint8_t> base, uint32_t lane_offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3"
                :
                : "s"(lds), "v"(lane_offset), "s"(base), "n"(kAt)
                : "memory");
 }
 __device__ __forceinline__ void load_lds4_at(Global<uint8_t> base, uint32_t lane_offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" : : "s"(lds), "v"(lane_offset), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, %2" : : "s"(lds), "v"(lane_offset), "s"(base) : "memory");
 }
 __device__ __forceinline__ void load_lds4(uint64_t from, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(from) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(from) : "memory");
 }
 
 // The workspace: two slots of a tile's rows for each workgroup (values, then each

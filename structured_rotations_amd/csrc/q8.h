@@ -240,6 +240,12 @@ __device__ __forceinline__ float load_scale(const void* scales, int64_t i) {
 // zeros.  Written out, because the compiler would wait for such a load before
 // any later LDS read, of the other buffer too; the kernels wait for all of
 // them (vmcnt) before the barrier that precedes their first use.
+// Of the scalar registers that a load reads, any may have been written by the
+// vector unit just before (readfirstlane, or a register that the compiler had put
+// away into a vector's lanes), and the load has to be 5 wait states behind that.
+// The compiler sees to it for its own loads, not for these: hence the waits, once
+// for two loads of a tile where a kernel has them (64 x 13824 x 5120, bf16 results:
+// without 18.3 us, which was not safe, one by one 19.6, in pairs 19.1).
 using TileSrc = __amdgpu_buffer_rsrc_t;
 __device__ __forceinline__ TileSrc tile_src(const void* base, int bytes) {
   // both are the same in every lane; said so, or the loads may loop over lanes
@@ -253,9 +259,20 @@ __device__ __forceinline__ uint32_t lds_address(const void* lds) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds;
 }
 __device__ __forceinline__ void load_lds16(TileSrc src, uint32_t lds, unsigned lane_offset, int offset) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(lane_offset), "s"(src),
+                 "s"(__builtin_amdgcn_readfirstlane(offset))
+               : "memory");
+}
+// Two such loads of one tile.
+__device__ __forceinline__ void load_lds16_twice(TileSrc src, uint32_t lds0, unsigned lane_offset0, uint32_t lds1,
+                                                 unsigned lane_offset1, int offset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %4, %5 offen lds\n\t"
+               "s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %4, %5 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane((int)lds0)), "v"(lane_offset0),
+                 "s"(__builtin_amdgcn_readfirstlane((int)lds1)), "v"(lane_offset1), "s"(src),
                  "s"(__builtin_amdgcn_readfirstlane(offset))
                : "memory");
 }
@@ -264,12 +281,12 @@ template <int kBytes>
 __device__ __forceinline__ void load_lds_word(TileSrc src, uint32_t lds, unsigned lane_offset, int offset) {
   const int at = __builtin_amdgcn_readfirstlane((int)lds), from = __builtin_amdgcn_readfirstlane(offset);
   if constexpr (kBytes == 4)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds"
                  :
                  : "s"(at), "v"(lane_offset), "s"(src), "s"(from)
                  : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
                  :
                  : "s"(at), "v"(lane_offset), "s"(src), "s"(from)
                  : "memory");

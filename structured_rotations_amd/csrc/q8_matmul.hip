@@ -658,6 +658,7 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_ring_kernel(MatmulArgs g,
   constexpr int kScales = (BM + BN) * kQBlk, kBytes = kScales + 1024;
   constexpr int kRing = std::min(144 * 1024 / kBytes, 12);
   constexpr int LA = (BM / 8 + WAVES - 1) / WAVES, LW = BN / 8 / WAVES, kLoads = LA + LW + 1;  // per wave and step
+  static_assert(LW % 2 == 0 && (LA == 1 || LA % 2 == 0), "");
   // a step: W, A, and 64 words each from four waves: the row scales (waves 0
   // and 1), the weight's (2), words that nobody reads (the others)
   __shared__ __align__(16) uint8_t ring[kRing][kBytes];
@@ -691,16 +692,18 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_ring_kernel(MatmulArgs g,
     const int kk = min(kb * kQBlk, last);
     const uint32_t at = lds_ring + (uint32_t)(slot * kBytes);
     const bool ia = kb < kb1 && kb * kQBlk + pca < g.k, iw = kb < kb1 && kb * kQBlk + pcw < g.k;
+    const auto lds_w = [&](int i) { return at + (uint32_t)(wave + WAVES * i) * 1024; };
+    const auto from_w = [&](int i) { return iw ? vw + 8 * WAVES * i * (unsigned)g.ldw : kNoLoad; };
 #pragma unroll
-    for (int i = 0; i < LW; ++i)
-      load_lds16(rw, at + (uint32_t)(wave + WAVES * i) * 1024, iw ? vw + 8 * WAVES * i * (unsigned)g.ldw : kNoLoad, kk);
+    for (int i = 0; i < LW; i += 2) load_lds16_twice(rw, lds_w(i), from_w(i), lds_w(i + 1), from_w(i + 1), kk);
+    // 16 rows: two waves' worth; the others' zeros go where nobody reads
+    const bool mine = BM >= 8 * WAVES || wave < BM / 8;
+    const auto lds_a = [&](int i) { return mine ? at + (uint32_t)(BN * kQBlk + (wave + WAVES * i) * 1024) : lds_spare; };
+    const auto from_a = [&](int i) { return ia && mine ? va + 8 * WAVES * i * (unsigned)g.lda : kNoLoad; };
+    if constexpr (LA == 1) load_lds16(ra, lds_a(0), from_a(0), kk);
+    else
 #pragma unroll
-    for (int i = 0; i < LA; ++i) {
-      // 16 rows: two waves' worth; the others' zeros go where nobody reads
-      const bool mine = BM >= 8 * WAVES || wave < BM / 8;
-      load_lds16(ra, mine ? at + (uint32_t)(BN * kQBlk + (wave + WAVES * i) * 1024) : lds_spare,
-                 ia && mine ? va + 8 * WAVES * i * (unsigned)g.lda : kNoLoad, kk);
-    }
+      for (int i = 0; i < LA; i += 2) load_lds16_twice(ra, lds_a(i), from_a(i), lds_a(i + 1), from_a(i + 1), kk);
     load_lds_word<kSB>(rs, at + (uint32_t)(kScales + min(wave, 3) * 256), vs, min(kb, kb1 - 1) * kSB);
   };
 
