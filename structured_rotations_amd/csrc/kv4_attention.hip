@@ -294,16 +294,22 @@ __device__ __forceinline__ void wait_loads() {
 // address.  kAt is added on both sides.  (The waits: see load_lds16 in q8.h.)
 template <int kAt>
 __device__ __forceinline__ void load_lds16_at(Global<uint8_t> base, uint32_t lane_offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3"
-               :
+  uint32_t m0;
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %2, %3 offset:%4"
+               : "={m0}"(m0)
                : "s"(lds), "v"(lane_offset), "s"(base), "n"(kAt)
                : "memory");
 }
 __device__ __forceinline__ void load_lds4_at(Global<uint8_t> base, uint32_t lane_offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, %2" : : "s"(lds), "v"(lane_offset), "s"(base) : "memory");
+  uint32_t m0;
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tglobal_load_lds_dword %2, %3"
+               : "={m0}"(m0)
+               : "s"(lds), "v"(lane_offset), "s"(base)
+               : "memory");
 }
 __device__ __forceinline__ void load_lds4(uint64_t from, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(from) : "memory");
+  uint32_t m0;
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tglobal_load_lds_dword %2, off" : "={m0}"(m0) : "s"(lds), "v"(from) : "memory");
 }
 
 // The workspace: two slots of a tile's rows for each workgroup (values, then each

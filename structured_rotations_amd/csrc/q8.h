@@ -239,7 +239,9 @@ __device__ __forceinline__ float load_scale(const void* scales, int64_t i) {
 // bytes of LDS at a wave-uniform address.  Lanes at or beyond `bytes` give
 // zeros.  Written out, because the compiler would wait for such a load before
 // any later LDS read, of the other buffer too; the kernels wait for all of
-// them (vmcnt) before the barrier that precedes their first use.
+// them (vmcnt) before the barrier that precedes their first use.  m0, which has
+// the place in LDS, is named as a result, or the compiler would not know that it
+// has changed (it takes no clobber of it).
 // Of the scalar registers that a load reads, any may have been written by the
 // vector unit just before (readfirstlane, or a register that the compiler had put
 // away into a vector's lanes), and the load has to be 5 wait states behind that.
@@ -259,8 +261,9 @@ __device__ __forceinline__ uint32_t lds_address(const void* lds) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds;
 }
 __device__ __forceinline__ void load_lds16(TileSrc src, uint32_t lds, unsigned lane_offset, int offset) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :
+  uint32_t m0;
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds"
+               : "={m0}"(m0)
                : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(lane_offset), "s"(src),
                  "s"(__builtin_amdgcn_readfirstlane(offset))
                : "memory");
@@ -268,9 +271,10 @@ __device__ __forceinline__ void load_lds16(TileSrc src, uint32_t lds, unsigned l
 // Two such loads of one tile.
 __device__ __forceinline__ void load_lds16_twice(TileSrc src, uint32_t lds0, unsigned lane_offset0, uint32_t lds1,
                                                  unsigned lane_offset1, int offset) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %4, %5 offen lds\n\t"
-               "s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %4, %5 offen lds"
-               :
+  uint32_t m0;
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tbuffer_load_dwordx4 %2, %5, %6 offen lds\n\t"
+               "s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, %5, %6 offen lds"
+               : "={m0}"(m0)
                : "s"(__builtin_amdgcn_readfirstlane((int)lds0)), "v"(lane_offset0),
                  "s"(__builtin_amdgcn_readfirstlane((int)lds1)), "v"(lane_offset1), "s"(src),
                  "s"(__builtin_amdgcn_readfirstlane(offset))
@@ -280,14 +284,15 @@ __device__ __forceinline__ void load_lds16_twice(TileSrc src, uint32_t lds0, uns
 template <int kBytes>
 __device__ __forceinline__ void load_lds_word(TileSrc src, uint32_t lds, unsigned lane_offset, int offset) {
   const int at = __builtin_amdgcn_readfirstlane((int)lds), from = __builtin_amdgcn_readfirstlane(offset);
+  uint32_t m0;
   if constexpr (kBytes == 4)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                 :
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tbuffer_load_dword %2, %3, %4 offen lds"
+                 : "={m0}"(m0)
                  : "s"(at), "v"(lane_offset), "s"(src), "s"(from)
                  : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
-                 :
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tbuffer_load_ubyte %2, %3, %4 offen lds"
+                 : "={m0}"(m0)
                  : "s"(at), "v"(lane_offset), "s"(src), "s"(from)
                  : "memory");
 }

@@ -44,6 +44,15 @@ def test_memory_instructions_wait_for_scalar_registers(path):
             states += int(code.split()[1]) + 1 if code.startswith("s_nop") else 1
 
 
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_m0_is_named_where_it_is_written(path):
+    """The compiler uses m0 for itself and takes no clobber of it: assembly that
+    writes it names it as a result."""
+    for block in asm_blocks(open(path).read()):
+        if any(re.match(r"s_\w+ m0,", code) for code in instructions(block)):
+            assert '"={m0}"(' in block, block
+
+
 def test_the_rules_see_what_they_are_for():
     found = [b for p in SOURCES for b in asm_blocks(open(p).read()) if any(re.match(MEMORY, c) for c in instructions(b))]
     assert len(found) == 7
