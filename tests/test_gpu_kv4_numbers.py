@@ -1,7 +1,7 @@
 """What attention over a 4-bit cache and its heads compute, where a little less
 would not be seen in ordinary values: weights of one dominant key, angles of far
-positions, heads at the ends of fp32's range, and gradients next to others that
-are not numbers.
+positions, heads at the ends of fp32's range, gradients next to others that are not
+numbers, and every code with every scale.
 
 Tolerances.  u = 2^-24 and h = 2^-8 are the largest relative errors of one
 rounding to fp32 and to bf16; half a step of bf16 at x is 2^(floor(log2 |x|) - 8).
@@ -190,3 +190,21 @@ def test_gradients_that_are_not_numbers_stay_with_their_own_gamma(hq, hk, d):
     assert torch.isnan(r.dgamma_k[20]) and not torch.isfinite(r.dgamma_k[30])
     r = kv4.harp_qk_norm_rope_vjp(q, k, pos, f, bad_q, dk, g, g)
     assert torch.equal(r.dgamma_k, good.dgamma_k) and torch.equal(r.dk, good.dk) and not torch.isfinite(r.dgamma_q[20])
+
+
+# ----------------------------------------------------------------- the format
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_every_code_and_scale_is_read_as_it_stands(out):
+    """All pairs of codes with all scales, also those that a cache written here
+    does not hold: exact where the type holds the value, infinite beyond it."""
+    say("all codes", out)
+    codes = np.arange(256, dtype=np.uint8).reshape(16, 16)
+    codes = np.ascontiguousarray(np.broadcast_to(codes[None, :, None], (16, 16, 16, 16)))          # page, head, place, byte
+    scales = np.arange(256, dtype=np.uint8).reshape(16, 1, 16, 1).repeat(16, 1)
+    cache = kv4.Cache4(gpu(codes), gpu(scales).view(kv4.SCALES), gpu(codes), gpu(scales).view(kv4.SCALES))
+    plan = ([0, 256], [256], [list(range(16))])
+    k, v = kv4.harp_kv4_read(cache, *(torch.tensor(x, dtype=torch.int32, device="cuda") for x in plan), 256, out)
+    want = K.sequence(codes, scales, np.arange(16), 256).transpose(1, 0, 2)
+    with np.errstate(over="ignore"):
+        want = want.astype(np.float32).astype(np.float64)
+    assert np.array_equal(cpu(k), want, equal_nan=True) and np.array_equal(cpu(v), want, equal_nan=True)
