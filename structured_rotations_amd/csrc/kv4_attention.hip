@@ -1374,8 +1374,9 @@ Cut cut_of(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t
   const int64_t items = std::max<int64_t>(1, std::max(rows / c.rows, std::min(sequences, tokens)) * kv_heads);
   if (c.rows < 128) {
     const int64_t room = kUnits * room_for((int)d / 32, c.rows / 16);
-    // steps, if every sequence fills the table
-    const int64_t most = c.tiles * kv_heads * ((keys + 31) / 32 + 2 + kItemSteps);
+    // steps, if every sequence fills the table; a million of one item are more than enough parts (and the product of all
+    // sizes at their ends is more than 63 bits)
+    const int64_t most = c.tiles * kv_heads * (std::min<int64_t>((keys + 31) / 32, 1 << 20) + 2 + kItemSteps);
     if (items < 4 * room) c.groups = (int)std::min(room, (most + kLeastSteps - 1) / kLeastSteps);
   } else {
     const int64_t most = std::max<int64_t>(1, (keys + 127) / 128);
