@@ -471,8 +471,9 @@ harp_status harp_matmul_q8_wgrad(const void* dy, int64_t lddy, const uint8_t* x,
  * gamma_q, gamma_k: d values of io_dtype.  positions: one per token, int32 or
  * int64 (wide_positions != 0), of magnitude up to 2^31.  freqs: `pairs` fp64
  * values, radians per position (at most 8 in magnitude).  signs: d int8, +1 or -1.
- * Computed in fp32 (squares beyond its range included, as in harp_rmsnorm_q8),
- * angles in fp64 until they are reduced; y is rounded once.
+ * Computed in fp32 (heads of any size: squares, and 1 / sqrt, beyond its range
+ * included), angles in fp64 until they are reduced (off by at most 2^-53 turns);
+ * y is rounded once.
  * d: a multiple of 8 up to 512, with signs a power of two; pairs: a multiple
  * of 8, 2 pairs <= d (0: no turn).  k NULL (k_heads 0): queries only.  q_out
  * may be q and k_out k, with the same distances; other overlaps are refused.

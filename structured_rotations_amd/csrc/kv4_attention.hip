@@ -19,15 +19,15 @@
 // the heaviest too, since a row's weights go by a reference that its largest score
 // may pass.
 // - Tiles of 16 rows: what the rounding left off goes into a second product, which
-//   leaves 2^-16 of a weight, and the result off by its own rounding only (1.6e-3 in
-//   relative l2 against 64 bits; with one product 1.8e-3).  Bytes bound this kernel:
+//   leaves 2^-16 of a weight, and the result off by its own rounding only (1.57e-3
+//   in relative l2 against 64 bits; with one product 1.7e-3).  Bytes bound this kernel:
 //   64 x 1 over 50 .. 8192 keys, 32/8 x 128, 71.5 us, with one product 69.8.
 // - Tiles of 32 and 128 rows: products and vector work count, and a second product
 //   costs more (64 x 8 over 4096, 64/8 x 128: 150 us, one 134; 4 x 2048 over 8192, 32/8 x
 //   128: 832, one 640).  There is one, and what divides it is the sum of the weights as
 //   they were rounded (138 and 656 us): rounding then moves a result by up to 2^-8 of the
 //   values' distances from it, not of the values, and a row with one heavy key not at
-//   all.  (4 x 2048 over 2048 .. 8192: off by 1.7e-3, by the result's rounding alone 1.5e-3.)
+//   all.  (4 x 2048 over 2048 .. 8192: off by 1.69e-3, by the result's rounding alone 1.57e-3.)
 //   lse takes the sum of the weights as they were.
 #include <algorithm>
 #include <climits>
@@ -206,7 +206,7 @@ constexpr float kSlack = 8.0f;
 // straight into a ring of its own in LDS, kDepth - 1 steps ahead: what keeps HBM
 // busy is bytes in flight, and registers are too few for them.  No barrier is
 // needed: a wave reads what it loaded itself.  (64 x 1 over 16384, 32/8 x 128:
-// 216 us, 5.3 TB/s; a copy of this kernel without its arithmetic reads 5.2 to 5.5
+// 218 us, 5.2 TB/s; a copy of this kernel without its arithmetic reads 5.2 to 5.5
 // TB/s, so what is left there is the order of the reads.)
 //
 // A step in LDS, of two halves of 16 keys each (their pages may differ):
@@ -237,13 +237,14 @@ struct Step4 {
 // finishes items that are its own as a whole; of others it leaves parts: in its
 // first slot that of the item that began before it, in its second slot that of
 // the one that it begins and does not end.  (64 x 1 over 50 .. 8192 keys, 32/8 x
-// 128: 70 us; cut as for sequences of the table's width, one workgroup for an
-// item or a fixed fraction of one: 82.  64 x 4 over 4096: 76, not 100.)
+// 128, with one product for V: 70 us; cut as for sequences of the table's width, one
+// workgroup for an item or a fixed fraction of one: 82.  64 x 4 over 4096: 76, not 100.)
 //
 // Where there are many items for each workgroup (see cut_of) each has one of its
 // own instead, and the chip's scheduler evens them out: the way from one item to
 // the next costs a workgroup about as much as 12 steps, mostly waiting, which
-// another workgroup's start does not (1024 x 1 over 1024: 235 us, not 257).
+// another workgroup's start does not (1024 x 1 over 1024, with one product for V: 235
+// us, not 257; with two 243).
 constexpr int kLeastSteps = 8;  // of a part
 constexpr int kItemSteps = 12;  // what an item weighs besides its steps, half of it on either side of them
 struct Work {
@@ -331,8 +332,9 @@ __device__ __forceinline__ Slots slots_of(float* workspace, int groups, int tile
 }
 
 // Workgroups a compute unit is to have room for, which bounds the registers: as
-// many as these and LDS allow without spilling (64 x 1 over 4096, d = 192: 2 58 us,
-// 3, of 168 registers, 63; d = 96: 3 and 4, of 128, 64).
+// many as these and LDS allow without spilling (one register of heads of 160 in tiles
+// of 32 rows is) (64 x 1 over 4096, d = 192, 16 heads: 2 58 us, 3, of 168 registers, 63;
+// d = 96: 3 and 4, of 128, 64).
 constexpr int room_for(int nd, int nq) {
   return nq == 1 ? (nd <= 2 ? 4 : nd <= 4 ? 3 : 2) : nd == 1 ? 4 : nd == 2 ? 3 : nd <= 5 ? 2 : 1;
 }
@@ -888,8 +890,8 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
 // next 64 keys, straight from memory into the fragments of the 32 x 32 x 16
 // instruction, and writes them to LDS as they are read, 16 bytes a lane one
 // after the other, while the products of the present 64 keys run.
-// 4 x 2048 over 8192, 32/8 x 128: 646 to 655 us, 930 to 945 TFLOP/s.  The matrix
-// units are busy 39% of the time, the vector units 52 to 61% (a third of it the
+// 4 x 2048 over 8192, 32/8 x 128: 656 to 680 us, 900 to 930 TFLOP/s.  The matrix
+// units are busy 38% of the time, the vector units 52 to 61% (a third of it the
 // exponentials), LDS half; two waves a SIMD, one with products and one with
 // vector work, take 1.5 times as long as the longer of them alone.
 // 256 rows a workgroup, four of its eight waves widening K and four V, halve the
@@ -897,8 +899,8 @@ __global__ __launch_bounds__(256, room_for(ND, NQ)) void kv4_attention_kernel(At
 // priority while products run (714).
 // Of kAll products and the reads of LDS that they need, in this order: kAhead reads,
 // then one after every product.  (Left alone, the reads come one or two ahead, and
-// each product waits: 4 x 2048 over 8192, 32/8 x 128: 663, not 655 us; 2 x 1024
-// over 4096 with d = 256: 251, not 233, 6 ahead 243.)
+// each product waits: 4 x 2048 over 8192, 32/8 x 128: 1% more; 2 x 1024 over 4096
+// with d = 256: 7%, and 6 ahead 4%.)
 template <int kAll, int kAhead>
 __device__ __forceinline__ void read_ahead() {
   constexpr int ahead = kAhead < kAll ? kAhead : kAll;
@@ -1354,10 +1356,17 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Attn4Args a, int groups, 
 constexpr int kMostSplits = 256, kUnits = 256;  // parts, compute units
 
 // How a call is cut: tiles of 16, 32 or 128 rows, by the rows that a sequence
-// has on average.  Few rows: equal parts (`groups`) for as many workgroups as
-// have room, or an item to each workgroup (0) from 4 items for each such place
-// on (256 x 1 over 1024 has 2.7: 77 us in parts, 71 in items; over 20 .. 2048: 83
-// and 83, and the worse the longer one sequence is next to the others).  Many:
+// has on average.  Over 4096 keys, 32/8 heads, in tiles of 16, 32 and 128:
+//   rows to a key head       16             20             64             80            128       256 (4 sequences)
+//   64 sequences, d = 128    76  74 112    106  76 201    194 139 209    261 208 223    309 243 289    65 46 45
+//   d = 64                   45  58  97     67  60  97    128 103 114    162 131 144    220 185 201
+//   d = 256                 114 167 419    180 169 619    303 380 634    428 505 642    574 600 876
+// (From 65 rows to about 128, and for d = 256 from 33, another choice would gain 5 to
+// 25%; beyond, the tiles of 128 win by the more the more rows there are.)
+// Tiles of 16 and 32: equal parts (`groups`) for as many workgroups as have room,
+// or an item to each workgroup (0) from 4 items for each such place on (256 x 1 over
+// 1024 has 2.7, with one product for V: 77 us in parts, 71 in items; over 20 .. 2048: 83
+// and 83, and the worse the longer one sequence is next to the others).  Tiles of 128:
 // the keys in `splits` parts until the chip has work enough.
 struct Cut {
   int rows, groups, splits;

@@ -292,7 +292,8 @@ __device__ __forceinline__ void load_gamma(const void* gamma, int col, bool has,
 __device__ __forceinline__ float least_of(float eps) { return eps < 0x1p-100f ? 0x1p-80f : 0.0f; }
 
 // A wave takes `per` heads of a token.  16384 x 32+8 x 128 in bf16, 336 MB: 63 to 66
-// us, 5.1 to 5.3 TB/s, which is a copy's rate; the vector unit is busy 86% of it.
+// us, 5.1 to 5.3 TB/s, which is a copy's rate; the vector unit is busy 86% of it.  In
+// fp32 148 us, 4.5 TB/s.
 // One token: 3.7 us.
 template <typename T, int kLanes, bool kInter, bool kStream>
 __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs a, int per, int parts) {
@@ -344,7 +345,8 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs a, int per, in
 // The reverse mode: workgroups walk over the parts of tokens, keeping their
 // lanes' shares of the two dgammas in registers; the shares of a workgroup are
 // added in order through LDS, those of the workgroups by the second kernel.  16384
-// x 32+8 x 128 in bf16, 503 MB: 99 to 104 us with it, 4.8 to 5.1 TB/s.
+// x 32+8 x 128 in bf16, 503 MB: 100 to 106 us with it, 4.7 to 5.0 TB/s; in fp32, 1007
+// MB, 216 us, 4.7 TB/s, though 13 of its 128 registers spill.
 template <typename T, int kLanes, bool kInter, bool kStream>
 __global__ __launch_bounds__(256, 4) void qk_norm_rope_vjp_kernel(QkArgs a, int per, int parts) {
   const HeadMap<kLanes> map(a.d);
